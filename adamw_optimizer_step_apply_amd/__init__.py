@@ -43,7 +43,7 @@ _STATUS = {0: "ADAMW_OK", 1: "ADAMW_E_INVALID", 2: "ADAMW_E_UNSUPPORTED", 3: "AD
 
 EXPORTED = ("adamw_step", "adamw_multi_tensor_step", "adamw_multi_tensor_step_noalloc", "adamw_multi_tensor_step_amp",
             "adamw_pure_multi_tensor_step",
-            "adamw_check_finite",
+            "adamw_check_finite", "adamw_grad_norm", "adamw_tensor_norms",
             "adamw_last_error", "adamw_release_workspace", "adamw_abi_version", "adamw_plan_inspect",
             "adamw_plan_inspect_bytes", "adamw_set_chunk_elems", "adamw_set_single_launch_max_workgroups",
             "adamw_blocked_state_bytes", "adamw_blocked_state_copy")
@@ -100,6 +100,10 @@ def _declare(_lib):
                                                   _vp, _vp, _vp]
     _lib.adamw_check_finite.restype = ctypes.c_int
     _lib.adamw_check_finite.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list), _vp, _vp]
+    _lib.adamw_grad_norm.restype = ctypes.c_int
+    _lib.adamw_grad_norm.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list), ctypes.c_int, _vp, _vp, _vp, _vp]
+    _lib.adamw_tensor_norms.restype = ctypes.c_int
+    _lib.adamw_tensor_norms.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list), _vp, _vp, _vp, _vp]
     _lib.adamw_last_error.restype = ctypes.c_char_p
     _lib.adamw_last_error.argtypes = []
     _lib.adamw_release_workspace.restype = None
@@ -126,7 +130,7 @@ def _declare(_lib):
 
 
 _load(LIB_PATH)
-ABI_VERSION = 8               # ADAMW_ABI_VERSION of the header this binding follows
+ABI_VERSION = 9               # ADAMW_ABI_VERSION of the header this binding follows
 if _lib.adamw_abi_version() != ABI_VERSION:
     raise ImportError(f"{LIB_PATH} has ABI version {_lib.adamw_abi_version()}, this binding expects {ABI_VERSION}: "
                       "rebuild the library")
@@ -324,6 +328,25 @@ def adamw_check_finite(g_dtype: int, grads: TensorList, d_found_inf, stream=None
     _check(_lib.adamw_check_finite(g_dtype, ctypes.byref(grads.c), _addr(d_found_inf), _stream(stream)))
 
 
+def adamw_grad_norm(g_dtype: int, grads: TensorList, d_sumsq, d_norm=None, d_found_inf=None,
+                    accumulate: bool = False, stream=None) -> None:
+    """The global gradient norm: the list's sum of squares into ``d_sumsq`` (one
+    float64; added to it with ``accumulate``), its square root into ``d_norm``
+    (one float32) and whether it is inf or NaN into ``d_found_inf`` (one int32)
+    (C ABI adamw_grad_norm)."""
+    _check(_lib.adamw_grad_norm(g_dtype, ctypes.byref(grads.c), int(bool(accumulate)), _addr(d_sumsq), _addr(d_norm),
+                                _addr(d_found_inf), _stream(stream)))
+
+
+def adamw_tensor_norms(g_dtype: int, grads: TensorList, d_tensor_norms=None, d_tensor_sumsq=None, d_sumsq=None,
+                       stream=None) -> None:
+    """Every tensor's norm into ``d_tensor_norms`` (float32, one per tensor) and sum
+    of squares into ``d_tensor_sumsq`` (float64), and the list's sum of squares into
+    ``d_sumsq`` (C ABI adamw_tensor_norms)."""
+    _check(_lib.adamw_tensor_norms(g_dtype, ctypes.byref(grads.c), _addr(d_tensor_norms), _addr(d_tensor_sumsq),
+                                   _addr(d_sumsq), _stream(stream)))
+
+
 def adamw_last_error() -> str:
     return (_lib.adamw_last_error() or b"").decode()
 
@@ -336,8 +359,9 @@ def adamw_abi_version() -> int:
     return _lib.adamw_abi_version()
 
 
-def adamw_plan_inspect(mode: int, p_dtype: int, tensors: TensorList, for_check: bool = False):
-    """The chunk plan as a list of (tensor, offset_in_tensor, count, is_vector, flat_pos, segment)."""
+def adamw_plan_inspect(mode: int, p_dtype: int, tensors: TensorList, for_check: int = False):
+    """The chunk plan as a list of (tensor, offset_in_tensor, count, kind, flat_pos, segment);
+    ``for_check`` 1 for the overflow check's, 2 for the gradient norms'."""
     n = _lib.adamw_plan_inspect(mode, p_dtype, ctypes.byref(tensors.c), int(for_check), None, 0)
     if n < 0:
         raise AdamWError(E_INVALID, adamw_last_error())

@@ -16,6 +16,7 @@
 #include <map>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 #include <utility>
 #include <vector>
@@ -47,8 +48,10 @@ adamw_status hip_fail(const char* what, hipError_t e)
 
 namespace {
 
-// A device-resident copy of one plan (segment table followed by chunk table),
-// uploaded through a pinned staging buffer.
+// A device-resident copy of one plan (segment table, chunk table and, for a
+// gradient sweep, the tensors' first chunks), uploaded through a pinned staging
+// buffer.  A sweep's plan is followed by room for its partial sums, so that two
+// lists, and a captured graph and later calls, never share them.
 struct PlanSlot {
     void* dev = nullptr;
     size_t dev_cap = 0;
@@ -59,12 +62,24 @@ struct PlanSlot {
     std::vector<int64_t> key;
     bool valid = false;
     bool pinned = false;   // used under graph capture: never evicted, resized or rewritten
-    int64_t n_segs = 0, n_chunks = 0;
+    int64_t n_segs = 0, n_chunks = 0, n_tensors = 0;
 
     const DevSeg* segs() const { return static_cast<const DevSeg*>(dev); }
     const DevChunk* chunks() const
     {
         return reinterpret_cast<const DevChunk*>(static_cast<const char*>(dev) + n_segs * sizeof(DevSeg));
+    }
+    const uint32_t* tensor_first() const { return reinterpret_cast<const uint32_t*>(chunks() + n_chunks); }
+    double* partials() const
+    {
+        return reinterpret_cast<double*>(static_cast<char*>(dev) + sweep_table_bytes(n_segs, n_chunks, n_tensors));
+    }
+    // A sweep's tables, rounded up to the alignment of what follows.
+    static size_t sweep_table_bytes(int64_t segs, int64_t chunks, int64_t tensors)
+    {
+        const size_t b = (size_t)segs * sizeof(DevSeg) + (size_t)chunks * sizeof(DevChunk) +
+                         (size_t)(tensors + 1) * sizeof(uint32_t);
+        return (b + 15) / 16 * 16;
     }
 
     void release()
@@ -101,9 +116,20 @@ std::atomic<int64_t> g_chunk_elems{0};   // 0: each kernel's own default chunk
 // forms the step's scalars itself) instead of prologue + update kernel.
 std::atomic<int64_t> g_single_launch_max_workgroups{kSingleLaunchMaxWorkgroups};
 
-// The chunk limit of a plan for `tag` (an update kernel id, or -1 for the
-// overflow check): the grid of one launch holds at most 2^32 - 1 lanes.
-int64_t max_chunks_of(int64_t tag) { return tag < 0 ? kMaxCheckChunks : kMaxUpdateChunks; }
+// The chunk limit of a plan for `tag` (an update kernel id, kTagCheck or
+// kTagSweep): the grid of one launch holds at most 2^32 - 1 lanes.
+int64_t max_chunks_of(int64_t tag)
+{
+    return tag == kTagSweep ? kMaxSweepChunks : tag == kTagCheck ? kMaxCheckChunks : kMaxUpdateChunks;
+}
+
+adamw_status plan_of(int64_t tag, const int esz[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,
+                     Plan* out, std::string& err)
+{
+    if (tag == kTagSweep)
+        return build_sweep_plan(esz[ADAMW_STREAM_GRAD], list, chunk_elems, max_chunks_of(tag), out, err);
+    return build_plan(esz, list, chunk_elems, max_chunks_of(tag), out, err);
+}
 
 // The workspace of a stream, on the stream's own device.
 adamw_status get_workspace(hipStream_t stream, StreamWorkspace** out)
@@ -150,7 +176,7 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     }
     Plan plan;
     std::string err;
-    adamw_status st = build_plan(esz, list, chunk_elems, max_chunks_of(tag), &plan, err);
+    adamw_status st = plan_of(tag, esz, list, chunk_elems, &plan, err);
     if (st != ADAMW_OK) return fail(st, err);
     if (under_capture)
         return fail(ADAMW_E_INVALID,
@@ -167,7 +193,14 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     *out = &slot;
 
     const size_t seg_bytes = plan.segs.size() * sizeof(DevSeg);
-    const size_t bytes = seg_bytes + plan.chunks.size() * sizeof(DevChunk);
+    const size_t chunk_bytes = plan.chunks.size() * sizeof(DevChunk);
+    const size_t first_bytes = plan.tensor_first.size() * sizeof(uint32_t);   // 0 but for a sweep
+    const size_t bytes = seg_bytes + chunk_bytes + first_bytes;
+    size_t dev_bytes = bytes;
+    if (tag == kTagSweep)
+        dev_bytes = PlanSlot::sweep_table_bytes((int64_t)plan.segs.size(), (int64_t)plan.chunks.size(),
+                                                list->n_tensors) +
+                    plan.chunks.size() * sizeof(double);
     hipError_t e;
     if (!slot.uploaded) {
         e = hipEventCreateWithFlags(&slot.uploaded, hipEventDisableTiming);
@@ -187,7 +220,7 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
         if (e != hipSuccess) { slot.host_cap = 0; slot.valid = false; return fail(ADAMW_E_NOMEM, "hipHostMalloc failed"); }
         slot.host_cap = cap;
     }
-    if (bytes > slot.dev_cap) {
+    if (dev_bytes > slot.dev_cap) {
         if (slot.dev) {
             // queued kernels on this stream may still read the old table
             e = hipStreamSynchronize(stream);
@@ -195,14 +228,16 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
             (void)hipFree(slot.dev);
             slot.dev = nullptr;
         }
-        size_t cap = bytes + bytes / 4 + 4096;
+        size_t cap = dev_bytes + dev_bytes / 4 + 4096;
         e = hipMalloc(&slot.dev, cap);
         if (e != hipSuccess) { slot.dev_cap = 0; slot.valid = false; return fail(ADAMW_E_NOMEM, "hipMalloc of the chunk table failed"); }
         slot.dev_cap = cap;
     }
     if (bytes) {
         memcpy(slot.host, plan.segs.data(), seg_bytes);
-        memcpy(static_cast<char*>(slot.host) + seg_bytes, plan.chunks.data(), plan.chunks.size() * sizeof(DevChunk));
+        memcpy(static_cast<char*>(slot.host) + seg_bytes, plan.chunks.data(), chunk_bytes);
+        if (first_bytes)
+            memcpy(static_cast<char*>(slot.host) + seg_bytes + chunk_bytes, plan.tensor_first.data(), first_bytes);
         e = hipMemcpyAsync(slot.dev, slot.host, bytes, hipMemcpyHostToDevice, stream);
         if (e != hipSuccess) { slot.valid = false; return hip_fail("hipMemcpyAsync (chunk table)", e); }
         e = hipEventRecord(slot.uploaded, stream);
@@ -211,6 +246,7 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     }
     slot.n_segs = (int64_t)plan.segs.size();
     slot.n_chunks = (int64_t)plan.chunks.size();
+    slot.n_tensors = list->n_tensors;
     slot.key.swap(key);
     slot.valid = true;
     return ADAMW_OK;
@@ -252,7 +288,7 @@ adamw_status validate_list(int64_t tag, const int esz[kStreams], const adamw_ten
     plan_key(tag, esz, list, chunk_elems, key);
     if (validated_before(key)) return ADAMW_OK;
     std::string err;
-    adamw_status st = build_plan(esz, list, chunk_elems, max_chunks_of(tag), nullptr, err);
+    adamw_status st = plan_of(tag, esz, list, chunk_elems, nullptr, err);
     if (st != ADAMW_OK) return fail(st, err);
     remember_validated(key);
     return ADAMW_OK;
@@ -317,6 +353,12 @@ int64_t check_chunk_elems()
     return c ? c : kCheckChunkElems;
 }
 
+int64_t sweep_chunk_elems(int esz)
+{
+    const int64_t c = g_chunk_elems.load(std::memory_order_relaxed);
+    return c ? c : kSweepChunkBytes / esz;
+}
+
 // Row i of adamw_plan_inspect: {tensor, offset in the tensor, count, kind, flat position, segment}.
 void inspect_row(const Plan& plan, size_t i, int64_t* r)
 {
@@ -325,7 +367,7 @@ void inspect_row(const Plan& plan, size_t i, int64_t* r)
     r[0] = si.tensor;
     r[1] = si.tensor_off + (int64_t)c.off;
     r[2] = (int64_t)(c.n_kind & kCountMask);
-    r[3] = (c.n_kind & kVecBit) ? 1 : 0;
+    r[3] = (c.n_kind & kVecBit) ? (plan.tensor_first.empty() ? 1 : 2) : 0;
     r[4] = si.flat + (int64_t)c.off;
     r[5] = (int64_t)c.seg;
 }
@@ -352,6 +394,58 @@ adamw_status do_step(const StepKind& kind, const adamw_tensor_list* list, const 
         return st;
     return enqueue_step(kind, plan->segs(), plan->chunks(), plan->n_chunks, ws->scalars, done, *hp, d_step,
                         d_found_inf, d_amp, scaler, stream);
+}
+
+// What a gradient sweep launches over: the plan on the device and the stream's
+// workspace.
+struct Sweep {
+    StreamWorkspace* ws = nullptr;
+    std::unique_lock<std::mutex> lk;
+    std::unique_ptr<DeviceGuard> dg;
+    PlanSlot* plan = nullptr;
+    uint32_t* done = nullptr;
+    hipStream_t stream = nullptr;
+};
+
+// Checks the list of a sweep over elements of `esz` bytes (before any HIP call)
+// and readies its plan.  The lock and the device stay with *out.
+adamw_status begin_sweep(int esz_g, const adamw_tensor_list* grads, void* hip_stream, Sweep* out)
+{
+    adamw_status st;
+    if ((st = basic_list_check(grads)) != ADAMW_OK) return st;
+    int esz[kStreams] = {0, 0, 0, 0, 0};
+    esz[ADAMW_STREAM_GRAD] = esz_g;
+    const int64_t chunk_elems = sweep_chunk_elems(esz_g);
+    if ((st = validate_list(kTagSweep, esz, grads, chunk_elems)) != ADAMW_OK) return st;
+    out->stream = static_cast<hipStream_t>(hip_stream);
+    if ((st = get_workspace(out->stream, &out->ws)) != ADAMW_OK) return st;
+    out->lk = std::unique_lock<std::mutex>(out->ws->mu);
+    out->dg.reset(new DeviceGuard(out->ws->device));
+    bool cap = false;
+    if ((st = capturing(out->stream, &cap)) != ADAMW_OK) return st;
+    if ((st = ensure_workspace_block(*out->ws, out->stream, cap, &out->done)) != ADAMW_OK) return st;
+    return ensure_plan(*out->ws, kTagSweep, esz, grads, chunk_elems, out->stream, cap, &out->plan);
+}
+
+adamw_status sum_of_squares(adamw_dtype g_dtype, const adamw_tensor_list* grads, const NormOut& out, void* hip_stream)
+{
+    std::string err;
+    int esz = 0;
+    adamw_status st = check_sweep_dtype(g_dtype, &esz, err);
+    if (st != ADAMW_OK) return fail(st, err);
+    if ((uintptr_t)out.sumsq % 8 || (uintptr_t)out.tensor_sumsq % 8)
+        return fail(ADAMW_E_INVALID, "d_sumsq / d_tensor_sumsq must be 8-byte aligned");
+    if ((uintptr_t)out.norm % 4 || (uintptr_t)out.found_inf % 4 || (uintptr_t)out.tensor_norm % 4)
+        return fail(ADAMW_E_INVALID, "d_norm / d_found_inf / d_tensor_norms must be 4-byte aligned");
+    if ((out.tensor_norm || out.tensor_sumsq) && grads && grads->n_tensors > kMaxSweepChunks)
+        return fail(ADAMW_E_INVALID, "too many tensors for per-tensor norms in one launch: split the list");
+    Sweep sw;
+    if ((st = begin_sweep(esz, grads, hip_stream, &sw)) != ADAMW_OK) return st;
+    const PlanSlot& p = *sw.plan;
+    hipError_t e = launch_sumsq(g_dtype, p.segs(), p.chunks(), p.n_chunks, p.tensor_first(), p.n_tensors, p.partials(),
+                                out, sw.stream);
+    if (e != hipSuccess) return hip_fail("sum of squares launch", e);
+    return ADAMW_OK;
 }
 
 }  // namespace
@@ -538,7 +632,7 @@ adamw_status adamw_check_finite(adamw_dtype g_dtype, const adamw_tensor_list* gr
     const int64_t chunk_elems = check_chunk_elems();
     int esz[kStreams];
     mode_esizes(ADAMW_MIXED, g_dtype, true, esz);
-    if ((st = validate_list(-1, esz, grads, chunk_elems)) != ADAMW_OK) return st;
+    if ((st = validate_list(kTagCheck, esz, grads, chunk_elems)) != ADAMW_OK) return st;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     StreamWorkspace* ws = nullptr;
     if ((st = get_workspace(stream, &ws)) != ADAMW_OK) return st;
@@ -549,11 +643,41 @@ adamw_status adamw_check_finite(adamw_dtype g_dtype, const adamw_tensor_list* gr
     uint32_t* done = nullptr;
     if ((st = ensure_workspace_block(*ws, stream, cap, &done)) != ADAMW_OK) return st;
     PlanSlot* plan = nullptr;
-    if ((st = ensure_plan(*ws, -1, esz, grads, chunk_elems, stream, cap, &plan)) != ADAMW_OK) return st;
+    if ((st = ensure_plan(*ws, kTagCheck, esz, grads, chunk_elems, stream, cap, &plan)) != ADAMW_OK) return st;
     hipError_t e = launch_check(g_dtype, plan->segs(), plan->chunks(), plan->n_chunks, d_found_inf, done,
                                 single_launch(plan->n_chunks), stream);
     if (e != hipSuccess) return hip_fail("check launch", e);
     return ADAMW_OK;
+}
+
+adamw_status adamw_grad_norm(adamw_dtype g_dtype, const adamw_tensor_list* grads, int accumulate, double* d_sumsq,
+                             float* d_norm, int32_t* d_found_inf, void* hip_stream)
+try {
+    g_err.clear();
+    if (!d_sumsq) return fail(ADAMW_E_INVALID, "d_sumsq is null");
+    NormOut out{};
+    out.sumsq = d_sumsq;
+    out.norm = d_norm;
+    out.found_inf = d_found_inf;
+    out.accumulate = accumulate != 0;
+    return sum_of_squares(g_dtype, grads, out, hip_stream);
+} catch (const std::bad_alloc&) {
+    return fail(ADAMW_E_NOMEM, "out of host memory");
+}
+
+adamw_status adamw_tensor_norms(adamw_dtype g_dtype, const adamw_tensor_list* grads, float* d_tensor_norms,
+                                double* d_tensor_sumsq, double* d_sumsq, void* hip_stream)
+try {
+    g_err.clear();
+    if (!d_tensor_norms && !d_tensor_sumsq)
+        return fail(ADAMW_E_INVALID, "d_tensor_norms and d_tensor_sumsq are both null");
+    NormOut out{};
+    out.sumsq = d_sumsq;
+    out.tensor_norm = d_tensor_norms;
+    out.tensor_sumsq = d_tensor_sumsq;
+    return sum_of_squares(g_dtype, grads, out, hip_stream);
+} catch (const std::bad_alloc&) {
+    return fail(ADAMW_E_NOMEM, "out of host memory");
 }
 
 const char* adamw_last_error(void) { return g_err.c_str(); }
@@ -580,12 +704,20 @@ int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_ten
     g_err.clear();
     Plan plan;
     std::string err;
-    adamw_status st = check_mode(mode, p_dtype, for_check != 0, err);
-    int esz[kStreams];
-    mode_esizes(mode, p_dtype, for_check != 0, esz);
-    const int64_t chunk = for_check ? check_chunk_elems()
-                                    : chunk_elems_of(st == ADAMW_OK ? kind_of_mode(mode, p_dtype).kernel : 0);
-    if (st == ADAMW_OK) st = build_plan(esz, list, chunk, for_check ? kMaxCheckChunks : kMaxUpdateChunks, &plan, err);
+    adamw_status st;
+    if (for_check == 2) {
+        int esz = 0;
+        st = check_sweep_dtype(p_dtype, &esz, err);
+        if (st == ADAMW_OK) st = build_sweep_plan(esz, list, sweep_chunk_elems(esz), kMaxSweepChunks, &plan, err);
+    } else {
+        st = check_mode(mode, p_dtype, for_check != 0, err);
+        int esz[kStreams];
+        mode_esizes(mode, p_dtype, for_check != 0, esz);
+        const int64_t chunk = for_check ? check_chunk_elems()
+                                        : chunk_elems_of(st == ADAMW_OK ? kind_of_mode(mode, p_dtype).kernel : 0);
+        if (st == ADAMW_OK)
+            st = build_plan(esz, list, chunk, for_check ? kMaxCheckChunks : kMaxUpdateChunks, &plan, err);
+    }
     if (st != ADAMW_OK) {
         g_err = err;
         return -1;
@@ -603,7 +735,9 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
     adamw_status st = ADAMW_OK;
     StepKind kind{};
     int64_t chunk = 0, max_chunks = kMaxUpdateChunks;
-    if (for_check) {
+    if (for_check == 2) {
+        st = check_sweep_dtype(p_dtype, &kind.esz[ADAMW_STREAM_GRAD], err);
+    } else if (for_check) {
         st = check_mode(mode, p_dtype, true, err);
         mode_esizes(mode, p_dtype, true, kind.esz);
         chunk = check_chunk_elems();
@@ -617,7 +751,12 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
     }
     if (st == ADAMW_OK && !for_check) chunk = chunk_elems_of(kind.kernel);
     Plan plan;
-    if (st == ADAMW_OK) st = build_plan(kind.esz, list, chunk, max_chunks, &plan, err);
+    if (st == ADAMW_OK && for_check == 2) {
+        const int esz = kind.esz[ADAMW_STREAM_GRAD];
+        st = build_sweep_plan(esz, list, sweep_chunk_elems(esz), kMaxSweepChunks, &plan, err);
+    } else if (st == ADAMW_OK) {
+        st = build_plan(kind.esz, list, chunk, max_chunks, &plan, err);
+    }
     if (st != ADAMW_OK) {
         g_err = err;
         return -1;

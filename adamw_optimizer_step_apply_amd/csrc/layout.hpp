@@ -37,6 +37,8 @@ constexpr int kBlockCheck = 256;
 constexpr int kPack = 8;               // elements per lane per dwordx4 of a 16-bit stream
 constexpr uint32_t kVecBit = 0x80000000u;
 constexpr uint32_t kCountMask = 0x7fffffffu;
+constexpr int64_t kTagCheck = -1;      // plan tags: an update kernel's id, the overflow check,
+constexpr int64_t kTagSweep = -2;      // or a gradient sweep
 constexpr int64_t kElemChunkElems = 4096;       // element chunk
 // An update kernel's chunk is shared by kXcdParts workgroups, consecutive in
 // launch order, so one on each XCD (the dispatcher hands workgroup b to XCD
@@ -102,9 +104,28 @@ constexpr int64_t kCheckChunkElems = (int64_t)kBlockCheck * kPack * kCheckChunkM
 constexpr int kMaxUpdateBlock = kBlockMixed > kBlockPure ? kBlockMixed : kBlockPure;
 constexpr int64_t kMaxUpdateChunks = (int64_t)UINT32_MAX / ((int64_t)kXcdParts * kMaxUpdateBlock);
 constexpr int64_t kMaxCheckChunks = (int64_t)UINT32_MAX / kBlockCheck;
+// The gradient sweeps (sum of squares, clipping) touch the gradient stream alone:
+// one workgroup per chunk of this many bytes, 8 16-byte words per lane.  A sweep's
+// chunks are not cut at 16-byte edges: the workgroup takes the elements before the
+// first edge and after the last one by themselves, so a tensor costs one workgroup
+// however short or misaligned it is.
+constexpr int kBlockSweep = 256;
+constexpr int kSweepUnroll = 8;
+constexpr int64_t kSweepChunkBytes = (int64_t)kBlockSweep * 16 * kSweepUnroll;
+constexpr int64_t kMaxSweepChunks = (int64_t)UINT32_MAX / kBlockSweep;
 // The state copy (setup and checkpoint) runs one 256-lane workgroup per chunk.
 constexpr int kBlockCopy = 256;
 constexpr int64_t kMaxCopyChunks = (int64_t)UINT32_MAX / kBlockCopy;
+
+// What a sum of squares leaves in device memory (null: not wanted).
+struct NormOut {
+    double* sumsq;          // the list's sum of squares (accumulate: added to what is there)
+    float* norm;            // its square root
+    int32_t* found_inf;     // 1 if the sum is not finite, else 0
+    int32_t accumulate;
+    float* tensor_norm;     // per tensor of the list
+    double* tensor_sumsq;
+};
 
 // Workgroup b of a grid of nb -> the chunk it processes.  The dispatcher hands
 // workgroup b to XCD b % 8 (the MI355X has 8 XCDs, each with its own L2); this

@@ -81,8 +81,18 @@ static void push_chunks(Plan& p, bool build, int64_t& n_chunks, uint32_t seg, in
     }
 }
 
-adamw_status build_plan(const int esz_in[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,
-                        int64_t max_chunks, Plan* outp, std::string& err)
+static std::string too_many_chunks(int64_t max_chunks)
+{
+    char buf[160];
+    snprintf(buf, sizeof buf,
+             "more than %lld chunks in one launch (a grid holds at most 2^32 - 1 lanes): "
+             "split the list or raise the chunk size",
+             (long long)max_chunks);
+    return buf;
+}
+
+static adamw_status plan_list(const int esz_in[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,
+                              int64_t max_chunks, bool sweep, Plan* outp, std::string& err)
 {
     char buf[256];
     Plan scratch;
@@ -174,6 +184,7 @@ adamw_status build_plan(const int esz_in[kStreams], const adamw_tensor_list* lis
         const int64_t n = list->numel[i];
         const int64_t lo = b > base ? b : base;
         const int64_t hi = e < base + n ? e : base + n;
+        if (build && sweep) out.tensor_first.push_back((uint32_t)n_chunks);
         // a blocked state splits the piece at block boundaries (relative to b)
         for (int64_t plo = lo; plo < hi;) {
             int64_t phi = hi;
@@ -212,6 +223,21 @@ adamw_status build_plan(const int esz_in[kStreams], const adamw_tensor_list* lis
                 out.info.push_back(si);
             }
 
+            if (sweep) {
+                // the first chunk reaches chunk_elems past the first 16-byte edge, so
+                // that every later one starts at an edge
+                const uint64_t esz_g = (uint64_t)esz[ADAMW_STREAM_GRAD];
+                const int64_t head = (int64_t)((16u - d.ptr[ADAMW_STREAM_GRAD] % 16u) % 16u / esz_g);
+                const int64_t first = si.count < head + chunk_elems ? si.count : head + chunk_elems;
+                push_chunks(out, build, n_chunks, seg, 0, first, first, true);
+                push_chunks(out, build, n_chunks, seg, first, si.count - first, chunk_elems, true);
+                if (n_chunks > max_chunks) {
+                    err = too_many_chunks(max_chunks);
+                    return ADAMW_E_INVALID;
+                }
+                continue;
+            }
+
             // head peel: smallest h in [0, 8) aligning every active stream to 16 bytes
             int head = -1;
             for (int h = 0; h < kPack && head < 0; ++h) {
@@ -231,18 +257,29 @@ adamw_status build_plan(const int esz_in[kStreams], const adamw_tensor_list* lis
                 push_chunks(out, build, n_chunks, seg, head + body, cnt - head - body, kElemChunkElems, false);
             }
             if (n_chunks > max_chunks) {
-                snprintf(buf, sizeof buf,
-                         "more than %lld chunks in one launch (a grid holds at most 2^32 - 1 lanes): "
-                         "split the list or raise the chunk size",
-                         (long long)max_chunks);
-                err = buf;
+                err = too_many_chunks(max_chunks);
                 return ADAMW_E_INVALID;
             }
         }
         base += (n + flat_align - 1) / flat_align * flat_align;
     }
+    if (build && sweep) out.tensor_first.push_back((uint32_t)n_chunks);
     out.total = e - b;
     return ADAMW_OK;
+}
+
+adamw_status build_plan(const int esz[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,
+                        int64_t max_chunks, Plan* out, std::string& err)
+{
+    return plan_list(esz, list, chunk_elems, max_chunks, false, out, err);
+}
+
+adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t chunk_elems, int64_t max_chunks,
+                              Plan* out, std::string& err)
+{
+    int streams[kStreams] = {0, 0, 0, 0, 0};
+    streams[ADAMW_STREAM_GRAD] = esz;
+    return plan_list(streams, list, chunk_elems, max_chunks, true, out, err);
 }
 
 void chunk_bytes(const Plan& plan, size_t c, const int esz[kStreams], uint64_t lo[kStreams], uint64_t hi[kStreams])

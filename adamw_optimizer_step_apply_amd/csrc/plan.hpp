@@ -24,6 +24,7 @@ struct Plan {
     std::vector<DevSeg> segs;
     std::vector<DevChunk> chunks;
     std::vector<SegInfo> info;   // parallel to segs
+    std::vector<uint32_t> tensor_first;   // sweep plans: tensor i's chunks are [tensor_first[i], tensor_first[i + 1])
     int64_t total = 0;           // elements covered
 };
 
@@ -40,6 +41,13 @@ void mode_esizes(adamw_mode mode, adamw_dtype p_dtype, bool for_check, int esz[k
 // limit of the kernel that runs it) is rejected.  No HIP call.
 adamw_status build_plan(const int esz[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,
                         int64_t max_chunks, Plan* out, std::string& err);
+
+// The same for a gradient sweep (adamw_grad_norm, adamw_clip_grads) over elements
+// of `esz` bytes: only the gradient stream is looked at, chunks hold up to
+// `chunk_elems` elements plus those before the segment's first 16-byte edge, are
+// marked with kVecBit, and are listed per tensor in Plan::tensor_first.
+adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t chunk_elems, int64_t max_chunks,
+                              Plan* out, std::string& err);
 
 // The plan of a state copy between per-tensor (or flat) state buffers and one
 // blocked buffer: `list` describes the state as a step would see it without
@@ -66,6 +74,8 @@ void chunk_bytes(const Plan& plan, size_t c, const int esz[kStreams], uint64_t l
 // The argument checks of the entry points (error text in `err`).
 adamw_status check_hparams(const adamw_hparams* hp, std::string& err);
 adamw_status check_scaler(const adamw_loss_scaler* sc, std::string& err);
+// g_dtype of a gradient sweep; its element size in *esz.
+adamw_status check_sweep_dtype(adamw_dtype g_dtype, int* esz, std::string& err);
 adamw_status basic_list_check(const adamw_tensor_list* list, std::string& err);
 adamw_status check_pure_precision(const adamw_pure_precision* prec, std::string& err);
 

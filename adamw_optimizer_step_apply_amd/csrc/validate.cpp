@@ -40,6 +40,16 @@ adamw_status check_scaler(const adamw_loss_scaler* sc, std::string& err)
     return ADAMW_OK;
 }
 
+adamw_status check_sweep_dtype(adamw_dtype g_dtype, int* esz, std::string& err)
+{
+    if (g_dtype != ADAMW_F16 && g_dtype != ADAMW_BF16 && g_dtype != ADAMW_F32) {
+        err = "g_dtype must be ADAMW_F16, ADAMW_BF16 or ADAMW_F32";
+        return ADAMW_E_UNSUPPORTED;
+    }
+    *esz = g_dtype == ADAMW_F32 ? 4 : 2;
+    return ADAMW_OK;
+}
+
 adamw_status basic_list_check(const adamw_tensor_list* list, std::string& err)
 {
     if (!list) { err = "tensor list is null"; return ADAMW_E_INVALID; }

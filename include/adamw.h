@@ -114,7 +114,7 @@
 extern "C" {
 #endif
 
-#define ADAMW_ABI_VERSION 8
+#define ADAMW_ABI_VERSION 9
 
 typedef enum {
     ADAMW_OK = 0,
@@ -342,6 +342,40 @@ adamw_status adamw_multi_tensor_step_amp(adamw_mode mode, adamw_dtype p_dtype, c
 adamw_status adamw_check_finite(adamw_dtype g_dtype, const adamw_tensor_list* grads, int32_t* d_found_inf,
                                 void* hip_stream);
 
+/* The global norm of a list's gradients, as gradient clipping (Pascanu et al., "On
+ * the difficulty of training recurrent neural networks", ICML 2013, section 3.2)
+ * and training logs need it: with S = the sum of g*g over the list's elements (stream 1 only;
+ * shard range, flat_mask bit 1 and ADAMW_FLAT_PAD8 honoured, as in
+ * adamw_check_finite),
+ *   *d_sumsq = S, or *d_sumsq + S with accumulate != 0 (required; binary64),
+ *   *d_norm = sqrt(*d_sumsq), rounded to binary32 (nullable),
+ *   *d_found_inf = 1 if *d_sumsq is not finite, else 0 (nullable).
+ * g_dtype: ADAMW_F16, ADAMW_BF16 or ADAMW_F32.  Squares and sums are binary64, so
+ * none overflows or underflows and S is within n * 2^-53 (relative) of the exact
+ * sum; S is not finite exactly if an element is inf or NaN, which makes
+ * *d_found_inf that of adamw_check_finite, in the same pass.  The order of the
+ * sum depends only on the list and the tuning knobs: the same call gives the
+ * same bits.  Scaled gradients are summed as stored: with a loss scale s the
+ * norm of the unscaled gradients is sqrt(S) / s (adamw_clip_grads and
+ * adamw_multi_tensor_step_clipped divide by it themselves).
+ * Several lists (parameter groups, other dtypes): the first call with accumulate
+ * = 0, the others with accumulate = 1, on one stream, d_norm and d_found_inf in
+ * the last.  Several ranks: each sums its own shard, then an all-reduce(sum) of
+ * *d_sumsq (one binary64 value).  An empty list (or shard) has S = 0. */
+adamw_status adamw_grad_norm(adamw_dtype g_dtype, const adamw_tensor_list* grads, int accumulate, double* d_sumsq,
+                             float* d_norm, int32_t* d_found_inf, void* hip_stream);
+
+/* The norm of every tensor of a list (stream 1: gradients, or any other tensors
+ * handed in there, such as master weights), as a training run logs them, in one
+ * pass: entry i of the device arrays of n_tensors entries
+ *   d_tensor_sumsq[i] = S_i = the sum of g*g over tensor i's elements inside the
+ *                       shard (binary64), d_tensor_norms[i] = sqrt(S_i) (binary32)
+ * (either may be null, not both; a tensor with no element in the shard gets 0),
+ * and *d_sumsq = the list's S, the value of adamw_grad_norm bit for bit
+ * (nullable).  dtypes, arithmetic and order as adamw_grad_norm. */
+adamw_status adamw_tensor_norms(adamw_dtype g_dtype, const adamw_tensor_list* grads, float* d_tensor_norms,
+                                double* d_tensor_sumsq, double* d_sumsq, void* hip_stream);
+
 /* Description of the last error on the calling thread ("" if none).  Valid
  * until the next call into the library on that thread. */
 const char* adamw_last_error(void);
@@ -390,11 +424,13 @@ adamw_status adamw_blocked_state_copy(adamw_mode mode, adamw_dtype p_dtype, cons
                                       const adamw_tensor_list* list, void* blocked, int to_blocked, void* hip_stream);
 
 /* Planner introspection, for tests: no GPU work, no HIP call.  Builds the
- * chunk plan that adamw_multi_tensor_step (for_check = 0) or
- * adamw_check_finite (for_check = 1) would launch, and writes up to cap rows
- * of 6 int64 each to out:
+ * chunk plan that adamw_multi_tensor_step (for_check = 0),
+ * adamw_check_finite (for_check = 1), or adamw_grad_norm and adamw_tensor_norms
+ * (for_check = 2, g_dtype = p_dtype; mode ignored) would launch, and writes up to
+ * cap rows of 6 int64 each to out:
  *   {tensor index, element offset inside the tensor, element count,
- *    kind (0 = element-wise, 1 = 16-byte vector), flat position, segment}.
+ *    kind (0 = element-wise, 1 = 16-byte vector, 2 = any elements, whose 16-byte
+ *    words the workgroup finds), flat position, segment}.
  * Returns the number of chunks (which may exceed cap), or -1 on an invalid
  * argument (see adamw_last_error). */
 int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_tensor_list* list, int for_check,
@@ -403,8 +439,8 @@ int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_ten
 /* Planner introspection, for tests: no GPU work, no HIP call.  The device
  * bytes each chunk of the plan covers: for the step of (mode, p_dtype), or with
  * prec non-null the step of adamw_pure_multi_tensor_step with *prec (mode and
- * p_dtype ignored), or with for_check the check of adamw_check_finite
- * (g_dtype = p_dtype), writes up to cap rows of 16 uint64 to out:
+ * p_dtype ignored), or with for_check the pass over the gradients of
+ * adamw_plan_inspect's for_check (g_dtype = p_dtype), writes up to cap rows of 16 uint64 to out:
  *   {the 6 fields of an adamw_plan_inspect row, lo[0], hi[0], ..., lo[4], hi[4]}
  * where [lo[s], hi[s]) is the address range of stream s that the chunk's
  * workgroups read and write (lo = hi = 0 for a stream the launch does not
