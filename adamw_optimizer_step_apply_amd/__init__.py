@@ -43,7 +43,7 @@ _STATUS = {0: "ADAMW_OK", 1: "ADAMW_E_INVALID", 2: "ADAMW_E_UNSUPPORTED", 3: "AD
 
 EXPORTED = ("adamw_step", "adamw_multi_tensor_step", "adamw_multi_tensor_step_noalloc", "adamw_multi_tensor_step_amp",
             "adamw_pure_multi_tensor_step",
-            "adamw_check_finite", "adamw_grad_norm", "adamw_tensor_norms",
+            "adamw_check_finite", "adamw_grad_norm", "adamw_tensor_norms", "adamw_clip_grads",
             "adamw_last_error", "adamw_release_workspace", "adamw_abi_version", "adamw_plan_inspect",
             "adamw_plan_inspect_bytes", "adamw_set_chunk_elems", "adamw_set_single_launch_max_workgroups",
             "adamw_blocked_state_bytes", "adamw_blocked_state_copy")
@@ -61,6 +61,10 @@ class adamw_pure_precision(ctypes.Structure):
 class adamw_loss_scaler(ctypes.Structure):
     _fields_ = [("growth_factor", ctypes.c_float), ("backoff_factor", ctypes.c_float),
                 ("growth_interval", ctypes.c_int32)]
+
+
+class adamw_grad_clip(ctypes.Structure):
+    _fields_ = [("d_sumsq", ctypes.c_void_p), ("max_norm", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class adamw_tensor_list(ctypes.Structure):
@@ -104,6 +108,9 @@ def _declare(_lib):
     _lib.adamw_grad_norm.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list), ctypes.c_int, _vp, _vp, _vp, _vp]
     _lib.adamw_tensor_norms.restype = ctypes.c_int
     _lib.adamw_tensor_norms.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list), _vp, _vp, _vp, _vp]
+    _lib.adamw_clip_grads.restype = ctypes.c_int
+    _lib.adamw_clip_grads.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list), ctypes.POINTER(adamw_grad_clip),
+                                      ctypes.c_float, _vp, _vp]
     _lib.adamw_last_error.restype = ctypes.c_char_p
     _lib.adamw_last_error.argtypes = []
     _lib.adamw_release_workspace.restype = None
@@ -345,6 +352,29 @@ def adamw_tensor_norms(g_dtype: int, grads: TensorList, d_tensor_norms=None, d_t
     ``d_sumsq`` (C ABI adamw_tensor_norms)."""
     _check(_lib.adamw_tensor_norms(g_dtype, ctypes.byref(grads.c), _addr(d_tensor_norms), _addr(d_tensor_sumsq),
                                    _addr(d_sumsq), _stream(stream)))
+
+
+@dataclass
+class GradClip:
+    """Clipping by the global norm: ``d_sumsq`` is adamw_grad_norm's sum of squares
+    (a float64 tensor of one element, or its device address), read when the call
+    that clips runs."""
+    d_sumsq: object
+    max_norm: float = 1.0
+    eps: float = 1e-6
+
+    def c(self) -> adamw_grad_clip:
+        return adamw_grad_clip(_addr(self.d_sumsq), self.max_norm, self.eps)
+
+
+def adamw_clip_grads(g_dtype: int, grads: TensorList, clip: GradClip, inv_loss_scale: float = 1.0, d_scale=None,
+                     stream=None) -> None:
+    """Multiplies the list's gradients by min(1, max_norm / (norm + eps)) in place; the
+    norm is the unscaled gradients', by ``d_scale`` (a device loss-scale state) or
+    ``inv_loss_scale`` (C ABI adamw_clip_grads)."""
+    c = clip.c()
+    _check(_lib.adamw_clip_grads(g_dtype, ctypes.byref(grads.c), ctypes.byref(c), inv_loss_scale, _addr(d_scale),
+                                 _stream(stream)))
 
 
 def adamw_last_error() -> str:

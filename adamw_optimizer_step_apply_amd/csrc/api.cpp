@@ -680,6 +680,29 @@ try {
     return fail(ADAMW_E_NOMEM, "out of host memory");
 }
 
+adamw_status adamw_clip_grads(adamw_dtype g_dtype, const adamw_tensor_list* grads, const adamw_grad_clip* clip,
+                              float inv_loss_scale, const adamw_loss_scale_state* d_scale, void* hip_stream)
+try {
+    g_err.clear();
+    std::string err;
+    int esz = 0;
+    adamw_status st = check_sweep_dtype(g_dtype, &esz, err);
+    if (st == ADAMW_OK) st = check_clip(clip, err);
+    if (st != ADAMW_OK) return fail(st, err);
+    if ((uintptr_t)d_scale % 4) return fail(ADAMW_E_INVALID, "d_scale is not 4-byte aligned");
+    if (!d_scale && (!std::isfinite(inv_loss_scale) || !(inv_loss_scale > 0.0f)))
+        return fail(ADAMW_E_INVALID, "inv_loss_scale must be finite and > 0");
+    Sweep sw;
+    if ((st = begin_sweep(esz, grads, hip_stream, &sw)) != ADAMW_OK) return st;
+    const PlanSlot& p = *sw.plan;
+    hipError_t e = launch_clip(g_dtype, p.segs(), p.chunks(), p.n_chunks,
+                               ClipRule{clip->d_sumsq, clip->max_norm, clip->eps}, inv_loss_scale, d_scale, sw.stream);
+    if (e != hipSuccess) return hip_fail("clip launch", e);
+    return ADAMW_OK;
+} catch (const std::bad_alloc&) {
+    return fail(ADAMW_E_NOMEM, "out of host memory");
+}
+
 const char* adamw_last_error(void) { return g_err.c_str(); }
 
 void adamw_release_workspace(void)

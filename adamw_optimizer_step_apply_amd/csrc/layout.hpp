@@ -117,6 +117,14 @@ constexpr int64_t kMaxSweepChunks = (int64_t)UINT32_MAX / kBlockSweep;
 constexpr int kBlockCopy = 256;
 constexpr int64_t kMaxCopyChunks = (int64_t)UINT32_MAX / kBlockCopy;
 
+// Clipping by the global norm: the factor min(1, max_norm / (sqrt(*sumsq) * inv + eps))
+// with inv the gradients' inverse loss scale (sumsq null: no clipping).
+struct ClipRule {
+    const double* sumsq;
+    float max_norm;
+    float eps;
+};
+
 // What a sum of squares leaves in device memory (null: not wanted).
 struct NormOut {
     double* sumsq;          // the list's sum of squares (accumulate: added to what is there)

@@ -1,5 +1,5 @@
-// norm.hip -- gfx950 (CDNA4) kernels of the gradient norms: the sum of squares
-// of a tensor list, over all its elements and per tensor.
+// norm.hip -- gfx950 (CDNA4) kernels of the gradient norms (the sum of squares of
+// a tensor list, over all its elements and per tensor) and of clipping by them.
 //
 //   S_i = sum over tensor i of g^2,  S = sum_i S_i,  norm = sqrt(S)
 //
@@ -154,7 +154,74 @@ __global__ __launch_bounds__(kBlockTotal) void total_kernel(const double* __rest
     }
 }
 
+// Clipping in place: g = round(g * f), f the clipping factor rounded to binary32,
+// one binary32 product and one rounding to the gradient's type per element.  A
+// factor of 1 changes no element and a sum that is not finite clips nothing:
+// nothing is written.
+template <int DT>
+__device__ __forceinline__ u32x4 scale_word(u32x4 q, float f)
+{
+    if constexpr (DT == kF32) {
+        return u32x4{__float_as_uint(__uint_as_float(q.x) * f), __float_as_uint(__uint_as_float(q.y) * f),
+                     __float_as_uint(__uint_as_float(q.z) * f), __float_as_uint(__uint_as_float(q.w) * f)};
+    } else {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f32x2 x = widen2<DT == kF16>(w[j]);
+            o[j] = narrow2<DT == kF16>(x.x * f, x.y * f);
+        }
+        return u32x4{o[0], o[1], o[2], o[3]};
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void scale1(uint64_t addr, float f)
+{
+    if constexpr (DT == kF32) {
+        GLOBAL float* p = gptr<float>(addr, 0);
+        *p = *p * f;
+    } else {
+        GLOBAL uint16_t* p = gptr<uint16_t>(addr, 0);
+        *p = narrow1<DT == kF16>(widen1<DT == kF16>(*p) * f);
+    }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kBlockSweep) void clip_kernel(const DevSeg* __restrict__ segs,
+                                                       const DevChunk* __restrict__ chunks, ClipRule rule,
+                                                       float inv_scale, const adamw_loss_scale_state* __restrict__ amp)
+{
+    if (amp) inv_scale = (float)(1.0 / (double)amp->scale);
+    double factor;
+    if (!clip_factor(rule, *rule.sumsq, inv_scale, factor)) return;
+    const float f = (float)factor;
+    if (f == 1.0f) return;
+    const DevChunk ch = chunks[xcd_chunk(blockIdx.x, gridDim.x)];
+    const Span<DT> sp(segs[ch.seg].ptr[ADAMW_STREAM_GRAD] + ch.off * Elem<DT>::size, ch.n_kind & kCountMask);
+    GLOBAL u32x4* __restrict__ g4 = gptr<u32x4>(sp.body, 0);
+    const uint32_t tid = threadIdx.x;
+    for (uint32_t k = tid; k < sp.words; k += kBlockSweep) st<2>(g4 + k, scale_word<DT>(ld<0>(g4 + k), f));
+    if (tid < sp.head) scale1<DT>(sp.head_addr(tid), f);
+    if (tid < sp.tail) scale1<DT>(sp.tail_addr(tid), f);
+}
+
 }  // namespace
+
+hipError_t launch_clip(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+                       const ClipRule& rule, float inv_scale, const adamw_loss_scale_state* d_amp, hipStream_t stream)
+{
+    if (n_chunks <= 0) return hipSuccess;
+    const dim3 grid((unsigned)n_chunks), block(kBlockSweep);
+    if (g_dtype == ADAMW_F16)
+        hipLaunchKernelGGL((clip_kernel<kF16>), grid, block, 0, stream, segs, chunks, rule, inv_scale, d_amp);
+    else if (g_dtype == ADAMW_BF16)
+        hipLaunchKernelGGL((clip_kernel<kBf16>), grid, block, 0, stream, segs, chunks, rule, inv_scale, d_amp);
+    else
+        hipLaunchKernelGGL((clip_kernel<kF32>), grid, block, 0, stream, segs, chunks, rule, inv_scale, d_amp);
+    return hipGetLastError();
+}
 
 hipError_t launch_sumsq(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
                         const uint32_t* tensor_first, int64_t n_tensors, double* partials, const NormOut& out,

@@ -74,6 +74,7 @@ void chunk_bytes(const Plan& plan, size_t c, const int esz[kStreams], uint64_t l
 // The argument checks of the entry points (error text in `err`).
 adamw_status check_hparams(const adamw_hparams* hp, std::string& err);
 adamw_status check_scaler(const adamw_loss_scaler* sc, std::string& err);
+adamw_status check_clip(const adamw_grad_clip* clip, std::string& err);
 // g_dtype of a gradient sweep; its element size in *esz.
 adamw_status check_sweep_dtype(adamw_dtype g_dtype, int* esz, std::string& err);
 adamw_status basic_list_check(const adamw_tensor_list* list, std::string& err);

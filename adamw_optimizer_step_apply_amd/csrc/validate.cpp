@@ -40,6 +40,24 @@ adamw_status check_scaler(const adamw_loss_scaler* sc, std::string& err)
     return ADAMW_OK;
 }
 
+adamw_status check_clip(const adamw_grad_clip* clip, std::string& err)
+{
+    if (!clip) { err = "clip is null"; return ADAMW_E_INVALID; }
+    if (!clip->d_sumsq || (uintptr_t)clip->d_sumsq % 8) {
+        err = "clip: d_sumsq is null or not 8-byte aligned";
+        return ADAMW_E_INVALID;
+    }
+    if (!std::isfinite(clip->max_norm) || clip->max_norm < 0.0f) {
+        err = "clip: max_norm must be finite and >= 0";
+        return ADAMW_E_INVALID;
+    }
+    if (!std::isfinite(clip->eps) || clip->eps < 0.0f) {
+        err = "clip: eps must be finite and >= 0";
+        return ADAMW_E_INVALID;
+    }
+    return ADAMW_OK;
+}
+
 adamw_status check_sweep_dtype(adamw_dtype g_dtype, int* esz, std::string& err)
 {
     if (g_dtype != ADAMW_F16 && g_dtype != ADAMW_BF16 && g_dtype != ADAMW_F32) {

@@ -376,6 +376,32 @@ adamw_status adamw_grad_norm(adamw_dtype g_dtype, const adamw_tensor_list* grads
 adamw_status adamw_tensor_norms(adamw_dtype g_dtype, const adamw_tensor_list* grads, float* d_tensor_norms,
                                 double* d_tensor_sumsq, double* d_sumsq, void* hip_stream);
 
+/* Clipping by the global norm: with S = *d_sumsq (adamw_grad_norm's sum over every
+ * list and rank), inv the inverse loss scale and total = sqrt(S) * inv the norm of
+ * the unscaled gradients, every gradient is multiplied by
+ *   f = min(1, max_norm / (total + eps)).
+ * S is read when the call runs, in stream order, so the norm's call and an
+ * all-reduce of it may be queued just before.  f is formed in binary64.
+ * d_sumsq: device, 8-byte aligned.  max_norm: finite, >= 0.  eps: finite, >= 0
+ * (usually 1e-6); with max_norm = eps = 0 a zero norm clips nothing. */
+typedef struct {
+    const double* d_sumsq;
+    float max_norm;
+    float eps;
+} adamw_grad_clip;
+
+/* Clips a list's gradients in place: g = round(g * f) for every element of the
+ * list (stream 1 only; shard range, flat_mask bit 1 and ADAMW_FLAT_PAD8 honoured),
+ * f rounded once to binary32, one binary32 product, rounded to nearest even in
+ * g_dtype (ADAMW_F16, ADAMW_BF16 or ADAMW_F32).  Scaled gradients stay scaled: inv
+ * is 1 / d_scale->scale read on the device if d_scale is non-null, else
+ * inv_loss_scale (finite, > 0), and only f depends on it.  With f = 1 no element
+ * changes and nothing is written.  If S is not finite (an inf or NaN gradient)
+ * nothing is written either: the step that follows is to be skipped
+ * (adamw_grad_norm's d_found_inf). */
+adamw_status adamw_clip_grads(adamw_dtype g_dtype, const adamw_tensor_list* grads, const adamw_grad_clip* clip,
+                              float inv_loss_scale, const adamw_loss_scale_state* d_scale, void* hip_stream);
+
 /* Description of the last error on the calling thread ("" if none).  Valid
  * until the next call into the library on that thread. */
 const char* adamw_last_error(void);
@@ -425,8 +451,8 @@ adamw_status adamw_blocked_state_copy(adamw_mode mode, adamw_dtype p_dtype, cons
 
 /* Planner introspection, for tests: no GPU work, no HIP call.  Builds the
  * chunk plan that adamw_multi_tensor_step (for_check = 0),
- * adamw_check_finite (for_check = 1), or adamw_grad_norm and adamw_tensor_norms
- * (for_check = 2, g_dtype = p_dtype; mode ignored) would launch, and writes up to
+ * adamw_check_finite (for_check = 1), or adamw_grad_norm, adamw_tensor_norms and
+ * adamw_clip_grads (for_check = 2, g_dtype = p_dtype; mode ignored) would launch, and writes up to
  * cap rows of 6 int64 each to out:
  *   {tensor index, element offset inside the tensor, element count,
  *    kind (0 = element-wise, 1 = 16-byte vector, 2 = any elements, whose 16-byte

@@ -1,0 +1,64 @@
+"""Clipping without a GPU: bad calls are refused before any HIP call."""
+import ctypes
+
+import pytest
+
+import adamw_optimizer_step_apply_amd as A
+from test_grad_norm_cpu import FAKE, grads
+
+
+def clip(**kw):
+    return A.GradClip(**{"d_sumsq": FAKE, **kw})
+
+
+@pytest.mark.parametrize("call,needle", [
+    (lambda: A.adamw_clip_grads(7, grads([10]), clip(), stream=0), "g_dtype"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(d_sumsq=0), stream=0), "d_sumsq"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(d_sumsq=FAKE + 4), stream=0), "8-byte"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(max_norm=-1.0), stream=0), "max_norm"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(max_norm=float("inf")), stream=0), "max_norm"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(max_norm=float("nan")), stream=0), "max_norm"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(eps=-1e-6), stream=0), "eps"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(eps=float("nan")), stream=0), "eps"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(), 0.0, stream=0), "inv_loss_scale"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(), float("inf"), stream=0), "inv_loss_scale"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(), d_scale=FAKE + 2, stream=0), "d_scale"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10], base=FAKE + 1), clip(), stream=0), "aligned"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10, 3], shard_begin=0, shard_end=14), clip(), stream=0), "shard"),
+    (lambda: A.adamw_clip_grads(A.BF16, grads([10, -3]), clip(), stream=0), "numel"),
+])
+def test_rejected_before_any_hip_call(call, needle):
+    with pytest.raises(A.AdamWError) as ei:
+        call()
+    assert ei.value.status in (A.E_INVALID, A.E_UNSUPPORTED)
+    assert needle.lower() in str(ei.value).lower(), str(ei.value)
+
+
+def test_null_clip_is_refused():
+    tl = grads([10])
+    assert A._lib.adamw_clip_grads(A.BF16, ctypes.byref(tl.c), None, 1.0, None, None) == A.E_INVALID
+    assert "clip" in A.adamw_last_error()
+
+
+@pytest.mark.parametrize("call", [lambda: A.adamw_clip_grads(A.F32, grads([10, 20], esz=4), clip(max_norm=0.0), stream=0),
+                                  lambda: A.adamw_clip_grads(A.F16, grads([10]), clip(), 0.0, FAKE, stream=0)])
+def test_valid_call_reaches_hip(call):
+    with pytest.raises(A.AdamWError) as ei:
+        call()
+    assert ei.value.status == A.E_HIP
+
+
+def test_binding_struct_matches_the_c_layout(tmp_path):
+    import os
+    import subprocess
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "adamw.h"\n'
+                   'int main(void) { printf("%zu %zu %zu %zu\\n", sizeof(adamw_grad_clip), '
+                   'offsetof(adamw_grad_clip, d_sumsq), offsetof(adamw_grad_clip, max_norm), '
+                   'offsetof(adamw_grad_clip, eps)); return 0; }\n')
+    exe = tmp_path / "layout"
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-I", inc, str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    s = A.adamw_grad_clip
+    assert got == [ctypes.sizeof(s), s.d_sumsq.offset, s.max_norm.offset, s.eps.offset]
