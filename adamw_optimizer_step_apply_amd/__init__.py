@@ -44,6 +44,7 @@ _STATUS = {0: "ADAMW_OK", 1: "ADAMW_E_INVALID", 2: "ADAMW_E_UNSUPPORTED", 3: "AD
 EXPORTED = ("adamw_step", "adamw_multi_tensor_step", "adamw_multi_tensor_step_noalloc", "adamw_multi_tensor_step_amp",
             "adamw_pure_multi_tensor_step",
             "adamw_check_finite", "adamw_grad_norm", "adamw_tensor_norms", "adamw_clip_grads",
+            "adamw_multi_tensor_step_clipped",
             "adamw_last_error", "adamw_release_workspace", "adamw_abi_version", "adamw_plan_inspect",
             "adamw_plan_inspect_bytes", "adamw_set_chunk_elems", "adamw_set_single_launch_max_workgroups",
             "adamw_blocked_state_bytes", "adamw_blocked_state_copy")
@@ -111,6 +112,11 @@ def _declare(_lib):
     _lib.adamw_clip_grads.restype = ctypes.c_int
     _lib.adamw_clip_grads.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list), ctypes.POINTER(adamw_grad_clip),
                                       ctypes.c_float, _vp, _vp]
+    _lib.adamw_multi_tensor_step_clipped.restype = ctypes.c_int
+    _lib.adamw_multi_tensor_step_clipped.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.POINTER(adamw_pure_precision),
+                                                     ctypes.POINTER(adamw_tensor_list), ctypes.POINTER(adamw_hparams),
+                                                     ctypes.POINTER(adamw_grad_clip), _vp, _vp, _vp,
+                                                     ctypes.POINTER(adamw_loss_scaler), _vp]
     _lib.adamw_last_error.restype = ctypes.c_char_p
     _lib.adamw_last_error.argtypes = []
     _lib.adamw_release_workspace.restype = None
@@ -375,6 +381,21 @@ def adamw_clip_grads(g_dtype: int, grads: TensorList, clip: GradClip, inv_loss_s
     c = clip.c()
     _check(_lib.adamw_clip_grads(g_dtype, ctypes.byref(grads.c), ctypes.byref(c), inv_loss_scale, _addr(d_scale),
                                  _stream(stream)))
+
+
+def adamw_multi_tensor_step_clipped(mode: int, p_dtype: int, tensors: TensorList, hp, clip: GradClip, d_step,
+                                    d_found_inf=None, d_scale=None, scaler: LossScaler = None,
+                                    prec: "PurePrecision" = None, stream=None, advance_scale: bool = True) -> None:
+    """One AdamW step that multiplies the gradients by the clipping factor as it reads
+    them, and is skipped if ``clip.d_sumsq`` is not finite; ``d_scale`` and ``scaler``
+    as adamw_multi_tensor_step_amp (``advance_scale`` false: the scale is only read, as
+    for every parameter group but the last), ``prec`` selects
+    adamw_pure_multi_tensor_step's step (C ABI adamw_multi_tensor_step_clipped)."""
+    h, c, sc = _hp(hp), clip.c(), (scaler or LossScaler()).c()
+    pc = ctypes.byref(prec.c()) if prec is not None else None
+    _check(_lib.adamw_multi_tensor_step_clipped(mode, p_dtype, pc, ctypes.byref(tensors.c), ctypes.byref(h),
+                                                ctypes.byref(c), _addr(d_step), _addr(d_found_inf), _addr(d_scale),
+                                                ctypes.byref(sc) if advance_scale else None, _stream(stream)))
 
 
 def adamw_last_error() -> str:

@@ -375,7 +375,7 @@ void inspect_row(const Plan& plan, size_t i, int64_t* r)
 // One step through the stream's workspace and plan cache.
 adamw_status do_step(const StepKind& kind, const adamw_tensor_list* list, const adamw_hparams* hp, int32_t* d_step,
                      const int32_t* d_found_inf, void* hip_stream, adamw_loss_scale_state* d_amp = nullptr,
-                     const adamw_loss_scaler* scaler = nullptr)
+                     const adamw_loss_scaler* scaler = nullptr, const ClipRule& clip = ClipRule{})
 {
     adamw_status st;
     if ((st = check_step_call(kind, list, hp, d_step, d_found_inf)) != ADAMW_OK) return st;
@@ -393,7 +393,7 @@ adamw_status do_step(const StepKind& kind, const adamw_tensor_list* list, const 
         ADAMW_OK)
         return st;
     return enqueue_step(kind, plan->segs(), plan->chunks(), plan->n_chunks, ws->scalars, done, *hp, d_step,
-                        d_found_inf, d_amp, scaler, stream);
+                        d_found_inf, d_amp, scaler, clip, stream);
 }
 
 // What a gradient sweep launches over: the plan on the device and the stream's
@@ -499,19 +499,19 @@ adamw_status check_step_call(const StepKind& kind, const adamw_tensor_list* list
 adamw_status enqueue_step(const StepKind& kind, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
                           LaunchScalars* scalars, uint32_t* done, const adamw_hparams& hp, int32_t* d_step,
                           const int32_t* d_found_inf, adamw_loss_scale_state* d_amp, const adamw_loss_scaler* scaler,
-                          hipStream_t stream)
+                          const ClipRule& clip, hipStream_t stream)
 {
-    const adamw_loss_scaler rule = scaler ? *scaler : adamw_loss_scaler{1.0f, 1.0f, 1};
+    const adamw_loss_scaler rule = scaler ? *scaler : adamw_loss_scaler{1.0f, 1.0f, 0};   // 0: no advance
     hipError_t e;
     // Small plans: one launch.  An empty plan, whose step still advances the
     // counter (and the loss scale), keeps the prologue kernel.
     if (single_launch(n_chunks * kXcdParts)) {
-        const FusedStep fs{hp, d_step, d_found_inf, done, d_amp, rule};
+        const FusedStep fs{hp, d_step, d_found_inf, done, d_amp, rule, clip};
         e = launch_update(kind.kernel, segs, chunks, n_chunks, nullptr, &fs, stream);
         if (e != hipSuccess) return hip_fail("update launch", e);
         return ADAMW_OK;
     }
-    e = launch_prologue(hp, d_step, d_found_inf, scalars, d_amp, rule, stream);
+    e = launch_prologue(hp, d_step, d_found_inf, scalars, d_amp, rule, clip, stream);
     if (e != hipSuccess) return hip_fail("prologue launch", e);
     e = launch_update(kind.kernel, segs, chunks, n_chunks, scalars, nullptr, stream);
     if (e != hipSuccess) return hip_fail("update launch", e);
@@ -539,6 +539,17 @@ int64_t chunk_elems_of(int kernel)
 {
     const int64_t c = g_chunk_elems.load(std::memory_order_relaxed);
     return c ? c : update_chunk_elems(kernel_block(kernel));
+}
+
+// The element sizes of a step of (mode, p_dtype), or of the pure step of *prec.
+static adamw_status state_kind(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec, StepKind* kind)
+{
+    if (!prec) return mode_kind(mode, p_dtype, kind);
+    std::string err;
+    adamw_status st = check_pure_precision(prec, err);
+    if (st != ADAMW_OK) return fail(st, err);
+    *kind = kind_of_pure(*prec);
+    return ADAMW_OK;
 }
 
 }  // namespace adamw
@@ -703,6 +714,26 @@ try {
     return fail(ADAMW_E_NOMEM, "out of host memory");
 }
 
+adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
+                                             const adamw_tensor_list* list, const adamw_hparams* hp,
+                                             const adamw_grad_clip* clip, int32_t* d_step, const int32_t* d_found_inf,
+                                             adamw_loss_scale_state* d_scale, const adamw_loss_scaler* scaler,
+                                             void* hip_stream)
+try {
+    g_err.clear();
+    std::string err;
+    adamw_status st = check_clip(clip, err);
+    if (st != ADAMW_OK) return fail(st, err);
+    if ((uintptr_t)d_scale % 4) return fail(ADAMW_E_INVALID, "d_scale is not 4-byte aligned");
+    if (d_scale && scaler && (st = check_scaler(scaler)) != ADAMW_OK) return st;
+    StepKind kind;
+    if ((st = state_kind(mode, p_dtype, prec, &kind)) != ADAMW_OK) return st;
+    return do_step(kind, list, hp, d_step, d_found_inf, hip_stream, d_scale, scaler,
+                   ClipRule{clip->d_sumsq, clip->max_norm, clip->eps});
+} catch (const std::bad_alloc&) {
+    return fail(ADAMW_E_NOMEM, "out of host memory");
+}
+
 const char* adamw_last_error(void) { return g_err.c_str(); }
 
 void adamw_release_workspace(void)
@@ -797,17 +828,6 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
         }
     }
     return n;
-}
-
-// The element sizes of a step of (mode, p_dtype), or of the pure step of *prec.
-static adamw_status state_kind(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec, StepKind* kind)
-{
-    if (!prec) return mode_kind(mode, p_dtype, kind);
-    std::string err;
-    adamw_status st = check_pure_precision(prec, err);
-    if (st != ADAMW_OK) return fail(st, err);
-    *kind = kind_of_pure(*prec);
-    return ADAMW_OK;
 }
 
 int64_t adamw_blocked_state_bytes(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,

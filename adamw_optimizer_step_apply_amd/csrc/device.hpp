@@ -143,12 +143,14 @@ __device__ __forceinline__ bool grid_done_verdict(uint32_t* done, uint32_t verdi
     return true;
 }
 
+__device__ __forceinline__ bool is_sum_of_squares(double s) { return s >= 0.0 && __builtin_isfinite(s); }
+
 // The clipping factor of a sum of squares S, in binary64.  Returns false if S is no
 // finite sum of squares (an inf or NaN gradient).  A factor of 0/0 (no gradient, no
 // eps) clips nothing.
 __device__ __forceinline__ bool clip_factor(const ClipRule& rule, double s, float inv_scale, double& factor)
 {
-    if (!(s >= 0.0 && __builtin_isfinite(s))) return false;
+    if (!is_sum_of_squares(s)) return false;
     const double c = (double)rule.max_norm / (__builtin_sqrt(s) * (double)inv_scale + (double)rule.eps);
     factor = c < 1.0 ? c : 1.0;
     return true;

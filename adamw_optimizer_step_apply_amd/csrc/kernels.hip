@@ -110,7 +110,9 @@ __device__ __forceinline__ uint32_t split_bits(uint32_t w, uint32_t& r16)
 // ---------------------------------------------------------------------------
 // Prologue: one lane.  skip = *found_inf != 0; otherwise t = *step + 1, the
 // step's scalars, and *step = t.  With a loss-scale state, the unscale factor
-// is 1/scale and the state advances by the dynamic loss-scaling rule.
+// is 1/scale and the state advances by the dynamic loss-scaling rule.  With a
+// clipping rule, the unscale factor is multiplied by the clipping factor, and a
+// sum of squares that is not finite skips the step as the flag does.
 // ---------------------------------------------------------------------------
 
 __device__ double pow_sq(double b, int64_t t)
@@ -123,6 +125,16 @@ __device__ double pow_sq(double b, int64_t t)
         b = b * b;
     }
     return r;
+}
+
+// Multiplies the gradients' multiplier by the clipping factor: one rounding of the
+// binary64 product.  Returns false if the step has to be skipped.
+__device__ __forceinline__ bool clip_scale(const ClipRule& clip, double sumsq, float& inv_scale)
+{
+    double factor;
+    if (!clip_factor(clip, sumsq, inv_scale, factor)) return false;
+    inv_scale = (float)((double)inv_scale * factor);
+    return true;
 }
 
 // The scalars of step t: binary64 from +, -, *, / only, each rounded once to
@@ -153,6 +165,7 @@ __device__ __forceinline__ Coef step_coef(const adamw_hparams& hp, int64_t t, fl
 __device__ __forceinline__ void advance_loss_scale(adamw_loss_scale_state* amp, const adamw_loss_scaler& scaler,
                                                    float scale, bool skip)
 {
+    if (scaler.growth_interval < 1) return;   // a scale that this call only reads
     if (skip) {
         amp->scale = scale * scaler.backoff_factor;
         amp->growth_tracker = 0;
@@ -175,7 +188,7 @@ __device__ __forceinline__ bool counter_in_range(int32_t step) { return step >= 
 
 __global__ void prologue_kernel(adamw_hparams hp, int32_t* __restrict__ step, const int32_t* __restrict__ found_inf,
                                 LaunchScalars* __restrict__ out, adamw_loss_scale_state* __restrict__ amp,
-                                adamw_loss_scaler scaler)
+                                adamw_loss_scaler scaler, ClipRule clip)
 {
     if (threadIdx.x != 0 || blockIdx.x != 0) return;
     LaunchScalars s{};
@@ -186,15 +199,13 @@ __global__ void prologue_kernel(adamw_hparams hp, int32_t* __restrict__ step, co
         *out = s;
         return;
     }
-    const bool skip = found_inf && *found_inf != 0;
-    float inv_scale = hp.inv_loss_scale;
-    if (amp) {
-        // this step unscales by the current scale; the scale for the next step
-        // follows from the flag
-        const float scale = amp->scale;
-        inv_scale = (float)(1.0 / (double)scale);
-        advance_loss_scale(amp, scaler, scale, skip);
-    }
+    bool skip = found_inf && *found_inf != 0;
+    const float scale = amp ? amp->scale : 0.0f;
+    float inv_scale = amp ? (float)(1.0 / (double)scale) : hp.inv_loss_scale;
+    if (clip.sumsq) skip |= !clip_scale(clip, *clip.sumsq, inv_scale);
+    // this step unscales by the current scale; the scale for the next step
+    // follows from the flag
+    if (amp) advance_loss_scale(amp, scaler, scale, skip);
     if (skip) {
         s.skip = 1;
         *out = s;
@@ -287,6 +298,14 @@ __device__ __forceinline__ Coef load_coef(const LaunchScalars* sc)
     return c;
 }
 
+// What a single-launch workgroup reads before its data: the step it takes, the loss
+// scale and the sum of squares to clip by.
+struct StepIn {
+    int64_t t;
+    float scale;
+    double sumsq;
+};
+
 // Start of a step in an update kernel.  Two-launch form: the prologue kernel
 // has written the skip flag and the scalars.  Single launch: the workgroup
 // reads the flag, the counter and (with a dynamic loss scale) the scale
@@ -295,23 +314,23 @@ __device__ __forceinline__ Coef load_coef(const LaunchScalars* sc)
 // written, the counter is kept; workgroup 0 backs the loss scale off) and on a
 // counter out of range (nothing is written at all).
 template <bool FUSED>
-__device__ __forceinline__ bool begin_step(const LaunchScalars* sc, const FusedStep& fs, Coef& c, int64_t& t,
-                                           float& scale)
+__device__ __forceinline__ bool begin_step(const LaunchScalars* sc, const FusedStep& fs, Coef& c, StepIn& in)
 {
     if constexpr (FUSED) {
-        // All three reads come before the one store a workgroup may make here,
+        // All four reads come before the one store a workgroup may make here,
         // so that the compiler can issue them as scalar loads (a store ahead of
         // a load in the kernel would turn it into a vector load with a full
         // wait before the data loads start).
         const int32_t flag = fs.found_inf ? *fs.found_inf : 0;
         const int32_t step = *fs.step;
-        scale = fs.amp ? fs.amp->scale : 0.0f;
+        in.scale = fs.amp ? fs.amp->scale : 0.0f;
+        in.sumsq = fs.clip.sumsq ? *fs.clip.sumsq : 0.0;
         if (!counter_in_range(step)) return false;
-        if (flag != 0) {
-            if (fs.amp && blockIdx.x == 0 && threadIdx.x == 0) advance_loss_scale(fs.amp, fs.scaler, scale, true);
+        if (flag != 0 || !is_sum_of_squares(in.sumsq)) {
+            if (fs.amp && blockIdx.x == 0 && threadIdx.x == 0) advance_loss_scale(fs.amp, fs.scaler, in.scale, true);
             return false;
         }
-        t = (int64_t)step + 1;   // as the prologue: no int32 overflow in the scalars
+        in.t = (int64_t)step + 1;   // as the prologue: no int32 overflow in the scalars
     } else {
         if (sc->skip) return false;
         c = load_coef(sc);
@@ -320,22 +339,26 @@ __device__ __forceinline__ bool begin_step(const LaunchScalars* sc, const FusedS
 }
 
 template <bool FUSED>
-__device__ __forceinline__ void fused_coef(const FusedStep& fs, int64_t t, float scale, Coef& c)
+__device__ __forceinline__ void fused_coef(const FusedStep& fs, const StepIn& in, Coef& c)
 {
-    if constexpr (FUSED) c = step_coef(fs.hp, t, fs.amp ? (float)(1.0 / (double)scale) : fs.hp.inv_loss_scale);
+    if constexpr (FUSED) {
+        float inv_scale = fs.amp ? (float)(1.0 / (double)in.scale) : fs.hp.inv_loss_scale;
+        if (fs.clip.sumsq) clip_scale(fs.clip, in.sumsq, inv_scale);
+        c = step_coef(fs.hp, in.t, inv_scale);
+    }
 }
 
 // End of a single-launch step: once every wave of this workgroup is past its
 // reads of the counter and the loss scale, one lane counts the workgroup; the
 // last one of the grid stores the new counter and advances the loss scale.
 template <bool FUSED>
-__device__ __forceinline__ void end_step(const FusedStep& fs, int64_t t, float scale)
+__device__ __forceinline__ void end_step(const FusedStep& fs, const StepIn& in)
 {
     if constexpr (FUSED) {
         __syncthreads();
         if (threadIdx.x == 0 && grid_done(fs.done)) {
-            __hip_atomic_store(fs.step, (int32_t)t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (fs.amp) advance_loss_scale(fs.amp, fs.scaler, scale, false);
+            __hip_atomic_store(fs.step, (int32_t)in.t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (fs.amp) advance_loss_scale(fs.amp, fs.scaler, in.scale, false);
         }
     }
 }
@@ -348,9 +371,8 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
                                                         const LaunchScalars* __restrict__ sc, FusedStep fs)
 {
     Coef c{};
-    int64_t t = 0;
-    float scale = 0.0f;
-    if (!begin_step<FUSED>(sc, fs, c, t, scale)) return;
+    StepIn in{};
+    if (!begin_step<FUSED>(sc, fs, c, in)) return;
     constexpr bool F16 = (MODE == 1);
     constexpr int NTM = ADAMW_NT_MIXED;
     constexpr int NTG = NTM | (ADAMW_NT_MIXED_GRAD ? 1 : 0);   // the gradient's loads
@@ -380,7 +402,7 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
             f32x4 W[2] = {ld<NTM>(w4 + 2 * k), ld<NTM>(w4 + 2 * k + 1)};
             f32x4 M[2] = {ld<NTM>(m4 + 2 * k), ld<NTM>(m4 + 2 * k + 1)};
             f32x4 V[2] = {ld<NTM>(v4 + 2 * k), ld<NTM>(v4 + 2 * k + 1)};
-            fused_coef<FUSED>(fs, t, scale, c);   // while the loads are in flight
+            fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
             float* wf = reinterpret_cast<float*>(W);
             float* mf = reinterpret_cast<float*>(M);
             float* vf = reinterpret_cast<float*>(V);
@@ -399,7 +421,7 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
             st<NTM>(p4 + k, u32x4{pw[0], pw[1], pw[2], pw[3]});
         }
     } else {
-        fused_coef<FUSED>(fs, t, scale, c);
+        fused_coef<FUSED>(fs, in, c);
         for (uint32_t i = part * kBlockMixed + tid; i < n; i += kStride) {
             float wi = w[i], mi = m[i], vi = v[i];
             const float nw = mixed_elem(widen1<F16>(g[i]), wi, mi, vi, c);
@@ -409,7 +431,7 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
             p[i] = narrow1<F16>(nw);
         }
     }
-    end_step<FUSED>(fs, t, scale);
+    end_step<FUSED>(fs, in);
 }
 
 // The aux stream of a pure-family step.
@@ -430,9 +452,8 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
                                                                             FusedStep fs)
 {
     Coef c{};
-    int64_t t = 0;
-    float scale = 0.0f;
-    if (!begin_step<FUSED>(sc, fs, c, t, scale)) return;
+    StepIn in{};
+    if (!begin_step<FUSED>(sc, fs, c, in)) return;
     constexpr bool KAHAN = AUX == kAuxKahan, SPLIT = AUX == kAuxSplit, KAHAN32 = AUX == kAuxKahan32;
     static_assert(!SPLIT || (M32 && V32), "the split master keeps fp32 moments");
     // The wide pure-family mixes (both moments in fp32, or an fp32
@@ -478,7 +499,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
 #pragma unroll
                 for (int q = 0; q < CW; ++q) C[q] = ld<NT>(c4 + CW * k + q);
             }
-            fused_coef<FUSED>(fs, t, scale, c);   // while the loads are in flight
+            fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
             const uint32_t* gw = reinterpret_cast<const uint32_t*>(&G);
             const uint32_t* pw = reinterpret_cast<const uint32_t*>(&Pv);
             uint32_t* cw = reinterpret_cast<uint32_t*>(C);   // 4 (bf16) or 8 (fp32) words
@@ -562,7 +583,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
             }
         }
     } else {
-        fused_coef<FUSED>(fs, t, scale, c);
+        fused_coef<FUSED>(fs, in, c);
         for (uint32_t i = part * kBlockPure + tid; i < n; i += kStride) {
             const float pf = widen1<false>(p[i]);
             float mi, vi;
@@ -597,7 +618,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
             if constexpr (V32) v[i] = vi; else v[i] = narrow1<false>(vi);
         }
     }
-    end_step<FUSED>(fs, t, scale);
+    end_step<FUSED>(fs, in);
 }
 
 // ---------------------------------------------------------------------------
@@ -669,10 +690,10 @@ __global__ __launch_bounds__(kBlockCheck) void check_kernel(const DevSeg* __rest
 
 hipError_t launch_prologue(const adamw_hparams& hp, int32_t* d_step, const int32_t* d_found_inf,
                            LaunchScalars* d_scalars, adamw_loss_scale_state* d_amp, const adamw_loss_scaler& scaler,
-                           hipStream_t stream)
+                           const ClipRule& clip, hipStream_t stream)
 {
     hipLaunchKernelGGL(prologue_kernel, dim3(1), dim3(64), 0, stream, hp, d_step, d_found_inf, d_scalars, d_amp,
-                       scaler);
+                       scaler, clip);
     return hipGetLastError();
 }
 

@@ -226,6 +226,7 @@ struct FusedStep {
     uint32_t* done;             // the finished-workgroup counters (kDoneLanes + 1 lines)
     adamw_loss_scale_state* amp;   // nullable: the device-resident dynamic loss scale
     adamw_loss_scaler scaler;      // its rule (with amp)
+    ClipRule clip;                 // its sumsq null: no clipping
 };
 
 }  // namespace adamw

@@ -170,5 +170,5 @@ extern "C" adamw_status adamw_multi_tensor_step_noalloc(adamw_mode mode, adamw_d
     const DevChunk* chunks = reinterpret_cast<const DevChunk*>(ds.ptr + kTableOffset + ds.n_segs * sizeof(DevSeg));
     return enqueue_step(kind, segs, chunks, ds.n_chunks, reinterpret_cast<LaunchScalars*>(ds.ptr),
                         reinterpret_cast<uint32_t*>(ds.ptr + kDoneOffset), *hp, d_step, d_found_inf, nullptr, nullptr,
-                        stream);
+                        ClipRule{}, stream);
 }

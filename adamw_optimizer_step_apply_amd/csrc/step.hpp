@@ -39,11 +39,12 @@ adamw_status check_step_call(const StepKind& kind, const adamw_tensor_list* list
 // Enqueues one step over a plan already on the device: small grids as one
 // launch of the update kernel (which uses the completion counters at `done`),
 // others as the prologue kernel (writing the scalars at `scalars`) and the
-// update kernel.  d_amp / scaler: the dynamic loss scale, or null.
+// update kernel.  d_amp / scaler: the dynamic loss scale, or null; clip: the
+// clipping rule, its sumsq null for none.
 adamw_status enqueue_step(const StepKind& kind, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
                           LaunchScalars* scalars, uint32_t* done, const adamw_hparams& hp, int32_t* d_step,
                           const int32_t* d_found_inf, adamw_loss_scale_state* d_amp, const adamw_loss_scaler* scaler,
-                          hipStream_t stream);
+                          const ClipRule& clip, hipStream_t stream);
 
 // The device a stream belongs to (the null stream: the calling thread's
 // current device), and whether the stream is being captured into a graph.
@@ -77,7 +78,7 @@ private:
 // Kernel launchers (kernels.hip).
 hipError_t launch_prologue(const adamw_hparams& hp, int32_t* d_step, const int32_t* d_found_inf,
                            LaunchScalars* d_scalars, adamw_loss_scale_state* d_amp, const adamw_loss_scaler& scaler,
-                           hipStream_t stream);
+                           const ClipRule& clip, hipStream_t stream);
 hipError_t launch_update(int kernel, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
                          const LaunchScalars* d_scalars, const FusedStep* fused, hipStream_t stream);
 hipError_t launch_zero_words(uint32_t* p, int64_t n, hipStream_t stream);

@@ -398,9 +398,33 @@ typedef struct {
  * inv_loss_scale (finite, > 0), and only f depends on it.  With f = 1 no element
  * changes and nothing is written.  If S is not finite (an inf or NaN gradient)
  * nothing is written either: the step that follows is to be skipped
- * (adamw_grad_norm's d_found_inf). */
+ * (adamw_grad_norm's d_found_inf).  For optimizers that take no clipping factor,
+ * and for gradients that others read; adamw_multi_tensor_step_clipped needs no such
+ * pass. */
 adamw_status adamw_clip_grads(adamw_dtype g_dtype, const adamw_tensor_list* grads, const adamw_grad_clip* clip,
                               float inv_loss_scale, const adamw_loss_scale_state* d_scale, void* hip_stream);
+
+/* AdamW step with its gradients clipped by the global norm as they are read: the
+ * step of (mode, p_dtype) -- or, with prec non-null, of
+ * adamw_pure_multi_tensor_step with *prec (mode and p_dtype ignored) -- whose
+ * gradient multiplier is round_f32(inv * f), inv the inverse loss scale and f the
+ * factor of *clip, in place of inv.  The gradients are read once and not written,
+ * and no 16-bit rounding comes between clipping and moments.  inv is
+ * hp->inv_loss_scale, or with d_scale non-null (float)(1 / (double)d_scale->scale)
+ * read on the device, which then also advances by *scaler as in
+ * adamw_multi_tensor_step_amp.  If *clip->d_sumsq is not finite, or *d_found_inf
+ * (nullable) is set, the step is skipped: nothing is written, the counter is kept
+ * and the loss scale backs off.  Typical sequence per iteration: adamw_grad_norm
+ * over every list, an all-reduce(sum) of *d_sumsq across ranks, then this call per
+ * list.  With scaler null *d_scale is read
+ * and not advanced: for every list but the last of a step that spans several
+ * (parameter groups, each with its own counter).  List, shard, state layouts,
+ * counter, graphs and errors as adamw_multi_tensor_step. */
+adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
+                                             const adamw_tensor_list* list, const adamw_hparams* hp,
+                                             const adamw_grad_clip* clip, int32_t* d_step, const int32_t* d_found_inf,
+                                             adamw_loss_scale_state* d_scale, const adamw_loss_scaler* scaler,
+                                             void* hip_stream);
 
 /* Description of the last error on the calling thread ("" if none).  Valid
  * until the next call into the library on that thread. */

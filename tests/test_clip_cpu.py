@@ -62,3 +62,47 @@ def test_binding_struct_matches_the_c_layout(tmp_path):
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     s = A.adamw_grad_clip
     assert got == [ctypes.sizeof(s), s.d_sumsq.offset, s.max_norm.offset, s.eps.offset]
+
+
+def _tl(numels, base=FAKE, esz=(2, 2, 4, 4, 4)):
+    import numpy as np
+    offs = np.concatenate([[0], np.cumsum(numels)[:-1]])
+    return A.TensorList(numels, [[base + s * (1 << 36) + int(o) * esz[s] for o in offs] for s in range(5)])
+
+
+def step(mode=A.MIXED, dt=A.BF16, tl=None, hp=None, c=None, d_step=FAKE, **kw):
+    A.adamw_multi_tensor_step_clipped(mode, dt, tl or _tl([10]), hp or A.HParams(), c or clip(), d_step, stream=0, **kw)
+
+
+@pytest.mark.parametrize("call,needle", [
+    (lambda: step(dt=A.F32), "p_dtype"),
+    (lambda: step(mode=9), "mode"),
+    (lambda: step(c=clip(d_sumsq=0)), "d_sumsq"),
+    (lambda: step(c=clip(d_sumsq=FAKE + 4)), "8-byte"),
+    (lambda: step(c=clip(max_norm=-0.5)), "max_norm"),
+    (lambda: step(c=clip(max_norm=float("inf"))), "max_norm"),
+    (lambda: step(c=clip(eps=float("inf"))), "eps"),
+    (lambda: step(hp=A.HParams(beta1=1.0)), "beta"),
+    (lambda: step(d_step=0), "d_step"),
+    (lambda: step(d_step=FAKE + 2), "aligned"),
+    (lambda: step(d_found_inf=FAKE + 1), "aligned"),
+    (lambda: step(d_scale=FAKE + 2), "d_scale"),
+    (lambda: step(d_scale=FAKE, scaler=A.LossScaler(0.5, 0.5, 10)), "growth_factor"),
+    (lambda: step(d_scale=FAKE, scaler=A.LossScaler(2.0, 0.5, 0)), "growth_interval"),
+    (lambda: step(prec=A.PurePrecision(A.F16, A.BF16, 1)), "exp_avg"),
+    (lambda: step(tl=_tl([10], base=FAKE + 1)), "aligned"),
+    (lambda: step(tl=A.TensorList([10], [[FAKE], None, [FAKE], [FAKE], [FAKE]])), "grad"),
+])
+def test_step_rejected_before_any_hip_call(call, needle):
+    with pytest.raises(A.AdamWError) as ei:
+        call()
+    assert ei.value.status in (A.E_INVALID, A.E_UNSUPPORTED)
+    assert needle.lower() in str(ei.value).lower(), str(ei.value)
+
+
+@pytest.mark.parametrize("kw", [{}, {"mode": A.PURE_KAHAN, "tl": _tl([10], esz=(2,) * 5)}, {"d_scale": FAKE, "dt": A.F16},
+                                {"d_scale": FAKE, "advance_scale": False, "scaler": A.LossScaler(2.0, 0.5, 0)}])
+def test_valid_step_reaches_hip(kw):
+    with pytest.raises(A.AdamWError) as ei:
+        step(**kw)
+    assert ei.value.status == A.E_HIP
