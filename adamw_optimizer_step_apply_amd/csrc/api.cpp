@@ -200,7 +200,7 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     if (tag == kTagSweep)
         dev_bytes = PlanSlot::sweep_table_bytes((int64_t)plan.segs.size(), (int64_t)plan.chunks.size(),
                                                 list->n_tensors) +
-                    plan.chunks.size() * sizeof(double);
+                    (size_t)partial_count((int64_t)plan.chunks.size()) * sizeof(double);
     hipError_t e;
     if (!slot.uploaded) {
         e = hipEventCreateWithFlags(&slot.uploaded, hipEventDisableTiming);
@@ -442,8 +442,9 @@ adamw_status sum_of_squares(adamw_dtype g_dtype, const adamw_tensor_list* grads,
     Sweep sw;
     if ((st = begin_sweep(esz, grads, hip_stream, &sw)) != ADAMW_OK) return st;
     const PlanSlot& p = *sw.plan;
+    const bool single = single_launch(p.n_chunks) && p.n_chunks <= kSingleSumMaxWorkgroups;
     hipError_t e = launch_sumsq(g_dtype, p.segs(), p.chunks(), p.n_chunks, p.tensor_first(), p.n_tensors, p.partials(),
-                                out, sw.stream);
+                                sw.done, single, out, sw.stream);
     if (e != hipSuccess) return hip_fail("sum of squares launch", e);
     return ADAMW_OK;
 }

@@ -99,18 +99,18 @@ struct DoneLane {
     uint32_t lanes, j, in_lane;
 };
 
-__device__ __forceinline__ DoneLane done_lane()
+__device__ __forceinline__ DoneLane done_lane(uint32_t b, uint32_t nb)
 {
-    const uint32_t nb = gridDim.x, b = blockIdx.x;
     const uint32_t lanes = nb < (uint32_t)kDoneLanes ? nb : (uint32_t)kDoneLanes;
     const uint32_t j = b % lanes;
     return DoneLane{lanes, j, nb / lanes + (j < nb % lanes ? 1u : 0u)};
 }
 
-// The count alone, on 32-bit words (the low words of the counter lines).
-__device__ __forceinline__ bool grid_done(uint32_t* done)
+// The count alone, on 32-bit words (the low words of the counter lines), of
+// workgroup b of nb that count themselves.
+__device__ __forceinline__ bool grid_done(uint32_t* done, uint32_t b, uint32_t nb)
 {
-    const DoneLane d = done_lane();
+    const DoneLane d = done_lane(b, nb);
     uint32_t* first = done + (size_t)d.j * kDoneStrideWords;
     uint32_t* second = done + (size_t)kDoneLanes * kDoneStrideWords;
     if (__hip_atomic_fetch_add(first, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != d.in_lane - 1) return false;
@@ -127,7 +127,7 @@ __device__ __forceinline__ bool grid_done(uint32_t* done)
 // zero, so the update and check kernels of one stream share the lines.
 __device__ __forceinline__ bool grid_done_verdict(uint32_t* done, uint32_t verdict, uint32_t* lanes_hit)
 {
-    const DoneLane d = done_lane();
+    const DoneLane d = done_lane(blockIdx.x, gridDim.x);
     uint64_t* first = reinterpret_cast<uint64_t*>(done + (size_t)d.j * kDoneStrideWords);
     uint64_t* second = reinterpret_cast<uint64_t*>(done + (size_t)kDoneLanes * kDoneStrideWords);
     const uint64_t prev = __hip_atomic_fetch_add(first, 1ull + ((uint64_t)verdict << 32), __ATOMIC_RELAXED,

@@ -356,7 +356,7 @@ __device__ __forceinline__ void end_step(const FusedStep& fs, const StepIn& in)
 {
     if constexpr (FUSED) {
         __syncthreads();
-        if (threadIdx.x == 0 && grid_done(fs.done)) {
+        if (threadIdx.x == 0 && grid_done(fs.done, blockIdx.x, gridDim.x)) {
             __hip_atomic_store(fs.step, (int32_t)in.t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             if (fs.amp) advance_loss_scale(fs.amp, fs.scaler, in.scale, false);
         }

@@ -113,6 +113,15 @@ constexpr int kBlockSweep = 256;
 constexpr int kSweepUnroll = 8;
 constexpr int64_t kSweepChunkBytes = (int64_t)kBlockSweep * 16 * kSweepUnroll;
 constexpr int64_t kMaxSweepChunks = (int64_t)UINT32_MAX / kBlockSweep;
+// A sum of squares runs as one launch (its last workgroup joins the partial sums) up
+// to this many workgroups, if the single-launch limit allows as many: measured on
+// MI355X (bf16, one tensor), one launch / two: 3.6 / 5.7 us at 0.26 MB, 3.7 / 5.6 at
+// 1 MB, 6.3 / 6.7 at 26 MB (800 workgroups), 41.2 / 38.2 at 252 MB (7,680), where the
+// counting atomics cost more than a launch.
+constexpr int64_t kSingleSumMaxWorkgroups = 1024;
+// Partial sums are joined by 256-lane workgroups, this many each.
+constexpr int kBlockJoin = 256;
+constexpr int kJoin = 4096;
 // The state copy (setup and checkpoint) runs one 256-lane workgroup per chunk.
 constexpr int kBlockCopy = 256;
 constexpr int64_t kMaxCopyChunks = (int64_t)UINT32_MAX / kBlockCopy;

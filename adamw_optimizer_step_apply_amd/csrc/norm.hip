@@ -9,9 +9,9 @@
 // finite exactly if an element is inf or NaN, so the overflow test of fp16
 // training comes with the norm.
 //
-// Each workgroup sums one chunk into one partial; a second launch joins the
-// partials in a fixed order (no floating-point atomics), so a list gives the
-// same bits at every call.
+// Each workgroup sums one chunk into one partial; the partials are joined in a fixed
+// order (no floating-point atomics), so a list gives the same bits at every call: by
+// a second launch, or for small lists by the last workgroup of the first.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -80,8 +80,8 @@ struct Span {
     }
 };
 
-// Sum over the workgroup, in lane 0 of wave 0: a butterfly in each wave, then the
-// waves in order.
+// Sum over the workgroup, in every lane: a butterfly in each wave, then the waves in
+// order.  A second call needs a barrier after the first.
 template <int BLOCK>
 __device__ __forceinline__ double block_sum(double x)
 {
@@ -97,10 +97,69 @@ __device__ __forceinline__ double block_sum(double x)
     return s;
 }
 
-template <int DT>
+// A value that another workgroup of the same launch reads: stored and loaded past
+// the XCDs' L2s (agent scope).  handed_over() waits until the stores before it have
+// reached memory; the relaxed count that follows then tells the reader that they
+// have.  A release fence would write back the whole L2 of the XCD instead: with one
+// per workgroup a 2.7 GB sum took 4,050 us instead of 390.
+__device__ __forceinline__ void hand_over(double* p, double x)
+{
+    __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ void handed_over() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// The sum of n <= kJoin values by one workgroup, lane l taking l, l + 256, ... in
+// order: however the values come (SHARED: from workgroups of this launch), the same
+// bits.
+template <bool SHARED>
+__device__ __forceinline__ double join(const double* p, uint32_t n)
+{
+    constexpr int kUnroll = 8;
+    double x = 0.0;
+    for (uint32_t k0 = threadIdx.x; k0 < n; k0 += kBlockJoin * kUnroll) {
+        double v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const uint32_t k = k0 + u * kBlockJoin;
+            if constexpr (SHARED)
+                v[u] = k < n ? __hip_atomic_load(p + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+            else
+                v[u] = k < n ? p[k] : 0.0;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) x += v[u];
+    }
+    return block_sum<kBlockJoin>(x);
+}
+
+__device__ __forceinline__ void write_total(const NormOut& out, double x)
+{
+    if (out.accumulate) x += *out.sumsq;
+    *out.sumsq = x;
+    if (out.norm) *out.norm = (float)__builtin_sqrt(x);
+    if (out.found_inf) *out.found_inf = __builtin_isfinite(x) ? 0 : 1;
+}
+
+// Whether this workgroup is the last of nb to hand a value over (uniform).
+__device__ __forceinline__ bool last_of(double* slot, double x, uint32_t* done, uint32_t b, uint32_t nb)
+{
+    __shared__ int last;
+    if (threadIdx.x == 0) {
+        hand_over(slot, x);
+        handed_over();
+        last = grid_done(done, b, nb);
+    }
+    __syncthreads();
+    return last != 0;
+}
+
+// FUSED: the only launch of a small sum, whose last workgroup joins the partials.
+template <int DT, bool FUSED>
 __global__ __launch_bounds__(kBlockSweep) void sumsq_kernel(const DevSeg* __restrict__ segs,
                                                         const DevChunk* __restrict__ chunks,
-                                                        double* __restrict__ partials)
+                                                        double* __restrict__ partials, uint32_t* __restrict__ done,
+                                                        NormOut out)
 {
     const uint32_t ci = xcd_chunk(blockIdx.x, gridDim.x);
     const DevChunk ch = chunks[ci];
@@ -121,36 +180,57 @@ __global__ __launch_bounds__(kBlockSweep) void sumsq_kernel(const DevSeg* __rest
     if (tid < sp.head) a += square1<DT>(sp.head_addr(tid));
     if (tid < sp.tail) b += square1<DT>(sp.tail_addr(tid));
     const double s = block_sum<kBlockSweep>(a + b);
-    if (tid == 0) partials[ci] = s;
-}
-
-// One workgroup per tensor: its chunks' partials (consecutive) to its sum.
-__global__ __launch_bounds__(256) void tensor_sum_kernel(const double* __restrict__ partials,
-                                                     const uint32_t* __restrict__ tensor_first, NormOut out)
-{
-    const uint32_t i = blockIdx.x;
-    const uint32_t first = tensor_first[i], last = tensor_first[i + 1];
-    double x = 0.0;
-    for (uint32_t k = first + threadIdx.x; k < last; k += 256) x += partials[k];
-    x = block_sum<256>(x);
-    if (threadIdx.x == 0) {
-        if (out.tensor_sumsq) out.tensor_sumsq[i] = x;
-        if (out.tensor_norm) out.tensor_norm[i] = (float)__builtin_sqrt(x);
+    if constexpr (FUSED) {
+        if (!last_of(partials + ci, s, done, blockIdx.x, gridDim.x)) return;
+        const double x = join<true>(partials, gridDim.x);
+        if (tid == 0) write_total(out, x);
+    } else {
+        if (tid == 0) partials[ci] = s;
     }
 }
 
-// One workgroup: all partials to the list's sum.
-constexpr int kBlockTotal = 1024;
-__global__ __launch_bounds__(kBlockTotal) void total_kernel(const double* __restrict__ partials, uint32_t n, NormOut out)
+// Joins the partials of a sum.  Workgroups [0, n_blocks): kJoin partials each; the
+// last of them to finish joins their sums.  The others: 4 tensors each (per-tensor
+// norms), one per wave, or by all waves one after the other for tensors of many
+// chunks.
+constexpr int kTensorsPerGroup = kBlockJoin / 64;
+constexpr uint32_t kWaveChunks = 256;   // chunks of a tensor that one wave sums
+__global__ __launch_bounds__(kBlockJoin) void join_kernel(double* __restrict__ partials, uint32_t n, uint32_t n_blocks,
+                                                      const uint32_t* __restrict__ tensor_first, uint32_t n_tensors,
+                                                      uint32_t* __restrict__ done, NormOut out)
 {
-    double x = 0.0;
-    for (uint32_t k = threadIdx.x; k < n; k += kBlockTotal) x += partials[k];
-    x = block_sum<kBlockTotal>(x);
-    if (threadIdx.x == 0) {
-        if (out.accumulate) x += *out.sumsq;
-        *out.sumsq = x;
-        if (out.norm) *out.norm = (float)__builtin_sqrt(x);
-        if (out.found_inf) *out.found_inf = __builtin_isfinite(x) ? 0 : 1;
+    const uint32_t b = blockIdx.x, tid = threadIdx.x;
+    if (b < n_blocks) {
+        const uint32_t at = b * (uint32_t)kJoin;
+        double x = join<false>(partials + at, n - at < (uint32_t)kJoin ? n - at : (uint32_t)kJoin);
+        if (n_blocks > 1) {
+            double* sums = partials + n;
+            if (!last_of(sums + b, x, done, b, n_blocks)) return;
+            x = join<true>(sums, n_blocks);
+        }
+        if (tid == 0) write_total(out, x);
+        return;
+    }
+    const uint32_t t0 = (b - n_blocks) * kTensorsPerGroup, lane = tid % 64, wave = tid / 64;
+    for (uint32_t w = 0; w < kTensorsPerGroup; ++w) {
+        const uint32_t i = t0 + w;
+        if (i >= n_tensors) return;
+        const uint32_t first = tensor_first[i], last = tensor_first[i + 1];
+        double x = 0.0;
+        if (last - first > kWaveChunks) {
+            for (uint32_t k = first + tid; k < last; k += kBlockJoin) x += partials[k];
+            x = block_sum<kBlockJoin>(x);
+            __syncthreads();
+            if (tid != 0) continue;
+        } else {
+            if (wave != w) continue;
+            for (uint32_t k = first + lane; k < last; k += 64) x += partials[k];
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+            if (lane != 0) continue;
+        }
+        if (out.tensor_sumsq) out.tensor_sumsq[i] = x;
+        if (out.tensor_norm) out.tensor_norm[i] = (float)__builtin_sqrt(x);
     }
 }
 
@@ -223,30 +303,43 @@ hipError_t launch_clip(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* 
     return hipGetLastError();
 }
 
-hipError_t launch_sumsq(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
-                        const uint32_t* tensor_first, int64_t n_tensors, double* partials, const NormOut& out,
-                        hipStream_t stream)
+int64_t partial_count(int64_t n_chunks) { return n_chunks + (n_chunks + kJoin - 1) / kJoin; }
+static_assert(kMaxSweepChunks <= (int64_t)kJoin * kJoin, "one workgroup joins the block sums");
+
+template <bool FUSED>
+static void launch_sums(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+                        double* partials, uint32_t* done, const NormOut& out, hipStream_t stream)
 {
-    hipError_t e = hipSuccess;
+    const dim3 grid((unsigned)n_chunks), block(kBlockSweep);
+    if (g_dtype == ADAMW_F16)
+        hipLaunchKernelGGL((sumsq_kernel<kF16, FUSED>), grid, block, 0, stream, segs, chunks, partials, done, out);
+    else if (g_dtype == ADAMW_BF16)
+        hipLaunchKernelGGL((sumsq_kernel<kBf16, FUSED>), grid, block, 0, stream, segs, chunks, partials, done, out);
+    else
+        hipLaunchKernelGGL((sumsq_kernel<kF32, FUSED>), grid, block, 0, stream, segs, chunks, partials, done, out);
+}
+
+hipError_t launch_sumsq(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+                        const uint32_t* tensor_first, int64_t n_tensors, double* partials, uint32_t* done, bool single,
+                        const NormOut& out, hipStream_t stream)
+{
+    const bool per_tensor = (out.tensor_norm || out.tensor_sumsq) && n_tensors > 0;
+    if (single && !per_tensor) {
+        launch_sums<true>(g_dtype, segs, chunks, n_chunks, partials, done, out, stream);
+        return hipGetLastError();
+    }
     if (n_chunks > 0) {
-        const dim3 grid((unsigned)n_chunks), block(kBlockSweep);
-        if (g_dtype == ADAMW_F16)
-            hipLaunchKernelGGL((sumsq_kernel<kF16>), grid, block, 0, stream, segs, chunks, partials);
-        else if (g_dtype == ADAMW_BF16)
-            hipLaunchKernelGGL((sumsq_kernel<kBf16>), grid, block, 0, stream, segs, chunks, partials);
-        else
-            hipLaunchKernelGGL((sumsq_kernel<kF32>), grid, block, 0, stream, segs, chunks, partials);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        launch_sums<false>(g_dtype, segs, chunks, n_chunks, partials, done, out, stream);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    if ((out.tensor_norm || out.tensor_sumsq) && n_tensors > 0) {
-        hipLaunchKernelGGL(tensor_sum_kernel, dim3((unsigned)n_tensors), dim3(256), 0, stream, partials, tensor_first, out);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (out.sumsq) {
-        hipLaunchKernelGGL(total_kernel, dim3(1), dim3(kBlockTotal), 0, stream, partials, (uint32_t)n_chunks, out);
-        e = hipGetLastError();
-    }
-    return e;
+    // an empty list's total is written by one workgroup all the same
+    const int64_t blocks = !out.sumsq ? 0 : n_chunks > 0 ? (n_chunks + kJoin - 1) / kJoin : 1;
+    const int64_t groups = blocks + (per_tensor ? (n_tensors + kTensorsPerGroup - 1) / kTensorsPerGroup : 0);
+    if (groups == 0) return hipSuccess;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)groups), dim3(kBlockJoin), 0, stream, partials, (uint32_t)n_chunks,
+                       (uint32_t)blocks, tensor_first, (uint32_t)n_tensors, done, out);
+    return hipGetLastError();
 }
 
 }  // namespace adamw

@@ -127,8 +127,8 @@ def test_range_of_the_inputs(dt, values):
     root = math.sqrt(want)
     if root > 3.402824e38:      # beyond binary32
         assert r == math.inf
-    else:
-        assert abs(r - root) <= NORM_TOL * root
+    else:      # below 2^-126 binary32 has steps of 2^-149, whose half is the rounding's bound
+        assert abs(r - root) <= NORM_TOL * root + 2.0 ** -150
 
 
 @pytest.mark.parametrize("dt", [A.BF16, A.F16, A.F32])
@@ -357,3 +357,49 @@ def test_workspace_release_between_calls():
     torch.cuda.synchronize()
     A.adamw_release_workspace()
     assert norm(A.F16, tl) == a
+
+
+@pytest.fixture
+def single_launch_limit():
+    yield A.adamw_set_single_launch_max_workgroups
+    A.adamw_set_single_launch_max_workgroups(-1)
+
+
+@pytest.mark.parametrize("chunks", [1, 2, 31, 33, 700, 1024])
+def test_one_launch_equals_two(chunks, single_launch_limit):
+    """The single launch's last workgroup sees every other's partial of this call, not of
+    an earlier one: 60 calls in a row with other gradients each, bit-identical to the
+    two-launch form."""
+    n = 16384 * (chunks - 1) + 5
+    base = torch.randn(n + 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(chunks)).to(torch.bfloat16)
+    x = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    tl = A.TensorList([n], [None, [x]])
+    assert len(A.adamw_plan_inspect(A.MIXED, A.BF16, tl, for_check=2)) == chunks
+    one, two = out64().repeat(60), out64().repeat(60)
+    for k in range(60):
+        x.copy_(base[k:k + n]).mul_(1.0 + k)
+        single_launch_limit(-1)
+        A.adamw_grad_norm(A.BF16, tl, one[k:k + 1])
+        single_launch_limit(0)
+        A.adamw_grad_norm(A.BF16, tl, two[k:k + 1])
+    torch.cuda.synchronize()
+    assert same_bits(one, two) and len(set(one.tolist())) == 60
+
+
+def test_joins_of_several_levels():
+    """More than 4,096 chunks (the partials are joined in blocks), and the whole-list sum
+    beside per-tensor norms, of tensors of many chunks and of one."""
+    numels = [16384 * 5000 + 3, 7, 0, 16384 * 300, 100, 16384 * 256, 16384 * 257]
+    buf = torch.randint(-3, 4, (sum(numels) + 1,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(5),
+                        dtype=torch.int8).to(torch.bfloat16)[1:]
+    ts, o = [], 0
+    for n in numels:
+        ts.append(buf[o:o + n])
+        o += n
+    want = [int((t.float() ** 2).sum(dtype=torch.float64)) for t in ts]      # whole numbers: every order is exact
+    tl = A.TensorList(numels, [None, ts])
+    assert norm(A.BF16, tl)[0] == sum(want)
+    q, s = out64().repeat(len(numels)), out64()
+    A.adamw_tensor_norms(A.BF16, tl, None, q, s)
+    assert q.tolist() == want and s.item() == sum(want)
+    free()
