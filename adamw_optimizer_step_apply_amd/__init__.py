@@ -412,7 +412,7 @@ def adamw_abi_version() -> int:
 
 def adamw_plan_inspect(mode: int, p_dtype: int, tensors: TensorList, for_check: int = False):
     """The chunk plan as a list of (tensor, offset_in_tensor, count, kind, flat_pos, segment);
-    ``for_check`` 1 for the overflow check's, 2 for the gradient norms'."""
+    ``for_check`` 1 for the overflow check's, 2 for the gradient norms', 3 for the clipping's."""
     n = _lib.adamw_plan_inspect(mode, p_dtype, ctypes.byref(tensors.c), int(for_check), None, 0)
     if n < 0:
         raise AdamWError(E_INVALID, adamw_last_error())

@@ -48,10 +48,10 @@ adamw_status hip_fail(const char* what, hipError_t e)
 
 namespace {
 
-// A device-resident copy of one plan (segment table, chunk table and, for a
-// gradient sweep, the tensors' first chunks), uploaded through a pinned staging
-// buffer.  A sweep's plan is followed by room for its partial sums, so that two
-// lists, and a captured graph and later calls, never share them.
+// A device-resident copy of one plan, uploaded through a pinned staging buffer: an
+// update's or the check's segment and chunk tables; a gradient sweep's workgroups
+// and, for the norms, the tensors' first chunks and room for the partial sums (so
+// that two lists, and a captured graph and later calls, never share them).
 struct PlanSlot {
     void* dev = nullptr;
     size_t dev_cap = 0;
@@ -69,17 +69,17 @@ struct PlanSlot {
     {
         return reinterpret_cast<const DevChunk*>(static_cast<const char*>(dev) + n_segs * sizeof(DevSeg));
     }
-    const uint32_t* tensor_first() const { return reinterpret_cast<const uint32_t*>(chunks() + n_chunks); }
+    // a sweep's: n_chunks workgroups
+    const DevSweep* groups() const { return static_cast<const DevSweep*>(dev); }
+    const uint32_t* tensor_first() const { return reinterpret_cast<const uint32_t*>(groups() + n_chunks); }
     double* partials() const
     {
-        return reinterpret_cast<double*>(static_cast<char*>(dev) + sweep_table_bytes(n_segs, n_chunks, n_tensors));
+        return reinterpret_cast<double*>(static_cast<char*>(dev) + norm_table_bytes(n_chunks, n_tensors));
     }
-    // A sweep's tables, rounded up to the alignment of what follows.
-    static size_t sweep_table_bytes(int64_t segs, int64_t chunks, int64_t tensors)
+    // A norm's tables, rounded up to the alignment of what follows.
+    static size_t norm_table_bytes(int64_t groups, int64_t tensors)
     {
-        const size_t b = (size_t)segs * sizeof(DevSeg) + (size_t)chunks * sizeof(DevChunk) +
-                         (size_t)(tensors + 1) * sizeof(uint32_t);
-        return (b + 15) / 16 * 16;
+        return ((size_t)groups * sizeof(DevSweep) + (size_t)(tensors + 1) * sizeof(uint32_t) + 15) / 16 * 16;
     }
 
     void release()
@@ -116,20 +116,37 @@ std::atomic<int64_t> g_chunk_elems{0};   // 0: each kernel's own default chunk
 // forms the step's scalars itself) instead of prologue + update kernel.
 std::atomic<int64_t> g_single_launch_max_workgroups{kSingleLaunchMaxWorkgroups};
 
-// The chunk limit of a plan for `tag` (an update kernel id, kTagCheck or
-// kTagSweep): the grid of one launch holds at most 2^32 - 1 lanes.
+bool is_sweep(int64_t tag) { return tag == kTagNorm || tag == kTagClip; }
+
+// The chunk limit of a plan for `tag` (an update kernel id, kTagCheck, kTagNorm or
+// kTagClip): the grid of one launch holds at most 2^32 - 1 lanes.
 int64_t max_chunks_of(int64_t tag)
 {
-    return tag == kTagSweep ? kMaxSweepChunks : tag == kTagCheck ? kMaxCheckChunks : kMaxUpdateChunks;
+    return tag == kTagNorm ? kMaxSweepChunks : tag == kTagClip ? kMaxSweepChunks / kXcdParts
+         : tag == kTagCheck ? kMaxCheckChunks : kMaxUpdateChunks;
 }
 
 adamw_status plan_of(int64_t tag, const int esz[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,
                      Plan* out, std::string& err)
 {
-    if (tag == kTagSweep)
+    if (is_sweep(tag))
         return build_sweep_plan(esz[ADAMW_STREAM_GRAD], list, chunk_elems, max_chunks_of(tag), out, err);
     return build_plan(esz, list, chunk_elems, max_chunks_of(tag), out, err);
 }
+
+// The tables of a plan as they go to the device, and the bytes to allocate for them.
+struct Tables {
+    std::vector<unsigned char> bytes;
+    int64_t n_segs = 0, n_chunks = 0;
+    size_t dev_bytes = 0;
+
+    template <typename T>
+    void add(const std::vector<T>& v)
+    {
+        const unsigned char* p = reinterpret_cast<const unsigned char*>(v.data());
+        bytes.insert(bytes.end(), p, p + v.size() * sizeof(T));
+    }
+};
 
 // The workspace of a stream, on the stream's own device.
 adamw_status get_workspace(hipStream_t stream, StreamWorkspace** out)
@@ -192,15 +209,25 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     slot.valid = false;
     *out = &slot;
 
-    const size_t seg_bytes = plan.segs.size() * sizeof(DevSeg);
-    const size_t chunk_bytes = plan.chunks.size() * sizeof(DevChunk);
-    const size_t first_bytes = plan.tensor_first.size() * sizeof(uint32_t);   // 0 but for a sweep
-    const size_t bytes = seg_bytes + chunk_bytes + first_bytes;
-    size_t dev_bytes = bytes;
-    if (tag == kTagSweep)
-        dev_bytes = PlanSlot::sweep_table_bytes((int64_t)plan.segs.size(), (int64_t)plan.chunks.size(),
-                                                list->n_tensors) +
-                    (size_t)partial_count((int64_t)plan.chunks.size()) * sizeof(double);
+    Tables tab;
+    if (is_sweep(tag)) {
+        const std::vector<DevSweep> groups = sweep_groups(plan, esz[ADAMW_STREAM_GRAD], tag == kTagClip);
+        tab.n_chunks = (int64_t)groups.size();
+        tab.add(groups);
+        tab.dev_bytes = tab.bytes.size();
+        if (tag == kTagNorm) {
+            tab.add(plan.tensor_first);
+            tab.dev_bytes = PlanSlot::norm_table_bytes(tab.n_chunks, list->n_tensors) +
+                            (size_t)partial_count(tab.n_chunks) * sizeof(double);
+        }
+    } else {
+        tab.n_segs = (int64_t)plan.segs.size();
+        tab.n_chunks = (int64_t)plan.chunks.size();
+        tab.add(plan.segs);
+        tab.add(plan.chunks);
+        tab.dev_bytes = tab.bytes.size();
+    }
+    const size_t bytes = tab.bytes.size(), dev_bytes = tab.dev_bytes;
     hipError_t e;
     if (!slot.uploaded) {
         e = hipEventCreateWithFlags(&slot.uploaded, hipEventDisableTiming);
@@ -234,18 +261,15 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
         slot.dev_cap = cap;
     }
     if (bytes) {
-        memcpy(slot.host, plan.segs.data(), seg_bytes);
-        memcpy(static_cast<char*>(slot.host) + seg_bytes, plan.chunks.data(), chunk_bytes);
-        if (first_bytes)
-            memcpy(static_cast<char*>(slot.host) + seg_bytes + chunk_bytes, plan.tensor_first.data(), first_bytes);
+        memcpy(slot.host, tab.bytes.data(), bytes);
         e = hipMemcpyAsync(slot.dev, slot.host, bytes, hipMemcpyHostToDevice, stream);
         if (e != hipSuccess) { slot.valid = false; return hip_fail("hipMemcpyAsync (chunk table)", e); }
         e = hipEventRecord(slot.uploaded, stream);
         if (e != hipSuccess) { slot.valid = false; return hip_fail("hipEventRecord", e); }
         slot.upload_in_flight = true;
     }
-    slot.n_segs = (int64_t)plan.segs.size();
-    slot.n_chunks = (int64_t)plan.chunks.size();
+    slot.n_segs = tab.n_segs;
+    slot.n_chunks = tab.n_chunks;
     slot.n_tensors = list->n_tensors;
     slot.key.swap(key);
     slot.valid = true;
@@ -353,11 +377,14 @@ int64_t check_chunk_elems()
     return c ? c : kCheckChunkElems;
 }
 
-int64_t sweep_chunk_elems(int esz)
+int64_t sweep_chunk_elems(int64_t tag, int esz)
 {
     const int64_t c = g_chunk_elems.load(std::memory_order_relaxed);
-    return c ? c : kSweepChunkBytes / esz;
+    return c ? c : (tag == kTagClip ? kClipChunkBytes : kNormChunkBytes) / esz;
 }
+
+// The sweep that an introspection call asks for, or 0.
+int64_t sweep_tag(int for_check) { return for_check == 2 ? kTagNorm : for_check == 3 ? kTagClip : 0; }
 
 // Row i of adamw_plan_inspect: {tensor, offset in the tensor, count, kind, flat position, segment}.
 void inspect_row(const Plan& plan, size_t i, int64_t* r)
@@ -408,15 +435,15 @@ struct Sweep {
 };
 
 // Checks the list of a sweep over elements of `esz` bytes (before any HIP call)
-// and readies its plan.  The lock and the device stay with *out.
-adamw_status begin_sweep(int esz_g, const adamw_tensor_list* grads, void* hip_stream, Sweep* out)
+// and readies its plan for `tag`.  The lock and the device stay with *out.
+adamw_status begin_sweep(int64_t tag, int esz_g, const adamw_tensor_list* grads, void* hip_stream, Sweep* out)
 {
     adamw_status st;
     if ((st = basic_list_check(grads)) != ADAMW_OK) return st;
     int esz[kStreams] = {0, 0, 0, 0, 0};
     esz[ADAMW_STREAM_GRAD] = esz_g;
-    const int64_t chunk_elems = sweep_chunk_elems(esz_g);
-    if ((st = validate_list(kTagSweep, esz, grads, chunk_elems)) != ADAMW_OK) return st;
+    const int64_t chunk_elems = sweep_chunk_elems(tag, esz_g);
+    if ((st = validate_list(tag, esz, grads, chunk_elems)) != ADAMW_OK) return st;
     out->stream = static_cast<hipStream_t>(hip_stream);
     if ((st = get_workspace(out->stream, &out->ws)) != ADAMW_OK) return st;
     out->lk = std::unique_lock<std::mutex>(out->ws->mu);
@@ -424,7 +451,7 @@ adamw_status begin_sweep(int esz_g, const adamw_tensor_list* grads, void* hip_st
     bool cap = false;
     if ((st = capturing(out->stream, &cap)) != ADAMW_OK) return st;
     if ((st = ensure_workspace_block(*out->ws, out->stream, cap, &out->done)) != ADAMW_OK) return st;
-    return ensure_plan(*out->ws, kTagSweep, esz, grads, chunk_elems, out->stream, cap, &out->plan);
+    return ensure_plan(*out->ws, tag, esz, grads, chunk_elems, out->stream, cap, &out->plan);
 }
 
 adamw_status sum_of_squares(adamw_dtype g_dtype, const adamw_tensor_list* grads, const NormOut& out, void* hip_stream)
@@ -440,10 +467,10 @@ adamw_status sum_of_squares(adamw_dtype g_dtype, const adamw_tensor_list* grads,
     if ((out.tensor_norm || out.tensor_sumsq) && grads && grads->n_tensors > kMaxSweepChunks)
         return fail(ADAMW_E_INVALID, "too many tensors for per-tensor norms in one launch: split the list");
     Sweep sw;
-    if ((st = begin_sweep(esz, grads, hip_stream, &sw)) != ADAMW_OK) return st;
+    if ((st = begin_sweep(kTagNorm, esz, grads, hip_stream, &sw)) != ADAMW_OK) return st;
     const PlanSlot& p = *sw.plan;
     const bool single = single_launch(p.n_chunks) && p.n_chunks <= kSingleSumMaxWorkgroups;
-    hipError_t e = launch_sumsq(g_dtype, p.segs(), p.chunks(), p.n_chunks, p.tensor_first(), p.n_tensors, p.partials(),
+    hipError_t e = launch_sumsq(g_dtype, p.groups(), p.n_chunks, p.tensor_first(), p.n_tensors, p.partials(),
                                 sw.done, single, out, sw.stream);
     if (e != hipSuccess) return hip_fail("sum of squares launch", e);
     return ADAMW_OK;
@@ -705,9 +732,9 @@ try {
     if (!d_scale && (!std::isfinite(inv_loss_scale) || !(inv_loss_scale > 0.0f)))
         return fail(ADAMW_E_INVALID, "inv_loss_scale must be finite and > 0");
     Sweep sw;
-    if ((st = begin_sweep(esz, grads, hip_stream, &sw)) != ADAMW_OK) return st;
+    if ((st = begin_sweep(kTagClip, esz, grads, hip_stream, &sw)) != ADAMW_OK) return st;
     const PlanSlot& p = *sw.plan;
-    hipError_t e = launch_clip(g_dtype, p.segs(), p.chunks(), p.n_chunks,
+    hipError_t e = launch_clip(g_dtype, p.groups(), p.n_chunks,
                                ClipRule{clip->d_sumsq, clip->max_norm, clip->eps}, inv_loss_scale, d_scale, sw.stream);
     if (e != hipSuccess) return hip_fail("clip launch", e);
     return ADAMW_OK;
@@ -760,10 +787,11 @@ int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_ten
     Plan plan;
     std::string err;
     adamw_status st;
-    if (for_check == 2) {
+    if (const int64_t tag = sweep_tag(for_check)) {
         int esz = 0;
         st = check_sweep_dtype(p_dtype, &esz, err);
-        if (st == ADAMW_OK) st = build_sweep_plan(esz, list, sweep_chunk_elems(esz), kMaxSweepChunks, &plan, err);
+        if (st == ADAMW_OK)
+            st = build_sweep_plan(esz, list, sweep_chunk_elems(tag, esz), max_chunks_of(tag), &plan, err);
     } else {
         st = check_mode(mode, p_dtype, for_check != 0, err);
         int esz[kStreams];
@@ -790,7 +818,8 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
     adamw_status st = ADAMW_OK;
     StepKind kind{};
     int64_t chunk = 0, max_chunks = kMaxUpdateChunks;
-    if (for_check == 2) {
+    const int64_t sweep = sweep_tag(for_check);
+    if (sweep) {
         st = check_sweep_dtype(p_dtype, &kind.esz[ADAMW_STREAM_GRAD], err);
     } else if (for_check) {
         st = check_mode(mode, p_dtype, true, err);
@@ -806,9 +835,9 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
     }
     if (st == ADAMW_OK && !for_check) chunk = chunk_elems_of(kind.kernel);
     Plan plan;
-    if (st == ADAMW_OK && for_check == 2) {
+    if (st == ADAMW_OK && sweep) {
         const int esz = kind.esz[ADAMW_STREAM_GRAD];
-        st = build_sweep_plan(esz, list, sweep_chunk_elems(esz), kMaxSweepChunks, &plan, err);
+        st = build_sweep_plan(esz, list, sweep_chunk_elems(sweep, esz), max_chunks_of(sweep), &plan, err);
     } else if (st == ADAMW_OK) {
         st = build_plan(kind.esz, list, chunk, max_chunks, &plan, err);
     }

@@ -38,7 +38,8 @@ constexpr int kPack = 8;               // elements per lane per dwordx4 of a 16-
 constexpr uint32_t kVecBit = 0x80000000u;
 constexpr uint32_t kCountMask = 0x7fffffffu;
 constexpr int64_t kTagCheck = -1;      // plan tags: an update kernel's id, the overflow check,
-constexpr int64_t kTagSweep = -2;      // or a gradient sweep
+constexpr int64_t kTagNorm = -2;       // or a gradient sweep: sum of squares, clipping
+constexpr int64_t kTagClip = -3;
 constexpr int64_t kElemChunkElems = 4096;       // element chunk
 // An update kernel's chunk is shared by kXcdParts workgroups, consecutive in
 // launch order, so one on each XCD (the dispatcher hands workgroup b to XCD
@@ -104,14 +105,21 @@ constexpr int64_t kCheckChunkElems = (int64_t)kBlockCheck * kPack * kCheckChunkM
 constexpr int kMaxUpdateBlock = kBlockMixed > kBlockPure ? kBlockMixed : kBlockPure;
 constexpr int64_t kMaxUpdateChunks = (int64_t)UINT32_MAX / ((int64_t)kXcdParts * kMaxUpdateBlock);
 constexpr int64_t kMaxCheckChunks = (int64_t)UINT32_MAX / kBlockCheck;
-// The gradient sweeps (sum of squares, clipping) touch the gradient stream alone:
-// one workgroup per chunk of this many bytes, 8 16-byte words per lane.  A sweep's
-// chunks are not cut at 16-byte edges: the workgroup takes the elements before the
-// first edge and after the last one by themselves, so a tensor costs one workgroup
-// however short or misaligned it is.
+// The gradient sweeps (sum of squares, clipping) touch the gradient stream alone.
+// A sweep's chunks are not cut at 16-byte edges: the workgroup takes the elements
+// before the first edge and after the last one by themselves, so a tensor costs one
+// workgroup however short or misaligned it is.
+//   sum of squares: one workgroup per chunk of 32 KiB, 8 16-byte words per lane;
+//   clipping: chunks of 128 KiB shared by 8 consecutive workgroups as in an update
+//     kernel, in tiles of 64 words (1 KiB), 4 words per lane; a chunk of at most 16 KiB
+//     is one workgroup's.
 constexpr int kBlockSweep = 256;
-constexpr int kSweepUnroll = 8;
-constexpr int64_t kSweepChunkBytes = (int64_t)kBlockSweep * 16 * kSweepUnroll;
+constexpr int kNormUnroll = 8;
+constexpr int kClipUnroll = 4;
+constexpr int kTileWords = 64;
+constexpr int64_t kNormChunkBytes = (int64_t)kBlockSweep * 16 * kNormUnroll;
+constexpr int64_t kClipWholeBytes = (int64_t)kBlockSweep * 16 * kClipUnroll;
+constexpr int64_t kClipChunkBytes = kXcdParts * kClipWholeBytes;
 constexpr int64_t kMaxSweepChunks = (int64_t)UINT32_MAX / kBlockSweep;
 // A sum of squares runs as one launch (its last workgroup joins the partial sums) up
 // to this many workgroups, if the single-launch limit allows as many: measured on
@@ -180,6 +188,15 @@ struct alignas(16) DevChunk {
     uint32_t seg;
     uint32_t n_kind;
     uint64_t off;
+};
+
+// One workgroup's work in a gradient sweep: n elements from address addr, shared by
+// kXcdParts workgroups of which this is number `part`, or its own (kWholeChunk).
+constexpr uint32_t kWholeChunk = UINT32_MAX;
+struct alignas(16) DevSweep {
+    uint64_t addr;
+    uint32_t n;
+    uint32_t part;
 };
 
 // One piece of a state copy between the blocked buffer and per-tensor (or flat)

@@ -80,20 +80,45 @@ struct Span {
     }
 };
 
-// Sum over the workgroup, in every lane: a butterfly in each wave, then the waves in
-// order.  A second call needs a barrier after the first.
+// x plus the x of another lane (0 from outside the row or mask), by data-parallel
+// moves of its two halves.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_lane(double x)
+{
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, true);
+    return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Sum over the wave, in lane 63: rows of 16 by shifts of 1, 2, 4 and 8 lanes, then
+// lane 15 of a row to the next and lane 31 to the upper half.  Lane exchanges through
+// the LDS unit instead kept a workgroup's last microsecond busy: at 8 waves per CU the
+// 2.7 GB sum took 595 us with them and 371 without.
+constexpr uint32_t kSumLane = 63;
+__device__ __forceinline__ double wave_sum(double x)
+{
+    x = add_lane<0x111, 0xf>(x);
+    x = add_lane<0x112, 0xf>(x);
+    x = add_lane<0x114, 0xf>(x);
+    x = add_lane<0x118, 0xf>(x);
+    x = add_lane<0x142, 0xa>(x);
+    return add_lane<0x143, 0xc>(x);
+}
+
+// Sum over the workgroup, in every lane: each wave, then the waves in order.  A second
+// call needs a barrier after the first.
 template <int BLOCK>
 __device__ __forceinline__ double block_sum(double x)
 {
     constexpr int kWaves = BLOCK / 64;
-    __shared__ double wave_sum[kWaves];
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-    if (threadIdx.x % 64 == 0) wave_sum[threadIdx.x / 64] = x;
+    __shared__ double sums[kWaves];
+    x = wave_sum(x);
+    if (threadIdx.x % 64 == kSumLane) sums[threadIdx.x / 64] = x;
     __syncthreads();
-    double s = wave_sum[0];
+    double s = sums[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += wave_sum[w];
+    for (int w = 1; w < kWaves; ++w) s += sums[w];
     return s;
 }
 
@@ -156,26 +181,32 @@ __device__ __forceinline__ bool last_of(double* slot, double x, uint32_t* done, 
 
 // FUSED: the only launch of a small sum, whose last workgroup joins the partials.
 template <int DT, bool FUSED>
-__global__ __launch_bounds__(kBlockSweep) void sumsq_kernel(const DevSeg* __restrict__ segs,
-                                                        const DevChunk* __restrict__ chunks,
+__global__ __launch_bounds__(kBlockSweep) void sumsq_kernel(const DevSweep* __restrict__ groups,
                                                         double* __restrict__ partials, uint32_t* __restrict__ done,
                                                         NormOut out)
 {
     const uint32_t ci = xcd_chunk(blockIdx.x, gridDim.x);
-    const DevChunk ch = chunks[ci];
-    const Span<DT> sp(segs[ch.seg].ptr[ADAMW_STREAM_GRAD] + ch.off * Elem<DT>::size, ch.n_kind & kCountMask);
+    const DevSweep gr = groups[ci];
+    const Span<DT> sp(gr.addr, gr.n);
     const GLOBAL u32x4* __restrict__ g4 = gptr<const u32x4>(sp.body, 0);
     const uint32_t tid = threadIdx.x;
+    constexpr uint32_t kPass = kBlockSweep * kNormUnroll;
     double a = 0.0, b = 0.0;
-    for (uint32_t k0 = tid; k0 < sp.words; k0 += kBlockSweep * kSweepUnroll) {
-        u32x4 q[kSweepUnroll];
+    uint32_t k = tid;
+    for (; k - tid + kPass <= sp.words; k += kPass) {
+        u32x4 q[kNormUnroll];
 #pragma unroll
-        for (int u = 0; u < kSweepUnroll; ++u) {
-            const uint32_t k = k0 + u * kBlockSweep;
-            q[u] = k < sp.words ? ld<1>(g4 + k) : u32x4{0u, 0u, 0u, 0u};
-        }
+        for (int u = 0; u < kNormUnroll; ++u) q[u] = ld<1>(g4 + k + u * kBlockSweep);
 #pragma unroll
-        for (int u = 0; u < kSweepUnroll; ++u) add_squares<DT>(q[u], a, b);
+        for (int u = 0; u < kNormUnroll; ++u) add_squares<DT>(q[u], a, b);
+    }
+    if (k - tid < sp.words) {
+        u32x4 q[kNormUnroll];
+#pragma unroll
+        for (int u = 0; u < kNormUnroll; ++u)
+            q[u] = k + u * kBlockSweep < sp.words ? ld<1>(g4 + k + u * kBlockSweep) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int u = 0; u < kNormUnroll; ++u) add_squares<DT>(q[u], a, b);
     }
     if (tid < sp.head) a += square1<DT>(sp.head_addr(tid));
     if (tid < sp.tail) b += square1<DT>(sp.tail_addr(tid));
@@ -225,9 +256,8 @@ __global__ __launch_bounds__(kBlockJoin) void join_kernel(double* __restrict__ p
         } else {
             if (wave != w) continue;
             for (uint32_t k = first + lane; k < last; k += 64) x += partials[k];
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-            if (lane != 0) continue;
+            x = wave_sum(x);
+            if (lane != kSumLane) continue;
         }
         if (out.tensor_sumsq) out.tensor_sumsq[i] = x;
         if (out.tensor_norm) out.tensor_norm[i] = (float)__builtin_sqrt(x);
@@ -269,8 +299,7 @@ __device__ __forceinline__ void scale1(uint64_t addr, float f)
 }
 
 template <int DT>
-__global__ __launch_bounds__(kBlockSweep) void clip_kernel(const DevSeg* __restrict__ segs,
-                                                       const DevChunk* __restrict__ chunks, ClipRule rule,
+__global__ __launch_bounds__(kBlockSweep) void clip_kernel(const DevSweep* __restrict__ groups, ClipRule rule,
                                                        float inv_scale, const adamw_loss_scale_state* __restrict__ amp)
 {
     if (amp) inv_scale = (float)(1.0 / (double)amp->scale);
@@ -278,28 +307,49 @@ __global__ __launch_bounds__(kBlockSweep) void clip_kernel(const DevSeg* __restr
     if (!clip_factor(rule, *rule.sumsq, inv_scale, factor)) return;
     const float f = (float)factor;
     if (f == 1.0f) return;
-    const DevChunk ch = chunks[xcd_chunk(blockIdx.x, gridDim.x)];
-    const Span<DT> sp(segs[ch.seg].ptr[ADAMW_STREAM_GRAD] + ch.off * Elem<DT>::size, ch.n_kind & kCountMask);
+    const DevSweep gr = groups[blockIdx.x];
+    const Span<DT> sp(gr.addr, gr.n);
     GLOBAL u32x4* __restrict__ g4 = gptr<u32x4>(sp.body, 0);
     const uint32_t tid = threadIdx.x;
-    for (uint32_t k = tid; k < sp.words; k += kBlockSweep) st<2>(g4 + k, scale_word<DT>(ld<0>(g4 + k), f));
+    const uint32_t parts = gr.part == kWholeChunk ? 1 : kXcdParts, part = gr.part == kWholeChunk ? 0 : gr.part;
+    // tile t of kTileWords words goes to part t % parts
+    const uint32_t first = (tid / kTileWords * parts + part) * kTileWords + tid % kTileWords;
+    const uint32_t stride = kBlockSweep * parts;
+    uint32_t at = 0;
+    for (; at + kClipUnroll * stride <= sp.words; at += kClipUnroll * stride) {
+        u32x4 q[kClipUnroll];
+#pragma unroll
+        for (int u = 0; u < kClipUnroll; ++u) q[u] = ld<3>(g4 + at + first + u * stride);
+#pragma unroll
+        for (int u = 0; u < kClipUnroll; ++u) st<3>(g4 + at + first + u * stride, scale_word<DT>(q[u], f));
+    }
+    for (uint32_t k = at + first; k < sp.words; k += stride) st<3>(g4 + k, scale_word<DT>(ld<3>(g4 + k), f));
+    if (part != 0) return;
     if (tid < sp.head) scale1<DT>(sp.head_addr(tid), f);
     if (tid < sp.tail) scale1<DT>(sp.tail_addr(tid), f);
 }
 
 }  // namespace
 
-hipError_t launch_clip(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
-                       const ClipRule& rule, float inv_scale, const adamw_loss_scale_state* d_amp, hipStream_t stream)
+// Occupancy caps by reserved LDS, as for the update kernels.
+#ifndef ADAMW_LDS_CLIP
+#define ADAMW_LDS_CLIP 40960
+#endif
+#ifndef ADAMW_LDS_NORM
+#define ADAMW_LDS_NORM 40000
+#endif
+
+hipError_t launch_clip(adamw_dtype g_dtype, const DevSweep* groups, int64_t n_groups, const ClipRule& rule,
+                       float inv_scale, const adamw_loss_scale_state* d_amp, hipStream_t stream)
 {
-    if (n_chunks <= 0) return hipSuccess;
-    const dim3 grid((unsigned)n_chunks), block(kBlockSweep);
+    if (n_groups <= 0) return hipSuccess;
+    const dim3 grid((unsigned)n_groups), block(kBlockSweep);
     if (g_dtype == ADAMW_F16)
-        hipLaunchKernelGGL((clip_kernel<kF16>), grid, block, 0, stream, segs, chunks, rule, inv_scale, d_amp);
+        hipLaunchKernelGGL((clip_kernel<kF16>), grid, block, ADAMW_LDS_CLIP, stream, groups, rule, inv_scale, d_amp);
     else if (g_dtype == ADAMW_BF16)
-        hipLaunchKernelGGL((clip_kernel<kBf16>), grid, block, 0, stream, segs, chunks, rule, inv_scale, d_amp);
+        hipLaunchKernelGGL((clip_kernel<kBf16>), grid, block, ADAMW_LDS_CLIP, stream, groups, rule, inv_scale, d_amp);
     else
-        hipLaunchKernelGGL((clip_kernel<kF32>), grid, block, 0, stream, segs, chunks, rule, inv_scale, d_amp);
+        hipLaunchKernelGGL((clip_kernel<kF32>), grid, block, ADAMW_LDS_CLIP, stream, groups, rule, inv_scale, d_amp);
     return hipGetLastError();
 }
 
@@ -307,37 +357,37 @@ int64_t partial_count(int64_t n_chunks) { return n_chunks + (n_chunks + kJoin - 
 static_assert(kMaxSweepChunks <= (int64_t)kJoin * kJoin, "one workgroup joins the block sums");
 
 template <bool FUSED>
-static void launch_sums(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+static void launch_sums(adamw_dtype g_dtype, const DevSweep* groups, int64_t n_chunks,
                         double* partials, uint32_t* done, const NormOut& out, hipStream_t stream)
 {
     const dim3 grid((unsigned)n_chunks), block(kBlockSweep);
     if (g_dtype == ADAMW_F16)
-        hipLaunchKernelGGL((sumsq_kernel<kF16, FUSED>), grid, block, 0, stream, segs, chunks, partials, done, out);
+        hipLaunchKernelGGL((sumsq_kernel<kF16, FUSED>), grid, block, ADAMW_LDS_NORM, stream, groups, partials, done, out);
     else if (g_dtype == ADAMW_BF16)
-        hipLaunchKernelGGL((sumsq_kernel<kBf16, FUSED>), grid, block, 0, stream, segs, chunks, partials, done, out);
+        hipLaunchKernelGGL((sumsq_kernel<kBf16, FUSED>), grid, block, ADAMW_LDS_NORM, stream, groups, partials, done, out);
     else
-        hipLaunchKernelGGL((sumsq_kernel<kF32, FUSED>), grid, block, 0, stream, segs, chunks, partials, done, out);
+        hipLaunchKernelGGL((sumsq_kernel<kF32, FUSED>), grid, block, ADAMW_LDS_NORM, stream, groups, partials, done, out);
 }
 
-hipError_t launch_sumsq(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+hipError_t launch_sumsq(adamw_dtype g_dtype, const DevSweep* groups, int64_t n_chunks,
                         const uint32_t* tensor_first, int64_t n_tensors, double* partials, uint32_t* done, bool single,
                         const NormOut& out, hipStream_t stream)
 {
     const bool per_tensor = (out.tensor_norm || out.tensor_sumsq) && n_tensors > 0;
     if (single && !per_tensor) {
-        launch_sums<true>(g_dtype, segs, chunks, n_chunks, partials, done, out, stream);
+        launch_sums<true>(g_dtype, groups, n_chunks, partials, done, out, stream);
         return hipGetLastError();
     }
     if (n_chunks > 0) {
-        launch_sums<false>(g_dtype, segs, chunks, n_chunks, partials, done, out, stream);
+        launch_sums<false>(g_dtype, groups, n_chunks, partials, done, out, stream);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     // an empty list's total is written by one workgroup all the same
     const int64_t blocks = !out.sumsq ? 0 : n_chunks > 0 ? (n_chunks + kJoin - 1) / kJoin : 1;
-    const int64_t groups = blocks + (per_tensor ? (n_tensors + kTensorsPerGroup - 1) / kTensorsPerGroup : 0);
-    if (groups == 0) return hipSuccess;
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)groups), dim3(kBlockJoin), 0, stream, partials, (uint32_t)n_chunks,
+    const int64_t joins = blocks + (per_tensor ? (n_tensors + kTensorsPerGroup - 1) / kTensorsPerGroup : 0);
+    if (joins == 0) return hipSuccess;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)joins), dim3(kBlockJoin), 0, stream, partials, (uint32_t)n_chunks,
                        (uint32_t)blocks, tensor_first, (uint32_t)n_tensors, done, out);
     return hipGetLastError();
 }

@@ -282,6 +282,21 @@ adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t ch
     return plan_list(streams, list, chunk_elems, max_chunks, true, out, err);
 }
 
+std::vector<DevSweep> sweep_groups(const Plan& plan, int esz, bool shared)
+{
+    std::vector<DevSweep> out;
+    out.reserve(plan.chunks.size());
+    for (const DevChunk& c : plan.chunks) {
+        DevSweep g{plan.segs[c.seg].ptr[ADAMW_STREAM_GRAD] + c.off * (uint64_t)esz, c.n_kind & kCountMask, kWholeChunk};
+        if (!shared || (int64_t)g.n * esz <= kClipWholeBytes) {
+            out.push_back(g);
+            continue;
+        }
+        for (g.part = 0; g.part < (uint32_t)kXcdParts; ++g.part) out.push_back(g);
+    }
+    return out;
+}
+
 void chunk_bytes(const Plan& plan, size_t c, const int esz[kStreams], uint64_t lo[kStreams], uint64_t hi[kStreams])
 {
     const DevChunk& ch = plan.chunks[c];

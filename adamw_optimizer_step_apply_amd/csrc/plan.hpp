@@ -48,6 +48,9 @@ adamw_status build_plan(const int esz[kStreams], const adamw_tensor_list* list, 
 // marked with kVecBit, and are listed per tensor in Plan::tensor_first.
 adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t chunk_elems, int64_t max_chunks,
                               Plan* out, std::string& err);
+// The workgroups of a sweep plan: one per chunk, or with `shared` kXcdParts per chunk
+// of more than kClipWholeBytes.
+std::vector<DevSweep> sweep_groups(const Plan& plan, int esz, bool shared);
 
 // The plan of a state copy between per-tensor (or flat) state buffers and one
 // blocked buffer: `list` describes the state as a step would see it without

@@ -88,12 +88,12 @@ hipError_t launch_check(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk*
 // partial_count(n_chunks) values; single: one launch, through the completion
 // counters at done.
 int64_t partial_count(int64_t n_chunks);
-hipError_t launch_sumsq(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+hipError_t launch_sumsq(adamw_dtype g_dtype, const DevSweep* groups, int64_t n_chunks,
                         const uint32_t* tensor_first, int64_t n_tensors, double* partials, uint32_t* done, bool single,
                         const NormOut& out, hipStream_t stream);
 // Scales the gradients of a sweep plan by the clipping factor, in place (norm.hip).
-hipError_t launch_clip(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
-                       const ClipRule& rule, float inv_scale, const adamw_loss_scale_state* d_amp, hipStream_t stream);
+hipError_t launch_clip(adamw_dtype g_dtype, const DevSweep* groups, int64_t n_groups, const ClipRule& rule,
+                       float inv_scale, const adamw_loss_scale_state* d_amp, hipStream_t stream);
 hipError_t launch_state_copy(const DevCopySeg* segs, const DevChunk* chunks, int64_t n_chunks, const int esz[3],
                              bool to_blocked, hipStream_t stream);
 

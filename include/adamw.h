@@ -475,8 +475,9 @@ adamw_status adamw_blocked_state_copy(adamw_mode mode, adamw_dtype p_dtype, cons
 
 /* Planner introspection, for tests: no GPU work, no HIP call.  Builds the
  * chunk plan that adamw_multi_tensor_step (for_check = 0),
- * adamw_check_finite (for_check = 1), or adamw_grad_norm, adamw_tensor_norms and
- * adamw_clip_grads (for_check = 2, g_dtype = p_dtype; mode ignored) would launch, and writes up to
+ * adamw_check_finite (for_check = 1), adamw_grad_norm and adamw_tensor_norms
+ * (for_check = 2), or adamw_clip_grads (3; both with g_dtype = p_dtype, mode ignored)
+ * would launch, and writes up to
  * cap rows of 6 int64 each to out:
  *   {tensor index, element offset inside the tensor, element count,
  *    kind (0 = element-wise, 1 = 16-byte vector, 2 = any elements, whose 16-byte

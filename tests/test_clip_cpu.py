@@ -106,3 +106,28 @@ def test_valid_step_reaches_hip(kw):
     with pytest.raises(A.AdamWError) as ei:
         step(**kw)
     assert ei.value.status == A.E_HIP
+
+
+@pytest.mark.parametrize("dt,esz", [(A.BF16, 2), (A.F32, 4)])
+@pytest.mark.parametrize("phase", [0, 1, 3])
+def test_plan_covers_the_list(dt, esz, phase):
+    """Chunks of 128 KiB, each but a piece's first starting at a 16-byte edge."""
+    chunk = 131072 // esz
+    numels = [0, 1, 7, chunk - 1, chunk, chunk + 1, 5, 3 * chunk + 17, 2 ** 32 + 5]
+    tl = grads(numels, FAKE + phase * esz, esz)
+    rows, ranges = A.adamw_plan_inspect_bytes(A.MIXED, dt, tl, for_check=3)
+    pos = {}
+    for (t, off, n, kind, _, _), r in zip(rows[:, :6].tolist(), ranges.tolist()):
+        assert kind == 2 and off == pos.get(t, 0) and 0 < n <= chunk + 16 // esz - 1
+        lo, hi = r[1]
+        assert hi - lo == n * esz and lo == tl.c.ptr[1][t] + off * esz and (off == 0 or lo % 16 == 0)
+        pos[t] = off + n
+    assert pos == {t: n for t, n in enumerate(numels) if n}
+
+
+def test_plan_beyond_the_grid_limit_is_refused():
+    """A chunk shared by 8 workgroups: at most (2^32 - 1) / 256 / 8 chunks."""
+    n = 2_097_151 * 65536
+    assert len(A.adamw_plan_inspect_bytes(A.MIXED, A.BF16, grads([n]), for_check=3)[0]) == 2_097_151
+    with pytest.raises(A.AdamWError, match="chunks"):
+        A.adamw_clip_grads(A.BF16, grads([n + 1]), clip(), stream=0)
