@@ -179,6 +179,15 @@ def _addr(x) -> int:
     return int(x)
 
 
+def _result(x, dtype: torch.dtype, numel: int, name: str) -> int:
+    """The address of a device result or input of the gradient norms; a tensor given has
+    to be of the type and length that the library reads or writes there."""
+    if isinstance(x, torch.Tensor) and not (x.is_cuda and x.dtype == dtype and x.numel() >= numel and x.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of at least {numel} on the GPU is needed, got "
+                         f"{tuple(x.shape)} {x.dtype} on {x.device}")
+    return _addr(x)
+
+
 # The current stream's address without a torch.cuda.Stream object around it, whose making takes
 # 2.7 us of host time per call (a small list's kernel takes 3.6); None on a torch without it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -354,8 +363,9 @@ def adamw_grad_norm(g_dtype: int, grads: TensorList, d_sumsq, d_norm=None, d_fou
     float64; added to it with ``accumulate``), its square root into ``d_norm``
     (one float32) and whether it is inf or NaN into ``d_found_inf`` (one int32)
     (C ABI adamw_grad_norm)."""
-    _check(_lib.adamw_grad_norm(g_dtype, ctypes.byref(grads.c), int(bool(accumulate)), _addr(d_sumsq), _addr(d_norm),
-                                _addr(d_found_inf), _stream(stream)))
+    _check(_lib.adamw_grad_norm(g_dtype, ctypes.byref(grads.c), int(bool(accumulate)),
+                                _result(d_sumsq, torch.float64, 1, "d_sumsq"), _result(d_norm, torch.float32, 1, "d_norm"),
+                                _result(d_found_inf, torch.int32, 1, "d_found_inf"), _stream(stream)))
 
 
 def adamw_tensor_norms(g_dtype: int, grads: TensorList, d_tensor_norms=None, d_tensor_sumsq=None, d_sumsq=None,
@@ -363,8 +373,11 @@ def adamw_tensor_norms(g_dtype: int, grads: TensorList, d_tensor_norms=None, d_t
     """Every tensor's norm into ``d_tensor_norms`` (float32, one per tensor) and sum
     of squares into ``d_tensor_sumsq`` (float64), and the list's sum of squares into
     ``d_sumsq`` (C ABI adamw_tensor_norms)."""
-    _check(_lib.adamw_tensor_norms(g_dtype, ctypes.byref(grads.c), _addr(d_tensor_norms), _addr(d_tensor_sumsq),
-                                   _addr(d_sumsq), _stream(stream)))
+    n = len(grads.numels)
+    _check(_lib.adamw_tensor_norms(g_dtype, ctypes.byref(grads.c),
+                                   _result(d_tensor_norms, torch.float32, n, "d_tensor_norms"),
+                                   _result(d_tensor_sumsq, torch.float64, n, "d_tensor_sumsq"),
+                                   _result(d_sumsq, torch.float64, 1, "d_sumsq"), _stream(stream)))
 
 
 @dataclass
@@ -377,7 +390,7 @@ class GradClip:
     eps: float = 1e-6
 
     def c(self) -> adamw_grad_clip:
-        return adamw_grad_clip(_addr(self.d_sumsq), self.max_norm, self.eps)
+        return adamw_grad_clip(_result(self.d_sumsq, torch.float64, 1, "d_sumsq"), self.max_norm, self.eps)
 
 
 def adamw_clip_grads(g_dtype: int, grads: TensorList, clip: GradClip, inv_loss_scale: float = 1.0, d_scale=None,

@@ -13,10 +13,10 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <exception>
 #include <map>
 #include <memory>
 #include <mutex>
-#include <new>
 #include <string>
 #include <utility>
 #include <vector>
@@ -313,6 +313,8 @@ adamw_status validate_list(int64_t tag, const int esz[kStreams], const adamw_ten
     if (validated_before(key)) return ADAMW_OK;
     std::string err;
     adamw_status st = plan_of(tag, esz, list, chunk_elems, nullptr, err);
+    // clipping multiplies in place: an element listed twice would be clipped once or twice
+    if (st == ADAMW_OK && tag == kTagClip) st = check_disjoint(esz[ADAMW_STREAM_GRAD], list, err);
     if (st != ADAMW_OK) return fail(st, err);
     remember_validated(key);
     return ADAMW_OK;
@@ -700,8 +702,8 @@ try {
     out.found_inf = d_found_inf;
     out.accumulate = accumulate != 0;
     return sum_of_squares(g_dtype, grads, out, hip_stream);
-} catch (const std::bad_alloc&) {
-    return fail(ADAMW_E_NOMEM, "out of host memory");
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_tensor_norms(adamw_dtype g_dtype, const adamw_tensor_list* grads, float* d_tensor_norms,
@@ -715,8 +717,8 @@ try {
     out.tensor_norm = d_tensor_norms;
     out.tensor_sumsq = d_tensor_sumsq;
     return sum_of_squares(g_dtype, grads, out, hip_stream);
-} catch (const std::bad_alloc&) {
-    return fail(ADAMW_E_NOMEM, "out of host memory");
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_clip_grads(adamw_dtype g_dtype, const adamw_tensor_list* grads, const adamw_grad_clip* clip,
@@ -738,8 +740,8 @@ try {
                                ClipRule{clip->d_sumsq, clip->max_norm, clip->eps}, inv_loss_scale, d_scale, sw.stream);
     if (e != hipSuccess) return hip_fail("clip launch", e);
     return ADAMW_OK;
-} catch (const std::bad_alloc&) {
-    return fail(ADAMW_E_NOMEM, "out of host memory");
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
@@ -758,8 +760,8 @@ try {
     if ((st = state_kind(mode, p_dtype, prec, &kind)) != ADAMW_OK) return st;
     return do_step(kind, list, hp, d_step, d_found_inf, hip_stream, d_scale, scaler,
                    ClipRule{clip->d_sumsq, clip->max_norm, clip->eps});
-} catch (const std::bad_alloc&) {
-    return fail(ADAMW_E_NOMEM, "out of host memory");
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 const char* adamw_last_error(void) { return g_err.c_str(); }

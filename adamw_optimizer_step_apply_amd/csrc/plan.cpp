@@ -17,6 +17,8 @@
 
 #include <stdio.h>
 
+#include <algorithm>
+
 namespace adamw {
 
 void mode_esizes(adamw_mode mode, adamw_dtype p_dtype, bool for_check, int esz[kStreams])
@@ -280,6 +282,35 @@ adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t ch
     int streams[kStreams] = {0, 0, 0, 0, 0};
     streams[ADAMW_STREAM_GRAD] = esz;
     return plan_list(streams, list, chunk_elems, max_chunks, true, out, err);
+}
+
+adamw_status check_disjoint(int esz, const adamw_tensor_list* list, std::string& err)
+{
+    // a flat shard buffer holds every element once
+    if ((list->flat_mask >> ADAMW_STREAM_GRAD) & 1u) return ADAMW_OK;
+    const int64_t align = (list->flat_mask & ADAMW_FLAT_PAD8) ? 8 : 1;
+    struct Range { uint64_t lo, hi; };
+    std::vector<Range> r;
+    int64_t base = 0;
+    for (int64_t i = 0; i < list->n_tensors; ++i) {
+        const int64_t n = list->numel[i];
+        const int64_t lo = list->shard_begin > base ? list->shard_begin - base : 0;
+        const int64_t hi = list->shard_end >= 0 && list->shard_end < base + n ? list->shard_end - base : n;
+        if (lo < hi) {
+            const uint64_t a = (uint64_t)(uintptr_t)list->ptr[ADAMW_STREAM_GRAD][i];
+            r.push_back(Range{a + (uint64_t)lo * esz, a + (uint64_t)hi * esz});
+        }
+        base += (n + align - 1) / align * align;
+    }
+    const auto before = [](const Range& x, const Range& y) { return x.lo < y.lo; };
+    if (!std::is_sorted(r.begin(), r.end(), before)) std::sort(r.begin(), r.end(), before);
+    for (size_t i = 1; i < r.size(); ++i) {
+        if (r[i].lo < r[i - 1].hi) {
+            err = "two grad buffers of the list overlap: each is clipped in place once";
+            return ADAMW_E_INVALID;
+        }
+    }
+    return ADAMW_OK;
 }
 
 std::vector<DevSweep> sweep_groups(const Plan& plan, int esz, bool shared)

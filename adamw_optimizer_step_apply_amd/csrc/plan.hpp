@@ -48,6 +48,8 @@ adamw_status build_plan(const int esz[kStreams], const adamw_tensor_list* list, 
 // marked with kVecBit, and are listed per tensor in Plan::tensor_first.
 adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t chunk_elems, int64_t max_chunks,
                               Plan* out, std::string& err);
+// Refuses a (valid) list whose gradient buffers overlap inside the shard.
+adamw_status check_disjoint(int esz, const adamw_tensor_list* list, std::string& err);
 // The workgroups of a sweep plan: one per chunk, or with `shared` kXcdParts per chunk
 // of more than kClipWholeBytes.
 std::vector<DevSweep> sweep_groups(const Plan& plan, int esz, bool shared);

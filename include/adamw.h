@@ -82,7 +82,7 @@
  * call under capture whose table is not yet on the device (or on a stream
  * without a workspace) is refused with ADAMW_E_INVALID.  A captured step may be
  * replayed any number of times.  It uses the capture stream's workspace
- * (launch scalars, completion counters, chunk table).  The chunk table a
+ * (launch scalars, completion counters, chunk table, a norm's partial sums).  The chunk table a
  * capture used is pinned: later calls on the stream, with however many other
  * lists, never evict, move or rewrite it (the stream keeps up to 8 unpinned
  * tables besides the pinned ones); pinned tables are freed only by
@@ -398,7 +398,8 @@ typedef struct {
  * inv_loss_scale (finite, > 0), and only f depends on it.  With f = 1 no element
  * changes and nothing is written.  If S is not finite (an inf or NaN gradient)
  * nothing is written either: the step that follows is to be skipped
- * (adamw_grad_norm's d_found_inf).  For optimizers that take no clipping factor,
+ * (adamw_grad_norm's d_found_inf).  A list whose buffers overlap inside the shard (a
+ * gradient listed twice) is refused.  For optimizers that take no clipping factor,
  * and for gradients that others read; adamw_multi_tensor_step_clipped needs no such
  * pass. */
 adamw_status adamw_clip_grads(adamw_dtype g_dtype, const adamw_tensor_list* grads, const adamw_grad_clip* clip,

@@ -131,3 +131,57 @@ def test_plan_beyond_the_grid_limit_is_refused():
     assert len(A.adamw_plan_inspect_bytes(A.MIXED, A.BF16, grads([n]), for_check=3)[0]) == 2_097_151
     with pytest.raises(A.AdamWError, match="chunks"):
         A.adamw_clip_grads(A.BF16, grads([n + 1]), clip(), stream=0)
+
+
+@pytest.mark.parametrize("tl", [
+    A.TensorList([10, 10], [None, [FAKE, FAKE]]),
+    A.TensorList([10, 4, 10], [None, [FAKE, FAKE + 4096, FAKE + 18]]),
+    A.TensorList([10, 4, 10], [None, [FAKE + 2, FAKE + 4096, FAKE]], 0, 17),
+], ids=["twice", "by one", "inside the shard"])
+def test_overlapping_buffers_are_refused(tl):
+    with pytest.raises(A.AdamWError, match="overlap"):
+        A.adamw_clip_grads(A.BF16, tl, clip(), stream=0)
+    with pytest.raises(A.AdamWError) as ei:          # the norm only reads: an element listed twice counts twice
+        A.adamw_grad_norm(A.BF16, tl, FAKE, stream=0)
+    assert ei.value.status == A.E_HIP
+
+
+@pytest.mark.parametrize("tl", [
+    A.TensorList([10, 10], [None, [FAKE + 20, FAKE]]),
+    A.TensorList([0, 10, 0], [None, [FAKE, FAKE, FAKE + 2]]),
+    A.TensorList([10, 10], [None, [FAKE, FAKE]], 0, 10),
+    A.TensorList([10, 10], [None, [FAKE, FAKE]], 5, 15),
+    A.TensorList([10, 10], [None, [FAKE]], 0, 20, 2),
+], ids=["touching", "empty", "outside the shard", "split", "flat"])
+def test_disjoint_buffers_are_not(tl):
+    with pytest.raises(A.AdamWError) as ei:
+        A.adamw_clip_grads(A.BF16, tl, clip(), stream=0)
+    assert ei.value.status == A.E_HIP
+
+
+def test_no_exception_leaves_the_c_entries():
+    """A count of tensors that no host array can have comes back as a status."""
+    tl = grads([10])
+    tl.c.n_tensors = 2 ** 61
+    c, h, sc = clip().c(), A.HParams().c(), A.LossScaler().c()
+    lib = A._lib
+    assert lib.adamw_grad_norm(A.BF16, ctypes.byref(tl.c), 0, FAKE, None, None, None) == A.E_NOMEM
+    assert lib.adamw_tensor_norms(A.BF16, ctypes.byref(tl.c), None, FAKE, None, None) in (A.E_NOMEM, A.E_INVALID)
+    assert lib.adamw_clip_grads(A.BF16, ctypes.byref(tl.c), ctypes.byref(c), 1.0, None, None) == A.E_NOMEM
+    assert lib.adamw_multi_tensor_step_clipped(A.MIXED, A.BF16, None, ctypes.byref(tl.c), ctypes.byref(h), ctypes.byref(c),
+                                               FAKE, None, None, ctypes.byref(sc), None) == A.E_NOMEM
+
+
+def test_results_of_another_type_or_place_are_refused():
+    """The binding hands the library no buffer that it would write past."""
+    import torch
+    d, f, i = torch.float64, torch.float32, torch.int32
+    for call in (lambda: A.adamw_grad_norm(A.BF16, grads([10]), torch.zeros(1, dtype=d), stream=0),
+                 lambda: A.adamw_grad_norm(A.BF16, grads([10]), torch.zeros(1, dtype=f, device="meta"), stream=0),
+                 lambda: A.adamw_grad_norm(A.BF16, grads([10]), FAKE, torch.zeros(1, dtype=f), stream=0),
+                 lambda: A.adamw_grad_norm(A.BF16, grads([10]), FAKE, None, torch.zeros(1, dtype=i), stream=0),
+                 lambda: A.adamw_tensor_norms(A.BF16, grads([10, 2]), torch.zeros(2, dtype=f), stream=0),
+                 lambda: A.adamw_clip_grads(A.BF16, grads([10]), clip(d_sumsq=torch.zeros(1, dtype=f)), stream=0),
+                 lambda: step(c=clip(d_sumsq=torch.zeros(1, dtype=d)))):
+        with pytest.raises(ValueError, match="is needed, got"):
+            call()

@@ -187,3 +187,25 @@ def test_beyond_32_bit_offsets():
     assert int((x[:2 ** 31] != 0).sum()) + int((x[2 ** 31:] != 0).sum()) == len(places) + 2
     del x, y
     free()
+
+
+@pytest.mark.parametrize("elems", [2048, 1 << 22])
+def test_chunk_knob(elems):
+    """Chunks of the smallest and the largest size give the same clipping, and norms within the bound."""
+    numels = [5, 9_000_001, 2048, 70_000]
+    _, a = make(numels, A.BF16, 47, phase=3)
+    _, b = make(numels, A.BF16, 47, phase=3)
+    s = sumsq_of(9.0)
+    A.adamw_clip_grads(A.BF16, A.TensorList(numels, [None, a]), A.GradClip(s, 1.0))
+    want, got = out64(), out64()
+    A.adamw_grad_norm(A.BF16, A.TensorList(numels, [None, a]), want)
+    try:
+        A.adamw_set_chunk_elems(elems)
+        A.adamw_clip_grads(A.BF16, A.TensorList(numels, [None, b]), A.GradClip(s, 1.0))
+        A.adamw_grad_norm(A.BF16, A.TensorList(numels, [None, b]), got)
+    finally:
+        A.adamw_set_chunk_elems(0)
+    assert all(same_bits(x, y) for x, y in zip(a, b))
+    # up to 4 M / 512 terms in a lane, each sum within that many roundings
+    assert abs(got.item() - want.item()) <= want.item() * (8192 + 256) * 2.0 ** -53
+    free()

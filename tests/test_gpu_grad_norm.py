@@ -403,3 +403,18 @@ def test_joins_of_several_levels():
     A.adamw_tensor_norms(A.BF16, tl, None, q, s)
     assert q.tolist() == want and s.item() == sum(want)
     free()
+
+
+def test_results_too_short_or_of_another_type_are_refused():
+    _, ts = make([100, 5], A.BF16, 34)
+    tl = A.TensorList([100, 5], [None, ts])
+    for bad in (out32(), out64().half(), torch.zeros(0, dtype=torch.float64, device="cuda")):
+        with pytest.raises(ValueError):
+            A.adamw_grad_norm(A.BF16, tl, bad)
+        with pytest.raises(ValueError):
+            A.adamw_clip_grads(A.BF16, tl, A.GradClip(bad))
+    with pytest.raises(ValueError):
+        A.adamw_tensor_norms(A.BF16, tl, out32())
+    with pytest.raises(ValueError):
+        A.adamw_tensor_norms(A.BF16, tl, torch.zeros(2, 2, device="cuda").t()[0])
+    assert bool(torch.isfinite(torch.cat([t.float() for t in ts])).all())
