@@ -134,17 +134,14 @@ adamw_status plan_of(int64_t tag, const int esz[kStreams], const adamw_tensor_li
     return build_plan(esz, list, chunk_elems, max_chunks_of(tag), out, err);
 }
 
-// The tables of a plan as they go to the device, and the bytes to allocate for them.
-struct Tables {
-    std::vector<unsigned char> bytes;
-    int64_t n_segs = 0, n_chunks = 0;
-    size_t dev_bytes = 0;
+// One table of a plan, as it goes to the device after the others.
+struct Table {
+    const void* data;
+    size_t bytes;
 
     template <typename T>
-    void add(const std::vector<T>& v)
+    explicit Table(const std::vector<T>& v) : data(v.data()), bytes(v.size() * sizeof(T))
     {
-        const unsigned char* p = reinterpret_cast<const unsigned char*>(v.data());
-        bytes.insert(bytes.end(), p, p + v.size() * sizeof(T));
     }
 };
 
@@ -209,25 +206,26 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     slot.valid = false;
     *out = &slot;
 
-    Tables tab;
+    std::vector<Table> tables;
+    std::vector<DevSweep> groups;
+    int64_t n_segs = 0, n_chunks = 0;
     if (is_sweep(tag)) {
-        const std::vector<DevSweep> groups = sweep_groups(plan, esz[ADAMW_STREAM_GRAD], tag == kTagClip);
-        tab.n_chunks = (int64_t)groups.size();
-        tab.add(groups);
-        tab.dev_bytes = tab.bytes.size();
-        if (tag == kTagNorm) {
-            tab.add(plan.tensor_first);
-            tab.dev_bytes = PlanSlot::norm_table_bytes(tab.n_chunks, list->n_tensors) +
-                            (size_t)partial_count(tab.n_chunks) * sizeof(double);
-        }
+        groups = sweep_groups(plan, esz[ADAMW_STREAM_GRAD], tag == kTagClip);
+        n_chunks = (int64_t)groups.size();
+        tables.emplace_back(groups);
+        if (tag == kTagNorm) tables.emplace_back(plan.tensor_first);
     } else {
-        tab.n_segs = (int64_t)plan.segs.size();
-        tab.n_chunks = (int64_t)plan.chunks.size();
-        tab.add(plan.segs);
-        tab.add(plan.chunks);
-        tab.dev_bytes = tab.bytes.size();
+        n_segs = (int64_t)plan.segs.size();
+        n_chunks = (int64_t)plan.chunks.size();
+        tables.emplace_back(plan.segs);
+        tables.emplace_back(plan.chunks);
     }
-    const size_t bytes = tab.bytes.size(), dev_bytes = tab.dev_bytes;
+    size_t bytes = 0;
+    for (const Table& t : tables) bytes += t.bytes;
+    size_t dev_bytes = bytes;
+    if (tag == kTagNorm)
+        dev_bytes = PlanSlot::norm_table_bytes(n_chunks, list->n_tensors) +
+                    (size_t)partial_count(n_chunks) * sizeof(double);
     hipError_t e;
     if (!slot.uploaded) {
         e = hipEventCreateWithFlags(&slot.uploaded, hipEventDisableTiming);
@@ -261,15 +259,19 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
         slot.dev_cap = cap;
     }
     if (bytes) {
-        memcpy(slot.host, tab.bytes.data(), bytes);
+        char* to = static_cast<char*>(slot.host);
+        for (const Table& t : tables) {
+            if (t.bytes) memcpy(to, t.data, t.bytes);
+            to += t.bytes;
+        }
         e = hipMemcpyAsync(slot.dev, slot.host, bytes, hipMemcpyHostToDevice, stream);
         if (e != hipSuccess) { slot.valid = false; return hip_fail("hipMemcpyAsync (chunk table)", e); }
         e = hipEventRecord(slot.uploaded, stream);
         if (e != hipSuccess) { slot.valid = false; return hip_fail("hipEventRecord", e); }
         slot.upload_in_flight = true;
     }
-    slot.n_segs = tab.n_segs;
-    slot.n_chunks = tab.n_chunks;
+    slot.n_segs = n_segs;
+    slot.n_chunks = n_chunks;
     slot.n_tensors = list->n_tensors;
     slot.key.swap(key);
     slot.valid = true;

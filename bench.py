@@ -726,7 +726,8 @@ def _kernel_sha():
     import hashlib
     import re
     h = hashlib.sha256()
-    for f in ("adamw_optimizer_step_apply_amd/csrc/kernels.hip", "adamw_optimizer_step_apply_amd/csrc/plan.cpp",
+    for f in ("adamw_optimizer_step_apply_amd/csrc/kernels.hip", "adamw_optimizer_step_apply_amd/csrc/device.hpp",
+              "adamw_optimizer_step_apply_amd/csrc/plan.cpp",
               "adamw_optimizer_step_apply_amd/csrc/layout.hpp", "include/adamw.h"):
         with open(os.path.join(ROOT, f)) as fh:
             src = fh.read()

@@ -98,8 +98,10 @@
  * kernel surface at the caller's next synchronisation.  One launch's grid
  * holds at most 2^32 - 1 lanes, so a step plan of more than 2,097,151 chunks
  * (8 workgroups of 256 lanes each: about 34e9 elements at the default chunk,
- * or that many tensors of under 8 elements), or a check plan of more than
- * 16,777,215, is rejected with ADAMW_E_INVALID.
+ * or that many tensors of under 8 elements), a check plan of more than
+ * 16,777,215, a norm of more than 16,777,215 (32 KiB each, or one per shorter
+ * tensor), or a clipping of more than 2,097,151 (128 KiB each) is rejected with
+ * ADAMW_E_INVALID.
  *
  * Concurrency.  Calls may come from several host threads.  Calls on different
  * streams run independently (each stream has its own workspace); two calls
