@@ -13,7 +13,10 @@ namespace adamw {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <int N>
+using words_t = uint32_t __attribute__((ext_vector_type(N)));
 
 // Device addresses taken from the segment table are plain integers; casting them
 // to the global address space lets the compiler emit global_load/global_store

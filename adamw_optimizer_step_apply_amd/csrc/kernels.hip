@@ -2,11 +2,10 @@
 //
 // The step is a pure stream: every element is read once and written once, with
 // no reuse, so there is nothing to stage in LDS and no contraction for the
-// matrix cores.  The kernels are shaped for HBM: every lane moves whole 16-byte
-// words (8 elements of a 16-bit stream, 4 of an fp32 stream), consecutive lanes
-// touch consecutive words, and each lane issues all loads of its 8-element pack
-// (one to two 16-byte words per stream) before it computes.  The math is fp32
-// in registers.
+// matrix cores.  The kernels are shaped for HBM: a lane moves a unit of a stream
+// with one access (16 bytes, or 8 of a 16-bit stream beside fp32 ones), consecutive
+// lanes touch consecutive units, and each lane issues all loads of its 8 elements
+// (one or two units per stream) before it computes.  The math is fp32 in registers.
 //
 // Kernels:
 //   prologue_kernel      one lane: reads the skip flag and the step counter,
@@ -233,34 +232,21 @@ __global__ void prologue_kernel(adamw_hparams hp, int32_t* __restrict__ step, co
 // Update kernel
 // ---------------------------------------------------------------------------
 
-// The cache policy of the streaming accesses per mode: bit 0 = non-temporal
-// loads, bit 1 = non-temporal stores (every element is touched exactly once
-// per step).
+// The cache policy of the streaming accesses: every element is touched exactly once
+// per step, so loads and stores are non-temporal (bit 0 = loads, bit 1 = stores).
+// The mixed family's gradient, which is not written back, is loaded plainly: on
+// MI355X (OPT-1.3B list) 84.4 % of peak against 82.4 with non-temporal loads on
+// blocked state, 79.3 against 79.6 per tensor; plain loads of the state streams gave
+// 83.7 and 76.9.  In the pure family, plain loads cost the Kahan step 8 %, and the
+// steps with fp32 moments 2-4 points.
 #ifndef ADAMW_NT_MIXED
-#define ADAMW_NT_MIXED 2
+#define ADAMW_NT_MIXED 3
 #endif
-// The mixed family loads the gradient, which nothing writes back, non-temporally
-// on top of ADAMW_NT_MIXED: measured +2-2.5 % for the mixed and split steps on
-// MI355X, while non-temporal loads of the read-modify-write state streams cost 9 %.
 #ifndef ADAMW_NT_MIXED_GRAD
-#define ADAMW_NT_MIXED_GRAD 1
+#define ADAMW_NT_MIXED_GRAD 2
 #endif
-// The pure family (every stream alike, the gradient included): non-temporal loads
-// and stores while the state is bf16 or has one fp32 moment; in the wide mixes
-// (both moments fp32, or an fp32 compensation buffer; the split master)
-// non-temporal stores only, measured on MI355X (OPT-1.3B list, blocked state)
-// 5-6 % faster with fp32 moments and compensation, 3.5 % with fp32 moments
-// alone, and 57 % -> 77 % of peak with bf16 moments and an fp32 compensation
-// buffer, while the bf16 Kahan step loses 8 % without non-temporal loads and
-// the one-fp32-moment mixes tie.
 #ifndef ADAMW_NT_PURE
 #define ADAMW_NT_PURE 3
-#endif
-#ifndef ADAMW_NT_PURE_WIDE
-#define ADAMW_NT_PURE_WIDE 2
-#endif
-#ifndef ADAMW_NT_SPLIT
-#define ADAMW_NT_SPLIT 2
 #endif
 #ifndef ADAMW_NT_CHECK
 #define ADAMW_NT_CHECK 1
@@ -272,14 +258,16 @@ constexpr int kCheckUnroll = kCheckChunkMult;
 __device__ __forceinline__ uint32_t chunk_index(uint32_t b, uint32_t nb) { return xcd_chunk(b, nb); }
 
 // An update kernel's chunk is processed by kXcdParts consecutive workgroups,
-// part = blockIdx.x % kXcdParts running on XCD `part`; lane tid takes the pack
-// tile_pack(tid, part, P) (layout.hpp) of every kXcdParts * BLOCK packs of the
-// chunk.  Element-wise chunks go to the parts in strides of the workgroup size.
-template <int P, int BLOCK>
-__device__ __forceinline__ uint32_t first_pack(uint32_t tid, uint32_t part)
+// part = blockIdx.x % kXcdParts running on XCD `part`.  Per kXcdParts * BLOCK * N
+// units of the chunk, wave w of a workgroup takes tiles w * N + h (h < N) of its
+// part, a lane one unit of each: access h of lane tid is unit_at(tid, part, h), and
+// every access of a wave is one contiguous stretch of its stream.  Element-wise
+// chunks go to the parts in strides of the workgroup size.
+template <int P, int N>
+__device__ __forceinline__ uint32_t unit_at(uint32_t tid, uint32_t part, int h)
 {
-    static_assert(BLOCK % P == 0, "a workgroup covers whole tiles");
-    return tile_pack(tid, part, P);
+    static_assert(P == 64, "a tile is one access of a wave");
+    return tile_pack((tid / P * N + (uint32_t)h) * P + tid % P, part, P);
 }
 
 __device__ __forceinline__ Coef load_coef(const LaunchScalars* sc)
@@ -374,10 +362,9 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
     StepIn in{};
     if (!begin_step<FUSED>(sc, fs, c, in)) return;
     constexpr bool F16 = (MODE == 1);
-    constexpr int NTM = ADAMW_NT_MIXED;
-    constexpr int NTG = NTM | (ADAMW_NT_MIXED_GRAD ? 1 : 0);   // the gradient's loads
-    constexpr int P = kTilePacksMixed;   // tiles of 256 elements
-    constexpr uint32_t kStride = kXcdParts * kBlockMixed;
+    constexpr int NTG = ADAMW_NT_MIXED_GRAD, NTS = ADAMW_NT_MIXED;   // gradient; state and param
+    constexpr int E = 4, N = kPack / E;   // elements of a unit, units of a lane and pass
+    constexpr uint32_t kPass = kXcdParts * kBlockMixed * N, kStride = kXcdParts * kBlockMixed;
     const uint32_t part = blockIdx.x % kXcdParts;
     const DevChunk ch = chunks[blockIdx.x / kXcdParts];
     const DevSeg& sg = segs[ch.seg];
@@ -391,34 +378,57 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
     GLOBAL float* __restrict__ v = gptr<float>(sg.ptr[ADAMW_STREAM_EXP_AVG_SQ], off);
     GLOBAL float* __restrict__ w = gptr<float>(sg.ptr[ADAMW_STREAM_AUX], off);
     if (ch.n_kind & kVecBit) {
-        const uint32_t npack = n / kPack;
-        const GLOBAL u32x4* __restrict__ g4 = reinterpret_cast<const GLOBAL u32x4*>(g);
-        GLOBAL u32x4* __restrict__ p4 = reinterpret_cast<GLOBAL u32x4*>(p);
+        const uint32_t units = n / E;
+        const GLOBAL u32x2* __restrict__ g2 = reinterpret_cast<const GLOBAL u32x2*>(g);
+        GLOBAL u32x2* __restrict__ p2 = reinterpret_cast<GLOBAL u32x2*>(p);
         GLOBAL f32x4* __restrict__ m4 = reinterpret_cast<GLOBAL f32x4*>(m);
         GLOBAL f32x4* __restrict__ v4 = reinterpret_cast<GLOBAL f32x4*>(v);
         GLOBAL f32x4* __restrict__ w4 = reinterpret_cast<GLOBAL f32x4*>(w);
-        for (uint32_t k = first_pack<P, kBlockMixed>(tid, part); k < npack; k += kStride) {
-            const u32x4 G = ld<NTG>(g4 + k);
-            f32x4 W[2] = {ld<NTM>(w4 + 2 * k), ld<NTM>(w4 + 2 * k + 1)};
-            f32x4 M[2] = {ld<NTM>(m4 + 2 * k), ld<NTM>(m4 + 2 * k + 1)};
-            f32x4 V[2] = {ld<NTM>(v4 + 2 * k), ld<NTM>(v4 + 2 * k + 1)};
-            fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
-            float* wf = reinterpret_cast<float*>(W);
-            float* mf = reinterpret_cast<float*>(M);
-            float* vf = reinterpret_cast<float*>(V);
-            const uint32_t gw[4] = {G.x, G.y, G.z, G.w};
-            uint32_t pw[4];
+        for (uint32_t at = 0; at < units; at += kPass) {
+            u32x2 G[N];
+            f32x4 W[N], M[N], V[N];
+            const bool whole = at + kPass <= units;   // uniform: no lane is past the chunk's end
+            // The test stands before each unit's loads also where it holds for all: with
+            // the loads of both units in one run the step on blocked state fell from
+            // 83 to 78 % of peak on MI355X.
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x2 gg = widen2<F16>(gw[j]);
-                const float a = mixed_elem(gg.x, wf[2 * j], mf[2 * j], vf[2 * j], c);
-                const float b = mixed_elem(gg.y, wf[2 * j + 1], mf[2 * j + 1], vf[2 * j + 1], c);
-                pw[j] = narrow2<F16>(a, b);
+            for (int h = 0; h < N; ++h) {
+                const uint32_t k = at + unit_at<kTilePacksMixed, N>(tid, part, h);
+                if (!whole && k >= units) continue;
+                G[h] = ld<NTG>(g2 + k);
+                W[h] = ld<NTS>(w4 + k);
+                M[h] = ld<NTS>(m4 + k);
+                V[h] = ld<NTS>(v4 + k);
             }
-            st<NTM>(w4 + 2 * k, W[0]); st<NTM>(w4 + 2 * k + 1, W[1]);
-            st<NTM>(m4 + 2 * k, M[0]); st<NTM>(m4 + 2 * k + 1, M[1]);
-            st<NTM>(v4 + 2 * k, V[0]); st<NTM>(v4 + 2 * k + 1, V[1]);
-            st<NTM>(p4 + k, u32x4{pw[0], pw[1], pw[2], pw[3]});
+            fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
+            u32x2 P[N];
+#pragma unroll
+            for (int h = 0; h < N; ++h) {
+                if (!whole && at + unit_at<kTilePacksMixed, N>(tid, part, h) >= units) continue;
+                float* wf = reinterpret_cast<float*>(&W[h]);
+                float* mf = reinterpret_cast<float*>(&M[h]);
+                float* vf = reinterpret_cast<float*>(&V[h]);
+                const uint32_t gw[2] = {G[h].x, G[h].y};
+                uint32_t pw[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f32x2 gg = widen2<F16>(gw[j]);
+                    const float a = mixed_elem(gg.x, wf[2 * j], mf[2 * j], vf[2 * j], c);
+                    const float b = mixed_elem(gg.y, wf[2 * j + 1], mf[2 * j + 1], vf[2 * j + 1], c);
+                    pw[j] = narrow2<F16>(a, b);
+                }
+                P[h] = u32x2{pw[0], pw[1]};
+            }
+            // all stores after all arithmetic: 1 point of peak ahead of unit by unit
+#pragma unroll
+            for (int h = 0; h < N; ++h) {
+                const uint32_t k = at + unit_at<kTilePacksMixed, N>(tid, part, h);
+                if (!whole && k >= units) continue;
+                st<NTS>(w4 + k, W[h]);
+                st<NTS>(m4 + k, M[h]);
+                st<NTS>(v4 + k, V[h]);
+                st<NTS>(p2 + k, P[h]);
+            }
         }
     } else {
         fused_coef<FUSED>(fs, in, c);
@@ -456,14 +466,11 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
     if (!begin_step<FUSED>(sc, fs, c, in)) return;
     constexpr bool KAHAN = AUX == kAuxKahan, SPLIT = AUX == kAuxSplit, KAHAN32 = AUX == kAuxKahan32;
     static_assert(!SPLIT || (M32 && V32), "the split master keeps fp32 moments");
-    // The wide pure-family mixes (both moments in fp32, or an fp32
-    // compensation buffer: 8-14 B of state per element, half or more of it in
-    // fp32 streams): non-temporal stores only and the mixed family's occupancy.
-    constexpr bool WIDE = (M32 && V32) || KAHAN32;
-    constexpr int NT = SPLIT ? ADAMW_NT_SPLIT : WIDE ? ADAMW_NT_PURE_WIDE : ADAMW_NT_PURE;
-    // tiles of 256 elements (split master) or 512 (the rest)
-    constexpr int P = SPLIT ? kTilePacksSplit : WIDE ? kTilePacksPureWide : kTilePacks;
-    constexpr uint32_t kStride = kXcdParts * kBlockPure;
+    constexpr int NT = ADAMW_NT_PURE;
+    // elements of a unit, 32-bit words of a 16-bit stream's unit, units of a lane and pass
+    constexpr int E = M32 || V32 || KAHAN32 ? 4 : kPack, H = E / 2, N = kPack / E;
+    constexpr int P = E == 4 ? kTilePacksMixed : kTilePacks;
+    constexpr uint32_t kPass = kXcdParts * kBlockPure * N, kStride = kXcdParts * kBlockPure;
     const uint32_t part = blockIdx.x % kXcdParts;
     const DevChunk ch = chunks[blockIdx.x / kXcdParts];
     const DevSeg& sg = segs[ch.seg];
@@ -480,106 +487,126 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
     GLOBAL CT* __restrict__ cc = gptr<CT>(sg.ptr[ADAMW_STREAM_AUX], off);
 
     if (ch.n_kind & kVecBit) {
-        const uint32_t npack = n / kPack;
-        const GLOBAL u32x4* __restrict__ g4 = reinterpret_cast<const GLOBAL u32x4*>(g);
-        GLOBAL u32x4* __restrict__ p4 = reinterpret_cast<GLOBAL u32x4*>(p);
-        GLOBAL u32x4* __restrict__ c4 = reinterpret_cast<GLOBAL u32x4*>(cc);
-        // a pack of 8 moments (or compensations) is one dwordx4 in bf16, two in fp32
-        constexpr int MW = M32 ? 2 : 1, VW = V32 ? 2 : 1, CW = KAHAN32 ? 2 : 1;
-        GLOBAL u32x4* __restrict__ m4 = reinterpret_cast<GLOBAL u32x4*>(m);
-        GLOBAL u32x4* __restrict__ v4 = reinterpret_cast<GLOBAL u32x4*>(v);
-        for (uint32_t k = first_pack<P, kBlockPure>(tid, part); k < npack; k += kStride) {
-            const u32x4 G = ld<NT>(g4 + k), Pv = ld<NT>(p4 + k);
-            u32x4 C[CW], M[MW], V[VW];
+        const uint32_t units = n / E;
+        using W16 = words_t<H>;   // a unit of a 16-bit stream
+        using WM = words_t<M32 ? E : H>;
+        using WV = words_t<V32 ? E : H>;
+        using WC = words_t<KAHAN32 ? E : H>;
+        const GLOBAL W16* __restrict__ gu = reinterpret_cast<const GLOBAL W16*>(g);
+        GLOBAL W16* __restrict__ pu = reinterpret_cast<GLOBAL W16*>(p);
+        GLOBAL WM* __restrict__ mu = reinterpret_cast<GLOBAL WM*>(m);
+        GLOBAL WV* __restrict__ vu = reinterpret_cast<GLOBAL WV*>(v);
+        GLOBAL WC* __restrict__ cu = reinterpret_cast<GLOBAL WC*>(cc);
+        for (uint32_t at = 0; at < units; at += kPass) {
+            W16 G[N], Pv[N];
+            WM M[N];
+            WV V[N];
+            WC C[N];
+            const auto load = [&](int h, uint32_t k) {
+                G[h] = ld<NT>(gu + k);
+                Pv[h] = ld<NT>(pu + k);
+                M[h] = ld<NT>(mu + k);
+                V[h] = ld<NT>(vu + k);
+                if constexpr (AUX != kAuxNone) C[h] = ld<NT>(cu + k);
+            };
+            const bool whole = at + kPass <= units;   // uniform: no lane is past the chunk's end
+            if (whole) {
 #pragma unroll
-            for (int q = 0; q < MW; ++q) M[q] = ld<NT>(m4 + MW * k + q);
+                for (int h = 0; h < N; ++h) load(h, at + unit_at<P, N>(tid, part, h));
+            } else {
 #pragma unroll
-            for (int q = 0; q < VW; ++q) V[q] = ld<NT>(v4 + VW * k + q);
-            if constexpr (AUX != kAuxNone) {
-#pragma unroll
-                for (int q = 0; q < CW; ++q) C[q] = ld<NT>(c4 + CW * k + q);
+                for (int h = 0; h < N; ++h) {
+                    const uint32_t k = at + unit_at<P, N>(tid, part, h);
+                    G[h] = Pv[h] = W16(0u);
+                    M[h] = WM(0u);
+                    V[h] = WV(0u);
+                    C[h] = WC(0u);
+                    if (k < units) load(h, k);
+                }
             }
             fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
-            const uint32_t* gw = reinterpret_cast<const uint32_t*>(&G);
-            const uint32_t* pw = reinterpret_cast<const uint32_t*>(&Pv);
-            uint32_t* cw = reinterpret_cast<uint32_t*>(C);   // 4 (bf16) or 8 (fp32) words
-            uint32_t* mw = reinterpret_cast<uint32_t*>(M);   // 4 (bf16) or 8 (fp32) words
-            uint32_t* vw = reinterpret_cast<uint32_t*>(V);
-            uint32_t po[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x2 gg = widen2<false>(gw[j]);
-                const f32x2 pp = widen2<false>(pw[j]);
-                float ma, mb, va, vb;
-                if constexpr (M32) {
-                    ma = __uint_as_float(mw[2 * j]);
-                    mb = __uint_as_float(mw[2 * j + 1]);
-                } else {
-                    const f32x2 t2 = widen2<false>(mw[j]);
-                    ma = t2.x;
-                    mb = t2.y;
-                }
-                if constexpr (V32) {
-                    va = __uint_as_float(vw[2 * j]);
-                    vb = __uint_as_float(vw[2 * j + 1]);
-                } else {
-                    const f32x2 t2 = widen2<false>(vw[j]);
-                    va = t2.x;
-                    vb = t2.y;
-                }
-                if constexpr (SPLIT) {
-                    float wa = __uint_as_float(join_bits(pw[j] & 0xffffu, cw[j] & 0xffffu));
-                    float wb = __uint_as_float(join_bits(pw[j] >> 16, cw[j] >> 16));
-                    mixed_elem(gg.x, wa, ma, va, c);
-                    mixed_elem(gg.y, wb, mb, vb, c);
-                    uint32_t ra, rb;
-                    const uint32_t pa = split_bits(__float_as_uint(wa), ra);
-                    const uint32_t pb = split_bits(__float_as_uint(wb), rb);
-                    po[j] = pa | (pb << 16);
-                    cw[j] = ra | (rb << 16);
-                } else if constexpr (KAHAN) {
-                    const f32x2 cf = widen2<false>(cw[j]);
-                    float sa, sb;
-                    const float ta = kahan_sum(gg.x, pp.x, cf.x, ma, va, c, sa);
-                    const float tb = kahan_sum(gg.y, pp.y, cf.y, mb, vb, c, sb);
-                    po[j] = narrow2<false>(ta, tb);
-                    const f32x2 pn = widen2<false>(po[j]);
-                    cw[j] = narrow2<false>(sa - (pn.x - pp.x), sb - (pn.y - pp.y));
-                } else if constexpr (KAHAN32) {
-                    float sa, sb;
-                    const float ta = kahan_sum(gg.x, pp.x, __uint_as_float(cw[2 * j]), ma, va, c, sa);
-                    const float tb = kahan_sum(gg.y, pp.y, __uint_as_float(cw[2 * j + 1]), mb, vb, c, sb);
-                    po[j] = narrow2<false>(ta, tb);
-                    const f32x2 pn = widen2<false>(po[j]);
-                    cw[2 * j] = __float_as_uint(sa - (pn.x - pp.x));
-                    cw[2 * j + 1] = __float_as_uint(sb - (pn.y - pp.y));
-                } else {
-                    float wa = pp.x, wb = pp.y;
-                    mixed_elem(gg.x, wa, ma, va, c);
-                    mixed_elem(gg.y, wb, mb, vb, c);
-                    po[j] = narrow2<false>(wa, wb);
-                }
-                if constexpr (M32) {
-                    mw[2 * j] = __float_as_uint(ma);
-                    mw[2 * j + 1] = __float_as_uint(mb);
-                } else {
-                    mw[j] = narrow2<false>(ma, mb);
-                }
-                if constexpr (V32) {
-                    vw[2 * j] = __float_as_uint(va);
-                    vw[2 * j + 1] = __float_as_uint(vb);
-                } else {
-                    vw[j] = narrow2<false>(va, vb);
+            for (int h = 0; h < N; ++h) {
+                const uint32_t* gw = reinterpret_cast<const uint32_t*>(&G[h]);
+                uint32_t* pw = reinterpret_cast<uint32_t*>(&Pv[h]);
+                uint32_t* cw = reinterpret_cast<uint32_t*>(&C[h]);
+                uint32_t* mw = reinterpret_cast<uint32_t*>(&M[h]);
+                uint32_t* vw = reinterpret_cast<uint32_t*>(&V[h]);
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    const f32x2 gg = widen2<false>(gw[j]);
+                    const f32x2 pp = widen2<false>(pw[j]);
+                    float ma, mb, va, vb;
+                    if constexpr (M32) {
+                        ma = __uint_as_float(mw[2 * j]);
+                        mb = __uint_as_float(mw[2 * j + 1]);
+                    } else {
+                        const f32x2 t2 = widen2<false>(mw[j]);
+                        ma = t2.x;
+                        mb = t2.y;
+                    }
+                    if constexpr (V32) {
+                        va = __uint_as_float(vw[2 * j]);
+                        vb = __uint_as_float(vw[2 * j + 1]);
+                    } else {
+                        const f32x2 t2 = widen2<false>(vw[j]);
+                        va = t2.x;
+                        vb = t2.y;
+                    }
+                    if constexpr (SPLIT) {
+                        float wa = __uint_as_float(join_bits(pw[j] & 0xffffu, cw[j] & 0xffffu));
+                        float wb = __uint_as_float(join_bits(pw[j] >> 16, cw[j] >> 16));
+                        mixed_elem(gg.x, wa, ma, va, c);
+                        mixed_elem(gg.y, wb, mb, vb, c);
+                        uint32_t ra, rb;
+                        const uint32_t pa = split_bits(__float_as_uint(wa), ra);
+                        const uint32_t pb = split_bits(__float_as_uint(wb), rb);
+                        pw[j] = pa | (pb << 16);
+                        cw[j] = ra | (rb << 16);
+                    } else if constexpr (KAHAN) {
+                        const f32x2 cf = widen2<false>(cw[j]);
+                        float sa, sb;
+                        const float ta = kahan_sum(gg.x, pp.x, cf.x, ma, va, c, sa);
+                        const float tb = kahan_sum(gg.y, pp.y, cf.y, mb, vb, c, sb);
+                        pw[j] = narrow2<false>(ta, tb);
+                        const f32x2 pn = widen2<false>(pw[j]);
+                        cw[j] = narrow2<false>(sa - (pn.x - pp.x), sb - (pn.y - pp.y));
+                    } else if constexpr (KAHAN32) {
+                        float sa, sb;
+                        const float ta = kahan_sum(gg.x, pp.x, __uint_as_float(cw[2 * j]), ma, va, c, sa);
+                        const float tb = kahan_sum(gg.y, pp.y, __uint_as_float(cw[2 * j + 1]), mb, vb, c, sb);
+                        pw[j] = narrow2<false>(ta, tb);
+                        const f32x2 pn = widen2<false>(pw[j]);
+                        cw[2 * j] = __float_as_uint(sa - (pn.x - pp.x));
+                        cw[2 * j + 1] = __float_as_uint(sb - (pn.y - pp.y));
+                    } else {
+                        float wa = pp.x, wb = pp.y;
+                        mixed_elem(gg.x, wa, ma, va, c);
+                        mixed_elem(gg.y, wb, mb, vb, c);
+                        pw[j] = narrow2<false>(wa, wb);
+                    }
+                    if constexpr (M32) {
+                        mw[2 * j] = __float_as_uint(ma);
+                        mw[2 * j + 1] = __float_as_uint(mb);
+                    } else {
+                        mw[j] = narrow2<false>(ma, mb);
+                    }
+                    if constexpr (V32) {
+                        vw[2 * j] = __float_as_uint(va);
+                        vw[2 * j + 1] = __float_as_uint(vb);
+                    } else {
+                        vw[j] = narrow2<false>(va, vb);
+                    }
                 }
             }
-            st<NT>(p4 + k, u32x4{po[0], po[1], po[2], po[3]});
 #pragma unroll
-            for (int q = 0; q < MW; ++q) st<NT>(m4 + MW * k + q, M[q]);
-#pragma unroll
-            for (int q = 0; q < VW; ++q) st<NT>(v4 + VW * k + q, V[q]);
-            if constexpr (AUX != kAuxNone) {
-#pragma unroll
-                for (int q = 0; q < CW; ++q) st<NT>(c4 + CW * k + q, C[q]);
+            for (int h = 0; h < N; ++h) {
+                const uint32_t k = at + unit_at<P, N>(tid, part, h);
+                if (!whole && k >= units) continue;
+                st<NT>(pu + k, Pv[h]);
+                st<NT>(mu + k, M[h]);
+                st<NT>(vu + k, V[h]);
+                if constexpr (AUX != kAuxNone) st<NT>(cu + k, C[h]);
             }
         }
     } else {
@@ -697,26 +724,23 @@ hipError_t launch_prologue(const adamw_hparams& hp, int32_t* d_step, const int32
     return hipGetLastError();
 }
 
-// Occupancy cap, per kernel family: the update kernels use no LDS, but
-// reserving this much per workgroup leaves room for only 160 KiB / bytes
-// workgroups on a CU.  Measured on MI355X with the OPT-1.3B list, 8 waves per CU
-// (mixed: two 256-lane workgroups) and 16 (pure: four 256-lane workgroups)
-// stream faster than the register-limited 20-32 waves: fewer concurrent address
-// streams per CU keep more DRAM rows open.  The wide pure-bf16 mixes (both
-// moments fp32, or an fp32 compensation buffer) run at the mixed family's 8
-// waves: 4 % faster than at 16 with fp32 moments and compensation on blocked
-// state, while the bf16-state steps lost 2-5 % at 8.
+// Occupancy cap, per kernel: the update kernels use no LDS, but reserving this much
+// per workgroup leaves room for only 160 KiB / bytes workgroups on a CU: fewer
+// concurrent address streams keep more DRAM rows open.  Two 256-lane workgroups (8
+// waves) for the mixed step and for fp32 moments beside an fp32 compensation buffer
+// (28 and 30 B per element), four for the others.  MI355X, OPT-1.3B list, % of peak
+// with two / four, state per tensor, then blocked: mixed 78.3 / 77.1, 84.2 / 82.0;
+// fp32 moments and compensation 78.5 / 73.9, 81.3 / 80.2; split master 75.6 / 75.5,
+// 76.2 / 77.7; fp32 moments and bf16 compensation 76.0 / 75.5, 77.4 / 77.7; fp32
+// moments alone 77.2 / 78.2, 74.3 / 82.4; bf16 state (Kahan) 73.5 / 76.9, 74.4 / 79.0.
 #ifndef ADAMW_LDS_MIXED
 #define ADAMW_LDS_MIXED 81920
 #endif
 #ifndef ADAMW_LDS_PURE
 #define ADAMW_LDS_PURE 40960
 #endif
-#ifndef ADAMW_LDS_PURE_WIDE
-#define ADAMW_LDS_PURE_WIDE 81920
-#endif
-#ifndef ADAMW_LDS_SPLIT
-#define ADAMW_LDS_SPLIT 81920
+#ifndef ADAMW_LDS_C32_WIDE
+#define ADAMW_LDS_C32_WIDE 81920
 #endif
 
 // Two-launch form (fused == nullptr): the update kernel reads the prologue's
@@ -735,14 +759,13 @@ static hipError_t launch_update_as(int kernel, const DevSeg* segs, const DevChun
         hipLaunchKernelGGL((update_kernel<1, FUSED>), grid, block, ADAMW_LDS_MIXED, stream, segs, chunks, d_scalars, fs);
         break;
     case kKernelSplit:
-        hipLaunchKernelGGL((update_pure_kernel<true, true, kAuxSplit, FUSED>), grid, block_pure, ADAMW_LDS_SPLIT, stream,
+        hipLaunchKernelGGL((update_pure_kernel<true, true, kAuxSplit, FUSED>), grid, block_pure, ADAMW_LDS_PURE, stream,
                            segs, chunks, d_scalars, fs);
         break;
 #define ADAMW_PURE_CASE(M, V, K)                                                                          \
     case kKernelPure + (M) * 4 + (V) * 2 + (K):                                                            \
         hipLaunchKernelGGL((update_pure_kernel<M, V, (K) ? kAuxKahan : kAuxNone, FUSED>), grid, block_pure,    \
-                           (M) && (V) ? ADAMW_LDS_PURE_WIDE : ADAMW_LDS_PURE, stream, segs,                     \
-                           chunks, d_scalars, fs);                                                         \
+                           ADAMW_LDS_PURE, stream, segs, chunks, d_scalars, fs);                           \
         break;
         ADAMW_PURE_CASE(0, 0, 0) ADAMW_PURE_CASE(0, 0, 1) ADAMW_PURE_CASE(0, 1, 0) ADAMW_PURE_CASE(0, 1, 1)
         ADAMW_PURE_CASE(1, 0, 0) ADAMW_PURE_CASE(1, 0, 1) ADAMW_PURE_CASE(1, 1, 0) ADAMW_PURE_CASE(1, 1, 1)
@@ -750,7 +773,7 @@ static hipError_t launch_update_as(int kernel, const DevSeg* segs, const DevChun
 #define ADAMW_PURE_C32_CASE(M, V)                                                                         \
     case kKernelPureC32 + (M) * 2 + (V):                                                                   \
         hipLaunchKernelGGL((update_pure_kernel<M, V, kAuxKahan32, FUSED>), grid, block_pure,                 \
-                           ADAMW_LDS_PURE_WIDE, stream, segs, chunks, d_scalars, fs);                     \
+                           (M) && (V) ? ADAMW_LDS_C32_WIDE : ADAMW_LDS_PURE, stream, segs, chunks, d_scalars, fs);                           \
         break;
         ADAMW_PURE_C32_CASE(0, 0) ADAMW_PURE_C32_CASE(0, 1) ADAMW_PURE_C32_CASE(1, 0) ADAMW_PURE_C32_CASE(1, 1)
 #undef ADAMW_PURE_C32_CASE

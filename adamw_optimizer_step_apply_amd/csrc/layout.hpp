@@ -43,39 +43,25 @@ constexpr int64_t kTagClip = -3;
 constexpr int64_t kElemChunkElems = 4096;       // element chunk
 // An update kernel's chunk is shared by kXcdParts workgroups, consecutive in
 // launch order, so one on each XCD (the dispatcher hands workgroup b to XCD
-// b % 8).  The chunk is cut into tiles of packs; tile t goes to part t % 8, and
-// each lane of a part takes one 8-element pack per 2048 packs of the chunk.
-// All XCDs thus sweep one contiguous region together.  On MI355X (OPT-1.3B
-// list, against giving each XCD one contiguous run of 2048-element chunks)
-// this streamed the mixed step 7 % faster on blocked state (16384-element
-// blocks) and 4-6.5 % per tensor, and the Kahan step 1 % faster blocked and
-// 5-9 % per tensor; only the split-master step on blocked state lost (4 %),
-// before its master split became branch-free.  Tile sizes, from interleaved
-// A/B runs: 256 elements (1 KiB of an fp32 stream) for the mixed step, whose
-// param stream is written only, and for the split-master step (ahead of 512
-// by 0.7 points of peak on blocked state, 2.2 per tensor); 512 elements
-// (1 KiB of a 16-bit param) for the pure-bf16 family, 1-2 % ahead of 256
-// there.  Smaller and larger tiles (64-128, 512-1024 elements for the mixed
-// step; 256 and 1024-2048 for Kahan) were slower.
+// b % 8).  The chunk is cut into tiles of 64 units, a unit being what one lane
+// moves of every stream in one access: 8 elements where all streams are 16-bit, 4
+// where one is fp32.  A tile is one access of a wave (1 KiB of its widest stream);
+// tile t goes to part t % 8, so that all XCDs sweep one contiguous region together.
+// On MI355X (OPT-1.3B list, against giving each XCD one contiguous run of
+// 2048-element chunks) the sharing streamed the mixed step 7 % faster on blocked
+// state (16384-element blocks) and 4-6.5 % per tensor, and the Kahan step 1 %
+// faster blocked and 5-9 % per tensor.  Units of 4 elements, against 8 elements
+// whose fp32 words lie 32 bytes apart from lane to lane (each wave access then
+// touches every 128-byte line of twice its length for half of its bytes, and
+// non-temporal loads fetch the lines twice): with non-temporal loads the mixed
+// step gained 1-1.5 points of peak, up to 4.6 per tensor on other placements, and
+// 14 % at 1 M elements; the steps with fp32 moments 3-8 points per tensor and 0-5
+// blocked.  Tiles of 32 units were 1-4 points slower, tiles of 128 units 1-3.
 constexpr int kXcdParts = 8;
-#ifndef ADAMW_TILE_PACKS_MIXED
-#define ADAMW_TILE_PACKS_MIXED 32
-#endif
-#ifndef ADAMW_TILE_PACKS_SPLIT
-#define ADAMW_TILE_PACKS_SPLIT 32
-#endif
-#ifndef ADAMW_TILE_PACKS_PURE
-#define ADAMW_TILE_PACKS_PURE 64
-#endif
-#ifndef ADAMW_TILE_PACKS_PURE_WIDE
-#define ADAMW_TILE_PACKS_PURE_WIDE ADAMW_TILE_PACKS_PURE
-#endif
-constexpr int kTilePacksMixed = ADAMW_TILE_PACKS_MIXED;
-constexpr int kTilePacksSplit = ADAMW_TILE_PACKS_SPLIT;
-constexpr int kTilePacks = ADAMW_TILE_PACKS_PURE;
-constexpr int kTilePacksPureWide = ADAMW_TILE_PACKS_PURE_WIDE;   // fp32 exp_avg and exp_avg_sq + compensation
-// The pack of a chunk taken by lane tid of part `part` (per kXcdParts * block
-// packs): tile t of p packs belongs to part t % kXcdParts, so
+constexpr int kTilePacksMixed = 64;   // units of a tile where a stream is fp32 (256 elements)
+constexpr int kTilePacks = 64;        // where all streams are 16-bit (512 elements)
+// The unit of a chunk taken by lane tid of part `part` (per kXcdParts * block
+// units): tile t of p units belongs to part t % kXcdParts, so
 //     ((tid / p) * kXcdParts + part) * p + tid % p,
 // a bijection of (part, tid) onto [0, kXcdParts * block) whenever p divides
 // the workgroup size.
@@ -83,7 +69,7 @@ constexpr uint32_t tile_pack(uint32_t tid, uint32_t part, uint32_t p)
 {
     return ((tid / p) * kXcdParts + part) * p + tid % p;
 }
-// Default vector chunk of an update kernel: one pack per lane of each part.
+// Default vector chunk of an update kernel: 8 elements per lane of each part.
 constexpr int64_t update_chunk_elems(int block) { return (int64_t)kXcdParts * block * kPack; }
 // Blocked state: elements per block, one update chunk (every mode).
 constexpr int64_t kStateBlockElems = ADAMW_STATE_BLOCK_ELEMS;
