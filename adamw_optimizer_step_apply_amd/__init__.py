@@ -516,7 +516,7 @@ def adamw_set_chunk_elems(elems: int) -> int:
 
 
 def adamw_set_single_launch_max_workgroups(max_workgroups: int) -> int:
-    """Largest grid (in workgroups: 8 per chunk of a step, 1 per check chunk)
+    """Largest grid (in workgroups: 8 per chunk of a step, 1 per short one and per check chunk)
     that runs as one launch; 0 = always two launches, < 0 = the default.
     Returns the value now in force."""
     return _lib.adamw_set_single_launch_max_workgroups(int(max_workgroups))

@@ -63,6 +63,7 @@ struct PlanSlot {
     bool valid = false;
     bool pinned = false;   // used under graph capture: never evicted, resized or rewritten
     int64_t n_segs = 0, n_chunks = 0, n_tensors = 0;
+    UpdateGrid grid;   // an update's
 
     const DevSeg* segs() const { return static_cast<const DevSeg*>(dev); }
     const DevChunk* chunks() const
@@ -208,6 +209,7 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
 
     std::vector<Table> tables;
     std::vector<DevSweep> groups;
+    UpdateTable update;
     int64_t n_segs = 0, n_chunks = 0;
     if (is_sweep(tag)) {
         groups = sweep_groups(plan, esz[ADAMW_STREAM_GRAD], tag == kTagClip);
@@ -216,8 +218,12 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
         if (tag == kTagNorm) tables.emplace_back(plan.tensor_first);
     } else {
         n_segs = (int64_t)plan.segs.size();
-        n_chunks = (int64_t)plan.chunks.size();
         tables.emplace_back(plan.segs);
+        if (tag != kTagCheck) {
+            update = update_table(plan);
+            plan.chunks.swap(update.items);
+        }
+        n_chunks = (int64_t)plan.chunks.size();
         tables.emplace_back(plan.chunks);
     }
     size_t bytes = 0;
@@ -272,6 +278,7 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     }
     slot.n_segs = n_segs;
     slot.n_chunks = n_chunks;
+    slot.grid = update.grid;
     slot.n_tensors = list->n_tensors;
     slot.key.swap(key);
     slot.valid = true;
@@ -423,7 +430,7 @@ adamw_status do_step(const StepKind& kind, const adamw_tensor_list* list, const 
     if ((st = ensure_plan(*ws, kind.kernel, kind.esz, list, chunk_elems_of(kind.kernel), stream, cap, &plan)) !=
         ADAMW_OK)
         return st;
-    return enqueue_step(kind, plan->segs(), plan->chunks(), plan->n_chunks, ws->scalars, done, *hp, d_step,
+    return enqueue_step(kind, plan->segs(), plan->chunks(), plan->grid, ws->scalars, done, *hp, d_step,
                         d_found_inf, d_amp, scaler, clip, stream);
 }
 
@@ -528,7 +535,7 @@ adamw_status check_step_call(const StepKind& kind, const adamw_tensor_list* list
     return validate_list(kind.kernel, kind.esz, list, chunk_elems_of(kind.kernel));
 }
 
-adamw_status enqueue_step(const StepKind& kind, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+adamw_status enqueue_step(const StepKind& kind, const DevSeg* segs, const DevChunk* items, const UpdateGrid& grid,
                           LaunchScalars* scalars, uint32_t* done, const adamw_hparams& hp, int32_t* d_step,
                           const int32_t* d_found_inf, adamw_loss_scale_state* d_amp, const adamw_loss_scaler* scaler,
                           const ClipRule& clip, hipStream_t stream)
@@ -537,15 +544,15 @@ adamw_status enqueue_step(const StepKind& kind, const DevSeg* segs, const DevChu
     hipError_t e;
     // Small plans: one launch.  An empty plan, whose step still advances the
     // counter (and the loss scale), keeps the prologue kernel.
-    if (single_launch(n_chunks * kXcdParts)) {
+    if (single_launch(grid.workgroups())) {
         const FusedStep fs{hp, d_step, d_found_inf, done, d_amp, rule, clip};
-        e = launch_update(kind.kernel, segs, chunks, n_chunks, nullptr, &fs, stream);
+        e = launch_update(kind.kernel, segs, items, grid, nullptr, &fs, stream);
         if (e != hipSuccess) return hip_fail("update launch", e);
         return ADAMW_OK;
     }
     e = launch_prologue(hp, d_step, d_found_inf, scalars, d_amp, rule, clip, stream);
     if (e != hipSuccess) return hip_fail("prologue launch", e);
-    e = launch_update(kind.kernel, segs, chunks, n_chunks, scalars, nullptr, stream);
+    e = launch_update(kind.kernel, segs, items, grid, scalars, nullptr, stream);
     if (e != hipSuccess) return hip_fail("update launch", e);
     return ADAMW_OK;
 }

@@ -13,7 +13,8 @@
 //   update_kernel<MODE, FUSED> / update_pure_kernel<M32, V32, AUX, FUSED>
 //                        eight workgroups per chunk, one on each XCD, the chunk
 //                        interleaved between them in tiles of 256 or 512
-//                        elements: the AdamW element update;
+//                        elements (a short chunk: one workgroup): the AdamW
+//                        element update;
 //                        FUSED: without a prologue, for small plans (each
 //                        workgroup forms the scalars, the last one advances
 //                        the counter)
@@ -257,18 +258,47 @@ constexpr int kCheckUnroll = kCheckChunkMult;
 // which each XCD walks one contiguous run of chunks.
 __device__ __forceinline__ uint32_t chunk_index(uint32_t b, uint32_t nb) { return xcd_chunk(b, nb); }
 
-// An update kernel's chunk is processed by kXcdParts consecutive workgroups,
-// part = blockIdx.x % kXcdParts running on XCD `part`.  Per kXcdParts * BLOCK * N
-// units of the chunk, wave w of a workgroup takes tiles w * N + h (h < N) of its
-// part, a lane one unit of each: access h of lane tid is unit_at(tid, part, h), and
-// every access of a wave is one contiguous stretch of its stream.  Element-wise
-// chunks go to the parts in strides of the workgroup size.
+// What a workgroup of an update kernel does of its item: `part` of `parts`, of the
+// `body` elements from `head` on in units, and of the `edge` elements before and after
+// them one by one.  An item shared by kXcdParts workgroups, consecutive in
+// launch order, has part blockIdx.x % kXcdParts on XCD `part`.
+struct Work {
+    uint64_t off;      // the item's first element in its segment
+    uint32_t seg, part, parts;
+    uint32_t head, body, edge;
+};
+
+__device__ __forceinline__ Work work_of(const DevChunk* items, uint32_t n_shared)
+{
+    const uint32_t b = blockIdx.x, shared = n_shared * kXcdParts;
+    const bool alone = b >= shared;
+    const DevChunk it = items[alone ? n_shared + (b - shared) : b / kXcdParts];
+    const uint32_t n = it.n_kind & kItemCountMask;
+    Work w;
+    w.off = it.off;
+    w.seg = it.seg;
+    w.part = alone ? 0 : b % kXcdParts;
+    w.parts = alone ? 1 : kXcdParts;
+    const bool vec = (it.n_kind & kVecBit) != 0;
+    w.head = vec ? it.n_kind >> kItemHeadShift & 7u : n;
+    w.body = vec ? (n - w.head) / kPack * kPack : 0;
+    w.edge = n - w.body;
+    return w;
+}
+
+// Per parts * BLOCK * N units of an item, wave w of a workgroup takes tiles w * N + h
+// (h < N) of its part, a lane one unit of each: access h of lane tid is
+// unit_at(tid, work, h), and every access of a wave is one contiguous stretch of
+// its stream.
 template <int P, int N>
-__device__ __forceinline__ uint32_t unit_at(uint32_t tid, uint32_t part, int h)
+__device__ __forceinline__ uint32_t unit_at(uint32_t tid, const Work& w, int h)
 {
     static_assert(P == 64, "a tile is one access of a wave");
-    return tile_pack((tid / P * N + (uint32_t)h) * P + tid % P, part, P);
+    return tile_pack((tid / P * N + (uint32_t)h) * P + tid % P, w.part, P, w.parts);
 }
+
+// The k-th of the elements outside the vector part.
+__device__ __forceinline__ uint32_t edge_at(const Work& w, uint32_t k) { return k < w.head ? k : k + w.body; }
 
 __device__ __forceinline__ Coef load_coef(const LaunchScalars* sc)
 {
@@ -355,7 +385,7 @@ __device__ __forceinline__ void end_step(const FusedStep& fs, const StepIn& in)
 // kernel below: its param is read as well as written)
 template <int MODE, bool FUSED>
 __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __restrict__ segs,
-                                                        const DevChunk* __restrict__ chunks,
+                                                        const DevChunk* __restrict__ items, uint32_t n_shared,
                                                         const LaunchScalars* __restrict__ sc, FusedStep fs)
 {
     Coef c{};
@@ -364,12 +394,9 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
     constexpr bool F16 = (MODE == 1);
     constexpr int NTG = ADAMW_NT_MIXED_GRAD, NTS = ADAMW_NT_MIXED;   // gradient; state and param
     constexpr int E = 4, N = kPack / E;   // elements of a unit, units of a lane and pass
-    constexpr uint32_t kPass = kXcdParts * kBlockMixed * N, kStride = kXcdParts * kBlockMixed;
-    const uint32_t part = blockIdx.x % kXcdParts;
-    const DevChunk ch = chunks[blockIdx.x / kXcdParts];
-    const DevSeg& sg = segs[ch.seg];
-    const uint32_t n = ch.n_kind & kCountMask;
-    const uint64_t off = ch.off;
+    const Work wk = work_of(items, n_shared);
+    const DevSeg& sg = segs[wk.seg];
+    const uint64_t off = wk.off;
     const uint32_t tid = threadIdx.x;
 
     GLOBAL uint16_t* __restrict__ p = gptr<uint16_t>(sg.ptr[ADAMW_STREAM_PARAM], off);
@@ -377,62 +404,75 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
     GLOBAL float* __restrict__ m = gptr<float>(sg.ptr[ADAMW_STREAM_EXP_AVG], off);
     GLOBAL float* __restrict__ v = gptr<float>(sg.ptr[ADAMW_STREAM_EXP_AVG_SQ], off);
     GLOBAL float* __restrict__ w = gptr<float>(sg.ptr[ADAMW_STREAM_AUX], off);
-    if (ch.n_kind & kVecBit) {
-        const uint32_t units = n / E;
-        const GLOBAL u32x2* __restrict__ g2 = reinterpret_cast<const GLOBAL u32x2*>(g);
-        GLOBAL u32x2* __restrict__ p2 = reinterpret_cast<GLOBAL u32x2*>(p);
-        GLOBAL f32x4* __restrict__ m4 = reinterpret_cast<GLOBAL f32x4*>(m);
-        GLOBAL f32x4* __restrict__ v4 = reinterpret_cast<GLOBAL f32x4*>(v);
-        GLOBAL f32x4* __restrict__ w4 = reinterpret_cast<GLOBAL f32x4*>(w);
-        for (uint32_t at = 0; at < units; at += kPass) {
-            u32x2 G[N];
+    if (wk.body) {
+        const uint32_t units = wk.body / E, pass = wk.parts * kBlockMixed * N;
+        const GLOBAL u32x2* __restrict__ g2 = reinterpret_cast<const GLOBAL u32x2*>(g + wk.head);
+        GLOBAL u32x2* __restrict__ p2 = reinterpret_cast<GLOBAL u32x2*>(p + wk.head);
+        GLOBAL f32x4* __restrict__ m4 = reinterpret_cast<GLOBAL f32x4*>(m + wk.head);
+        GLOBAL f32x4* __restrict__ v4 = reinterpret_cast<GLOBAL f32x4*>(v + wk.head);
+        GLOBAL f32x4* __restrict__ w4 = reinterpret_cast<GLOBAL f32x4*>(w + wk.head);
+        const auto update = [&](u32x2 G, f32x4& W, f32x4& M, f32x4& V) {
+            float* wf = reinterpret_cast<float*>(&W);
+            float* mf = reinterpret_cast<float*>(&M);
+            float* vf = reinterpret_cast<float*>(&V);
+            const uint32_t gw[2] = {G.x, G.y};
+            uint32_t pw[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x2 gg = widen2<F16>(gw[j]);
+                const float a = mixed_elem(gg.x, wf[2 * j], mf[2 * j], vf[2 * j], c);
+                const float b = mixed_elem(gg.y, wf[2 * j + 1], mf[2 * j + 1], vf[2 * j + 1], c);
+                pw[j] = narrow2<F16>(a, b);
+            }
+            return u32x2{pw[0], pw[1]};
+        };
+        // Whole passes without a test, then the last units one by one: with a test before
+        // each unit's accesses the compiler waits for one unit's loads before it issues
+        // the next one's (blocked state: 83.8 % of peak on MI355X at best, 77.9 with some
+        // register assignments, against 86.1).
+        uint32_t at = 0;
+        for (; at + pass <= units; at += pass) {
+            u32x2 G[N], P[N];
             f32x4 W[N], M[N], V[N];
-            const bool whole = at + kPass <= units;   // uniform: no lane is past the chunk's end
-            // The test stands before each unit's loads also where it holds for all: with
-            // the loads of both units in one run the step on blocked state fell from
-            // 83 to 78 % of peak on MI355X.
 #pragma unroll
             for (int h = 0; h < N; ++h) {
-                const uint32_t k = at + unit_at<kTilePacksMixed, N>(tid, part, h);
-                if (!whole && k >= units) continue;
+                const uint32_t k = at + unit_at<kTilePacksMixed, N>(tid, wk, h);
                 G[h] = ld<NTG>(g2 + k);
                 W[h] = ld<NTS>(w4 + k);
                 M[h] = ld<NTS>(m4 + k);
                 V[h] = ld<NTS>(v4 + k);
             }
-            fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
-            u32x2 P[N];
+            if (at == 0) fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
+#pragma unroll
+            for (int h = 0; h < N; ++h) P[h] = update(G[h], W[h], M[h], V[h]);
 #pragma unroll
             for (int h = 0; h < N; ++h) {
-                if (!whole && at + unit_at<kTilePacksMixed, N>(tid, part, h) >= units) continue;
-                float* wf = reinterpret_cast<float*>(&W[h]);
-                float* mf = reinterpret_cast<float*>(&M[h]);
-                float* vf = reinterpret_cast<float*>(&V[h]);
-                const uint32_t gw[2] = {G[h].x, G[h].y};
-                uint32_t pw[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const f32x2 gg = widen2<F16>(gw[j]);
-                    const float a = mixed_elem(gg.x, wf[2 * j], mf[2 * j], vf[2 * j], c);
-                    const float b = mixed_elem(gg.y, wf[2 * j + 1], mf[2 * j + 1], vf[2 * j + 1], c);
-                    pw[j] = narrow2<F16>(a, b);
-                }
-                P[h] = u32x2{pw[0], pw[1]};
-            }
-            // all stores after all arithmetic: 1 point of peak ahead of unit by unit
-#pragma unroll
-            for (int h = 0; h < N; ++h) {
-                const uint32_t k = at + unit_at<kTilePacksMixed, N>(tid, part, h);
-                if (!whole && k >= units) continue;
+                const uint32_t k = at + unit_at<kTilePacksMixed, N>(tid, wk, h);
                 st<NTS>(w4 + k, W[h]);
                 st<NTS>(m4 + k, M[h]);
                 st<NTS>(v4 + k, V[h]);
                 st<NTS>(p2 + k, P[h]);
             }
         }
-    } else {
-        fused_coef<FUSED>(fs, in, c);
-        for (uint32_t i = part * kBlockMixed + tid; i < n; i += kStride) {
+        if (at < units) {   // the last units, which do not fill a pass
+            if (at == 0) fused_coef<FUSED>(fs, in, c);
+#pragma unroll
+            for (int h = 0; h < N; ++h) {
+                const uint32_t k = at + unit_at<kTilePacksMixed, N>(tid, wk, h);
+                if (k >= units) continue;
+                f32x4 W = ld<NTS>(w4 + k), M = ld<NTS>(m4 + k), V = ld<NTS>(v4 + k);
+                const u32x2 P = update(ld<NTG>(g2 + k), W, M, V);
+                st<NTS>(w4 + k, W);
+                st<NTS>(m4 + k, M);
+                st<NTS>(v4 + k, V);
+                st<NTS>(p2 + k, P);
+            }
+        }
+    }
+    if (wk.edge) {
+        if (wk.body == 0) fused_coef<FUSED>(fs, in, c);
+        for (uint32_t e = wk.part * kBlockMixed + tid; e < wk.edge; e += wk.parts * kBlockMixed) {
+            const uint32_t i = edge_at(wk, e);
             float wi = w[i], mi = m[i], vi = v[i];
             const float nw = mixed_elem(widen1<F16>(g[i]), wi, mi, vi, c);
             w[i] = wi;
@@ -457,7 +497,8 @@ constexpr int kAuxKahan32 = 3; // fp32 Kahan compensation c (the residual kept u
 // kAuxSplit>).
 template <bool M32, bool V32, int AUX, bool FUSED>
 __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* __restrict__ segs,
-                                                                            const DevChunk* __restrict__ chunks,
+                                                                            const DevChunk* __restrict__ items,
+                                                                            uint32_t n_shared,
                                                                             const LaunchScalars* __restrict__ sc,
                                                                             FusedStep fs)
 {
@@ -470,12 +511,9 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
     // elements of a unit, 32-bit words of a 16-bit stream's unit, units of a lane and pass
     constexpr int E = M32 || V32 || KAHAN32 ? 4 : kPack, H = E / 2, N = kPack / E;
     constexpr int P = E == 4 ? kTilePacksMixed : kTilePacks;
-    constexpr uint32_t kPass = kXcdParts * kBlockPure * N, kStride = kXcdParts * kBlockPure;
-    const uint32_t part = blockIdx.x % kXcdParts;
-    const DevChunk ch = chunks[blockIdx.x / kXcdParts];
-    const DevSeg& sg = segs[ch.seg];
-    const uint32_t n = ch.n_kind & kCountMask;
-    const uint64_t off = ch.off;
+    const Work wk = work_of(items, n_shared);
+    const DevSeg& sg = segs[wk.seg];
+    const uint64_t off = wk.off;
     const uint32_t tid = threadIdx.x;
     using MT = typename std::conditional<M32, float, uint16_t>::type;
     using VT = typename std::conditional<V32, float, uint16_t>::type;
@@ -486,18 +524,18 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
     using CT = typename std::conditional<KAHAN32, float, uint16_t>::type;
     GLOBAL CT* __restrict__ cc = gptr<CT>(sg.ptr[ADAMW_STREAM_AUX], off);
 
-    if (ch.n_kind & kVecBit) {
-        const uint32_t units = n / E;
+    if (wk.body) {
+        const uint32_t units = wk.body / E, pass = wk.parts * kBlockPure * N;
         using W16 = words_t<H>;   // a unit of a 16-bit stream
         using WM = words_t<M32 ? E : H>;
         using WV = words_t<V32 ? E : H>;
         using WC = words_t<KAHAN32 ? E : H>;
-        const GLOBAL W16* __restrict__ gu = reinterpret_cast<const GLOBAL W16*>(g);
-        GLOBAL W16* __restrict__ pu = reinterpret_cast<GLOBAL W16*>(p);
-        GLOBAL WM* __restrict__ mu = reinterpret_cast<GLOBAL WM*>(m);
-        GLOBAL WV* __restrict__ vu = reinterpret_cast<GLOBAL WV*>(v);
-        GLOBAL WC* __restrict__ cu = reinterpret_cast<GLOBAL WC*>(cc);
-        for (uint32_t at = 0; at < units; at += kPass) {
+        const GLOBAL W16* __restrict__ gu = reinterpret_cast<const GLOBAL W16*>(g + wk.head);
+        GLOBAL W16* __restrict__ pu = reinterpret_cast<GLOBAL W16*>(p + wk.head);
+        GLOBAL WM* __restrict__ mu = reinterpret_cast<GLOBAL WM*>(m + wk.head);
+        GLOBAL WV* __restrict__ vu = reinterpret_cast<GLOBAL WV*>(v + wk.head);
+        GLOBAL WC* __restrict__ cu = reinterpret_cast<GLOBAL WC*>(cc + wk.head);
+        for (uint32_t at = 0; at < units; at += pass) {
             W16 G[N], Pv[N];
             WM M[N];
             WV V[N];
@@ -509,14 +547,16 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
                 V[h] = ld<NT>(vu + k);
                 if constexpr (AUX != kAuxNone) C[h] = ld<NT>(cu + k);
             };
-            const bool whole = at + kPass <= units;   // uniform: no lane is past the chunk's end
+            // Uniform: no lane is past the item's end.  Here the stores keep a test each: a
+            // straight pass as in the mixed kernel was 0.5-3 points of peak slower.
+            const bool whole = at + pass <= units;
             if (whole) {
 #pragma unroll
-                for (int h = 0; h < N; ++h) load(h, at + unit_at<P, N>(tid, part, h));
+                for (int h = 0; h < N; ++h) load(h, at + unit_at<P, N>(tid, wk, h));
             } else {
 #pragma unroll
                 for (int h = 0; h < N; ++h) {
-                    const uint32_t k = at + unit_at<P, N>(tid, part, h);
+                    const uint32_t k = at + unit_at<P, N>(tid, wk, h);
                     G[h] = Pv[h] = W16(0u);
                     M[h] = WM(0u);
                     V[h] = WV(0u);
@@ -524,7 +564,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
                     if (k < units) load(h, k);
                 }
             }
-            fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
+            if (at == 0) fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
 #pragma unroll
             for (int h = 0; h < N; ++h) {
                 const uint32_t* gw = reinterpret_cast<const uint32_t*>(&G[h]);
@@ -601,7 +641,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
             }
 #pragma unroll
             for (int h = 0; h < N; ++h) {
-                const uint32_t k = at + unit_at<P, N>(tid, part, h);
+                const uint32_t k = at + unit_at<P, N>(tid, wk, h);
                 if (!whole && k >= units) continue;
                 st<NT>(pu + k, Pv[h]);
                 st<NT>(mu + k, M[h]);
@@ -609,9 +649,11 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
                 if constexpr (AUX != kAuxNone) st<NT>(cu + k, C[h]);
             }
         }
-    } else {
-        fused_coef<FUSED>(fs, in, c);
-        for (uint32_t i = part * kBlockPure + tid; i < n; i += kStride) {
+    }
+    if (wk.edge) {
+        if (wk.body == 0) fused_coef<FUSED>(fs, in, c);
+        for (uint32_t e = wk.part * kBlockPure + tid; e < wk.edge; e += wk.parts * kBlockPure) {
+            const uint32_t i = edge_at(wk, e);
             const float pf = widen1<false>(p[i]);
             float mi, vi;
             if constexpr (M32) mi = m[i]; else mi = widen1<false>(m[i]);
@@ -746,26 +788,27 @@ hipError_t launch_prologue(const adamw_hparams& hp, int32_t* d_step, const int32
 // Two-launch form (fused == nullptr): the update kernel reads the prologue's
 // scalars at d_scalars.  Single launch: the kernel forms them from *fused.
 template <bool FUSED>
-static hipError_t launch_update_as(int kernel, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+static hipError_t launch_update_as(int kernel, const DevSeg* segs, const DevChunk* items, const UpdateGrid& work,
                                    const LaunchScalars* d_scalars, const FusedStep& fs, hipStream_t stream)
 {
-    // kXcdParts workgroups per chunk (the plan's chunk limit keeps the grid in range)
-    const dim3 grid((unsigned)(n_chunks * kXcdParts)), block(kBlockMixed), block_pure(kBlockPure);
+    // at most kXcdParts workgroups per chunk (the plan's chunk limit keeps the grid in range)
+    const uint32_t n_shared = (uint32_t)work.n_shared;
+    const dim3 grid((unsigned)work.workgroups()), block(kBlockMixed), block_pure(kBlockPure);
     switch (kernel) {
     case kKernelMixedBf16:
-        hipLaunchKernelGGL((update_kernel<0, FUSED>), grid, block, ADAMW_LDS_MIXED, stream, segs, chunks, d_scalars, fs);
+        hipLaunchKernelGGL((update_kernel<0, FUSED>), grid, block, ADAMW_LDS_MIXED, stream, segs, items, n_shared, d_scalars, fs);
         break;
     case kKernelMixedF16:
-        hipLaunchKernelGGL((update_kernel<1, FUSED>), grid, block, ADAMW_LDS_MIXED, stream, segs, chunks, d_scalars, fs);
+        hipLaunchKernelGGL((update_kernel<1, FUSED>), grid, block, ADAMW_LDS_MIXED, stream, segs, items, n_shared, d_scalars, fs);
         break;
     case kKernelSplit:
         hipLaunchKernelGGL((update_pure_kernel<true, true, kAuxSplit, FUSED>), grid, block_pure, ADAMW_LDS_PURE, stream,
-                           segs, chunks, d_scalars, fs);
+                           segs, items, n_shared, d_scalars, fs);
         break;
 #define ADAMW_PURE_CASE(M, V, K)                                                                          \
     case kKernelPure + (M) * 4 + (V) * 2 + (K):                                                            \
         hipLaunchKernelGGL((update_pure_kernel<M, V, (K) ? kAuxKahan : kAuxNone, FUSED>), grid, block_pure,    \
-                           ADAMW_LDS_PURE, stream, segs, chunks, d_scalars, fs);                           \
+                           ADAMW_LDS_PURE, stream, segs, items, n_shared, d_scalars, fs);                           \
         break;
         ADAMW_PURE_CASE(0, 0, 0) ADAMW_PURE_CASE(0, 0, 1) ADAMW_PURE_CASE(0, 1, 0) ADAMW_PURE_CASE(0, 1, 1)
         ADAMW_PURE_CASE(1, 0, 0) ADAMW_PURE_CASE(1, 0, 1) ADAMW_PURE_CASE(1, 1, 0) ADAMW_PURE_CASE(1, 1, 1)
@@ -773,7 +816,7 @@ static hipError_t launch_update_as(int kernel, const DevSeg* segs, const DevChun
 #define ADAMW_PURE_C32_CASE(M, V)                                                                         \
     case kKernelPureC32 + (M) * 2 + (V):                                                                   \
         hipLaunchKernelGGL((update_pure_kernel<M, V, kAuxKahan32, FUSED>), grid, block_pure,                 \
-                           (M) && (V) ? ADAMW_LDS_C32_WIDE : ADAMW_LDS_PURE, stream, segs, chunks, d_scalars, fs);                           \
+                           (M) && (V) ? ADAMW_LDS_C32_WIDE : ADAMW_LDS_PURE, stream, segs, items, n_shared, d_scalars, fs);                           \
         break;
         ADAMW_PURE_C32_CASE(0, 0) ADAMW_PURE_C32_CASE(0, 1) ADAMW_PURE_C32_CASE(1, 0) ADAMW_PURE_C32_CASE(1, 1)
 #undef ADAMW_PURE_C32_CASE
@@ -783,12 +826,12 @@ static hipError_t launch_update_as(int kernel, const DevSeg* segs, const DevChun
     return hipGetLastError();
 }
 
-hipError_t launch_update(int kernel, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+hipError_t launch_update(int kernel, const DevSeg* segs, const DevChunk* items, const UpdateGrid& grid,
                          const LaunchScalars* d_scalars, const FusedStep* fused, hipStream_t stream)
 {
-    if (n_chunks <= 0) return hipSuccess;
-    if (fused) return launch_update_as<true>(kernel, segs, chunks, n_chunks, nullptr, *fused, stream);
-    return launch_update_as<false>(kernel, segs, chunks, n_chunks, d_scalars, FusedStep{}, stream);
+    if (grid.workgroups() <= 0) return hipSuccess;
+    if (fused) return launch_update_as<true>(kernel, segs, items, grid, nullptr, *fused, stream);
+    return launch_update_as<false>(kernel, segs, items, grid, d_scalars, FusedStep{}, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -42,7 +42,8 @@ struct DeviceScratch {
     unsigned char* ptr = nullptr;      // this device's `scratch` (hipGetSymbolAddress)
     std::vector<int64_t> key;          // the plan whose table the array holds (empty: none)
     bool pinned = false;               // a graph captured a step with that table
-    int64_t n_segs = 0, n_chunks = 0;
+    int64_t n_segs = 0;
+    UpdateGrid grid;
     std::vector<unsigned char> table;  // host image of that table
 };
 
@@ -114,11 +115,12 @@ adamw_status ensure_table(DeviceScratch& ds, const StepKind& kind, const adamw_t
                  (long long)bytes, plan.segs.size(), plan.chunks.size(), (long long)kTableBytes);
         return fail(ADAMW_E_INVALID, buf);
     }
+    const UpdateTable update = update_table(plan);   // no more items than chunks
     ds.key.clear();   // until the copy below is enqueued, the array's table is unknown
     ds.table.resize((size_t)bytes);
     if (bytes) {
         memcpy(ds.table.data(), plan.segs.data(), (size_t)seg_bytes);
-        memcpy(ds.table.data() + seg_bytes, plan.chunks.data(), plan.chunks.size() * sizeof(DevChunk));
+        memcpy(ds.table.data() + seg_bytes, update.items.data(), update.items.size() * sizeof(DevChunk));
         // A copy from pageable host memory: the source has been consumed when
         // the call returns, so the host image may change afterwards.
         hipError_t e = hipMemcpyAsync(ds.ptr + kTableOffset, ds.table.data(), (size_t)bytes, hipMemcpyHostToDevice,
@@ -126,7 +128,7 @@ adamw_status ensure_table(DeviceScratch& ds, const StepKind& kind, const adamw_t
         if (e != hipSuccess) return hip_fail("hipMemcpyAsync (allocation-free chunk table)", e);
     }
     ds.n_segs = (int64_t)plan.segs.size();
-    ds.n_chunks = (int64_t)plan.chunks.size();
+    ds.grid = update.grid;
     ds.key.swap(key);
     return ADAMW_OK;
 }
@@ -167,8 +169,8 @@ extern "C" adamw_status adamw_multi_tensor_step_noalloc(adamw_mode mode, adamw_d
     if ((st = init_device(ds, stream)) != ADAMW_OK) return st;
     if ((st = ensure_table(ds, kind, list, stream)) != ADAMW_OK) return st;
     const DevSeg* segs = reinterpret_cast<const DevSeg*>(ds.ptr + kTableOffset);
-    const DevChunk* chunks = reinterpret_cast<const DevChunk*>(ds.ptr + kTableOffset + ds.n_segs * sizeof(DevSeg));
-    return enqueue_step(kind, segs, chunks, ds.n_chunks, reinterpret_cast<LaunchScalars*>(ds.ptr),
+    const DevChunk* items = reinterpret_cast<const DevChunk*>(ds.ptr + kTableOffset + ds.n_segs * sizeof(DevSeg));
+    return enqueue_step(kind, segs, items, ds.grid, reinterpret_cast<LaunchScalars*>(ds.ptr),
                         reinterpret_cast<uint32_t*>(ds.ptr + kDoneOffset), *hp, d_step, d_found_inf, nullptr, nullptr,
                         ClipRule{}, stream);
 }

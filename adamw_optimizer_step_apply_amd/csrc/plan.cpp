@@ -284,6 +284,43 @@ adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t ch
     return plan_list(streams, list, chunk_elems, max_chunks, true, out, err);
 }
 
+UpdateTable update_table(const Plan& plan)
+{
+    UpdateTable t;
+    std::vector<DevChunk> single;
+    t.items.reserve(plan.chunks.size());
+    const size_t n = plan.chunks.size();
+    const auto vec = [&](size_t i) { return (plan.chunks[i].n_kind & kVecBit) != 0; };
+    const auto joined = [&](size_t i) {   // chunk i continues chunk i - 1
+        return plan.chunks[i].seg == plan.chunks[i - 1].seg &&
+               plan.chunks[i].off == plan.chunks[i - 1].off + (plan.chunks[i - 1].n_kind & kCountMask);
+    };
+    for (size_t i = 0; i < n;) {
+        DevChunk item = plan.chunks[i];
+        uint32_t count = item.n_kind & kCountMask, head = 0;
+        size_t next = i + 1;
+        bool v = vec(i);
+        if (!v && count < (uint32_t)kPack && next < n && vec(next) && joined(next)) {
+            head = count;
+            count += plan.chunks[next].n_kind & kCountMask;
+            v = true;
+            ++next;
+        }
+        if (v && next < n && !vec(next) && joined(next) && (plan.chunks[next].n_kind & kCountMask) < (uint32_t)kPack) {
+            count += plan.chunks[next].n_kind & kCountMask;
+            ++next;
+        }
+        item.n_kind = count | head << kItemHeadShift | (v ? kVecBit : 0u);
+        const bool alone = count <= (v ? kSingleVecElems : kSingleElems);
+        (alone ? single : t.items).push_back(item);
+        i = next;
+    }
+    t.grid.n_shared = (int64_t)t.items.size();
+    t.grid.n_single = (int64_t)single.size();
+    t.items.insert(t.items.end(), single.begin(), single.end());
+    return t;
+}
+
 adamw_status check_disjoint(int esz, const adamw_tensor_list* list, std::string& err)
 {
     // a flat shard buffer holds every element once

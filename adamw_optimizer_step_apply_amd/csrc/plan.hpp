@@ -42,6 +42,16 @@ void mode_esizes(adamw_mode mode, adamw_dtype p_dtype, bool for_check, int esz[k
 adamw_status build_plan(const int esz[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,
                         int64_t max_chunks, Plan* out, std::string& err);
 
+// The update table of a step's plan: each run of element chunk, vector chunks and
+// element chunk of a segment becomes the items of its vector chunks, the ends of the
+// run with the first and the last; the items that kXcdParts workgroups share come
+// first, each kind in plan order.
+struct UpdateTable {
+    std::vector<DevChunk> items;
+    UpdateGrid grid;
+};
+UpdateTable update_table(const Plan& plan);
+
 // The same for a gradient sweep (adamw_grad_norm, adamw_clip_grads) over elements
 // of `esz` bytes: only the gradient stream is looked at, chunks hold up to
 // `chunk_elems` elements plus those before the segment's first 16-byte edge, are

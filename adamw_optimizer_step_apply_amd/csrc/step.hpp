@@ -41,7 +41,7 @@ adamw_status check_step_call(const StepKind& kind, const adamw_tensor_list* list
 // others as the prologue kernel (writing the scalars at `scalars`) and the
 // update kernel.  d_amp / scaler: the dynamic loss scale, or null; clip: the
 // clipping rule, its sumsq null for none.
-adamw_status enqueue_step(const StepKind& kind, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+adamw_status enqueue_step(const StepKind& kind, const DevSeg* segs, const DevChunk* items, const UpdateGrid& grid,
                           LaunchScalars* scalars, uint32_t* done, const adamw_hparams& hp, int32_t* d_step,
                           const int32_t* d_found_inf, adamw_loss_scale_state* d_amp, const adamw_loss_scaler* scaler,
                           const ClipRule& clip, hipStream_t stream);
@@ -79,7 +79,7 @@ private:
 hipError_t launch_prologue(const adamw_hparams& hp, int32_t* d_step, const int32_t* d_found_inf,
                            LaunchScalars* d_scalars, adamw_loss_scale_state* d_amp, const adamw_loss_scaler& scaler,
                            const ClipRule& clip, hipStream_t stream);
-hipError_t launch_update(int kernel, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,
+hipError_t launch_update(int kernel, const DevSeg* segs, const DevChunk* items, const UpdateGrid& grid,
                          const LaunchScalars* d_scalars, const FusedStep* fused, hipStream_t stream);
 hipError_t launch_zero_words(uint32_t* p, int64_t n, hipStream_t stream);
 hipError_t launch_check(adamw_dtype g_dtype, const DevSeg* segs, const DevChunk* chunks, int64_t n_chunks,

@@ -504,7 +504,8 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
                                  const adamw_tensor_list* list, int for_check, uint64_t* out, int64_t cap);
 
 /* Launch form.  A step whose grid has at most max_workgroups workgroups
- * (default 4096: 512 chunks of 16384 elements, about 8.4e6 elements) runs as
+ * (default 4096: 512 chunks of 16384 elements, about 8.4e6 elements, or 4096 tensors
+ * of at most 4096 elements) runs as
  * ONE kernel launch: every workgroup reads *d_found_inf, *d_step and the loss
  * scale itself, forms the step's scalars (the same binary64 formulas, so the
  * same bits), and the last workgroup to finish stores t into *d_step and
@@ -513,17 +514,19 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
  * max_workgroups (one per check chunk) is one launch whose last workgroup
  * stores the flag, instead of a zeroing kernel and the check.  The results are
  * bit-identical either way; the single launch saves a kernel launch and its
- * dependency, which dominate steps of a few million elements.  An update plan
- * of c chunks launches 8c workgroups.  max_workgroups: 0 = always two
+ * dependency, which dominate steps of a few million elements.  A chunk
+ * of an update plan takes 8 workgroups, one of at most 4096 elements (element-wise:
+ * 512) one; the element-wise ends of a tensor go with its vector chunks.  max_workgroups: 0 = always two
  * launches, < 0 = restore the default.  Affects later calls on every stream.
  * Returns the value now in force. */
 int64_t adamw_set_single_launch_max_workgroups(int64_t max_workgroups);
 
 /* Tuning knob: elements per vector chunk, a multiple of 2048 in [2048, 1<<22],
- * for every kernel (an update chunk is shared by 8 workgroups, one per XCD,
- * each lane taking one 8-element pack per 16384 elements; a check chunk is one
- * workgroup's); 0 restores the built-in defaults (16384 for the update kernels
- * and the check).  Affects plans built after the call.  Returns the value now
+ * for every kernel (an update chunk of more than 4096 is shared by 8 workgroups,
+ * one per XCD, each lane taking 8 elements per 16384; a check chunk, or a norm's, is
+ * one workgroup's; a clipping chunk of more than 16 KiB is shared by 8); 0 restores
+ * the built-in defaults (16384 for the update kernels and the check, 32 KiB for the
+ * norms, 128 KiB for clipping).  Affects plans built after the call.  Returns the value now
  * in force (0 = defaults), or -1 if rejected. */
 int64_t adamw_set_chunk_elems(int64_t elems);
 

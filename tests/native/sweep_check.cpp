@@ -1,5 +1,5 @@
-// sweep_check.cpp -- the planner of the gradient sweeps (norms, clipping) under
-// AddressSanitizer and UndefinedBehaviorSanitizer, on the CPU with synthetic (never
+// sweep_check.cpp -- the planner of the gradient sweeps (norms, clipping) and the
+// update kernels' tables under AddressSanitizer and UndefinedBehaviorSanitizer, on the CPU with synthetic (never
 // dereferenced) device addresses.  Built by tests/test_sweep_sanitizers.py with g++
 // together with plan.cpp and validate.cpp; prints "sweep_check ok" and a checksum of
 // every plan (the same with and without the sanitizers), or aborts.
@@ -122,12 +122,77 @@ void one_list(Rng& r)
     mix(overlap);
 }
 
+// The update table of a step's plan: its items cover the plan's chunks once and in
+// order within each of the two kinds, vector parts keep their alignment in every
+// stream, ends of up to 7 elements go with them, and short items are one workgroup's.
+void one_update(Rng& r)
+{
+    int esz[kStreams] = {2, 2, 4, 4, 4};
+    if (r.below(2))
+        for (int s = 2; s < kStreams; ++s) esz[s] = 2;
+    const int64_t nt = 1 + r.below(12);
+    static const int64_t lens[] = {0, 1, 6, 7, 8, 9, 15, 16, 500, 512, 513, 4089, 4096, 4097, 4111, 16384, 16400, 50000};
+    std::vector<int64_t> numel;
+    std::vector<std::vector<void*>> ptr(kStreams);
+    uint64_t at[kStreams];
+    const bool apart = r.below(4) == 0;   // streams that cannot be aligned together
+    const int64_t phase = r.below(8);
+    for (int s = 0; s < kStreams; ++s)
+        at[s] = 0x7f0000000000ull + ((uint64_t)s << 36) + (uint64_t)(apart ? r.below(8) : phase) * esz[s];
+    for (int64_t i = 0; i < nt; ++i) {
+        numel.push_back(lens[r.below(18)]);
+        for (int s = 0; s < kStreams; ++s) {
+            ptr[s].push_back((void*)(uintptr_t)at[s]);
+            at[s] += (uint64_t)numel[i] * esz[s];
+        }
+    }
+    adamw_tensor_list l{};
+    l.n_tensors = nt;
+    l.numel = numel.data();
+    for (int s = 0; s < kStreams; ++s) l.ptr[s] = ptr[s].data();
+    l.shard_end = -1;
+    Plan plan;
+    std::string err;
+    const int64_t chunk = 2048 << r.below(4);
+    CHECK(build_plan(esz, &l, chunk, kMaxUpdateChunks, &plan, err) == ADAMW_OK);
+    const UpdateTable t = update_table(plan);
+    CHECK(t.grid.n_shared + t.grid.n_single == (int64_t)t.items.size() && t.items.size() <= plan.chunks.size());
+    CHECK(t.grid.workgroups() == 8 * t.grid.n_shared + t.grid.n_single);
+    std::vector<std::vector<uint8_t>> seen(plan.segs.size());
+    for (size_t i = 0; i < seen.size(); ++i) seen[i].assign((size_t)plan.info[i].count, 0);
+    int64_t vector_elems = 0, planned_vector = 0;
+    for (const DevChunk& c : plan.chunks)
+        if (c.n_kind & kVecBit) planned_vector += c.n_kind & kCountMask;
+    for (size_t i = 0; i < t.items.size(); ++i) {
+        const DevChunk& it = t.items[i];
+        const bool vec = (it.n_kind & kVecBit) != 0, alone = (int64_t)i >= t.grid.n_shared;
+        const uint32_t n = it.n_kind & kItemCountMask, head = vec ? it.n_kind >> kItemHeadShift & 7u : n;
+        const uint32_t body = vec ? (n - head) / kPack * kPack : 0;
+        CHECK(n > 0 && (!vec || body > 0) && (vec || (it.n_kind >> kItemHeadShift) == 0));
+        CHECK(alone == (n <= (vec ? kSingleVecElems : kSingleElems)));
+        if (i > 0 && (int64_t)i != t.grid.n_shared) {
+            const DevChunk& before = t.items[i - 1];
+            CHECK(before.seg < it.seg || (before.seg == it.seg && before.off < it.off));
+        }
+        for (int s = 0; s < kStreams && vec; ++s) CHECK((plan.segs[it.seg].ptr[s] + (it.off + head) * esz[s]) % 16 == 0);
+        CHECK(it.off + n <= seen[it.seg].size());
+        for (uint32_t k = 0; k < n; ++k) ++seen[it.seg][it.off + k];
+        vector_elems += body;
+        mix(it.off);
+        mix(it.n_kind);
+    }
+    for (const auto& v : seen)
+        for (uint8_t x : v) CHECK(x == 1);
+    CHECK(vector_elems == planned_vector);
+}
+
 }  // namespace
 
 int main()
 {
     Rng r{88172645463325252ull};
     for (int i = 0; i < 3000; ++i) one_list(r);
+    for (int i = 0; i < 2000; ++i) one_update(r);
     // the grid limit, and the arguments of clipping
     int64_t n = 0;
     void* p = (void*)(uintptr_t)0x7f0000000000ull;

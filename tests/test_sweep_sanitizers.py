@@ -1,6 +1,6 @@
-"""The planner of the gradient norms and of clipping under AddressSanitizer and
-UndefinedBehaviorSanitizer (CPU only): tests/native/sweep_check.cpp over 3,000 random
-lists, built with and without the sanitizers; both print the same checksum."""
+"""The planner of the gradient norms and of clipping, and the update kernels' tables,
+under AddressSanitizer and UndefinedBehaviorSanitizer (CPU only):
+tests/native/sweep_check.cpp over 5,000 random lists, built with and without the sanitizers; both print the same checksum."""
 import os
 
 from test_sanitizers import CSRC, NATIVE, ROOT, SAN, _build_and_run
