@@ -236,9 +236,9 @@ __global__ void prologue_kernel(adamw_hparams hp, int32_t* __restrict__ step, co
 // The cache policy of the streaming accesses: every element is touched exactly once
 // per step, so loads and stores are non-temporal (bit 0 = loads, bit 1 = stores).
 // The mixed family's gradient, which is not written back, is loaded plainly: on
-// MI355X (OPT-1.3B list) 84.4 % of peak against 82.4 with non-temporal loads on
-// blocked state, 79.3 against 79.6 per tensor; plain loads of the state streams gave
-// 83.7 and 76.9.  In the pure family, plain loads cost the Kahan step 8 %, and the
+// MI355X (OPT-1.3B list) 85.7 % of peak against 83.1 with non-temporal loads on
+// blocked state, 78.7 against 79.1 per tensor; plain loads of the state streams lost
+// 0.7 and 2.4 points.  In the pure family, plain loads cost the Kahan step 8 %, and the
 // steps with fp32 moments 2-4 points.
 #ifndef ADAMW_NT_MIXED
 #define ADAMW_NT_MIXED 3
@@ -426,12 +426,16 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
             }
             return u32x2{pw[0], pw[1]};
         };
-        // Whole passes without a test, then the last units one by one: with a test before
-        // each unit's accesses the compiler waits for one unit's loads before it issues
-        // the next one's (blocked state: 83.8 % of peak on MI355X at best, 77.9 with some
-        // register assignments, against 86.1).
+        // A wave's whole passes without a test, then its last units one by one: with a test
+        // before each unit's accesses the compiler waits for one unit's loads before it
+        // issues the next one's (blocked state: 83.8 % of peak on MI355X at best, 77.9 with
+        // some register assignments, against 86).  The scheduling barrier keeps every load
+        // ahead of the arithmetic; left to itself the compiler moved one gradient load
+        // behind a wait in some variants (blocked 81 %).  Whole by wave rather than by pass of the
+        // workgroup: 0.2 points blocked, 0.3 to 1.1 per tensor.
+        const uint32_t last = __builtin_amdgcn_readfirstlane(unit_at<kTilePacksMixed, N>(tid | 63u, wk, N - 1));
         uint32_t at = 0;
-        for (; at + pass <= units; at += pass) {
+        for (; at + last < units; at += pass) {
             u32x2 G[N], P[N];
             f32x4 W[N], M[N], V[N];
 #pragma unroll
@@ -442,6 +446,7 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
                 M[h] = ld<NTS>(m4 + k);
                 V[h] = ld<NTS>(v4 + k);
             }
+            __builtin_amdgcn_sched_barrier(0);
             if (at == 0) fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
 #pragma unroll
             for (int h = 0; h < N; ++h) P[h] = update(G[h], W[h], M[h], V[h]);
@@ -454,7 +459,7 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
                 st<NTS>(p2 + k, P[h]);
             }
         }
-        if (at < units) {   // the last units, which do not fill a pass
+        if (at < units) {   // the last units, which do not fill a pass of the wave
             if (at == 0) fused_coef<FUSED>(fs, in, c);
 #pragma unroll
             for (int h = 0; h < N; ++h) {
