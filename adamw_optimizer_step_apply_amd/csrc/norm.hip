@@ -179,8 +179,8 @@ __device__ __forceinline__ bool last_of(double* slot, double x, uint32_t* done, 
     return last != 0;
 }
 
-// Non-temporal loads: 394 us for the OPT-1.3B bf16 gradients in two lists on
-// MI355X, against 412 without.
+// Non-temporal loads: 376 us for the OPT-1.3B bf16 gradients in two lists on
+// MI355X, against 402 without.
 constexpr int kNtNorm = 1;
 // FUSED: the only launch of a small sum, whose last workgroup joins the partials.
 template <int DT, bool FUSED>
@@ -302,8 +302,8 @@ __device__ __forceinline__ void scale1(uint64_t addr, float f)
 }
 
 // Each element is touched once: non-temporal loads and stores.  MI355X, OPT-1.3B
-// bf16 gradients: 788 us, against 859 with non-temporal stores only and 860 without;
-// 52 MB of fp32 whose three copies take turns in the last-level cache: 17.6 against
+// bf16 gradients: 787 us, against 861 with non-temporal stores only and 863 without;
+// 52 MB of fp32 whose three copies take turns in the last-level cache: 17.7 against
 // 16.9 us, one copy alone 15.4 against 17.0.
 constexpr int kNtClip = 3;
 template <int DT>
@@ -340,9 +340,13 @@ __global__ __launch_bounds__(kBlockSweep) void clip_kernel(const DevSweep* __res
 }  // namespace
 
 // Occupancy caps by reserved LDS, as for the update kernels: four 256-lane workgroups
-// per CU.  MI355X, clipping the OPT-1.3B bf16 gradients: 788 us with four, 801 with
-// eight, 842 with two; 2,000 fp32 tensors' norms (580 MB): 89.2 us with four, 91.0 with
-// eight, 92.4 with three, 101 with two.  (The sum's own 32 bytes of LDS count too.)
+// per CU.  MI355X, clipping the OPT-1.3B bf16 gradients: 788 us with four, 789 with
+// three, 804 with eight, 831 with two; norms of 26 MB of fp16: 8.0 us with four, 8.1 with
+// five, 8.8 with three; of 2,000 fp32 tensors (580 MB): 86.7 with four, 87.4 with three, 88.4
+// with eight, 96.0 with two; of 10,000 fp16 tensors: 765 with four, 771 with three, 769 with
+// five.  Three gain on lists of long tensors among other passes (OPT-1.3B bf16 377 -> 365
+// us, 4.3 GB of fp32 609 -> 601) and lose on a pass by itself (the sum's kernel 357 -> 370).
+// (The sum's own 32 bytes of LDS count too.)
 #ifndef ADAMW_LDS_CLIP
 #define ADAMW_LDS_CLIP 40960
 #endif
