@@ -6,6 +6,7 @@ min(1, max_norm / (sqrt(S) * inv + eps)) formed here in binary64, is what the
 clipped step computes: only the last bit of a binary64 square root lies between
 the two multipliers before they are rounded to binary32."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -276,4 +277,59 @@ def test_clipping_in_place_then_the_plain_step():
     a.oracle_step(ho)
     a.compare_all("clip-in-place")
     assert all(same_bits(a.arena.bufs[k], b.arena.bufs[k]) for k in a.keys)
+    free()
+
+
+@pytest.mark.parametrize("mode", ["mixed", "kahan"])
+def test_one_list_with_blocked_state_for_norm_and_step(mode):
+    """The norm and the clipped step on one list whose state is blocked on the padded flat
+    index: the norm looks at the gradients alone."""
+    case = Case(mode, SIZES, seed=311, align_elems=8, random_moments=True)
+    n = range(len(SIZES))
+    state = [[case.arena.view(k, i) for i in n] for k in case.keys[2:]]
+    blocked, mask = A.make_blocked_state(MODE[mode], A.BF16, SIZES, *state)
+    tl = A.TensorList(SIZES, [[case.arena.view(k, i) for i in n] for k in ("p", "g")] + [[blocked], None, None],
+                      flat_mask=mask)
+    s = torch.zeros(1, dtype=torch.float64, device="cuda")
+    for _ in range(2):
+        A.adamw_grad_norm(A.BF16, tl, s)
+        clipped(case, hp_pair()[0], A.GradClip(s, 0.01), tl=tl)
+        case.oracle_step(hp_pair(inv_scale=multiplier(s.item(), 1.0, 0.01, 1e-6)[0])[1])
+    want = math.fsum(float((case.arena.view("g", i).double() ** 2).sum()) for i in n)
+    # each of the two sums is within n * 2^-53 of the exact one
+    assert abs(s.item() - want) <= 2 * sum(SIZES) * 2.0 ** -53 * want
+    A.adamw_blocked_state_copy(MODE[mode], A.BF16, A.TensorList(SIZES, [None, None, *state], flat_mask=A.FLAT_PAD8), blocked,
+                               to_blocked=False)
+    case.compare_all(f"norm-and-step-blocked-{mode}")
+    free()
+
+
+def test_host_threads_each_on_their_stream():
+    """Four host threads, each with lists and a stream of its own, run norm, clipping and step
+    at once; each gets what it gets alone."""
+    def work(k, out):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            case = Case("mixed", [20_000 + 7 * k, 5, 300], seed=320 + k, align_elems=1)
+            s = torch.zeros(1, dtype=torch.float64, device="cuda")
+            st.synchronize()
+            for _ in range(5):
+                A.adamw_grad_norm(A.BF16, grads_of(case), s)
+                A.adamw_clip_grads(A.BF16, grads_of(case), A.GradClip(s, 0.05))
+                clipped(case, hp_pair()[0], A.GradClip(s, 0.03))
+            st.synchronize()
+            out[k] = (case, s.item())
+
+    alone, together = {}, {}
+    for k in range(4):
+        work(k, alone)
+    threads = [threading.Thread(target=work, args=(k, together)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for k in range(4):
+        (a, sa), (b, sb) = alone[k], together[k]
+        assert sa == sb and b.d_step.item() == 5
+        assert all(same_bits(a.arena.bufs[x], b.arena.bufs[x]) for x in a.keys), k
     free()
