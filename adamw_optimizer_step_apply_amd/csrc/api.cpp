@@ -4,8 +4,9 @@
 //   [step:  prologue  -> update kernel]  (adamw_step / adamw_multi_tensor_step[_amp])
 //   small grids (up to a few thousand workgroups): the check kernel alone, the
 //   update kernel alone
-// Nothing here synchronises with the device except when a workspace has to
-// grow (the old buffer may still be read by work queued on its stream).
+// Nothing here synchronises with the device but a new list's table that takes the place
+// of an older one: it waits until that one's own upload has run (its staging buffer is
+// read then), and, where it is larger, for the stream (queued work reads the old table).
 #include <hip/hip_runtime.h>
 #include <stdio.h>
 #include <string.h>
@@ -60,6 +61,7 @@ struct PlanSlot {
     hipEvent_t uploaded = nullptr;
     bool upload_in_flight = false;
     std::vector<int64_t> key;
+    int64_t tag = 0;       // the kind of plan (key[0])
     bool valid = false;
     bool pinned = false;   // used under graph capture: never evicted, resized or rewritten
     int64_t n_segs = 0, n_chunks = 0, n_tensors = 0;
@@ -97,15 +99,12 @@ struct PlanSlot {
     }
 };
 
-// Plans cached per stream, most recently used first: at most this many slots
-// that no captured graph holds, plus every pinned one.  A training loop that
-// alternates a few lists (e.g. two parameter groups, or a step and its
-// overflow check) keeps each one's table resident instead of re-uploading it.
-constexpr size_t kPlansPerStream = 8;
-
 struct StreamWorkspace {
     int device = 0;                     // the stream's device: the workspace lives there
     LaunchScalars* scalars = nullptr;   // device, kWorkspaceBytes: scalars, then the completion counters
+    // Most recently used first.  A training loop that goes through its parameter groups,
+    // each with its norm, clipping, check and step, keeps every table resident instead of
+    // uploading it again (choose_plan_slot).
     std::vector<std::unique_ptr<PlanSlot>> plans;
     std::mutex mu;                      // one call at a time per stream
 };
@@ -198,15 +197,6 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
                     "this list's chunk table is not on the device: make the same call once on this stream "
                     "before capturing it into a graph");
 
-    std::vector<bool> pinned(plans.size());
-    for (size_t i = 0; i < plans.size(); ++i) pinned[i] = plans[i]->pinned;
-    const size_t pick = choose_plan_slot(pinned, kPlansPerStream);
-    if (pick == plans.size()) plans.emplace_back(new PlanSlot());
-    std::rotate(plans.begin(), plans.begin() + (ptrdiff_t)pick, plans.begin() + (ptrdiff_t)pick + 1);
-    PlanSlot& slot = *plans.front();
-    slot.valid = false;
-    *out = &slot;
-
     std::vector<Table> tables;
     std::vector<DevSweep> groups;
     UpdateTable update;
@@ -232,6 +222,16 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     if (tag == kTagNorm)
         dev_bytes = PlanSlot::norm_table_bytes(n_chunks, list->n_tensors) +
                     (size_t)partial_count(n_chunks) * sizeof(double);
+
+    std::vector<SlotInfo> slots(plans.size());
+    for (size_t i = 0; i < plans.size(); ++i) slots[i] = SlotInfo{plans[i]->tag, plans[i]->dev_cap, plans[i]->pinned};
+    const size_t pick = choose_plan_slot(slots, tag, dev_bytes);
+    if (pick == plans.size()) plans.emplace_back(new PlanSlot());
+    std::rotate(plans.begin(), plans.begin() + (ptrdiff_t)pick, plans.begin() + (ptrdiff_t)pick + 1);
+    PlanSlot& slot = *plans.front();
+    slot.valid = false;
+    slot.tag = tag;
+    *out = &slot;
     hipError_t e;
     if (!slot.uploaded) {
         e = hipEventCreateWithFlags(&slot.uploaded, hipEventDisableTiming);
@@ -285,32 +285,22 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
     return ADAMW_OK;
 }
 
-// Keys of the lists validated most recently (full keys, not hashes).  A call
-// whose key is here skips the validation walk, which for a blocked-state list
-// of 10^5-10^6 pieces costs milliseconds of host time per call; a new key is
-// validated before any HIP call.
-constexpr size_t kValidatedKeys = 16;
+// The lists validated most recently.  A call whose key is here skips the validation
+// walk, which for a blocked-state list of 10^5-10^6 pieces costs milliseconds of host
+// time per call; a new key is validated before any HIP call.
 std::mutex g_validated_mu;
-std::vector<std::vector<int64_t>> g_validated;   // most recent first
+ValidatedKeys g_validated;
 
 bool validated_before(const std::vector<int64_t>& key)
 {
     std::lock_guard<std::mutex> lk(g_validated_mu);
-    for (size_t i = 0; i < g_validated.size(); ++i) {
-        if (g_validated[i] == key) {
-            std::rotate(g_validated.begin(), g_validated.begin() + (ptrdiff_t)i,
-                        g_validated.begin() + (ptrdiff_t)i + 1);
-            return true;
-        }
-    }
-    return false;
+    return g_validated.seen(key);
 }
 
 void remember_validated(const std::vector<int64_t>& key)
 {
     std::lock_guard<std::mutex> lk(g_validated_mu);
-    if (g_validated.size() >= kValidatedKeys) g_validated.pop_back();
-    g_validated.insert(g_validated.begin(), key);
+    g_validated.remember(key);
 }
 
 // Validates the list for a plan of `tag` (unless the same key passed before),

@@ -15,6 +15,7 @@
 // segment is cut into element chunks.
 #include "plan.hpp"
 
+#include <stddef.h>
 #include <stdio.h>
 
 #include <algorithm>
@@ -432,6 +433,36 @@ size_t choose_plan_slot(const std::vector<bool>& pinned, size_t cap)
         lru = i;   // the last unpinned slot in MRU order
     }
     return unpinned < cap ? pinned.size() : lru;
+}
+
+size_t choose_plan_slot(const std::vector<SlotInfo>& slots, int64_t tag, size_t bytes)
+{
+    std::vector<bool> taken(slots.size());
+    for (size_t i = 0; i < slots.size(); ++i) {
+        taken[i] = slots[i].pinned || slots[i].tag != tag;
+        if (!slots[i].pinned) bytes += slots[i].bytes;
+    }
+    return choose_plan_slot(taken, bytes <= kPlanBytes ? kPlansMost : kPlansKept);
+}
+
+bool ValidatedKeys::seen(const std::vector<int64_t>& key)
+{
+    for (size_t i = 0; i < keys_.size(); ++i) {
+        if (keys_[i] != key) continue;
+        std::rotate(keys_.begin(), keys_.begin() + (ptrdiff_t)i, keys_.begin() + (ptrdiff_t)i + 1);
+        return true;
+    }
+    return false;
+}
+
+void ValidatedKeys::remember(const std::vector<int64_t>& key)
+{
+    keys_.insert(keys_.begin(), key);
+    words_ += key.size();
+    while (keys_.size() > kKeysKept && (keys_.size() > kKeysMost || words_ > kKeyWords)) {
+        words_ -= keys_.back().size();
+        keys_.pop_back();
+    }
 }
 
 void plan_key(int64_t tag, const int esz[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,

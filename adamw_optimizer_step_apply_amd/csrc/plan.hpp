@@ -3,6 +3,7 @@
 // chunks) and the argument checks made before anything is enqueued.
 #pragma once
 
+#include <stddef.h>
 #include <stdint.h>
 
 #include <string>
@@ -102,6 +103,33 @@ adamw_status check_pure_precision(const adamw_pure_precision* prec, std::string&
 // than `cap` slots are unpinned, else the least recently used unpinned slot.
 // A pinned slot is never chosen.
 size_t choose_plan_slot(const std::vector<bool>& pinned, size_t cap);
+
+// The same for a plan of `tag` whose table takes `bytes` on the device: a list's step,
+// check, norm and clipping have a plan each, and those of one kind are evicted among
+// themselves only.  Of every kind the last kPlansKept lists stay, up to kPlansMost while
+// the stream's unpinned tables take no more than kPlanBytes together.  With 8 slots for
+// all kinds, norm and clipped step over 5 parameter groups (10 plans in turn) found
+// none of their tables again.
+struct SlotInfo {
+    int64_t tag;
+    size_t bytes;
+    bool pinned;
+};
+constexpr size_t kPlansKept = 8, kPlansMost = 32, kPlanBytes = (size_t)64 << 20;
+size_t choose_plan_slot(const std::vector<SlotInfo>& slots, int64_t tag, size_t bytes);
+
+// Full keys (not hashes) of the lists validated most recently, most recent first: the
+// last kKeysKept, up to kKeysMost while they hold no more than kKeyWords words.
+class ValidatedKeys {
+public:
+    bool seen(const std::vector<int64_t>& key);
+    void remember(const std::vector<int64_t>& key);
+
+private:
+    static constexpr size_t kKeysKept = 16, kKeysMost = 128, kKeyWords = (size_t)4 << 20;
+    std::vector<std::vector<int64_t>> keys_;
+    size_t words_ = 0;
+};
 
 // The exact inputs a plan depends on, for caching (`tag` distinguishes kernels).
 void plan_key(int64_t tag, const int esz[kStreams], const adamw_tensor_list* list, int64_t chunk_elems,

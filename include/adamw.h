@@ -69,7 +69,10 @@
  * Ownership and execution.  The caller owns every tensor, d_step, d_found_inf
  * and the stream; the library never frees or reallocates them.  All work is
  * enqueued on hip_stream (a hipStream_t; NULL = the null stream of the calling
- * thread's current device) and the call returns without synchronising.  Every
+ * thread's current device) and the call returns without synchronising, unless a list
+ * whose chunk table is not on the device takes the place of another list's table: the
+ * call then waits until that table's upload, queued by an earlier call, has run, and if
+ * the new table is larger than the old one's buffer, for the work queued on the stream.  Every
  * buffer must live on the stream's device.  The library owns only a small
  * device workspace per (device, stream), on the stream's device, holding the
  * launch scalars, the single-launch completion counters (about 8.7 KB) and the
@@ -84,8 +87,10 @@
  * replayed any number of times.  It uses the capture stream's workspace
  * (launch scalars, completion counters, chunk table, a norm's partial sums).  The chunk table a
  * capture used is pinned: later calls on the stream, with however many other
- * lists, never evict, move or rewrite it (the stream keeps up to 8 unpinned
- * tables besides the pinned ones); pinned tables are freed only by
+ * lists, never evict, move or rewrite it (besides the pinned ones, the stream keeps
+ * the tables of the last 8 lists for each kind of call -- a step of one mode, a check, a
+ * norm, a clipping -- and of the last 32 while all of them take 64 MiB or less); pinned
+ * tables are freed only by
  * adamw_release_workspace(), which therefore must not run while such a graph
  * is in use.  A replay must not overlap other work that uses that workspace:
  * steps enqueued on the capture stream, or replays of other graphs captured on
