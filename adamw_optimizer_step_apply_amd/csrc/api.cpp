@@ -709,7 +709,8 @@ adamw_status adamw_tensor_norms(adamw_dtype g_dtype, const adamw_tensor_list* gr
                                 double* d_tensor_sumsq, double* d_sumsq, void* hip_stream)
 try {
     g_err.clear();
-    if (!d_tensor_norms && !d_tensor_sumsq)
+    // an empty list's arrays of no entries may have no address (a torch tensor's is null)
+    if (!d_tensor_norms && !d_tensor_sumsq && grads && grads->n_tensors > 0)
         return fail(ADAMW_E_INVALID, "d_tensor_norms and d_tensor_sumsq are both null");
     NormOut out{};
     out.sumsq = d_sumsq;

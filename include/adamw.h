@@ -377,7 +377,8 @@ adamw_status adamw_grad_norm(adamw_dtype g_dtype, const adamw_tensor_list* grads
  * pass: entry i of the device arrays of n_tensors entries
  *   d_tensor_sumsq[i] = S_i = the sum of g*g over tensor i's elements inside the
  *                       shard (binary64), d_tensor_norms[i] = sqrt(S_i) (binary32)
- * (either may be null, not both; a tensor with no element in the shard gets 0),
+ * (either may be null, not both unless the list is empty; a tensor with no element in
+ * the shard gets 0),
  * and *d_sumsq = the list's S, the value of adamw_grad_norm bit for bit
  * (nullable).  dtypes, arithmetic and order as adamw_grad_norm. */
 adamw_status adamw_tensor_norms(adamw_dtype g_dtype, const adamw_tensor_list* grads, float* d_tensor_norms,
