@@ -590,30 +590,34 @@ extern "C" {
 adamw_status adamw_multi_tensor_step(adamw_mode mode, adamw_dtype p_dtype, const adamw_tensor_list* list,
                                      const adamw_hparams* hp, int32_t* d_step, const int32_t* d_found_inf,
                                      void* hip_stream)
-{
+try {
     g_err.clear();
     StepKind kind;
     adamw_status st = mode_kind(mode, p_dtype, &kind);
     if (st != ADAMW_OK) return st;
     return do_step(kind, list, hp, d_step, d_found_inf, hip_stream);
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_pure_multi_tensor_step(const adamw_pure_precision* prec, const adamw_tensor_list* list,
                                           const adamw_hparams* hp, int32_t* d_step, const int32_t* d_found_inf,
                                           void* hip_stream)
-{
+try {
     g_err.clear();
     std::string err;
     adamw_status st = check_pure_precision(prec, err);
     if (st != ADAMW_OK) return fail(st, err);
     return do_step(kind_of_pure(*prec), list, hp, d_step, d_found_inf, hip_stream);
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_multi_tensor_step_amp(adamw_mode mode, adamw_dtype p_dtype, const adamw_tensor_list* list,
                                          const adamw_hparams* hp, int32_t* d_step, const int32_t* d_found_inf,
                                          adamw_loss_scale_state* d_scale, const adamw_loss_scaler* scaler,
                                          void* hip_stream)
-{
+try {
     g_err.clear();
     if (!d_found_inf) return fail(ADAMW_E_INVALID, "d_found_inf is required with a dynamic loss scale");
     if (!d_scale || (uintptr_t)d_scale % 4) return fail(ADAMW_E_INVALID, "d_scale is null or not 4-byte aligned");
@@ -622,12 +626,14 @@ adamw_status adamw_multi_tensor_step_amp(adamw_mode mode, adamw_dtype p_dtype, c
     StepKind kind;
     if ((st = mode_kind(mode, p_dtype, &kind)) != ADAMW_OK) return st;
     return do_step(kind, list, hp, d_step, d_found_inf, hip_stream, d_scale, scaler);
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_step(adamw_mode mode, adamw_dtype p_dtype, int64_t n, void* param, const void* grad,
                         void* exp_avg, void* exp_avg_sq, void* aux, const adamw_hparams* hp, int32_t* d_step,
                         const int32_t* d_found_inf, void* hip_stream)
-{
+try {
     g_err.clear();
     if (n < 0) return fail(ADAMW_E_INVALID, "n < 0");
     void* p0 = param;
@@ -658,11 +664,13 @@ adamw_status adamw_step(adamw_mode mode, adamw_dtype p_dtype, int64_t n, void* p
     adamw_status st = mode_kind(mode, p_dtype, &kind);
     if (st != ADAMW_OK) return st;
     return do_step(kind, &list, hp, d_step, d_found_inf, hip_stream);
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_check_finite(adamw_dtype g_dtype, const adamw_tensor_list* grads, int32_t* d_found_inf,
                                 void* hip_stream)
-{
+try {
     g_err.clear();
     std::string err;
     adamw_status st = check_mode(ADAMW_MIXED, g_dtype, true, err);
@@ -688,6 +696,8 @@ adamw_status adamw_check_finite(adamw_dtype g_dtype, const adamw_tensor_list* gr
                                 single_launch(plan->n_chunks), stream);
     if (e != hipSuccess) return hip_fail("check launch", e);
     return ADAMW_OK;
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 adamw_status adamw_grad_norm(adamw_dtype g_dtype, const adamw_tensor_list* grads, int accumulate, double* d_sumsq,
@@ -784,7 +794,7 @@ int adamw_abi_version(void) { return ADAMW_ABI_VERSION; }
 
 int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_tensor_list* list, int for_check,
                            int64_t* out, int64_t cap)
-{
+try {
     g_err.clear();
     Plan plan;
     std::string err;
@@ -810,11 +820,14 @@ int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_ten
     const int64_t n = (int64_t)plan.chunks.size();
     for (int64_t i = 0; i < n && i < cap && out; ++i) inspect_row(plan, (size_t)i, out + 6 * i);
     return n;
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    g_err = e.what();
+    return -1;
 }
 
 int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
                                  const adamw_tensor_list* list, int for_check, uint64_t* out, int64_t cap)
-{
+try {
     g_err.clear();
     std::string err;
     adamw_status st = ADAMW_OK;
@@ -860,11 +873,14 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
         }
     }
     return n;
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    g_err = e.what();
+    return -1;
 }
 
 int64_t adamw_blocked_state_bytes(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
                                   const adamw_tensor_list* list)
-{
+try {
     g_err.clear();
     StepKind kind;
     if (state_kind(mode, p_dtype, prec, &kind) != ADAMW_OK) return -1;
@@ -876,11 +892,14 @@ int64_t adamw_blocked_state_bytes(adamw_mode mode, adamw_dtype p_dtype, const ad
         return -1;
     }
     return cp.blocked_bytes;
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    g_err = e.what();
+    return -1;
 }
 
 adamw_status adamw_blocked_state_copy(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
                                       const adamw_tensor_list* list, void* blocked, int to_blocked, void* hip_stream)
-{
+try {
     g_err.clear();
     StepKind kind;
     adamw_status st = state_kind(mode, p_dtype, prec, &kind);
@@ -919,6 +938,8 @@ adamw_status adamw_blocked_state_copy(adamw_mode mode, adamw_dtype p_dtype, cons
     if (e != hipSuccess) return hip_fail("state copy", e);
     if (e2 != hipSuccess) return hip_fail("hipStreamSynchronize (state copy)", e2);
     return ADAMW_OK;
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
 
 int64_t adamw_set_single_launch_max_workgroups(int64_t max_workgroups)

@@ -18,6 +18,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <exception>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -154,7 +155,7 @@ using namespace adamw;
 extern "C" adamw_status adamw_multi_tensor_step_noalloc(adamw_mode mode, adamw_dtype p_dtype,
                                                         const adamw_tensor_list* list, const adamw_hparams* hp,
                                                         int32_t* d_step, const int32_t* d_found_inf, void* hip_stream)
-{
+try {
     clear_error();
     StepKind kind;
     adamw_status st = mode_kind(mode, p_dtype, &kind);
@@ -173,4 +174,6 @@ extern "C" adamw_status adamw_multi_tensor_step_noalloc(adamw_mode mode, adamw_d
     return enqueue_step(kind, segs, items, ds.grid, reinterpret_cast<LaunchScalars*>(ds.ptr),
                         reinterpret_cast<uint32_t*>(ds.ptr + kDoneOffset), *hp, d_step, d_found_inf, nullptr, nullptr,
                         ClipRule{}, stream);
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
 }
