@@ -129,8 +129,13 @@ __device__ double pow_sq(double b, int64_t t)
 
 // Multiplies the gradients' multiplier by the clipping factor: one rounding of the
 // binary64 product.  Returns false if the step has to be skipped.
+// Callers test clip.sumsq first.  The empty statement keeps the square root and the
+// division behind that test: without it the compiler formed them in every step, clipped or not,
+// ahead of the single launch's data loads: 0.1 to 0.25 us of a plain step of up to 1 M
+// elements (of 5 to 7 us) on MI355X.
 __device__ __forceinline__ bool clip_scale(const ClipRule& clip, double sumsq, float& inv_scale)
 {
+    asm volatile("" : "+s"(sumsq));
     double factor;
     if (!clip_factor(clip, sumsq, inv_scale, factor)) return false;
     inv_scale = (float)((double)inv_scale * factor);
