@@ -263,47 +263,11 @@ constexpr int kCheckUnroll = kCheckChunkMult;
 // which each XCD walks one contiguous run of chunks.
 __device__ __forceinline__ uint32_t chunk_index(uint32_t b, uint32_t nb) { return xcd_chunk(b, nb); }
 
-// What a workgroup of an update kernel does of its item: `part` of `parts`, of the
-// `body` elements from `head` on in units, and of the `edge` elements before and after
-// them one by one.  An item shared by kXcdParts workgroups, consecutive in
-// launch order, has part blockIdx.x % kXcdParts on XCD `part`.
-struct Work {
-    uint64_t off;      // the item's first element in its segment
-    uint32_t seg, part, parts;
-    uint32_t head, body, edge;
-};
-
-__device__ __forceinline__ Work work_of(const DevChunk* items, uint32_t n_shared)
+__device__ __forceinline__ Work work_of(const DevChunk* items, uint32_t n_shared, uint32_t n_single)
 {
-    const uint32_t b = blockIdx.x, shared = n_shared * kXcdParts;
-    const bool alone = b >= shared;
-    const DevChunk it = items[alone ? n_shared + (b - shared) : b / kXcdParts];
-    const uint32_t n = it.n_kind & kItemCountMask;
-    Work w;
-    w.off = it.off;
-    w.seg = it.seg;
-    w.part = alone ? 0 : b % kXcdParts;
-    w.parts = alone ? 1 : kXcdParts;
-    const bool vec = (it.n_kind & kVecBit) != 0;
-    w.head = vec ? it.n_kind >> kItemHeadShift & 7u : n;
-    w.body = vec ? (n - w.head) / kPack * kPack : 0;
-    w.edge = n - w.body;
-    return w;
+    const ItemPart ip = update_item(blockIdx.x, n_shared, n_single);
+    return item_work(items[ip.item], ip);
 }
-
-// Per parts * BLOCK * N units of an item, wave w of a workgroup takes tiles w * N + h
-// (h < N) of its part, a lane one unit of each: access h of lane tid is
-// unit_at(tid, work, h), and every access of a wave is one contiguous stretch of
-// its stream.
-template <int P, int N>
-__device__ __forceinline__ uint32_t unit_at(uint32_t tid, const Work& w, int h)
-{
-    static_assert(P == 64, "a tile is one access of a wave");
-    return tile_pack((tid / P * N + (uint32_t)h) * P + tid % P, w.part, P, w.parts);
-}
-
-// The k-th of the elements outside the vector part.
-__device__ __forceinline__ uint32_t edge_at(const Work& w, uint32_t k) { return k < w.head ? k : k + w.body; }
 
 __device__ __forceinline__ Coef load_coef(const LaunchScalars* sc)
 {
@@ -391,6 +355,7 @@ __device__ __forceinline__ void end_step(const FusedStep& fs, const StepIn& in)
 template <int MODE, bool FUSED>
 __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __restrict__ segs,
                                                         const DevChunk* __restrict__ items, uint32_t n_shared,
+                                                        uint32_t n_single,
                                                         const LaunchScalars* __restrict__ sc, FusedStep fs)
 {
     Coef c{};
@@ -399,7 +364,7 @@ __global__ __launch_bounds__(kBlockMixed) void update_kernel(const DevSeg* __res
     constexpr bool F16 = (MODE == 1);
     constexpr int NTG = ADAMW_NT_MIXED_GRAD, NTS = ADAMW_NT_MIXED;   // gradient; state and param
     constexpr int E = 4, N = kPack / E;   // elements of a unit, units of a lane and pass
-    const Work wk = work_of(items, n_shared);
+    const Work wk = work_of(items, n_shared, n_single);
     const DevSeg& sg = segs[wk.seg];
     const uint64_t off = wk.off;
     const uint32_t tid = threadIdx.x;
@@ -508,7 +473,7 @@ constexpr int kAuxKahan32 = 3; // fp32 Kahan compensation c (the residual kept u
 template <bool M32, bool V32, int AUX, bool FUSED>
 __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* __restrict__ segs,
                                                                             const DevChunk* __restrict__ items,
-                                                                            uint32_t n_shared,
+                                                                            uint32_t n_shared, uint32_t n_single,
                                                                             const LaunchScalars* __restrict__ sc,
                                                                             FusedStep fs)
 {
@@ -521,7 +486,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
     // elements of a unit, 32-bit words of a 16-bit stream's unit, units of a lane and pass
     constexpr int E = M32 || V32 || KAHAN32 ? 4 : kPack, H = E / 2, N = kPack / E;
     constexpr int P = E == 4 ? kTilePacksMixed : kTilePacks;
-    const Work wk = work_of(items, n_shared);
+    const Work wk = work_of(items, n_shared, n_single);
     const DevSeg& sg = segs[wk.seg];
     const uint64_t off = wk.off;
     const uint32_t tid = threadIdx.x;
@@ -776,25 +741,6 @@ hipError_t launch_prologue(const adamw_hparams& hp, int32_t* d_step, const int32
     return hipGetLastError();
 }
 
-// Occupancy cap, per kernel: the update kernels use no LDS, but reserving this much
-// per workgroup leaves room for only 160 KiB / bytes workgroups on a CU: fewer
-// concurrent address streams keep more DRAM rows open.  Two 256-lane workgroups (8
-// waves) for the mixed step and for fp32 moments beside an fp32 compensation buffer
-// (28 and 30 B per element), four for the others.  MI355X, OPT-1.3B list, % of peak
-// with two / four, state per tensor, then blocked: mixed 78.3 / 77.1, 84.2 / 82.0;
-// fp32 moments and compensation 78.5 / 73.9, 81.3 / 80.2; split master 75.6 / 75.5,
-// 76.2 / 77.7; fp32 moments and bf16 compensation 76.0 / 75.5, 77.4 / 77.7; fp32
-// moments alone 77.2 / 78.2, 74.3 / 82.4; bf16 state (Kahan) 73.5 / 76.9, 74.4 / 79.0.
-#ifndef ADAMW_LDS_MIXED
-#define ADAMW_LDS_MIXED 81920
-#endif
-#ifndef ADAMW_LDS_PURE
-#define ADAMW_LDS_PURE 40960
-#endif
-#ifndef ADAMW_LDS_C32_WIDE
-#define ADAMW_LDS_C32_WIDE 81920
-#endif
-
 // Two-launch form (fused == nullptr): the update kernel reads the prologue's
 // scalars at d_scalars.  Single launch: the kernel forms them from *fused.
 template <bool FUSED>
@@ -802,37 +748,30 @@ static hipError_t launch_update_as(int kernel, const DevSeg* segs, const DevChun
                                    const LaunchScalars* d_scalars, const FusedStep& fs, hipStream_t stream)
 {
     // at most kXcdParts workgroups per chunk (the plan's chunk limit keeps the grid in range)
-    const uint32_t n_shared = (uint32_t)work.n_shared;
+    const uint32_t n_shared = (uint32_t)work.n_shared, n_single = (uint32_t)work.n_single;
     const dim3 grid((unsigned)work.workgroups()), block(kBlockMixed), block_pure(kBlockPure);
+    const size_t lds = update_lds(kernel);
+#define ADAMW_UPDATE(KERNEL, BLOCK) \
+    hipLaunchKernelGGL(KERNEL, grid, BLOCK, lds, stream, segs, items, n_shared, n_single, d_scalars, fs)
     switch (kernel) {
-    case kKernelMixedBf16:
-        hipLaunchKernelGGL((update_kernel<0, FUSED>), grid, block, ADAMW_LDS_MIXED, stream, segs, items, n_shared, d_scalars, fs);
-        break;
-    case kKernelMixedF16:
-        hipLaunchKernelGGL((update_kernel<1, FUSED>), grid, block, ADAMW_LDS_MIXED, stream, segs, items, n_shared, d_scalars, fs);
-        break;
-    case kKernelSplit:
-        hipLaunchKernelGGL((update_pure_kernel<true, true, kAuxSplit, FUSED>), grid, block_pure, ADAMW_LDS_PURE, stream,
-                           segs, items, n_shared, d_scalars, fs);
-        break;
-#define ADAMW_PURE_CASE(M, V, K)                                                                          \
-    case kKernelPure + (M) * 4 + (V) * 2 + (K):                                                            \
-        hipLaunchKernelGGL((update_pure_kernel<M, V, (K) ? kAuxKahan : kAuxNone, FUSED>), grid, block_pure,    \
-                           ADAMW_LDS_PURE, stream, segs, items, n_shared, d_scalars, fs);                           \
-        break;
+    case kKernelMixedBf16: ADAMW_UPDATE((update_kernel<0, FUSED>), block); break;
+    case kKernelMixedF16: ADAMW_UPDATE((update_kernel<1, FUSED>), block); break;
+    case kKernelSplit: ADAMW_UPDATE((update_pure_kernel<true, true, kAuxSplit, FUSED>), block_pure); break;
+#define ADAMW_PURE_CASE(M, V, K)                                                                         \
+    case kKernelPure + (M) * 4 + (V) * 2 + (K):                                                          \
+        ADAMW_UPDATE((update_pure_kernel<M, V, (K) ? kAuxKahan : kAuxNone, FUSED>), block_pure); break;
         ADAMW_PURE_CASE(0, 0, 0) ADAMW_PURE_CASE(0, 0, 1) ADAMW_PURE_CASE(0, 1, 0) ADAMW_PURE_CASE(0, 1, 1)
         ADAMW_PURE_CASE(1, 0, 0) ADAMW_PURE_CASE(1, 0, 1) ADAMW_PURE_CASE(1, 1, 0) ADAMW_PURE_CASE(1, 1, 1)
 #undef ADAMW_PURE_CASE
-#define ADAMW_PURE_C32_CASE(M, V)                                                                         \
-    case kKernelPureC32 + (M) * 2 + (V):                                                                   \
-        hipLaunchKernelGGL((update_pure_kernel<M, V, kAuxKahan32, FUSED>), grid, block_pure,                 \
-                           (M) && (V) ? ADAMW_LDS_C32_WIDE : ADAMW_LDS_PURE, stream, segs, items, n_shared, d_scalars, fs);                           \
-        break;
+#define ADAMW_PURE_C32_CASE(M, V)                                                                        \
+    case kKernelPureC32 + (M) * 2 + (V):                                                                 \
+        ADAMW_UPDATE((update_pure_kernel<M, V, kAuxKahan32, FUSED>), block_pure); break;
         ADAMW_PURE_C32_CASE(0, 0) ADAMW_PURE_C32_CASE(0, 1) ADAMW_PURE_C32_CASE(1, 0) ADAMW_PURE_C32_CASE(1, 1)
 #undef ADAMW_PURE_C32_CASE
     default:
         return hipErrorInvalidValue;
     }
+#undef ADAMW_UPDATE
     return hipGetLastError();
 }
 

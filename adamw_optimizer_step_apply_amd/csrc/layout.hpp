@@ -161,6 +161,29 @@ constexpr int kKernelPure = 4;
 constexpr int kKernelKahan = kKernelPure + 1;   // bf16 moments + compensation
 constexpr int kKernelPureC32 = kKernelPure + 8;
 
+// Occupancy cap, per kernel: the update kernels use no LDS, but reserving this much
+// per workgroup leaves room for only 160 KiB / bytes workgroups on a CU: fewer
+// concurrent address streams keep more DRAM rows open.  Two 256-lane workgroups (8
+// waves) for the mixed step and for fp32 moments beside an fp32 compensation buffer
+// (28 and 30 B per element), four for the others.  MI355X, OPT-1.3B list, % of peak
+// with two / four, state per tensor, then blocked: mixed 78.3 / 77.1, 84.2 / 82.0;
+// fp32 moments and compensation 78.5 / 73.9, 81.3 / 80.2; split master 75.6 / 75.5,
+// 76.2 / 77.7; fp32 moments and bf16 compensation 76.0 / 75.5, 77.4 / 77.7; fp32
+// moments alone 77.2 / 78.2, 74.3 / 82.4; bf16 state (Kahan) 73.5 / 76.9, 74.4 / 79.0.
+#ifndef ADAMW_LDS_MIXED
+#define ADAMW_LDS_MIXED 81920
+#endif
+#ifndef ADAMW_LDS_PURE
+#define ADAMW_LDS_PURE 40960
+#endif
+#ifndef ADAMW_LDS_C32_WIDE
+#define ADAMW_LDS_C32_WIDE 81920
+#endif
+constexpr int64_t update_lds(int kernel)
+{
+    return kernel == kKernelMixedBf16 || kernel == kKernelMixedF16 ? ADAMW_LDS_MIXED
+         : kernel == kKernelPureC32 + 3 ? ADAMW_LDS_C32_WIDE : ADAMW_LDS_PURE;
+}
 // One segment: the device address of its element 0 in each stream (0 for a
 // stream the launch does not touch).
 struct alignas(64) DevSeg {
@@ -168,8 +191,9 @@ struct alignas(64) DevSeg {
     uint64_t pad[3];
 };
 
-// One workgroup's work: elements [off, off + count) of segment `seg`;
-// kVecBit in n_kind marks the vector kind.
+// One chunk of a plan: elements [off, off + count) of segment `seg`; kVecBit in n_kind
+// marks the vector kind.  The overflow check's kernel takes the chunks as they are, one
+// workgroup each; the update kernels take items made of them (below).
 struct alignas(16) DevChunk {
     uint32_t seg;
     uint32_t n_kind;
@@ -198,6 +222,50 @@ struct UpdateGrid {
     int64_t n_shared = 0, n_single = 0;
     int64_t workgroups() const { return n_shared * kXcdParts + n_single; }
 };
+
+// The item and part of workgroup b of an update grid.  The items of one workgroup come
+// first: at the end of the grid their latency showed (Kahan step, OPT-125m 1-2 %, BERT 1 %).
+// The workgroups of a shared item follow one another, so that part p of every item runs
+// on XCD (p + n_single) % 8.
+struct ItemPart {
+    uint32_t item, part, parts;
+};
+constexpr ItemPart update_item(uint32_t b, uint32_t n_shared, uint32_t n_single)
+{
+    return b < n_single ? ItemPart{n_shared + b, 0, 1}
+                        : ItemPart{(b - n_single) / kXcdParts, (b - n_single) % kXcdParts, kXcdParts};
+}
+
+// What a workgroup of an update kernel does of its item: `part` of `parts`, of the
+// `body` elements from `head` on in units, and of the `edge` elements before and after
+// them one by one.
+struct Work {
+    uint64_t off;      // the item's first element in its segment
+    uint32_t seg, part, parts;
+    uint32_t head, body, edge;
+};
+constexpr Work item_work(const DevChunk& it, const ItemPart& ip)
+{
+    const uint32_t n = it.n_kind & kItemCountMask;
+    const bool vec = (it.n_kind & kVecBit) != 0;
+    const uint32_t head = vec ? it.n_kind >> kItemHeadShift & 7u : n;
+    const uint32_t body = vec ? (n - head) / kPack * kPack : 0;
+    return Work{it.off, it.seg, ip.part, ip.parts, head, body, n - body};
+}
+
+// Per parts * BLOCK * N units of an item, wave w of a workgroup takes tiles w * N + h
+// (h < N) of its part, a lane one unit of each: access h of lane tid is
+// unit_at(tid, work, h), and every access of a wave is one contiguous stretch of
+// its stream.
+template <int P, int N>
+constexpr uint32_t unit_at(uint32_t tid, const Work& w, int h)
+{
+    static_assert(P == 64, "a tile is one access of a wave");
+    return tile_pack((tid / P * N + (uint32_t)h) * P + tid % P, w.part, P, w.parts);
+}
+
+// The k-th of the elements outside the vector part.
+constexpr uint32_t edge_at(const Work& w, uint32_t k) { return k < w.head ? k : k + w.body; }
 
 // One workgroup's work in a gradient sweep: n elements from address addr, shared by
 // kXcdParts workgroups of which this is number `part`, or its own (kWholeChunk).
