@@ -210,7 +210,7 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
         n_segs = (int64_t)plan.segs.size();
         tables.emplace_back(plan.segs);
         if (tag != kTagCheck) {
-            update = update_table(plan);
+            update = update_table(plan, resident_workgroups((int)tag));
             plan.chunks.swap(update.items);
         }
         n_chunks = (int64_t)plan.chunks.size();

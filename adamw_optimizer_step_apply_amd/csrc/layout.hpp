@@ -184,6 +184,9 @@ constexpr int64_t update_lds(int kernel)
     return kernel == kKernelMixedBf16 || kernel == kKernelMixedF16 ? ADAMW_LDS_MIXED
          : kernel == kKernelPureC32 + 3 ? ADAMW_LDS_C32_WIDE : ADAMW_LDS_PURE;
 }
+// The workgroups of an update kernel that the card holds at once: 256 CUs of 160 KiB.
+constexpr int64_t resident_workgroups(int kernel) { return 256 * (160 * 1024 / update_lds(kernel)); }
+
 // One segment: the device address of its element 0 in each stream (0 for a
 // stream the launch does not touch).
 struct alignas(64) DevSeg {
@@ -218,6 +221,12 @@ constexpr uint32_t kItemCountMask = (1u << kItemHeadShift) - 1;
 #endif
 constexpr uint32_t kSingleVecElems = ADAMW_SINGLE_VEC_ELEMS;
 constexpr uint32_t kSingleElems = 512;
+// A list whose chunks fit on the card all at once with 8 workgroups each
+// (resident_workgroups) is taken as planned instead, every chunk shared: such a step is
+// one latency, and a chunk of 4,096 elements that one workgroup takes alone is two passes of
+// it.  Graph replays of mixed steps, shared / alone: one tensor of 4,096 elements 5.0 /
+// 5.8 us, 64 of them 5.7 / 6.5; beyond, 128 of them 9.0 / 6.7 (Kahan, four workgroups per
+// CU: 128 5.9 / 6.8, 256 9.8 / 7.2).
 struct UpdateGrid {
     int64_t n_shared = 0, n_single = 0;
     int64_t workgroups() const { return n_shared * kXcdParts + n_single; }

@@ -116,7 +116,7 @@ adamw_status ensure_table(DeviceScratch& ds, const StepKind& kind, const adamw_t
                  (long long)bytes, plan.segs.size(), plan.chunks.size(), (long long)kTableBytes);
         return fail(ADAMW_E_INVALID, buf);
     }
-    const UpdateTable update = update_table(plan);   // no more items than chunks
+    const UpdateTable update = update_table(plan, resident_workgroups(kind.kernel));   // no more items than chunks
     ds.key.clear();   // until the copy below is enqueued, the array's table is unknown
     ds.table.resize((size_t)bytes);
     if (bytes) {

@@ -285,9 +285,14 @@ adamw_status build_sweep_plan(int esz, const adamw_tensor_list* list, int64_t ch
     return plan_list(streams, list, chunk_elems, max_chunks, true, out, err);
 }
 
-UpdateTable update_table(const Plan& plan)
+UpdateTable update_table(const Plan& plan, int64_t resident)
 {
     UpdateTable t;
+    if ((int64_t)plan.chunks.size() * kXcdParts <= resident) {
+        t.items = plan.chunks;
+        t.grid.n_shared = (int64_t)t.items.size();
+        return t;
+    }
     std::vector<DevChunk> single;
     t.items.reserve(plan.chunks.size());
     const size_t n = plan.chunks.size();

@@ -46,12 +46,13 @@ adamw_status build_plan(const int esz[kStreams], const adamw_tensor_list* list, 
 // The update table of a step's plan: each run of element chunk, vector chunks and
 // element chunk of a segment becomes the items of its vector chunks, the ends of the
 // run with the first and the last; the items that kXcdParts workgroups share come
-// first, each kind in plan order.
+// first, each kind in plan order.  A plan whose chunks take no more than `resident`
+// workgroups, kXcdParts each, is its own table.
 struct UpdateTable {
     std::vector<DevChunk> items;
     UpdateGrid grid;
 };
-UpdateTable update_table(const Plan& plan);
+UpdateTable update_table(const Plan& plan, int64_t resident = 0);
 
 // The same for a gradient sweep (adamw_grad_norm, adamw_clip_grads) over elements
 // of `esz` bytes: only the gradient stream is looked at, chunks hold up to

@@ -522,7 +522,9 @@ int64_t adamw_plan_inspect_bytes(adamw_mode mode, adamw_dtype p_dtype, const ada
  * bit-identical either way; the single launch saves a kernel launch and its
  * dependency, which dominate steps of a few million elements.  A chunk
  * of an update plan takes 8 workgroups, one of at most 4096 elements (element-wise:
- * 512) one; the element-wise ends of a tensor go with its vector chunks.  max_workgroups: 0 = always two
+ * 512) one; the element-wise ends of a tensor go with its vector chunks.  (A plan of at
+ * most 128 chunks -- 64 in ADAMW_MIXED and with fp32 moments and compensation -- takes 8
+ * for every chunk.)  max_workgroups: 0 = always two
  * launches, < 0 = restore the default.  Affects later calls on every stream.
  * Returns the value now in force. */
 int64_t adamw_set_single_launch_max_workgroups(int64_t max_workgroups);

@@ -141,9 +141,20 @@ void one_list(Rng& r, int it)
     std::string err;
     const int64_t chunk = r.below(3) ? 16384 : 2048 << r.below(6);
     CHECK(build_plan(esz, &l, chunk, kMaxUpdateChunks, &plan, err) == ADAMW_OK);
-    const UpdateTable t = update_table(plan);
-    check_table(plan, t, esz);
-    CHECK(t.items.size() <= plan.chunks.size());
+    const int64_t all = (int64_t)plan.chunks.size() * kXcdParts;
+    for (int64_t resident : {(int64_t)0, (int64_t)512, (int64_t)1024, all, all - 1}) {
+        const UpdateTable t = update_table(plan, resident);
+        check_table(plan, t, esz);
+        CHECK(t.items.size() <= plan.chunks.size());
+        // a list that fits on the card whole is launched as planned, all its chunks shared
+        if (all <= resident) CHECK(t.grid.n_single == 0 && t.items.size() == plan.chunks.size());
+        else
+            for (size_t i = 0; i < t.items.size(); ++i) {
+                const uint32_t n = t.items[i].n_kind & kItemCountMask;
+                const bool vec = (t.items[i].n_kind & kVecBit) != 0;
+                CHECK(((int64_t)i >= t.grid.n_shared) == (n <= (vec ? kSingleVecElems : kSingleElems)));
+            }
+    }
 }
 
 }  // namespace
@@ -152,6 +163,10 @@ int main()
 {
     Rng r{0x2545f4914f6cdd1dull};
     for (int it = 0; it < 240; ++it) one_list(r, it);
+    // the workgroups that the card holds, as the occupancy caps leave them
+    CHECK(resident_workgroups(kKernelMixedBf16) == 512 && resident_workgroups(kKernelMixedF16) == 512);
+    CHECK(resident_workgroups(kKernelKahan) == 1024 && resident_workgroups(kKernelSplit) == 1024);
+    CHECK(resident_workgroups(kKernelPureC32 + 3) == 512 && resident_workgroups(kKernelPureC32) == 1024);
     printf("launch_check ok %016llx\n", (unsigned long long)g_sum);
     return 0;
 }

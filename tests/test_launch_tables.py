@@ -1,6 +1,6 @@
 """The tables that the update kernels receive and the maps from workgroup and lane to
 elements (CPU): tests/native/launch_check.cpp walks every workgroup and lane of 240 random
-lists, built with and without the sanitizers."""
+lists in five launch forms each, built with and without the sanitizers."""
 import os
 
 from test_sanitizers import CSRC, NATIVE, ROOT, SAN, _build_and_run
