@@ -510,123 +510,190 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
         GLOBAL WM* __restrict__ mu = reinterpret_cast<GLOBAL WM*>(m + wk.head);
         GLOBAL WV* __restrict__ vu = reinterpret_cast<GLOBAL WV*>(v + wk.head);
         GLOBAL WC* __restrict__ cu = reinterpret_cast<GLOBAL WC*>(cc + wk.head);
-        for (uint32_t at = 0; at < units; at += pass) {
-            W16 G[N], Pv[N];
-            WM M[N];
-            WV V[N];
-            WC C[N];
-            const auto load = [&](int h, uint32_t k) {
-                G[h] = ld<NT>(gu + k);
-                Pv[h] = ld<NT>(pu + k);
-                M[h] = ld<NT>(mu + k);
-                V[h] = ld<NT>(vu + k);
-                if constexpr (AUX != kAuxNone) C[h] = ld<NT>(cu + k);
-            };
-            // Uniform: no lane is past the item's end.  Here the stores keep a test each: a
-            // straight pass as in the mixed kernel was 0.5-3 points of peak slower.
-            const bool whole = at + pass <= units;
-            if (whole) {
+        const auto update = [&](const W16& G, W16& Pv, WM& M, WV& V, WC& C) {
+            const uint32_t* gw = reinterpret_cast<const uint32_t*>(&G);
+            uint32_t* pw = reinterpret_cast<uint32_t*>(&Pv);
+            uint32_t* cw = reinterpret_cast<uint32_t*>(&C);
+            uint32_t* mw = reinterpret_cast<uint32_t*>(&M);
+            uint32_t* vw = reinterpret_cast<uint32_t*>(&V);
 #pragma unroll
-                for (int h = 0; h < N; ++h) load(h, at + unit_at<P, N>(tid, wk, h));
-            } else {
+            for (int j = 0; j < H; ++j) {
+                const f32x2 gg = widen2<false>(gw[j]);
+                const f32x2 pp = widen2<false>(pw[j]);
+                float ma, mb, va, vb;
+                if constexpr (M32) {
+                    ma = __uint_as_float(mw[2 * j]);
+                    mb = __uint_as_float(mw[2 * j + 1]);
+                } else {
+                    const f32x2 t2 = widen2<false>(mw[j]);
+                    ma = t2.x;
+                    mb = t2.y;
+                }
+                if constexpr (V32) {
+                    va = __uint_as_float(vw[2 * j]);
+                    vb = __uint_as_float(vw[2 * j + 1]);
+                } else {
+                    const f32x2 t2 = widen2<false>(vw[j]);
+                    va = t2.x;
+                    vb = t2.y;
+                }
+                if constexpr (SPLIT) {
+                    float wa = __uint_as_float(join_bits(pw[j] & 0xffffu, cw[j] & 0xffffu));
+                    float wb = __uint_as_float(join_bits(pw[j] >> 16, cw[j] >> 16));
+                    mixed_elem(gg.x, wa, ma, va, c);
+                    mixed_elem(gg.y, wb, mb, vb, c);
+                    uint32_t ra, rb;
+                    const uint32_t pa = split_bits(__float_as_uint(wa), ra);
+                    const uint32_t pb = split_bits(__float_as_uint(wb), rb);
+                    pw[j] = pa | (pb << 16);
+                    cw[j] = ra | (rb << 16);
+                } else if constexpr (KAHAN) {
+                    const f32x2 cf = widen2<false>(cw[j]);
+                    float sa, sb;
+                    const float ta = kahan_sum(gg.x, pp.x, cf.x, ma, va, c, sa);
+                    const float tb = kahan_sum(gg.y, pp.y, cf.y, mb, vb, c, sb);
+                    pw[j] = narrow2<false>(ta, tb);
+                    const f32x2 pn = widen2<false>(pw[j]);
+                    cw[j] = narrow2<false>(sa - (pn.x - pp.x), sb - (pn.y - pp.y));
+                } else if constexpr (KAHAN32) {
+                    float sa, sb;
+                    const float ta = kahan_sum(gg.x, pp.x, __uint_as_float(cw[2 * j]), ma, va, c, sa);
+                    const float tb = kahan_sum(gg.y, pp.y, __uint_as_float(cw[2 * j + 1]), mb, vb, c, sb);
+                    pw[j] = narrow2<false>(ta, tb);
+                    const f32x2 pn = widen2<false>(pw[j]);
+                    cw[2 * j] = __float_as_uint(sa - (pn.x - pp.x));
+                    cw[2 * j + 1] = __float_as_uint(sb - (pn.y - pp.y));
+                } else {
+                    float wa = pp.x, wb = pp.y;
+                    mixed_elem(gg.x, wa, ma, va, c);
+                    mixed_elem(gg.y, wb, mb, vb, c);
+                    pw[j] = narrow2<false>(wa, wb);
+                }
+                if constexpr (M32) {
+                    mw[2 * j] = __float_as_uint(ma);
+                    mw[2 * j + 1] = __float_as_uint(mb);
+                } else {
+                    mw[j] = narrow2<false>(ma, mb);
+                }
+                if constexpr (V32) {
+                    vw[2 * j] = __float_as_uint(va);
+                    vw[2 * j + 1] = __float_as_uint(vb);
+                } else {
+                    vw[j] = narrow2<false>(va, vb);
+                }
+            }
+        };
+        const auto load = [&](uint32_t k, W16& G, W16& Pv, WM& M, WV& V, WC& C) {
+            G = ld<NT>(gu + k);
+            Pv = ld<NT>(pu + k);
+            M = ld<NT>(mu + k);
+            V = ld<NT>(vu + k);
+            if constexpr (AUX != kAuxNone) C = ld<NT>(cu + k);
+            else C = WC(0u);
+        };
+        const auto store = [&](uint32_t k, const W16& Pv, const WM& M, const WV& V, const WC& C) {
+            st<NT>(pu + k, Pv);
+            st<NT>(mu + k, M);
+            st<NT>(vu + k, V);
+            if constexpr (AUX != kAuxNone) st<NT>(cu + k, C);
+        };
+        if constexpr (N == 1) {
+            // One unit per lane and pass, lane by lane.  With the tests of the wide mixes below,
+            // a Kahan step of 1 M elements took 6.9 us instead of 6.8, of OPT-125m per
+            // tensor 371 instead of 365.
+            for (uint32_t k = unit_at<P, 1>(tid, wk, 0); k < units; k += pass) {
+                W16 G[N], Pv[N];
+                WM M[N];
+                WV V[N];
+                WC C[N];
+                load(k, G[0], Pv[0], M[0], V[0], C[0]);
+                fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
+                update(G[0], Pv[0], M[0], V[0], C[0]);
+                store(k, Pv[0], M[0], V[0], C[0]);
+            }
+        } else if constexpr (FUSED) {
+            // A wave's whole passes without a test, as in the mixed kernel: a single launch is
+            // short of time, not of bandwidth (split step, 4,096 elements 5.4 -> 5.0 us,
+            // 1 M 7.8 -> 7.5; fp32 moments and bf16 compensation 1 M 7.05 -> 6.65).
+            const uint32_t last = __builtin_amdgcn_readfirstlane(unit_at<P, N>(tid | 63u, wk, N - 1));
+            uint32_t at = 0;
+            for (; at + last < units; at += pass) {
+                W16 G[N], Pv[N];
+                WM M[N];
+                WV V[N];
+                WC C[N];
+#pragma unroll
+                for (int h = 0; h < N; ++h) load(at + unit_at<P, N>(tid, wk, h), G[h], Pv[h], M[h], V[h], C[h]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (at == 0) fused_coef<FUSED>(fs, in, c);
+#pragma unroll
+                for (int h = 0; h < N; ++h) update(G[h], Pv[h], M[h], V[h], C[h]);
+#pragma unroll
+                for (int h = 0; h < N; ++h) store(at + unit_at<P, N>(tid, wk, h), Pv[h], M[h], V[h], C[h]);
+            }
+            if (at < units) {   // the last units, which do not fill a pass of the wave
+                if (at == 0) fused_coef<FUSED>(fs, in, c);
 #pragma unroll
                 for (int h = 0; h < N; ++h) {
                     const uint32_t k = at + unit_at<P, N>(tid, wk, h);
-                    G[h] = Pv[h] = W16(0u);
-                    M[h] = WM(0u);
-                    V[h] = WV(0u);
-                    C[h] = WC(0u);
-                    if (k < units) load(h, k);
+                    if (k >= units) continue;
+                    W16 G, Pv;
+                    WM M;
+                    WV V;
+                    WC C;
+                    load(k, G, Pv, M, V, C);
+                    update(G, Pv, M, V, C);
+                    store(k, Pv, M, V, C);
                 }
             }
-            if (at == 0) fused_coef<FUSED>(fs, in, c);   // while the loads are in flight
+        } else {
+            for (uint32_t at = 0; at < units; at += pass) {
+                W16 G[N], Pv[N];
+                WM M[N];
+                WV V[N];
+                WC C[N];
+                const auto load_unit = [&](int h, uint32_t k) {
+                    G[h] = ld<NT>(gu + k);
+                    Pv[h] = ld<NT>(pu + k);
+                    M[h] = ld<NT>(mu + k);
+                    V[h] = ld<NT>(vu + k);
+                    if constexpr (AUX != kAuxNone) C[h] = ld<NT>(cu + k);
+                };
+                // Uniform: no lane is past the item's end.  Here the stores keep a test each: a
+                // straight pass as in the mixed kernel was 0.5-3 points of peak slower.
+                const bool whole = at + pass <= units;
+                if (whole) {
 #pragma unroll
-            for (int h = 0; h < N; ++h) {
-                const uint32_t* gw = reinterpret_cast<const uint32_t*>(&G[h]);
-                uint32_t* pw = reinterpret_cast<uint32_t*>(&Pv[h]);
-                uint32_t* cw = reinterpret_cast<uint32_t*>(&C[h]);
-                uint32_t* mw = reinterpret_cast<uint32_t*>(&M[h]);
-                uint32_t* vw = reinterpret_cast<uint32_t*>(&V[h]);
+                    for (int h = 0; h < N; ++h) load_unit(h, at + unit_at<P, N>(tid, wk, h));
+                } else {
 #pragma unroll
-                for (int j = 0; j < H; ++j) {
-                    const f32x2 gg = widen2<false>(gw[j]);
-                    const f32x2 pp = widen2<false>(pw[j]);
-                    float ma, mb, va, vb;
-                    if constexpr (M32) {
-                        ma = __uint_as_float(mw[2 * j]);
-                        mb = __uint_as_float(mw[2 * j + 1]);
-                    } else {
-                        const f32x2 t2 = widen2<false>(mw[j]);
-                        ma = t2.x;
-                        mb = t2.y;
-                    }
-                    if constexpr (V32) {
-                        va = __uint_as_float(vw[2 * j]);
-                        vb = __uint_as_float(vw[2 * j + 1]);
-                    } else {
-                        const f32x2 t2 = widen2<false>(vw[j]);
-                        va = t2.x;
-                        vb = t2.y;
-                    }
-                    if constexpr (SPLIT) {
-                        float wa = __uint_as_float(join_bits(pw[j] & 0xffffu, cw[j] & 0xffffu));
-                        float wb = __uint_as_float(join_bits(pw[j] >> 16, cw[j] >> 16));
-                        mixed_elem(gg.x, wa, ma, va, c);
-                        mixed_elem(gg.y, wb, mb, vb, c);
-                        uint32_t ra, rb;
-                        const uint32_t pa = split_bits(__float_as_uint(wa), ra);
-                        const uint32_t pb = split_bits(__float_as_uint(wb), rb);
-                        pw[j] = pa | (pb << 16);
-                        cw[j] = ra | (rb << 16);
-                    } else if constexpr (KAHAN) {
-                        const f32x2 cf = widen2<false>(cw[j]);
-                        float sa, sb;
-                        const float ta = kahan_sum(gg.x, pp.x, cf.x, ma, va, c, sa);
-                        const float tb = kahan_sum(gg.y, pp.y, cf.y, mb, vb, c, sb);
-                        pw[j] = narrow2<false>(ta, tb);
-                        const f32x2 pn = widen2<false>(pw[j]);
-                        cw[j] = narrow2<false>(sa - (pn.x - pp.x), sb - (pn.y - pp.y));
-                    } else if constexpr (KAHAN32) {
-                        float sa, sb;
-                        const float ta = kahan_sum(gg.x, pp.x, __uint_as_float(cw[2 * j]), ma, va, c, sa);
-                        const float tb = kahan_sum(gg.y, pp.y, __uint_as_float(cw[2 * j + 1]), mb, vb, c, sb);
-                        pw[j] = narrow2<false>(ta, tb);
-                        const f32x2 pn = widen2<false>(pw[j]);
-                        cw[2 * j] = __float_as_uint(sa - (pn.x - pp.x));
-                        cw[2 * j + 1] = __float_as_uint(sb - (pn.y - pp.y));
-                    } else {
-                        float wa = pp.x, wb = pp.y;
-                        mixed_elem(gg.x, wa, ma, va, c);
-                        mixed_elem(gg.y, wb, mb, vb, c);
-                        pw[j] = narrow2<false>(wa, wb);
-                    }
-                    if constexpr (M32) {
-                        mw[2 * j] = __float_as_uint(ma);
-                        mw[2 * j + 1] = __float_as_uint(mb);
-                    } else {
-                        mw[j] = narrow2<false>(ma, mb);
-                    }
-                    if constexpr (V32) {
-                        vw[2 * j] = __float_as_uint(va);
-                        vw[2 * j + 1] = __float_as_uint(vb);
-                    } else {
-                        vw[j] = narrow2<false>(va, vb);
+                    for (int h = 0; h < N; ++h) {
+                        const uint32_t k = at + unit_at<P, N>(tid, wk, h);
+                        G[h] = Pv[h] = W16(0u);
+                        M[h] = WM(0u);
+                        V[h] = WV(0u);
+                        C[h] = WC(0u);
+                        if (k < units) load_unit(h, k);
                     }
                 }
-            }
 #pragma unroll
-            for (int h = 0; h < N; ++h) {
-                const uint32_t k = at + unit_at<P, N>(tid, wk, h);
-                if (!whole && k >= units) continue;
-                st<NT>(pu + k, Pv[h]);
-                st<NT>(mu + k, M[h]);
-                st<NT>(vu + k, V[h]);
-                if constexpr (AUX != kAuxNone) st<NT>(cu + k, C[h]);
+                for (int h = 0; h < N; ++h) update(G[h], Pv[h], M[h], V[h], C[h]);
+#pragma unroll
+                for (int h = 0; h < N; ++h) {
+                    const uint32_t k = at + unit_at<P, N>(tid, wk, h);
+                    if (!whole && k >= units) continue;
+                    st<NT>(pu + k, Pv[h]);
+                    st<NT>(mu + k, M[h]);
+                    st<NT>(vu + k, V[h]);
+                    if constexpr (AUX != kAuxNone) st<NT>(cu + k, C[h]);
+                }
             }
         }
     }
     if (wk.edge) {
-        if (wk.body == 0) fused_coef<FUSED>(fs, in, c);
+        // where the lanes that take the ends (up to 14, the first of part 0) may have had no
+        // unit to form the scalars at, they do it here
+        if (wk.body < (N == 1 ? 16u * kPack : 1u)) fused_coef<FUSED>(fs, in, c);
         for (uint32_t e = wk.part * kBlockPure + tid; e < wk.edge; e += wk.parts * kBlockPure) {
             const uint32_t i = edge_at(wk, e);
             const float pf = widen1<false>(p[i]);

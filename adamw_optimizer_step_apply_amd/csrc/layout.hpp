@@ -234,15 +234,14 @@ struct UpdateGrid {
 
 // The item and part of workgroup b of an update grid.  The items of one workgroup come
 // first: at the end of the grid their latency showed (Kahan step, OPT-125m 1-2 %, BERT 1 %).
-// The workgroups of a shared item follow one another, so that part p of every item runs
-// on XCD (p + n_single) % 8.
+// The 8 workgroups of a shared item follow one another, in the order that puts part p on
+// XCD p.
 struct ItemPart {
     uint32_t item, part, parts;
 };
 constexpr ItemPart update_item(uint32_t b, uint32_t n_shared, uint32_t n_single)
 {
-    return b < n_single ? ItemPart{n_shared + b, 0, 1}
-                        : ItemPart{(b - n_single) / kXcdParts, (b - n_single) % kXcdParts, kXcdParts};
+    return b < n_single ? ItemPart{n_shared + b, 0, 1} : ItemPart{(b - n_single) / kXcdParts, b % kXcdParts, kXcdParts};
 }
 
 // What a workgroup of an update kernel does of its item: `part` of `parts`, of the

@@ -75,7 +75,7 @@ void check_table(const Plan& plan, const UpdateTable& t, const int esz[kStreams]
         const ItemPart ip = update_item(b, n_shared, n_single);
         CHECK(ip.item < t.items.size() && ip.part < ip.parts);
         CHECK((ip.parts == 1) == (b < n_single));                       // one workgroup's items run first
-        if (ip.parts > 1) CHECK((ip.part + n_single) % 8 == b % 8);     // a part's XCD is the same for every item
+        if (ip.parts > 1) CHECK(ip.part == b % 8);                      // part p runs on XCD p
         CHECK(!(parts_seen[ip.item] >> ip.part & 1u));
         parts_seen[ip.item] |= 1u << ip.part;
         const Work w = item_work(t.items[ip.item], ip);
