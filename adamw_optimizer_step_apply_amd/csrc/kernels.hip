@@ -244,7 +244,12 @@ __global__ void prologue_kernel(adamw_hparams hp, int32_t* __restrict__ step, co
 // MI355X (OPT-1.3B list) 85.7 % of peak against 83.1 with non-temporal loads on
 // blocked state, 78.7 against 79.1 per tensor; plain loads of the state streams lost
 // 0.7 and 2.4 points.  In the pure family, plain loads cost the Kahan step 8 %, and the
-// steps with fp32 moments 2-4 points.
+// steps with an fp32 stream 2-12 points; there too the gradient alone is loaded plainly
+// where a stream is fp32.  Non-temporal / plain gradient, per tensor and blocked: split
+// master, BERT 222 / 212 and 215 / 207 us, OPT-1.3B 5,528 / 5,541 and 5,369 / 5,315, 10,000
+// ragged tensors 12,363 / 12,402 and 12,449 / 12,164; bf16 moments with fp32
+// compensation, OPT-125m 453 / 427 and 433 / 415, ragged 10,544 / 10,510 and 10,625 /
+// 10,021.
 #ifndef ADAMW_NT_MIXED
 #define ADAMW_NT_MIXED 3
 #endif
@@ -486,6 +491,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
     // elements of a unit, 32-bit words of a 16-bit stream's unit, units of a lane and pass
     constexpr int E = M32 || V32 || KAHAN32 ? 4 : kPack, H = E / 2, N = kPack / E;
     constexpr int P = E == 4 ? kTilePacksMixed : kTilePacks;
+    constexpr int NTG = E == 4 ? ADAMW_NT_MIXED_GRAD : NT;   // the gradient
     const Work wk = work_of(items, n_shared, n_single);
     const DevSeg& sg = segs[wk.seg];
     const uint64_t off = wk.off;
@@ -584,7 +590,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
             }
         };
         const auto load = [&](uint32_t k, W16& G, W16& Pv, WM& M, WV& V, WC& C) {
-            G = ld<NT>(gu + k);
+            G = ld<NTG>(gu + k);
             Pv = ld<NT>(pu + k);
             M = ld<NT>(mu + k);
             V = ld<NT>(vu + k);
@@ -653,7 +659,7 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
                 WV V[N];
                 WC C[N];
                 const auto load_unit = [&](int h, uint32_t k) {
-                    G[h] = ld<NT>(gu + k);
+                    G[h] = ld<NTG>(gu + k);
                     Pv[h] = ld<NT>(pu + k);
                     M[h] = ld<NT>(mu + k);
                     V[h] = ld<NT>(vu + k);
