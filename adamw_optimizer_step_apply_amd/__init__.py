@@ -442,11 +442,12 @@ def adamw_plan_inspect(mode: int, p_dtype: int, tensors: TensorList, for_check: 
     return [tuple(buf[6 * i:6 * i + 6]) for i in range(n)]
 
 
-def adamw_plan_inspect_bytes(mode: int, p_dtype: int, tensors: TensorList, for_check: bool = False,
+def adamw_plan_inspect_bytes(mode: int, p_dtype: int, tensors: TensorList, for_check: int = False,
                              prec: "PurePrecision" = None):
     """The chunk plan with the device bytes of every chunk: (rows, ranges), rows
     an int64 array (chunks, 6) of adamw_plan_inspect's fields, ranges a uint64
-    array (chunks, 5, 2) of [lo, hi) per stream, (0, 0) for an untouched stream."""
+    array (chunks, 5, 2) of [lo, hi) per stream, (0, 0) for an untouched stream;
+    ``for_check`` 4: the items of the step's launch table instead of its plan's chunks."""
     import numpy as np
     pc = ctypes.byref(prec.c()) if prec is not None else None
     n = _lib.adamw_plan_inspect_bytes(mode, p_dtype, pc, ctypes.byref(tensors.c), int(for_check), None, 0)

@@ -384,6 +384,9 @@ int64_t sweep_chunk_elems(int64_t tag, int esz)
     return c ? c : (tag == kTagClip ? kClipChunkBytes : kNormChunkBytes) / esz;
 }
 
+// for_check of the introspection: a step's launch table instead of its plan.
+constexpr int kInspectLaunch = 4;
+
 // The sweep that an introspection call asks for, or 0.
 int64_t sweep_tag(int for_check) { return for_check == 2 ? kTagNorm : for_check == 3 ? kTagClip : 0; }
 
@@ -796,6 +799,10 @@ int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_ten
                            int64_t* out, int64_t cap)
 try {
     g_err.clear();
+    if (for_check == kInspectLaunch) {
+        g_err = "for_check 4 is adamw_plan_inspect_bytes's";
+        return -1;
+    }
     Plan plan;
     std::string err;
     adamw_status st;
@@ -834,9 +841,10 @@ try {
     StepKind kind{};
     int64_t chunk = 0, max_chunks = kMaxUpdateChunks;
     const int64_t sweep = sweep_tag(for_check);
+    const bool launch = for_check == kInspectLaunch;
     if (sweep) {
         st = check_sweep_dtype(p_dtype, &kind.esz[ADAMW_STREAM_GRAD], err);
-    } else if (for_check) {
+    } else if (for_check && !launch) {
         st = check_mode(mode, p_dtype, true, err);
         mode_esizes(mode, p_dtype, true, kind.esz);
         chunk = check_chunk_elems();
@@ -848,7 +856,7 @@ try {
         st = check_mode(mode, p_dtype, false, err);
         if (st == ADAMW_OK) kind = kind_of_mode(mode, p_dtype);
     }
-    if (st == ADAMW_OK && !for_check) chunk = chunk_elems_of(kind.kernel);
+    if (st == ADAMW_OK && (!for_check || launch)) chunk = chunk_elems_of(kind.kernel);
     Plan plan;
     if (st == ADAMW_OK && sweep) {
         const int esz = kind.esz[ADAMW_STREAM_GRAD];
@@ -860,11 +868,26 @@ try {
         g_err = err;
         return -1;
     }
+    // a step's items in the chunks' place, their ends and sharing in the kind
+    std::vector<int64_t> kinds;
+    if (launch) {
+        UpdateTable table = update_table(plan, resident_workgroups(kind.kernel));
+        plan.chunks.swap(table.items);
+        kinds.reserve(plan.chunks.size());
+        for (size_t i = 0; i < plan.chunks.size(); ++i) {
+            DevChunk& c = plan.chunks[i];
+            const Work w = item_work(c, ItemPart{0, 0, 1});
+            const int64_t parts = (int64_t)i < table.grid.n_shared ? kXcdParts : 1;
+            kinds.push_back(w.body ? 1 + ((int64_t)w.head << 4) + (parts << 8) : parts << 8);
+            c.n_kind = (w.body + w.edge) | (w.body ? kVecBit : 0u);
+        }
+    }
     const int64_t n = (int64_t)plan.chunks.size();
     constexpr int64_t kRow = 6 + 2 * kStreams;
     for (int64_t i = 0; i < n && i < cap && out; ++i) {
         uint64_t* r = out + kRow * i;
         inspect_row(plan, (size_t)i, reinterpret_cast<int64_t*>(r));
+        if (launch) r[3] = (uint64_t)kinds[(size_t)i];
         uint64_t lo[kStreams], hi[kStreams];
         chunk_bytes(plan, (size_t)i, kind.esz, lo, hi);
         for (int s = 0; s < kStreams; ++s) {

@@ -483,11 +483,11 @@ adamw_status adamw_blocked_state_copy(adamw_mode mode, adamw_dtype p_dtype, cons
                                       const adamw_tensor_list* list, void* blocked, int to_blocked, void* hip_stream);
 
 /* Planner introspection, for tests: no GPU work, no HIP call.  Builds the
- * chunk plan that adamw_multi_tensor_step (for_check = 0),
+ * chunk plan of adamw_multi_tensor_step (for_check = 0),
  * adamw_check_finite (for_check = 1), adamw_grad_norm and adamw_tensor_norms
- * (for_check = 2), or adamw_clip_grads (3; both with g_dtype = p_dtype, mode ignored)
- * would launch, and writes up to
- * cap rows of 6 int64 each to out:
+ * (for_check = 2), or adamw_clip_grads (3; both with g_dtype = p_dtype, mode ignored),
+ * and writes up to cap rows of 6 int64 each to out (a step's workgroups take items made
+ * of these chunks, see adamw_plan_inspect_bytes; the other calls' take the chunks):
  *   {tensor index, element offset inside the tensor, element count,
  *    kind (0 = element-wise, 1 = 16-byte vector, 2 = any elements, whose 16-byte
  *    words the workgroup finds), flat position, segment}.
@@ -502,7 +502,11 @@ int64_t adamw_plan_inspect(adamw_mode mode, adamw_dtype p_dtype, const adamw_ten
  * p_dtype ignored), or with for_check the pass over the gradients of
  * adamw_plan_inspect's for_check (g_dtype = p_dtype), writes up to cap rows of 16 uint64 to out:
  *   {the 6 fields of an adamw_plan_inspect row, lo[0], hi[0], ..., lo[4], hi[4]}
- * where [lo[s], hi[s]) is the address range of stream s that the chunk's
+ * With for_check = 4 (this call only) a row is an item of the step's launch table, in the
+ * table's order: one or several neighbouring chunks, its kind 256 * the workgroups that
+ * share it + 16 * the elements before its vector part + 1, or 256 * the workgroups for an
+ * item without a vector part.
+ * [lo[s], hi[s]) is the address range of stream s that the chunk's (item's)
  * workgroups read and write (lo = hi = 0 for a stream the launch does not
  * touch; a blocked state buffer shows as streams 2-4 at their places inside
  * the blocks).  Returns the number of chunks, or -1 on an invalid argument. */
