@@ -94,10 +94,13 @@ __device__ __forceinline__ void st(GLOBAL T* p, T v)
 // second level, and the one completing that rearms it and returns true.
 // Spreading the count over separate 256-byte lines keeps the same-address
 // atomics, which the memory side serialises, to about nb / kDoneLanes +
-// kDoneLanes per launch.  The counts order nothing but reads that every wave
-// has consumed before the workgroup's barrier, so the atomics are relaxed:
-// acquire-release ones at device scope would write back and invalidate the
-// XCD's L2 in every workgroup.
+// kDoneLanes per launch.  The atomics are relaxed: acquire-release ones at device scope
+// would write back and invalidate the XCD's L2 in every workgroup.  So a count by
+// itself orders only reads that every wave has consumed before the workgroup's barrier (an update's
+// counter and loss scale).  A workgroup that hands a value over stores it at agent scope
+// from the lane that counts, and that lane waits for the store (vmcnt 0) before it
+// counts; the last workgroup loads such values at agent scope after its barrier
+// (last_of and join in norm.hip).
 struct DoneLane {
     uint32_t lanes, j, in_lane;
 };
