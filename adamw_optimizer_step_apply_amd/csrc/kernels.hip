@@ -604,9 +604,10 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
             if constexpr (AUX != kAuxNone) st<NT>(cu + k, C);
         };
         if constexpr (N == 1) {
-            // One unit per lane and pass, lane by lane.  With the tests of the wide mixes below,
-            // a Kahan step of 1 M elements took 6.9 us instead of 6.8, of OPT-125m per
-            // tensor 371 instead of 365.
+            // One unit per lane and pass, lane by lane.  With the tests of the wide mixes below /
+            // so: Kahan steps of 1 M elements 7.0 / 6.9 us, 128 tensors of 4,096 6.8 / 6.0, BERT
+            // blocked 147.8 / 146.7, OPT-1.3B 3,664 / 3,670 blocked and 4,062 / 4,070 per tensor;
+            // bf16 moments without compensation, OPT-1.3B blocked, 2,822 / 2,854.
             for (uint32_t k = unit_at<P, 1>(tid, wk, 0); k < units; k += pass) {
                 W16 G[N], Pv[N];
                 WM M[N];
@@ -619,8 +620,8 @@ __global__ __launch_bounds__(kBlockPure) void update_pure_kernel(const DevSeg* _
             }
         } else if constexpr (FUSED) {
             // A wave's whole passes without a test, as in the mixed kernel: a single launch is
-            // short of time, not of bandwidth (split step, 4,096 elements 5.4 -> 5.0 us,
-            // 1 M 7.8 -> 7.5; fp32 moments and bf16 compensation 1 M 7.05 -> 6.65).
+            // short of time, not of bandwidth (split step, 4,096 elements 5.4 -> 5.2 us,
+            // 1 M 7.9 -> 7.65; fp32 moments and bf16 compensation 1 M 7.1 -> 6.8).
             const uint32_t last = __builtin_amdgcn_readfirstlane(unit_at<P, N>(tid | 63u, wk, N - 1));
             uint32_t at = 0;
             for (; at + last < units; at += pass) {
