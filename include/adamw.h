@@ -266,7 +266,9 @@ adamw_status adamw_multi_tensor_step(adamw_mode mode, adamw_dtype p_dtype, const
  * such a graph may still be replayed.  Every call on a GPU shares that GPU's
  * array and its contents: calls on one GPU that may overlap (on different
  * streams, or from host threads without an order between them) race on it and
- * must be ordered by the caller, e.g. by issuing them on one stream. */
+ * must be ordered by the caller, e.g. by issuing them on one stream.  It has no
+ * clipped form: adamw_clip_grads before it clips the gradients in place (whose own
+ * workspace and table the first call on a stream allocates). */
 #define ADAMW_NOALLOC_SCRATCH_BYTES (16u << 20)
 adamw_status adamw_multi_tensor_step_noalloc(adamw_mode mode, adamw_dtype p_dtype, const adamw_tensor_list* list,
                                              const adamw_hparams* hp, int32_t* d_step, const int32_t* d_found_inf,
