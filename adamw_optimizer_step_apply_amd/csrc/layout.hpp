@@ -108,10 +108,11 @@ constexpr int64_t kClipWholeBytes = (int64_t)kBlockSweep * 16 * kClipUnroll;
 constexpr int64_t kClipChunkBytes = kXcdParts * kClipWholeBytes;
 constexpr int64_t kMaxSweepChunks = (int64_t)UINT32_MAX / kBlockSweep;
 // A sum of squares runs as one launch (its last workgroup joins the partial sums) up
-// to this many workgroups, if the single-launch limit allows as many: measured on
-// MI355X (bf16, one tensor), one launch / two: 3.6 / 5.7 us at 0.26 MB, 3.7 / 5.6 at
-// 1 MB, 6.3 / 6.7 at 26 MB (800 workgroups), 41.2 / 38.2 at 252 MB (7,680), where the
-// counting atomics cost more than a launch.
+// to this many workgroups, if the single-launch limit allows as many: past it the
+// counting atomics cost more than a launch.  MI355X, one launch / two, in graphs of 30
+// norms of one bf16 tensor: 4.0 / 4.25 us at 16 workgroups, 5.6 / 5.9 at 512, 8.4 / 8.6 at
+// 1,024 (33.6 MB), 11.3 / 11.05 at 1,536, 14.3 / 13.9 at 2,048, 25.4 / 24.1 at 4,096; fp32 the
+// same within 0.3 us up to 2,048, 26.4 / 24.6 at 4,096.
 constexpr int64_t kSingleSumMaxWorkgroups = 1024;
 // Partial sums are joined by 256-lane workgroups, this many each.
 constexpr int kBlockJoin = 256;
