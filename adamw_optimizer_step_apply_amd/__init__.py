@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 from typing import Sequence
 
 import torch  # loads the HIP runtime the library then binds to
@@ -37,6 +37,8 @@ BLOCKED_STATE = 1 << 8        # flat_mask bit: exp_avg / exp_avg_sq / aux in one
 FLAT_PAD8 = 1 << 9            # flat_mask bit: every tensor starts at a multiple of 8 in the flat index
 STATE_BLOCK_ELEMS = 16384     # elements per block of a blocked state buffer (ADAMW_STATE_BLOCK_ELEMS)
 NOALLOC_SCRATCH_BYTES = 16 << 20   # the allocation-free step's per-GPU workspace (ADAMW_NOALLOC_SCRATCH_BYTES)
+MUON_SCALE_NONE, MUON_SCALE_SPECTRAL, MUON_SCALE_RMS = 0, 1, 2   # factor of a Muon step's update (MuonHParams.scaling)
+NS_MAX_STEPS = 16             # most Newton-Schulz steps (ADAMW_NS_MAX_STEPS)
 NUM_STREAMS = 5
 _STATUS = {0: "ADAMW_OK", 1: "ADAMW_E_INVALID", 2: "ADAMW_E_UNSUPPORTED", 3: "ADAMW_E_NOMEM", 4: "ADAMW_E_HIP"}
 
@@ -45,6 +47,7 @@ EXPORTED = ("adamw_step", "adamw_multi_tensor_step", "adamw_multi_tensor_step_no
             "adamw_pure_multi_tensor_step",
             "adamw_check_finite", "adamw_grad_norm", "adamw_tensor_norms", "adamw_clip_grads",
             "adamw_multi_tensor_step_clipped",
+           "adamw_orthogonalize_workspace_bytes", "adamw_orthogonalize", "adamw_muon_multi_tensor_step",
             "adamw_last_error", "adamw_release_workspace", "adamw_abi_version", "adamw_plan_inspect",
             "adamw_plan_inspect_bytes", "adamw_set_chunk_elems", "adamw_set_single_launch_max_workgroups",
             "adamw_blocked_state_bytes", "adamw_blocked_state_copy")
@@ -66,6 +69,17 @@ class adamw_loss_scaler(ctypes.Structure):
 
 class adamw_grad_clip(ctypes.Structure):
     _fields_ = [("d_sumsq", ctypes.c_void_p), ("max_norm", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class adamw_newton_schulz(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float),
+                ("steps", ctypes.c_int32)]
+
+
+class adamw_muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("inv_loss_scale", ctypes.c_float), ("nesterov", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("ns", adamw_newton_schulz)]
 
 
 class adamw_tensor_list(ctypes.Structure):
@@ -117,6 +131,18 @@ def _declare(_lib):
                                                      ctypes.POINTER(adamw_tensor_list), ctypes.POINTER(adamw_hparams),
                                                      ctypes.POINTER(adamw_grad_clip), _vp, _vp, _vp,
                                                      ctypes.POINTER(adamw_loss_scaler), _vp]
+    _lib.adamw_orthogonalize_workspace_bytes.restype = ctypes.c_int64
+    _lib.adamw_orthogonalize_workspace_bytes.argtypes = [ctypes.POINTER(adamw_tensor_list),
+                                                         ctypes.POINTER(ctypes.c_int64), ctypes.c_int]
+    _lib.adamw_orthogonalize.restype = ctypes.c_int
+    _lib.adamw_orthogonalize.argtypes = [ctypes.c_int, ctypes.POINTER(adamw_tensor_list),
+                                         ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(adamw_newton_schulz), _vp,
+                                         ctypes.c_int64, _vp]
+    _lib.adamw_muon_multi_tensor_step.restype = ctypes.c_int
+    _lib.adamw_muon_multi_tensor_step.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.POINTER(adamw_pure_precision),
+                                                  ctypes.POINTER(adamw_tensor_list), ctypes.POINTER(ctypes.c_int64),
+                                                  ctypes.POINTER(adamw_muon_hparams), ctypes.POINTER(adamw_grad_clip),
+                                                  _vp, _vp, _vp, _vp, ctypes.c_int64, _vp]
     _lib.adamw_last_error.restype = ctypes.c_char_p
     _lib.adamw_last_error.argtypes = []
     _lib.adamw_release_workspace.restype = None
@@ -143,7 +169,7 @@ def _declare(_lib):
 
 
 _load(LIB_PATH)
-ABI_VERSION = 9               # ADAMW_ABI_VERSION of the header this binding follows
+ABI_VERSION = 10              # ADAMW_ABI_VERSION of the header this binding follows
 if _lib.adamw_abi_version() != ABI_VERSION:
     raise ImportError(f"{LIB_PATH} has ABI version {_lib.adamw_abi_version()}, this binding expects {ABI_VERSION}: "
                       "rebuild the library")
@@ -416,6 +442,111 @@ def adamw_multi_tensor_step_clipped(mode: int, p_dtype: int, tensors: TensorList
     _check(_lib.adamw_multi_tensor_step_clipped(mode, p_dtype, pc, ctypes.byref(tensors.c), ctypes.byref(h),
                                                 ctypes.byref(c), _addr(d_step), _addr(d_found_inf), _addr(d_scale),
                                                 ctypes.byref(sc) if advance_scale else None, _stream(stream)))
+
+
+class MatrixList(TensorList):
+    """A list of row-major matrices: a TensorList with each tensor's (rows, columns).
+    Tensors given have to be contiguous and of rows * columns elements (a flat
+    shard buffer: of the shard's), since only their addresses go to the library."""
+
+    def __init__(self, shapes: Sequence[Sequence[int]], streams, shard_begin: int = 0, shard_end: int = -1,
+                 flat_mask: int = 0):
+        self.shapes = [(int(r), int(c)) for r, c in shapes]
+        numels = [r * c for r, c in self.shapes]
+        for k, items in enumerate(streams):
+            for i, x in enumerate(items or ()):
+                if not isinstance(x, torch.Tensor):
+                    continue
+                if not x.is_contiguous():
+                    raise ValueError(f"stream {k}, tensor {i}: a contiguous tensor is needed, got strides {x.stride()}")
+                if not (flat_mask >> k) & 1 and x.numel() != numels[i]:
+                    raise ValueError(f"stream {k}, tensor {i}: {x.numel()} elements are no matrix of {self.shapes[i]}")
+        super().__init__(numels, streams, shard_begin, shard_end, flat_mask)
+        self.cols = (ctypes.c_int64 * max(len(numels), 1))(*[max(c, 1) for _, c in self.shapes])
+
+
+@dataclass
+class NewtonSchulz:
+    """Newton-Schulz products: ``steps`` times X <- a X + b (X X^T) X + c (X X^T)^2 X
+    from X = U / (|U| + eps)."""
+    a: float = 3.4445
+    b: float = -4.7750
+    c: float = 2.0315
+    steps: int = 5
+    eps: float = 1e-7
+
+    def struct(self) -> adamw_newton_schulz:
+        return adamw_newton_schulz(self.a, self.b, self.c, self.eps, int(self.steps))
+
+
+@dataclass
+class MuonHParams:
+    """Hyper-parameters of a Muon step; lr and weight decay as in the AdamW step's
+    recipe, which MUON_SCALE_RMS makes fit."""
+    lr: float = 2e-4
+    momentum: float = 0.95
+    weight_decay: float = 0.1
+    inv_loss_scale: float = 1.0
+    nesterov: bool = True
+    scaling: int = MUON_SCALE_RMS
+    ns: NewtonSchulz = field(default_factory=NewtonSchulz)
+
+    def c(self) -> adamw_muon_hparams:
+        return adamw_muon_hparams(self.lr, self.momentum, self.weight_decay, self.inv_loss_scale,
+                                  int(self.nesterov), int(self.scaling), self.ns.struct())
+
+
+def adamw_orthogonalize_workspace_bytes(matrices: MatrixList, least: bool = False) -> int:
+    """Bytes of device workspace for the two calls below: for full speed, or with
+    ``least`` the smallest that they take."""
+    n = _lib.adamw_orthogonalize_workspace_bytes(ctypes.byref(matrices.c), matrices.cols, int(bool(least)))
+    if n < 0:
+        raise AdamWError(E_INVALID, adamw_last_error())
+    return n
+
+
+def make_orthogonalize_workspace(matrices: MatrixList, device=None) -> torch.Tensor:
+    """A workspace of adamw_orthogonalize_workspace_bytes on ``device`` (default: the
+    list's tensors')."""
+    if device is None:
+        if not matrices._tensors:
+            raise ValueError("make_orthogonalize_workspace: pass device= when the matrices are given as addresses")
+        device = matrices._tensors[0].device
+    return torch.empty(adamw_orthogonalize_workspace_bytes(matrices), dtype=torch.uint8, device=device)
+
+
+def _workspace(x):
+    """Address and bytes of a workspace: a contiguous tensor, or (address, bytes)."""
+    if isinstance(x, torch.Tensor):
+        if not x.is_contiguous():
+            raise ValueError("workspace: a contiguous tensor is needed")
+        return x.data_ptr(), x.numel() * x.element_size()
+    address, nbytes = x
+    return int(address), int(nbytes)
+
+
+def adamw_orthogonalize(u_dtype: int, matrices: MatrixList, workspace, ns: NewtonSchulz = None, stream=None) -> None:
+    """Orthogonalises every matrix of a list: the Newton-Schulz products of stream 1
+    (``u_dtype``) into stream 0 (bf16), which may be the same bf16 tensors; ``workspace``
+    from make_orthogonalize_workspace (C ABI adamw_orthogonalize)."""
+    c = (ns or NewtonSchulz()).struct()
+    _check(_lib.adamw_orthogonalize(u_dtype, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(c),
+                                    *_workspace(workspace), _stream(stream)))
+
+
+def adamw_muon_multi_tensor_step(mode: int, p_dtype: int, matrices: MatrixList, hp, d_step, workspace,
+                                 d_found_inf=None, clip: GradClip = None, d_scale=None, prec: "PurePrecision" = None,
+                                 stream=None) -> None:
+    """One Muon step over a list of matrices: momentum, Newton-Schulz products of it,
+    decoupled weight decay and the update of the weights.  ``clip`` and ``d_scale`` as
+    adamw_multi_tensor_step_clipped with ``advance_scale`` false, ``prec`` selects the pure-bf16
+    precisions (C ABI adamw_muon_multi_tensor_step)."""
+    h = (hp or MuonHParams()).c()
+    pc = ctypes.byref(prec.c()) if prec is not None else None
+    cc = ctypes.byref(clip.c()) if clip is not None else None
+    _check(_lib.adamw_muon_multi_tensor_step(mode, p_dtype, pc, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(h),
+                                             cc, _addr(d_step), _addr(d_found_inf), _addr(d_scale),
+                                             *_workspace(workspace), _stream(stream)))
 
 
 def adamw_last_error() -> str:

@@ -24,6 +24,7 @@
 
 #include "adamw.h"
 #include "layout.hpp"
+#include "muon_launch.hpp"
 #include "plan.hpp"
 #include "step.hpp"
 
@@ -66,6 +67,7 @@ struct PlanSlot {
     bool pinned = false;   // used under graph capture: never evicted, resized or rewritten
     int64_t n_segs = 0, n_chunks = 0, n_tensors = 0;
     UpdateGrid grid;   // an update's
+    std::vector<NsBatch> batches;   // the Newton-Schulz products'
 
     const DevSeg* segs() const { return static_cast<const DevSeg*>(dev); }
     const DevChunk* chunks() const
@@ -79,6 +81,9 @@ struct PlanSlot {
     {
         return reinterpret_cast<double*>(static_cast<char*>(dev) + norm_table_bytes(n_chunks, n_tensors));
     }
+    // the Newton-Schulz products': n_segs matrices, then their tiles
+    const DevMatrix* matrices() const { return static_cast<const DevMatrix*>(dev); }
+    const DevTile* tiles() const { return reinterpret_cast<const DevTile*>(matrices() + n_segs); }
     // A norm's tables, rounded up to the alignment of what follows.
     static size_t norm_table_bytes(int64_t groups, int64_t tensors)
     {
@@ -161,68 +166,43 @@ adamw_status get_workspace(hipStream_t stream, StreamWorkspace** out)
     return ADAMW_OK;
 }
 
-// Returns (in *out) a slot of `ws` holding the device plan of (mode, dtype,
-// list, for_check): a cached one if every input matches (the key holds every
-// input the plan depends on, so a hit was validated when it was built), else
-// the list is validated and planned, and a slot chosen by choose_plan_slot
-// takes the new plan.  An invalid list returns its error before any HIP call
-// and leaves the cache as it was.
-//
-// Under graph capture the graph records the slot's device address: a hit pins
-// the slot, so that later calls never evict, resize or rewrite it while the
-// graph may replay (pinned slots are freed by adamw_release_workspace only).
-// A miss under capture is refused: uploading a table would need a copy, and a
-// table that grows a stream synchronisation, neither of which belongs in the
-// graph.
-adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStreams], const adamw_tensor_list* list,
-                         int64_t chunk_elems, hipStream_t stream, bool under_capture, PlanSlot** out)
+// The slot of `ws` whose plan has this key, or null.  Under graph capture the graph
+// records the slot's device address: the slot is pinned, so that later calls never evict,
+// resize or rewrite it while the graph may replay (pinned slots are freed by
+// adamw_release_workspace only).
+PlanSlot* find_plan(StreamWorkspace& ws, const std::vector<int64_t>& key, bool under_capture)
 {
-    std::vector<int64_t> key;
-    plan_key(tag, esz, list, chunk_elems, key);
     auto& plans = ws.plans;
     for (size_t i = 0; i < plans.size(); ++i) {
         if (plans[i]->valid && plans[i]->key == key) {
             std::rotate(plans.begin(), plans.begin() + (ptrdiff_t)i, plans.begin() + (ptrdiff_t)i + 1);
-            *out = plans.front().get();
-            if (under_capture) (*out)->pinned = true;
-            return ADAMW_OK;
+            if (under_capture) plans.front()->pinned = true;
+            return plans.front().get();
         }
     }
-    Plan plan;
-    std::string err;
-    adamw_status st = plan_of(tag, esz, list, chunk_elems, &plan, err);
-    if (st != ADAMW_OK) return fail(st, err);
-    if (under_capture)
-        return fail(ADAMW_E_INVALID,
-                    "this list's chunk table is not on the device: make the same call once on this stream "
-                    "before capturing it into a graph");
+    return nullptr;
+}
 
-    std::vector<Table> tables;
-    std::vector<DevSweep> groups;
-    UpdateTable update;
-    int64_t n_segs = 0, n_chunks = 0;
-    if (is_sweep(tag)) {
-        groups = sweep_groups(plan, esz[ADAMW_STREAM_GRAD], tag == kTagClip);
-        n_chunks = (int64_t)groups.size();
-        tables.emplace_back(groups);
-        if (tag == kTagNorm) tables.emplace_back(plan.tensor_first);
-    } else {
-        n_segs = (int64_t)plan.segs.size();
-        tables.emplace_back(plan.segs);
-        if (tag != kTagCheck) {
-            update = update_table(plan, resident_workgroups((int)tag));
-            plan.chunks.swap(update.items);
-        }
-        n_chunks = (int64_t)plan.chunks.size();
-        tables.emplace_back(plan.chunks);
-    }
+// A plan that is not on the device cannot be used under capture: uploading a table would
+// need a copy, and a table that grows a stream synchronisation, neither of which belongs
+// in the graph.
+adamw_status refuse_under_capture()
+{
+    return fail(ADAMW_E_INVALID,
+                "this list's chunk table is not on the device: make the same call once on this stream "
+                "before capturing it into a graph");
+}
+
+// Copies a new plan's tables, one after another, to a slot chosen by choose_plan_slot
+// with room for dev_bytes, and gives it the key (key[0] is its tag).
+adamw_status upload_plan(StreamWorkspace& ws, std::vector<int64_t>& key, const std::vector<Table>& tables,
+                         size_t dev_bytes, hipStream_t stream, PlanSlot** out)
+{
+    const int64_t tag = key[0];
+    auto& plans = ws.plans;
     size_t bytes = 0;
     for (const Table& t : tables) bytes += t.bytes;
-    size_t dev_bytes = bytes;
-    if (tag == kTagNorm)
-        dev_bytes = PlanSlot::norm_table_bytes(n_chunks, list->n_tensors) +
-                    (size_t)partial_count(n_chunks) * sizeof(double);
-
+    dev_bytes = std::max(dev_bytes, bytes);
     std::vector<SlotInfo> slots(plans.size());
     for (size_t i = 0; i < plans.size(); ++i) slots[i] = SlotInfo{plans[i]->tag, plans[i]->dev_cap, plans[i]->pinned};
     const size_t pick = choose_plan_slot(slots, tag, dev_bytes);
@@ -276,12 +256,57 @@ adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStream
         if (e != hipSuccess) { slot.valid = false; return hip_fail("hipEventRecord", e); }
         slot.upload_in_flight = true;
     }
+    slot.key.swap(key);
+    slot.valid = true;
+    return ADAMW_OK;
+}
+
+// Returns (in *out) a slot of `ws` holding the device plan of (mode, dtype,
+// list, for_check): a cached one if every input matches (the key holds every
+// input the plan depends on, so a hit was validated when it was built), else
+// the list is validated and planned, and uploaded.  An invalid list returns its error
+// before any HIP call and leaves the cache as it was.
+adamw_status ensure_plan(StreamWorkspace& ws, int64_t tag, const int esz[kStreams], const adamw_tensor_list* list,
+                         int64_t chunk_elems, hipStream_t stream, bool under_capture, PlanSlot** out)
+{
+    std::vector<int64_t> key;
+    plan_key(tag, esz, list, chunk_elems, key);
+    if ((*out = find_plan(ws, key, under_capture))) return ADAMW_OK;
+    Plan plan;
+    std::string err;
+    adamw_status st = plan_of(tag, esz, list, chunk_elems, &plan, err);
+    if (st != ADAMW_OK) return fail(st, err);
+    if (under_capture) return refuse_under_capture();
+
+    std::vector<Table> tables;
+    std::vector<DevSweep> groups;
+    UpdateTable update;
+    int64_t n_segs = 0, n_chunks = 0;
+    if (is_sweep(tag)) {
+        groups = sweep_groups(plan, esz[ADAMW_STREAM_GRAD], tag == kTagClip);
+        n_chunks = (int64_t)groups.size();
+        tables.emplace_back(groups);
+        if (tag == kTagNorm) tables.emplace_back(plan.tensor_first);
+    } else {
+        n_segs = (int64_t)plan.segs.size();
+        tables.emplace_back(plan.segs);
+        if (tag != kTagCheck) {
+            update = update_table(plan, resident_workgroups((int)tag));
+            plan.chunks.swap(update.items);
+        }
+        n_chunks = (int64_t)plan.chunks.size();
+        tables.emplace_back(plan.chunks);
+    }
+    size_t dev_bytes = 0;
+    if (tag == kTagNorm)
+        dev_bytes = PlanSlot::norm_table_bytes(n_chunks, list->n_tensors) +
+                    (size_t)partial_count(n_chunks) * sizeof(double);
+    if ((st = upload_plan(ws, key, tables, dev_bytes, stream, out)) != ADAMW_OK) return st;
+    PlanSlot& slot = **out;
     slot.n_segs = n_segs;
     slot.n_chunks = n_chunks;
     slot.grid = update.grid;
     slot.n_tensors = list->n_tensors;
-    slot.key.swap(key);
-    slot.valid = true;
     return ADAMW_OK;
 }
 
@@ -477,6 +502,68 @@ adamw_status sum_of_squares(adamw_dtype g_dtype, const adamw_tensor_list* grads,
     hipError_t e = launch_sumsq(g_dtype, p.groups(), p.n_chunks, p.tensor_first(), p.n_tensors, p.partials(),
                                 sw.done, single, out, sw.stream);
     if (e != hipSuccess) return hip_fail("sum of squares launch", e);
+    return ADAMW_OK;
+}
+
+// The key of a plan of the Newton-Schulz products.
+void ns_key(const NsKind& kind, const adamw_tensor_list* list, const int64_t* cols, int scaling,
+            int64_t workspace_bytes, std::vector<int64_t>& key)
+{
+    plan_key(kTagMuon, kind.esz, list, kind.end | (int64_t)kind.in << 8 | (int64_t)scaling << 16, key);
+    key.insert(key.end(), cols, cols + list->n_tensors);
+    key.push_back(workspace_bytes);
+}
+
+// Validates a list of matrices (once per key), readies its plan on the stream's device and enqueues
+// the batches; for a step (d_step non-null) behind its prologue.
+adamw_status run_ns(const NsKind& kind, const NsScales& scales, const adamw_tensor_list* list, const int64_t* cols,
+                    const adamw_muon_hparams& hp, const ClipRule& clip, int32_t* d_step, const int32_t* d_found_inf,
+                    const adamw_loss_scale_state* d_amp, void* workspace, int64_t workspace_bytes, void* hip_stream)
+{
+    adamw_status st;
+    std::string err;
+    if ((st = basic_list_check(list)) != ADAMW_OK) return st;
+    if (list->n_tensors > 0 && !cols) return fail(ADAMW_E_INVALID, "cols array is null");
+    std::vector<int64_t> key, seen;
+    ns_key(kind, list, cols, hp.scaling, workspace_bytes, key);
+    seen = key;
+    seen.push_back((int64_t)(uintptr_t)workspace);
+    if (!validated_before(seen)) {
+        st = build_ns_plan(kind, list, cols, hp.scaling, (uint64_t)(uintptr_t)workspace, workspace_bytes, nullptr, err);
+        if (st != ADAMW_OK) return fail(st, err);
+        remember_validated(seen);
+    }
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    StreamWorkspace* ws = nullptr;
+    if ((st = get_workspace(stream, &ws)) != ADAMW_OK) return st;
+    std::lock_guard<std::mutex> lk(ws->mu);
+    DeviceGuard dg(ws->device);
+    bool cap = false;
+    if ((st = capturing(stream, &cap)) != ADAMW_OK) return st;
+    PlanSlot* slot = find_plan(*ws, key, cap);
+    if (!slot) {
+        NsPlan plan;
+        st = build_ns_plan(kind, list, cols, hp.scaling, (uint64_t)(uintptr_t)workspace, workspace_bytes, &plan, err);
+        if (st != ADAMW_OK) return fail(st, err);
+        if (cap) return refuse_under_capture();
+        std::vector<Table> tables;
+        tables.emplace_back(plan.mats);
+        tables.emplace_back(plan.tiles);
+        if ((st = upload_plan(*ws, key, tables, 0, stream, &slot)) != ADAMW_OK) return st;
+        slot->n_segs = (int64_t)plan.mats.size();
+        slot->batches.swap(plan.batches);
+    }
+    hipError_t e;
+    char* at = static_cast<char*>(workspace);
+    if (d_step) {
+        e = launch_ns_prologue(hp, clip, d_step, d_found_inf, d_amp, at, stream);
+        if (e != hipSuccess) return hip_fail("Muon prologue launch", e);
+    }
+    const NsCall call{kind, slot->matrices(), slot->tiles(), at, hp.ns, scales, hp};
+    for (const NsBatch& b : slot->batches) {
+        e = launch_ns_batch(call, b, stream);
+        if (e != hipSuccess) return hip_fail("Newton-Schulz launch", e);
+    }
     return ADAMW_OK;
 }
 
@@ -773,6 +860,77 @@ try {
     if ((st = state_kind(mode, p_dtype, prec, &kind)) != ADAMW_OK) return st;
     return do_step(kind, list, hp, d_step, d_found_inf, hip_stream, d_scale, scaler,
                    ClipRule{clip->d_sumsq, clip->max_norm, clip->eps});
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
+}
+
+int64_t adamw_orthogonalize_workspace_bytes(const adamw_tensor_list* list, const int64_t* cols, int least)
+try {
+    g_err.clear();
+    std::string err;
+    int64_t bytes = 0;
+    if (ns_workspace_bytes(list, cols, least != 0, &bytes, err) != ADAMW_OK) {
+        g_err = err;
+        return -1;
+    }
+    return bytes;
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    g_err = e.what();
+    return -1;
+}
+
+adamw_status adamw_orthogonalize(adamw_dtype u_dtype, const adamw_tensor_list* list, const int64_t* cols,
+                                 const adamw_newton_schulz* ns, void* workspace, int64_t workspace_bytes,
+                                 void* hip_stream)
+try {
+    g_err.clear();
+    std::string err;
+    NsKind kind{};
+    adamw_status st = check_sweep_dtype(u_dtype, &kind.esz[ADAMW_STREAM_GRAD], err);
+    if (st != ADAMW_OK) return fail(st, "u_dtype must be ADAMW_F16, ADAMW_BF16 or ADAMW_F32");
+    NsScales scales{};
+    if ((st = check_ns(ns, &scales, err)) != ADAMW_OK) return fail(st, err);
+    kind.esz[ADAMW_STREAM_PARAM] = 2;
+    kind.end = kEndOrtho;
+    kind.in = u_dtype;
+    adamw_muon_hparams hp{};
+    hp.ns = *ns;
+    return run_ns(kind, scales, list, cols, hp, ClipRule{}, nullptr, nullptr, nullptr, workspace, workspace_bytes,
+                  hip_stream);
+} catch (const std::exception& e) {   // no C++ exception leaves the C ABI
+    return fail(ADAMW_E_NOMEM, e.what());
+}
+
+adamw_status adamw_muon_multi_tensor_step(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
+                                          const adamw_tensor_list* list, const int64_t* cols,
+                                          const adamw_muon_hparams* hp, const adamw_grad_clip* clip, int32_t* d_step,
+                                          const int32_t* d_found_inf, const adamw_loss_scale_state* d_scale,
+                                          void* workspace, int64_t workspace_bytes, void* hip_stream)
+try {
+    g_err.clear();
+    std::string err;
+    NsScales scales{};
+    adamw_status st = check_muon_hparams(hp, &scales, err);
+    if (st == ADAMW_OK && clip) st = check_clip(clip, err);
+    if (st != ADAMW_OK) return fail(st, err);
+    if (!d_step) return fail(ADAMW_E_INVALID, "d_step is null");
+    if ((uintptr_t)d_step % 4 || (uintptr_t)d_found_inf % 4)
+        return fail(ADAMW_E_INVALID, "d_step / d_found_inf must be 4-byte aligned");
+    if ((uintptr_t)d_scale % 4) return fail(ADAMW_E_INVALID, "d_scale is not 4-byte aligned");
+    StepKind step;
+    if ((st = state_kind(mode, p_dtype, prec, &step)) != ADAMW_OK) return st;
+    NsKind kind{};
+    for (int s = 0; s < kStreams; ++s) kind.esz[s] = step.esz[s];
+    kind.esz[ADAMW_STREAM_EXP_AVG_SQ] = 0;
+    kind.m16 = kind.esz[ADAMW_STREAM_EXP_AVG] == 2;
+    const bool mixed = !prec && mode == ADAMW_MIXED;
+    kind.in = mixed ? p_dtype : ADAMW_BF16;
+    kind.end = mixed ? (p_dtype == ADAMW_F16 ? kEndMixedF16 : kEndMixedBf16)
+             : !prec && mode == ADAMW_MIXED_SPLIT ? kEndSplit
+             : kind.esz[ADAMW_STREAM_AUX] == 0 ? kEndPure
+             : kind.esz[ADAMW_STREAM_AUX] == 2 ? kEndKahan : kEndKahan32;
+    return run_ns(kind, scales, list, cols, *hp, clip ? ClipRule{clip->d_sumsq, clip->max_norm, clip->eps} : ClipRule{},
+                  d_step, d_found_inf, d_scale, workspace, workspace_bytes, hip_stream);
 } catch (const std::exception& e) {   // no C++ exception leaves the C ABI
     return fail(ADAMW_E_NOMEM, e.what());
 }

@@ -1,0 +1,128 @@
+// muon.hpp -- the Newton-Schulz products and the Muon step over a list of matrices:
+// what the host planner (muon_plan.cpp, no HIP calls) lays out and the gfx950 kernels
+// (muon.hip) work through.
+//
+// A list is worked through in batches of matrices that fit the caller's workspace
+// together.  One batch is a fixed sequence of launches, each over every matrix of it:
+//
+//   moments    sum of squares of each matrix; a step also advances m and writes u
+//   normalise  X = u / (|u| + eps) as fp16 pairs, in both orders
+//   per product step:  gram  A = X X^T (the shorter side),  poly  B = b A + c A A,
+//                      apply X = a X + B X, the last one with the result's own epilogue
+//
+// The matrices of the products are held in the workspace with both sides padded to
+// kPad by zeros, so that the product kernels have no ragged edge in the summed dimension.
+#pragma once
+
+#include <stdint.h>
+
+#include <string>
+#include <vector>
+
+#include "adamw.h"
+#include "layout.hpp"
+
+namespace adamw {
+
+constexpr int64_t kTagMuon = -4;          // plan tag
+constexpr int kPad = 64;                  // padding of both sides, and elements of a summing step
+constexpr int64_t kNsAlign = 256;         // of every part of the workspace
+constexpr int64_t kNsHeadBytes = 256;     // the step's scalars, at the workspace's start
+constexpr int64_t kNsBatchBytes = INT64_C(4) << 30;   // workspace of a batch of a long list
+constexpr int64_t kMomentElems = 16384;   // elements of a workgroup of the moments kernel
+constexpr int kBlockMoments = 256;
+
+// Square tiles of the product kernels: side, and lanes of a workgroup.
+constexpr int kTileKinds = 3;
+constexpr int kTileSide[kTileKinds] = {256, 128, 64};
+constexpr int kTileLanes[kTileKinds] = {512, 256, 256};
+
+// Tiles that a launch should have before it takes the larger kind: one for every CU.
+constexpr int64_t kTilesWanted = 256;
+constexpr int64_t kMaxNsSide = INT64_C(1) << 30, kMaxNsShort = INT64_C(1) << 20;
+// A grid counts at most 2^32 - 1 lanes.
+constexpr int64_t kMaxNsTiles = (int64_t)UINT32_MAX / 512;
+
+// One matrix of a batch.  Parts of the workspace are byte offsets from its start.
+// hi, lo: X in its own order (rows x cp), the value is (hi + lo * 2^-11) * 2^-sx; t: hi's
+// transpose (cols x rp).  y: the other buffer of the one of hi and t that the product with
+// B reads (t of a wide matrix, hi of a tall one), since workgroups write the new
+// values while others read the old.  u (a step's fp32 matrix, not padded) lies where y, a and b
+// come to lie later.
+struct alignas(16) DevMatrix {
+    uint64_t ptr[4];          // element 0: result or param; u or grad; exp_avg; aux
+    uint64_t u, hi, lo, t, y, a, b, da, db, partials;
+    double factor;            // s of the step
+    int32_t rows, cols, rp, cp;
+    int32_t s, sp;            // the shorter side, padded
+    int32_t tall;             // rows > cols
+    uint32_t n_partials;
+    uint32_t flat16;          // every stream's element 0 is 16-byte aligned
+    uint32_t row16;           // and so is every row of 8 elements' multiples
+    uint32_t pad[2];
+};
+
+// One workgroup's part of a matrix: a tile of the products (row and column of the tile),
+// a 64 x 64 tile of the normalisation, or a run of elements (its number).
+struct alignas(16) DevTile {
+    uint32_t mat, row, col, pad;
+};
+
+struct NsLaunch {
+    int64_t first = 0, count = 0;   // workgroups, in the tile table
+    int kind = 0;                   // tile kind of a product
+};
+
+struct NsBatch {
+    NsLaunch moments, normalise, square, apply;   // square: gram and poly
+};
+
+struct NsPlan {
+    std::vector<DevMatrix> mats;
+    std::vector<DevTile> tiles;
+    std::vector<NsBatch> batches;
+};
+
+// What the two entry points do at both ends of the products.
+enum NsEnd {
+    kEndOrtho = 0,
+    kEndMixedBf16,
+    kEndMixedF16,
+    kEndSplit,
+    kEndPure,
+    kEndKahan,
+    kEndKahan32,
+    kNumEnds
+};
+struct NsKind {
+    int esz[kStreams];
+    int end;
+    adamw_dtype in;        // of stream 1
+    bool m16;              // exp_avg is bf16
+};
+
+// Powers of two under which X, A and B are held in fp16, and their limits.
+struct NsScales {
+    int sx, sa, sb;
+};
+
+adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::string& err);
+adamw_status check_muon_hparams(const adamw_muon_hparams* hp, NsScales* scales, std::string& err);
+
+// Bytes for all matrices (at most kNsBatchBytes, or the largest one's), or with `least`
+// the largest matrix's.
+adamw_status ns_workspace_bytes(const adamw_tensor_list* list, const int64_t* cols, bool least, int64_t* bytes,
+                                std::string& err);
+
+// Validates the list and, with `out`, lays the work out for a workspace of
+// `workspace_bytes` at address `workspace`.
+adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, const int64_t* cols, int scaling,
+                           uint64_t workspace, int64_t workspace_bytes, NsPlan* out, std::string& err);
+
+// Scalars of one step, at the start of the workspace.
+struct NsScalars {
+    int32_t skip;
+    float mult;
+};
+
+}  // namespace adamw

@@ -1,0 +1,382 @@
+// muon_plan.cpp -- host planner of the Newton-Schulz products (no HIP calls): shapes,
+// overlaps, the batches that fit a workspace, and the tiles of each launch.
+#include "muon.hpp"
+
+#include <stdio.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "plan.hpp"
+
+namespace adamw {
+
+namespace {
+
+struct Shape {
+    int64_t tensor, rows, cols;
+};
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// The whole matrices inside the shard, in list order.
+adamw_status shapes_of(const adamw_tensor_list* list, const int64_t* cols, std::vector<Shape>* out, std::string& err)
+{
+    char buf[200];
+    adamw_status st = basic_list_check(list, err);
+    if (st != ADAMW_OK) return st;
+    if (list->flat_mask & ~(0x1fu | ADAMW_BLOCKED_STATE | ADAMW_FLAT_PAD8)) {
+        err = "flat_mask has unknown bits";
+        return ADAMW_E_INVALID;
+    }
+    if (list->flat_mask & ADAMW_BLOCKED_STATE) {
+        err = "matrices with blocked state are not provided";
+        return ADAMW_E_UNSUPPORTED;
+    }
+    const int64_t nt = list->n_tensors, align = (list->flat_mask & ADAMW_FLAT_PAD8) ? 8 : 1;
+    if (nt > 0 && !cols) { err = "cols array is null"; return ADAMW_E_INVALID; }
+    int64_t total = 0;
+    for (int64_t i = 0; i < nt; ++i) {
+        const int64_t n = list->numel[i];
+        if (n < 0 || n > (INT64_C(1) << 56) || total > (INT64_C(1) << 56)) {
+            snprintf(buf, sizeof buf, "numel[%lld] = %lld < 0 or too large", (long long)i, (long long)n);
+            err = buf;
+            return ADAMW_E_INVALID;
+        }
+        total += round_up(n, align);
+    }
+    const int64_t b = list->shard_begin, e = list->shard_end < 0 ? total : list->shard_end;
+    if (list->shard_end < -1 || b < 0 || b > e || e > total) {
+        snprintf(buf, sizeof buf, "shard range [%lld, %lld) outside [0, %lld]", (long long)b,
+                 (long long)list->shard_end, (long long)total);
+        err = buf;
+        return ADAMW_E_INVALID;
+    }
+    int64_t base = 0;
+    for (int64_t i = 0; i < nt; ++i) {
+        const int64_t n = list->numel[i], c = cols[i];
+        if (c < 1 || n % c != 0) {
+            snprintf(buf, sizeof buf, "cols[%lld] = %lld does not divide numel %lld", (long long)i, (long long)c,
+                     (long long)n);
+            err = buf;
+            return ADAMW_E_INVALID;
+        }
+        const int64_t lo = std::max(b, base), hi = std::min(e, base + n);
+        if (lo < hi) {
+            if (hi - lo != n) {
+                snprintf(buf, sizeof buf, "matrix %lld lies in the shard in part: shards take whole matrices",
+                         (long long)i);
+                err = buf;
+                return ADAMW_E_INVALID;
+            }
+            const Shape s{i, n / c, c};
+            // 32-bit row numbers, and byte counts that stay far from 2^63
+            if (s.rows > kMaxNsSide || s.cols > kMaxNsSide || std::min(s.rows, s.cols) > kMaxNsShort) {
+                snprintf(buf, sizeof buf, "matrix %lld of %lld x %lld is larger than 2^30 on a side or 2^20 on both",
+                         (long long)i, (long long)s.rows, (long long)s.cols);
+                err = buf;
+                return ADAMW_E_INVALID;
+            }
+            out->push_back(s);
+        }
+        base += round_up(n, align);
+    }
+    return ADAMW_OK;
+}
+
+// Lays one matrix out from byte `at` of the workspace; returns the end.
+int64_t place(const Shape& sh, bool step, int64_t at, DevMatrix* m)
+{
+    const int64_t rp = round_up(sh.rows, kPad), cp = round_up(sh.cols, kPad), s = std::min(sh.rows, sh.cols);
+    const int64_t sp = round_up(s, kPad), part = round_up(2 * rp * cp, kNsAlign), square = round_up(2 * sp * sp, kNsAlign);
+    const int64_t chunks = (sh.rows * sh.cols + kMomentElems - 1) / kMomentElems;
+    m->rows = (int32_t)sh.rows;
+    m->cols = (int32_t)sh.cols;
+    m->rp = (int32_t)rp;
+    m->cp = (int32_t)cp;
+    m->s = (int32_t)s;
+    m->sp = (int32_t)sp;
+    m->tall = sh.rows > sh.cols;
+    m->n_partials = (uint32_t)chunks;
+    m->hi = (uint64_t)at;
+    m->lo = m->hi + (uint64_t)part;
+    m->t = m->lo + (uint64_t)part;
+    m->y = m->t + (uint64_t)part;
+    m->a = m->y + (uint64_t)part;
+    m->b = m->a + (uint64_t)square;
+    m->u = m->y;
+    int64_t room = part + 2 * square;
+    if (step) room = std::max(room, round_up(4 * sh.rows * sh.cols, kNsAlign));
+    m->da = m->y + (uint64_t)room;
+    m->db = m->da + (uint64_t)round_up(4 * sp, kNsAlign);
+    m->partials = m->db + (uint64_t)round_up(4 * sp, kNsAlign);
+    return (int64_t)m->partials + round_up(8 * chunks, kNsAlign);
+}
+
+// Bytes of a matrix's part of the workspace, the same for both calls.
+int64_t bytes_of(const Shape& s)
+{
+    DevMatrix m;
+    return place(s, true, 0, &m);
+}
+
+// Workgroup order of a launch's tiles: those of the longest sums first, and runs of
+// neighbouring tiles (which read the same rows) to one XCD, whose L2 they then share.
+// Workgroup b runs on XCD b % 8.
+void deal_tiles(const std::vector<DevTile>& in, std::vector<DevTile>* out)
+{
+    const size_t n = in.size(), run = std::min<size_t>(32, std::max<size_t>(1, n / 64));
+    std::vector<std::vector<DevTile>> of(kXcdParts);
+    for (size_t i = 0; i < n; ++i) of[i / run % kXcdParts].push_back(in[i]);
+    for (size_t q = 0, left = n; left; ++q)
+        for (auto& v : of)
+            if (q < v.size()) {
+                out->push_back(v[q]);
+                --left;
+            }
+}
+
+int64_t tiles_of(int64_t n, int side) { return (n + side - 1) / side; }
+
+int64_t square_tiles(int64_t s, int side)
+{
+    const int64_t t = tiles_of(s, side);
+    return t * (t + 1) / 2;
+}
+
+// The largest tile with which a launch has work for every CU.
+template <typename Count>
+int pick_kind(const Count& count)
+{
+    for (int k = 0; k < kTileKinds - 1; ++k)
+        if (count(kTileSide[k]) >= kTilesWanted) return k;
+    return kTileKinds - 1;
+}
+
+}  // namespace
+
+adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::string& err)
+{
+    if (!ns) { err = "Newton-Schulz coefficients are null"; return ADAMW_E_INVALID; }
+    if (!std::isfinite(ns->a) || !std::isfinite(ns->b) || !std::isfinite(ns->c) || !std::isfinite(ns->eps)) {
+        err = "Newton-Schulz coefficients and eps must be finite";
+        return ADAMW_E_INVALID;
+    }
+    if (ns->eps < 0.0f) { err = "Newton-Schulz eps < 0"; return ADAMW_E_INVALID; }
+    if (ns->steps < 1 || ns->steps > ADAMW_NS_MAX_STEPS) {
+        err = "Newton-Schulz steps must lie in [1, ADAMW_NS_MAX_STEPS]";
+        return ADAMW_E_INVALID;
+    }
+    // The largest singular value on the way, from a grid on [0, top] with each step (the
+    // polynomial is smooth there: 4096 points miss less than the margin taken below).
+    double top = 1.0, most = 1.0, poly = 0.0;
+    for (int k = 0; k < ns->steps; ++k) {
+        double next = 0.0;
+        for (int i = 0; i <= 4096; ++i) {
+            const double x = top * i / 4096.0, q = x * x, p = q * (ns->b + ns->c * q);
+            next = std::max(next, std::fabs(x * (ns->a + p)));
+            poly = std::max(poly, std::fabs(p));
+        }
+        top = next * 1.01;   // rounding, and the grid
+        most = std::max(most, top);
+        if (!(most <= 64.0)) {
+            err = "Newton-Schulz coefficients take singular values of [0, 1] past 64";
+            return ADAMW_E_INVALID;
+        }
+    }
+    // no element of a matrix passes its largest singular value
+    const auto under = [](double v) { return (int)std::floor(std::log2(61440.0 / std::max(v, 1e-3))); };
+    scales->sx = under(most);
+    scales->sa = under(most * most);
+    scales->sb = under(poly * 1.02);
+    return ADAMW_OK;
+}
+
+adamw_status check_muon_hparams(const adamw_muon_hparams* hp, NsScales* scales, std::string& err)
+{
+    if (!hp) { err = "hparams is null"; return ADAMW_E_INVALID; }
+    const float v[4] = {hp->lr, hp->momentum, hp->weight_decay, hp->inv_loss_scale};
+    for (float x : v)
+        if (!std::isfinite(x)) { err = "hyper-parameters must be finite"; return ADAMW_E_INVALID; }
+    if (!(hp->momentum >= 0.0f && hp->momentum < 1.0f)) { err = "momentum must lie in [0, 1)"; return ADAMW_E_INVALID; }
+    if (hp->lr < 0.0f) { err = "lr < 0"; return ADAMW_E_INVALID; }
+    if (hp->weight_decay < 0.0f) { err = "weight_decay < 0"; return ADAMW_E_INVALID; }
+    if (!(hp->inv_loss_scale > 0.0f)) { err = "inv_loss_scale must be > 0"; return ADAMW_E_INVALID; }
+    if (hp->nesterov != 0 && hp->nesterov != 1) { err = "nesterov must be 0 or 1"; return ADAMW_E_INVALID; }
+    if (hp->scaling < ADAMW_MUON_SCALE_NONE || hp->scaling > ADAMW_MUON_SCALE_RMS) {
+        err = "unknown scaling of a Muon step";
+        return ADAMW_E_INVALID;
+    }
+    return check_ns(&hp->ns, scales, err);
+}
+
+adamw_status ns_workspace_bytes(const adamw_tensor_list* list, const int64_t* cols, bool least, int64_t* bytes,
+                                std::string& err)
+{
+    std::vector<Shape> shapes;
+    adamw_status st = shapes_of(list, cols, &shapes, err);
+    if (st != ADAMW_OK) return st;
+    int64_t all = 0, largest = 0;
+    for (const Shape& s : shapes) {
+        const int64_t n = bytes_of(s);
+        largest = std::max(largest, n);
+        if (all <= kNsBatchBytes) all += n;
+    }
+    *bytes = kNsHeadBytes + (least ? largest : std::max(largest, std::min(all, kNsBatchBytes)));
+    return ADAMW_OK;
+}
+
+adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, const int64_t* cols, int scaling,
+                           uint64_t workspace, int64_t workspace_bytes, NsPlan* out, std::string& err)
+{
+    char buf[200];
+    std::vector<Shape> shapes;
+    adamw_status st = shapes_of(list, cols, &shapes, err);
+    if (st != ADAMW_OK) return st;
+    // the streams' addresses: each whole matrix is one segment of a step's plan
+    Plan plan;
+    st = build_plan(kind.esz, list, INT64_C(1) << 30, INT64_MAX, &plan, err);
+    if (st != ADAMW_OK) return st;
+    if (plan.segs.size() != shapes.size()) { err = "matrix list: internal error"; return ADAMW_E_INVALID; }
+
+    int64_t least = kNsHeadBytes;
+    for (const Shape& s : shapes) least = std::max(least, kNsHeadBytes + bytes_of(s));
+    if (!workspace || workspace % kNsAlign) {
+        err = "workspace is null or not 256-byte aligned";
+        return ADAMW_E_INVALID;
+    }
+    if (workspace_bytes < least) {
+        snprintf(buf, sizeof buf, "workspace of %lld bytes: the list's largest matrix needs %lld",
+                 (long long)workspace_bytes, (long long)least);
+        err = buf;
+        return ADAMW_E_INVALID;
+    }
+
+    // what is written overlaps nothing else
+    const bool step = kind.end != kEndOrtho;
+    struct Range {
+        uint64_t lo, hi;
+        size_t mat;
+        int stream;   // -1: the workspace
+    };
+    std::vector<Range> r;
+    const auto written = [&](int s) { return s != ADAMW_STREAM_GRAD; };
+    for (size_t i = 0; i < shapes.size(); ++i)
+        for (int s = 0; s < kStreams; ++s)
+            if (kind.esz[s]) {
+                const uint64_t a = plan.segs[i].ptr[s];
+                r.push_back(Range{a, a + (uint64_t)(shapes[i].rows * shapes[i].cols) * (uint64_t)kind.esz[s], i, s});
+            }
+    r.push_back(Range{workspace, workspace + (uint64_t)workspace_bytes, 0, -1});
+    std::sort(r.begin(), r.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    // the furthest ends of what is written and of what is read so far
+    uint64_t end_w = 0, end_r = 0;
+    for (size_t i = 0; i < r.size(); ++i) {
+        const bool w = written(r[i].stream);
+        // a bf16 matrix that is its own result: the two ranges are one
+        if (!step && kind.in == ADAMW_BF16 && i + 1 < r.size() && r[i + 1].lo == r[i].lo && r[i].stream >= 0 &&
+            r[i + 1].stream >= 0 && r[i + 1].mat == r[i].mat) {
+            if (r[i].lo < end_w || r[i].lo < end_r) { err = "buffers of the matrix list overlap"; return ADAMW_E_INVALID; }
+            end_w = r[i].hi;
+            ++i;
+            continue;
+        }
+        if (r[i].lo < end_w || (w && r[i].lo < end_r)) {
+            err = r[i].stream < 0 ? "the workspace overlaps a buffer of the matrix list"
+                                  : "buffers of the matrix list overlap each other or the workspace";
+            return ADAMW_E_INVALID;
+        }
+        (w ? end_w : end_r) = std::max(w ? end_w : end_r, r[i].hi);
+    }
+    // The normalisation's launch has the most workgroups, one for 64 x 64 elements: a batch
+    // that passes the limit is counted before its tiles are listed.
+    for (const Shape& s : shapes)
+        if (tiles_of(s.rows, kPad) * tiles_of(s.cols, kPad) > kMaxNsTiles) {
+            err = "a matrix needs more than 8,421,504 tiles in one launch";
+            return ADAMW_E_INVALID;
+        }
+    if (!out) return ADAMW_OK;
+
+    *out = NsPlan();
+    const size_t n = shapes.size();
+    out->mats.resize(n);
+    for (size_t i = 0; i < n;) {
+        size_t end = i;
+        int64_t at = kNsHeadBytes, n_tiles = 0;
+        for (; end < n; ++end) {
+            DevMatrix m{};
+            const int64_t next = place(shapes[end], true, at, &m);
+            const int64_t t = tiles_of(shapes[end].rows, kPad) * tiles_of(shapes[end].cols, kPad);
+            if (next > workspace_bytes || (end > i && n_tiles + t > kMaxNsTiles)) break;
+            at = next;
+            n_tiles += t;
+            static const int kOf[4] = {ADAMW_STREAM_PARAM, ADAMW_STREAM_GRAD, ADAMW_STREAM_EXP_AVG, ADAMW_STREAM_AUX};
+            m.flat16 = 1;
+            for (int s = 0; s < 4; ++s) {
+                m.ptr[s] = plan.segs[end].ptr[kOf[s]];
+                if (m.ptr[s] % 16) m.flat16 = 0;
+            }
+            m.row16 = m.flat16 && m.cols % 8 == 0;
+            const double R = (double)m.rows, C = (double)m.cols;
+            m.factor = scaling == ADAMW_MUON_SCALE_SPECTRAL ? std::sqrt(std::max(1.0, R / C))
+                     : scaling == ADAMW_MUON_SCALE_RMS ? 0.2 * std::sqrt(std::max(R, C)) : 1.0;
+            out->mats[end] = m;
+        }
+        // the longest sums first
+        std::vector<size_t> order;
+        for (size_t k = i; k < end; ++k) order.push_back(k);
+        const auto long_side = [&](size_t k) { return std::max(out->mats[k].rp, out->mats[k].cp); };
+        NsBatch b;
+        std::vector<DevTile> tiles;
+        const auto take = [&](NsLaunch* l) {
+            l->first = (int64_t)out->tiles.size();
+            l->count = (int64_t)tiles.size();
+            deal_tiles(tiles, &out->tiles);
+            tiles.clear();
+        };
+        for (size_t k : order)
+            for (uint32_t c = 0; c < out->mats[k].n_partials; ++c) tiles.push_back(DevTile{(uint32_t)k, c, 0, 0});
+        take(&b.moments);
+        for (size_t k : order)
+            for (int32_t y = 0; y < out->mats[k].rp / kPad; ++y)
+                for (int32_t x = 0; x < out->mats[k].cp / kPad; ++x)
+                    tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
+        take(&b.normalise);
+        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return long_side(x) > long_side(y); });
+        b.square.kind = pick_kind([&](int side) {
+            int64_t t = 0;
+            for (size_t k : order) t += square_tiles(out->mats[k].s, side);
+            return t;
+        });
+        b.apply.kind = pick_kind([&](int side) {
+            int64_t t = 0;
+            for (size_t k : order) t += tiles_of(out->mats[k].rows, side) * tiles_of(out->mats[k].cols, side);
+            return t;
+        });
+        // bands of 4 tile rows, column by column
+        constexpr int64_t kBand = 4;
+        for (size_t k : order) {
+            const int64_t t = tiles_of(out->mats[k].s, kTileSide[b.square.kind]);
+            for (int64_t y0 = 0; y0 < t; y0 += kBand)
+                for (int64_t x = 0; x < std::min(t, y0 + kBand); ++x)
+                    for (int64_t y = std::max(y0, x); y < std::min(t, y0 + kBand); ++y)
+                        tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
+        }
+        take(&b.square);
+        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].sp > out->mats[y].sp; });
+        for (size_t k : order) {
+            const int64_t ty = tiles_of(out->mats[k].rows, kTileSide[b.apply.kind]);
+            const int64_t tx = tiles_of(out->mats[k].cols, kTileSide[b.apply.kind]);
+            for (int64_t y0 = 0; y0 < ty; y0 += kBand)
+                for (int64_t x = 0; x < tx; ++x)
+                    for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
+                        tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
+        }
+        take(&b.apply);
+        out->batches.push_back(b);
+        i = end;
+    }
+    return ADAMW_OK;
+}
+
+}  // namespace adamw

@@ -121,7 +121,7 @@
 extern "C" {
 #endif
 
-#define ADAMW_ABI_VERSION 9
+#define ADAMW_ABI_VERSION 10
 
 typedef enum {
     ADAMW_OK = 0,
@@ -436,6 +436,120 @@ adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtyp
                                              const adamw_grad_clip* clip, int32_t* d_step, const int32_t* d_found_inf,
                                              adamw_loss_scale_state* d_scale, const adamw_loss_scaler* scaler,
                                              void* hip_stream);
+
+/* Matrices.  A list of matrices is an adamw_tensor_list with a host array `cols` of
+ * n_tensors column counts (each >= 1): tensor i is the row-major matrix of
+ * numel[i] / cols[i] rows (numel[i] a multiple of cols[i]; 0 elements: nothing is done
+ * for it).  A convolution's weight is the matrix of its flattened filters, the experts of
+ * a stacked weight are matrices at consecutive addresses, and so are the parts of a fused
+ * projection that lie one under another.  A shard takes whole matrices: shard_begin and
+ * shard_end have to lie between matrices (the matrices of a ZeRO job are dealt out whole,
+ * since a matrix's singular values are no rank's share of it).  flat_mask bits of the streams
+ * used and ADAMW_FLAT_PAD8 are honoured; ADAMW_BLOCKED_STATE is refused
+ * (ADAMW_E_UNSUPPORTED).
+ *
+ * Newton-Schulz products.  For a matrix U let X = U / (|U| + eps), |U| the root of the
+ * sum of its squares, and `steps` times
+ *     X <- a X + b (X X^T) X + c (X X^T)^2 X ,
+ * which moves every singular value x of X to a x + b x^3 + c x^5 and keeps the singular
+ * vectors; coefficients that take (0, 1] towards 1 make X the nearest
+ * (semi-)orthogonal matrix U (U^T U)^(-1/2), approximately (Higham, "Functions of Matrices",
+ * SIAM 2008, section 8.3).  With the default coefficients (3.4445, -4.7750, 2.0315) and
+ * five steps singular values above about a hundredth of |U| end between 0.68 and 1.14, as
+ * the Muon optimizer uses them.
+ *
+ * Numerics.  |U| is summed in binary64.  X is held as a sum of two fp16 values (22 bits)
+ * under a power of two, X X^T and the polynomial of it as fp16 with their diagonals in
+ * fp32; products are of fp16 values with fp32 sums, and the linear term a X keeps all 22 bits, so
+ * that small singular values, which a step multiplies by a, are not drowned in rounding.
+ * The result is within about 1e-3 (relative, in the Frobenius norm) of the definition's value;
+ * the same call gives the same bits.  A matrix with an inf or NaN element has NaN in
+ * every element of its result, a zero matrix zeros; no matrix changes another's.
+ *
+ * Requirements: a, b, c finite, eps finite and >= 0, 1 <= steps <= ADAMW_NS_MAX_STEPS;
+ * coefficients under which a singular value of [0, 1] passes 64 on the way are refused. */
+enum { ADAMW_NS_MAX_STEPS = 16 };
+typedef struct {
+    float a;
+    float b;
+    float c;
+    float eps;
+    int32_t steps;
+} adamw_newton_schulz;
+
+/* Bytes of device workspace with which the two calls below work through `list` (its
+ * numel, shard and ADAMW_FLAT_PAD8; pointers are not looked at) at full speed: room for
+ * all its matrices, about 12 bytes an element, or of a longer list for 4 GiB of them at
+ * a time.  With `least` != 0, the smallest workspace that they take: room for the
+ * largest matrix.  -1 on an invalid argument.  No GPU work, no HIP call. */
+int64_t adamw_orthogonalize_workspace_bytes(const adamw_tensor_list* list, const int64_t* cols, int least);
+
+/* Orthogonalises every matrix of a list: stream 0 (bf16, written) = the result of the
+ * Newton-Schulz products of stream 1 (u_dtype: ADAMW_F32, ADAMW_BF16 or ADAMW_F16; read
+ * only), for optimizers with a rule of their own.  A bf16 matrix may be its own
+ * result (equal addresses); any other overlap of a result with a matrix, a result or the
+ * workspace is refused.
+ * workspace: device memory of the caller, 256-byte aligned, of at least
+ * adamw_orthogonalize_workspace_bytes(list, cols, 1) bytes; its contents need not be kept between
+ * calls and are not read before they are written.  Calls that may overlap in time,
+ * replays of captured ones among them, need a workspace each.
+ * Execution, graphs and errors as adamw_multi_tensor_step. */
+adamw_status adamw_orthogonalize(adamw_dtype u_dtype, const adamw_tensor_list* list, const int64_t* cols,
+                                 const adamw_newton_schulz* ns, void* workspace, int64_t workspace_bytes,
+                                 void* hip_stream);
+
+/* The factor s of a Muon step's update of an R x C matrix. */
+enum {
+    ADAMW_MUON_SCALE_NONE = 0,      /* 1 */
+    ADAMW_MUON_SCALE_SPECTRAL = 1,  /* sqrt(max(1, R / C)) */
+    ADAMW_MUON_SCALE_RMS = 2        /* 0.2 sqrt(max(R, C)): the usual root mean square of an AdamW update, so
+                                       that learning rate and weight decay may be those of the AdamW step */
+};
+
+/* Hyper-parameters of a Muon step.  Requirements: all finite; lr, weight_decay >= 0;
+ * 0 <= momentum < 1; inv_loss_scale > 0; nesterov 0 or 1; scaling as above. */
+typedef struct {
+    float lr;
+    float momentum;
+    float weight_decay;
+    float inv_loss_scale;
+    int32_t nesterov;
+    int32_t scaling;
+    adamw_newton_schulz ns;
+} adamw_muon_hparams;
+
+/* One Muon step over a list of matrices, for the hidden layers' weights beside an AdamW
+ * step over everything else (embeddings, vectors).  Momentum, orthogonalised,
+ * with decoupled weight decay:
+ *
+ *   g = grad * mult
+ *   m = momentum*m + (1-momentum)*g
+ *   u = momentum*m + (1-momentum)*g if nesterov, else m
+ *   O = the Newton-Schulz products of u (above)
+ *   ADAMW_MIXED:       w = w*(1 - lr*wd) - (lr*s)*O;  param = round16(w)
+ *   ADAMW_MIXED_SPLIT: the same on the split master
+ *   ADAMW_PURE_KAHAN, or with prec non-null the pure-bf16 step of *prec (mode and p_dtype
+ *                      ignored; its exp_avg_sq is not used): d = -(lr*wd)*p - (lr*s)*O;
+ *                      s' = c + d;  p' = round_bf16(p + s');  c = s' - (p' - p) rounded to its
+ *                      dtype; without compensation p = round_bf16(p*(1 - lr*wd) - (lr*s)*O)
+ *
+ * Streams, dtypes and roundings as in the AdamW step of the same mode; exp_avg is m (bf16
+ * m is widened, updated and used in fp32 and stored rounded), stream 3 (exp_avg_sq) is
+ * not used.  Each line but O's is in binary32, as written, without fused multiply-add; lr*s, lr*wd and
+ * 1 - lr*wd are formed in binary64 and rounded once.  O is used as the fp32 sum it is, without a 16-bit rounding.
+ * mult is the inverse loss scale, hp->inv_loss_scale or with d_scale non-null
+ * (float)(1 / (double)d_scale->scale) read on the device, and with clip non-null
+ * round_f32(that * f), f the clipping factor of adamw_multi_tensor_step_clipped.  *d_scale is
+ * never advanced here: the AdamW call of the same iteration does that, and comes last.  The step is skipped, and nothing written,
+ * if *d_found_inf (nullable) is set or *clip->d_sumsq is not finite; else the counter
+ * *d_step advances as in adamw_multi_tensor_step.  The buffers of the list may not overlap each other
+ * or the workspace, which is that of adamw_orthogonalize.  Execution, graphs and
+ * errors as adamw_multi_tensor_step. */
+adamw_status adamw_muon_multi_tensor_step(adamw_mode mode, adamw_dtype p_dtype, const adamw_pure_precision* prec,
+                                          const adamw_tensor_list* list, const int64_t* cols,
+                                          const adamw_muon_hparams* hp, const adamw_grad_clip* clip, int32_t* d_step,
+                                          const int32_t* d_found_inf, const adamw_loss_scale_state* d_scale,
+                                          void* workspace, int64_t workspace_bytes, void* hip_stream);
 
 /* Description of the last error on the calling thread ("" if none).  Valid
  * until the next call into the library on that thread. */

@@ -1,0 +1,242 @@
+// muon_check.cpp -- the planner of the Newton-Schulz products under AddressSanitizer and
+// UndefinedBehaviorSanitizer, on the CPU with synthetic (never dereferenced) device
+// addresses.  Built by tests/test_muon_cpu.py with g++ together with muon_plan.cpp, plan.cpp and
+// validate.cpp; prints "muon_check ok" and a checksum of every plan (the same with and without
+// the sanitizers), or aborts.
+//
+// Every plan is checked: each matrix lies in one batch; its parts of the workspace lie inside the
+// workspace and apart from each other and from the other matrices' of the batch; and each launch's
+// workgroups cover every matrix of the batch exactly once (the square ones: the tiles on and below
+// the diagonal).  The overlap search is compared with a quadratic one.
+#include <stdio.h>
+#include <stdlib.h>
+
+#include <algorithm>
+#include <map>
+#include <string>
+#include <utility>
+#include <vector>
+
+#include "muon.hpp"
+#include "plan.hpp"
+
+using namespace adamw;
+
+namespace {
+
+uint64_t g_sum = 1469598103934665603ull;
+void mix(uint64_t x) { g_sum = (g_sum ^ x) * 1099511628211ull; }
+
+#define CHECK(c)                                                                  \
+    do {                                                                          \
+        if (!(c)) {                                                               \
+            fprintf(stderr, "%s:%d: check failed: %s\n", __FILE__, __LINE__, #c); \
+            abort();                                                              \
+        }                                                                         \
+    } while (0)
+
+struct Rng {
+    uint64_t s;
+    uint64_t next()
+    {
+        s ^= s << 13;
+        s ^= s >> 7;
+        s ^= s << 17;
+        return s;
+    }
+    int64_t below(int64_t n) { return n > 0 ? (int64_t)(next() % (uint64_t)n) : 0; }
+};
+
+struct Range {
+    uint64_t lo, hi;
+};
+bool apart(const Range& x, const Range& y) { return x.hi <= y.lo || y.hi <= x.lo; }
+
+struct List {
+    std::vector<int64_t> numel, cols;
+    std::vector<void*> ptr[kStreams];
+    adamw_tensor_list c;
+    adamw_tensor_list* get()
+    {
+        c.n_tensors = (int64_t)numel.size();
+        c.numel = numel.data();
+        for (int s = 0; s < kStreams; ++s) c.ptr[s] = ptr[s].data();
+        return &c;
+    }
+};
+
+void check_batch(const NsPlan& plan, const NsBatch& b, std::vector<int>& seen, int64_t bytes, bool step)
+{
+    // the matrices of the batch, by its moments' workgroups
+    std::map<uint32_t, std::vector<int>> runs;
+    for (int64_t i = 0; i < b.moments.count; ++i) {
+        const DevTile& t = plan.tiles[(size_t)(b.moments.first + i)];
+        CHECK(t.mat < plan.mats.size());
+        auto& v = runs[t.mat];
+        if (v.empty()) v.resize(plan.mats[t.mat].n_partials);
+        CHECK(t.row < v.size() && !v[t.row]);
+        v[t.row] = 1;
+    }
+    std::vector<Range> parts;
+    for (auto& kv : runs) {
+        CHECK(!seen[kv.first]);
+        seen[kv.first] = 1;
+        const DevMatrix& m = plan.mats[kv.first];
+        for (int x : kv.second) CHECK(x);
+        const int64_t n = (int64_t)m.rows * m.cols, pad = (int64_t)m.rp * m.cp, sq = (int64_t)m.sp * m.sp;
+        CHECK((int64_t)m.n_partials * kMomentElems >= n && ((int64_t)m.n_partials - 1) * kMomentElems < n);
+        CHECK(m.rp % kPad == 0 && m.rp >= m.rows && m.rp < m.rows + kPad && m.cp % kPad == 0 && m.cp >= m.cols &&
+              m.cp < m.cols + kPad);
+        CHECK(m.s == std::min(m.rows, m.cols) && m.sp == (m.tall ? m.cp : m.rp) && (m.tall != 0) == (m.rows > m.cols));
+        const Range r[8] = {{m.hi, m.hi + 2 * pad}, {m.lo, m.lo + 2 * pad}, {m.t, m.t + 2 * pad}, {m.y, m.y + 2 * pad},
+                            {m.a, m.a + 2 * sq}, {m.b, m.b + 2 * sq}, {m.da, m.da + 4 * m.sp}, {m.db, m.db + 4 * m.sp}};
+        for (const Range& x : r) parts.push_back(x);
+        parts.push_back(Range{m.partials, m.partials + 8 * (uint64_t)m.n_partials});
+        if (step) {   // u's room: that of y, a and b, and nothing else's
+            const Range u{m.u, m.u + 4 * (uint64_t)n};
+            CHECK(u.hi <= (uint64_t)bytes && apart(u, r[0]) && apart(u, r[1]) && apart(u, r[2]) && apart(u, r[6]) &&
+                  apart(u, r[7]) && u.hi <= m.partials);
+        }
+        for (int k : {0, 1, 2, 3, 4, 5, 6, 7}) CHECK(r[k].lo % kNsAlign == 0);
+        for (uint64_t x : {m.rows, m.cols, m.sp, m.tall}) mix(x);
+        mix(m.hi);
+        mix(m.partials);
+    }
+    for (const Range& x : parts) CHECK(x.lo >= (uint64_t)kNsHeadBytes && x.hi <= (uint64_t)bytes);
+    std::sort(parts.begin(), parts.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    for (size_t i = 1; i < parts.size(); ++i) CHECK(apart(parts[i - 1], parts[i]));
+
+    const auto cover = [&](const NsLaunch& l, int side, bool square, bool padded) {
+        std::map<uint32_t, std::map<std::pair<uint32_t, uint32_t>, int>> got;
+        for (int64_t i = 0; i < l.count; ++i) {
+            const DevTile& t = plan.tiles[(size_t)(l.first + i)];
+            CHECK(runs.count(t.mat) && !got[t.mat][std::make_pair(t.row, t.col)]++);
+            mix(t.mat * 31 + t.row * 7 + t.col);
+        }
+        CHECK(got.size() == runs.size());
+        for (auto& kv : got) {
+            const DevMatrix& m = plan.mats[kv.first];
+            const int64_t h = square ? m.sp : padded ? m.rp : m.rows, w = square ? m.sp : padded ? m.cp : m.cols;
+            const int64_t ty = (h + side - 1) / side, tx = (w + side - 1) / side;
+            CHECK((int64_t)kv.second.size() == (square ? ty * (ty + 1) / 2 : ty * tx));
+            for (auto& t : kv.second) {
+                CHECK(t.first.first < ty && t.first.second < tx);
+                if (square) CHECK(t.first.second <= t.first.first);
+            }
+        }
+        CHECK(l.count <= kMaxNsTiles);
+    };
+    cover(b.normalise, kPad, false, true);
+    cover(b.square, kTileSide[b.square.kind], true, true);
+    cover(b.apply, kTileSide[b.apply.kind], false, true);
+}
+
+void one_list(Rng& r)
+{
+    const bool step = r.below(2), f32 = r.below(2);
+    NsKind kind{};
+    kind.end = step ? kEndMixedBf16 : kEndOrtho;
+    kind.in = !step && f32 ? ADAMW_F32 : ADAMW_BF16;
+    kind.esz[ADAMW_STREAM_PARAM] = 2;
+    kind.esz[ADAMW_STREAM_GRAD] = kind.in == ADAMW_F32 ? 4 : 2;
+    if (step) kind.esz[ADAMW_STREAM_EXP_AVG] = kind.esz[ADAMW_STREAM_AUX] = 4;
+    List l{};
+    const int64_t nt = r.below(12), pad8 = r.below(2);
+    const int64_t most = r.below(4) == 0 ? 3000 : 200;
+    uint64_t at = 0x7f0000000000ull;
+    std::vector<Range> buffers;
+    std::vector<int> writes;
+    int64_t total = 0;
+    std::vector<int64_t> starts;
+    for (int64_t i = 0; i < nt; ++i) {
+        const int64_t rows = r.below(20) ? 1 + r.below(most) : 0, cols = 1 + r.below(most);
+        l.numel.push_back(rows * cols);
+        l.cols.push_back(cols);
+        starts.push_back(total);
+        total += pad8 ? (rows * cols + 7) / 8 * 8 : rows * cols;
+        for (int s = 0; s < kStreams; ++s) {
+            if (!kind.esz[s]) {
+                l.ptr[s].push_back(nullptr);
+                continue;
+            }
+            at += (uint64_t)kind.esz[s] * (uint64_t)r.below(9);
+            at = (at + 3) / 4 * 4;
+            l.ptr[s].push_back(reinterpret_cast<void*>(at));
+            if (rows) {
+                buffers.push_back(Range{at, at + (uint64_t)(rows * cols * kind.esz[s])});
+                writes.push_back(s != ADAMW_STREAM_GRAD);
+            }
+            at += (uint64_t)(rows * cols * kind.esz[s]);
+        }
+    }
+    starts.push_back(total);
+    l.c.shard_begin = 0;
+    l.c.shard_end = -1;
+    l.c.flat_mask = pad8 ? ADAMW_FLAT_PAD8 : 0;
+    std::string err;
+    int64_t bytes = 0, least = 0;
+    CHECK(ns_workspace_bytes(l.get(), l.cols.data(), false, &bytes, err) == ADAMW_OK);
+    CHECK(ns_workspace_bytes(l.get(), l.cols.data(), true, &least, err) == ADAMW_OK);
+    CHECK(least <= bytes && least >= kNsHeadBytes);
+    const int64_t take = r.below(2) ? bytes : least + r.below(bytes - least + 1);
+    const uint64_t ws = 0x600000000000ull;
+    NsPlan plan;
+    CHECK(build_ns_plan(kind, l.get(), l.cols.data(), (int)r.below(3), ws, take, &plan, err) == ADAMW_OK);
+    std::vector<int> seen(plan.mats.size());
+    for (const NsBatch& b : plan.batches) check_batch(plan, b, seen, take, step);
+    for (int x : seen) CHECK(x);
+    if (take == bytes) CHECK(plan.batches.size() <= 1);
+    CHECK(build_ns_plan(kind, l.get(), l.cols.data(), 0, ws, least - 1, nullptr, err) == ADAMW_E_INVALID);
+    CHECK(build_ns_plan(kind, l.get(), l.cols.data(), 0, ws + 8, take, nullptr, err) == ADAMW_E_INVALID);
+
+    // a buffer moved somewhere near another one
+    if (buffers.size() >= 2) {
+        const int64_t i = r.below(nt);
+        int s = (int)r.below(kStreams);
+        while (!kind.esz[s]) s = (s + 1) % kStreams;
+        if (l.numel[(size_t)i]) {
+            const uint64_t to = (buffers[(size_t)r.below((int64_t)buffers.size())].lo + 4 * (uint64_t)r.below(64)) / 4 * 4;
+            l.ptr[s][(size_t)i] = reinterpret_cast<void*>(to);
+            std::vector<Range> now;
+            std::vector<int> w, mat;
+            for (int64_t k = 0; k < nt; ++k)
+                for (int q = 0; q < kStreams; ++q)
+                    if (kind.esz[q] && l.numel[(size_t)k]) {
+                        const uint64_t a = (uint64_t)(uintptr_t)l.ptr[q][(size_t)k];
+                        now.push_back(Range{a, a + (uint64_t)(l.numel[(size_t)k] * kind.esz[q])});
+                        w.push_back(q != ADAMW_STREAM_GRAD);
+                        mat.push_back((int)k);
+                    }
+            bool bad = false;
+            for (size_t x = 0; x < now.size(); ++x)
+                for (size_t y = 0; y < x; ++y) {
+                    const bool own = !step && kind.in == ADAMW_BF16 && mat[x] == mat[y] && now[x].lo == now[y].lo;
+                    if (!own && (w[x] || w[y]) && !apart(now[x], now[y])) bad = true;
+                }
+            const adamw_status st = build_ns_plan(kind, l.get(), l.cols.data(), 0, ws, take, nullptr, err);
+            CHECK((st != ADAMW_OK) == bad);
+            mix((uint64_t)bad);
+        }
+    }
+    // a shard between two matrices, and one that cuts a matrix
+    if (nt >= 2) {
+        l.c.shard_begin = starts[(size_t)r.below(nt)];
+        l.c.shard_end = starts[(size_t)nt];
+        CHECK(ns_workspace_bytes(l.get(), l.cols.data(), true, &least, err) == ADAMW_OK);
+        const size_t k = (size_t)r.below(nt);
+        if (l.numel[k] >= 2) {
+            l.c.shard_begin = starts[k] + 1;
+            CHECK(ns_workspace_bytes(l.get(), l.cols.data(), true, &least, err) == ADAMW_E_INVALID);
+        }
+    }
+}
+
+}  // namespace
+
+int main()
+{
+    Rng r{88172645463325252ull};
+    for (int i = 0; i < 1500; ++i) one_list(r);
+    printf("muon_check ok %016llx\n", (unsigned long long)g_sum);
+    return 0;
+}
