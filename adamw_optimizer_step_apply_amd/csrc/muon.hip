@@ -6,14 +6,11 @@
 // shorter side; both are symmetric, and only the tiles on and below the diagonal are
 // computed and written to both places.
 //
-// All three products are sums over the last index of both factors, C[i][j] = sum_k
-// P[i][k] Q[j][k], the form in which every lane's operand of a matrix instruction
-// is 16 bytes of a row:
-//   gram   P = Q = X in the order whose rows are the shorter side
-//   poly   P = Q = A
-//   apply  wide: P = B, Q = X^T;  tall: P = X, Q = B
-// X is therefore kept in both orders (hi and t); the tile leaves the accumulators through
-// LDS, from where it is read once by rows and once by columns.
+// X is held wide, transposed where the matrix is tall, so that A and B belong to its rows.  A tile of a product
+// C[i][j] = sum_k P[i][k] Q[k][j] takes P by rows, 16 bytes of a row for a lane's operand of a matrix
+// instruction; A and B are symmetric, so Q is by rows too in gram (Q = P = X, transposed) and
+// poly (Q = P = A), while in apply (P = B, Q = X) its operands are columns, which LDS
+// returns transposed (ds_read_b64_tr_b16).
 //
 // Numerics.  A step multiplies a small singular value by a, five of them by 485, and with
 // it the rounding of X.  So X is the pair hi + lo of fp16 (22 bits) under the power of two
@@ -29,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "adamw.h"
 #include "device.hpp"
 #include "layout.hpp"
@@ -37,6 +36,8 @@
 namespace adamw {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLoScale = 2048.0f;   // lo is held as lo * 2^11, of the size of hi
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(kBlockMoments) void ns_moments_kernel(const DevMatr
 }
 
 // ---------------------------------------------------------------------------
-// Normalisation: X = u / (|u| + eps) into hi, lo and t, zeros in the padding.
+// Normalisation: X = u / (|u| + eps) into hi and lo, zeros in the padding.
 // ---------------------------------------------------------------------------
 
 // x * 2^sx as hi + lo * 2^-11
@@ -209,6 +210,19 @@ __device__ __forceinline__ void split_pair(float x, _Float16& hi, _Float16& lo)
 {
     hi = (_Float16)x;
     lo = (_Float16)((x - (float)hi) * kLoScale);
+}
+
+// 4 neighbouring elements, from an address aligned to their size
+template <int IN>
+__device__ __forceinline__ f32x4 load4(uint64_t base, uint64_t i)
+{
+    if constexpr (IN == kInF32) {
+        return *reinterpret_cast<const GLOBAL f32x4*>(gptr<const float>(base, i));
+    } else {
+        const u32x2 w = *reinterpret_cast<const GLOBAL u32x2*>(gptr<const uint16_t>(base, i));
+        const f32x2 a = widen2<IN == kInF16>(w.x), b = widen2<IN == kInF16>(w.y);
+        return f32x4{a.x, a.y, b.x, b.y};
+    }
 }
 
 template <int IN>
@@ -228,6 +242,28 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
 #pragma unroll
     for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
     if (tid % 64 == 0) part[tid / 64] = sum;
+
+    // the tile as it lies in the matrix: rows of `u`, by fours where every row starts at a multiple of 4 elements
+    const bool tall = mx.tall != 0;
+    const uint32_t r0 = (tall ? t.col : t.row) * kPad, c0 = (tall ? t.row : t.col) * kPad;
+    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols;
+    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + mx.u : mx.ptr[1];
+    const bool by4 = cols % 4 == 0 && (step || in % 16 == 0);
+    f32x4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t r = r0 + (uint32_t)k * 16 + tid / 16, c = c0 + tid % 16 * 4;
+        x[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (r >= rows) continue;
+        const uint64_t i = (uint64_t)r * cols + c;
+        if (by4) {
+            if (c < cols) x[k] = load4<IN>(in, i);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols) x[k][e] = load1<IN>(in, i + e);
+        }
+    }
     __syncthreads();
     sum = ((part[0] + part[1]) + part[2]) + part[3];
     const double len = __builtin_sqrt(sum) + (double)eps;
@@ -237,25 +273,29 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
     constexpr int kLd = 72;   // 144-byte rows: 16-byte reads stay aligned
     __shared__ alignas(16) _Float16 hi[kPad * kLd];
     __shared__ alignas(16) _Float16 lo[kPad * kLd];
-    const uint32_t r0 = t.row * kPad, c0 = t.col * kPad;
-    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + mx.u : mx.ptr[1];
-    for (uint32_t k = 0; k < kPad / 4; ++k) {
-        const uint32_t r = k * 4 + tid / 64, c = tid % 64;
-        float x = 0.0f;
-        if (r0 + r < (uint32_t)mx.rows && c0 + c < (uint32_t)mx.cols)
-            x = (float)((double)load1<IN>(in, (uint64_t)(r0 + r) * (uint64_t)mx.cols + c0 + c) * scale);
-        split_pair(x, hi[r * kLd + c], lo[r * kLd + c]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t o = ((uint32_t)k * 16 + tid / 16) * kLd + tid % 16 * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_pair((float)((double)x[k][e] * scale), hi[o + e], lo[o + e]);
     }
     __syncthreads();
     for (uint32_t k = tid; k < kPad * 8; k += 256) {
         const uint32_t r = k / 8, c = k % 8 * 8;
-        const uint64_t o = (uint64_t)(r0 + r) * (uint64_t)mx.cp + c0 + c;
-        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.hi) + o) = *reinterpret_cast<const f16x8*>(hi + r * kLd + c);
-        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.lo) + o) = *reinterpret_cast<const f16x8*>(lo + r * kLd + c);
-        f16x8 v;
+        const uint64_t o = (uint64_t)(t.row * kPad + r) * (uint64_t)mx.lp + t.col * kPad + c;
+        f16x8 h, l;
+        if (tall) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = hi[(c + e) * kLd + r];
-        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.t) + (uint64_t)(c0 + r) * (uint64_t)mx.rp + r0 + c) = v;
+            for (int e = 0; e < 8; ++e) {
+                h[e] = hi[(c + e) * kLd + r];
+                l[e] = lo[(c + e) * kLd + r];
+            }
+        } else {
+            h = *reinterpret_cast<const f16x8*>(hi + r * kLd + c);
+            l = *reinterpret_cast<const f16x8*>(lo + r * kLd + c);
+        }
+        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.hi[0]) + o) = h;
+        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.lo) + o) = l;
     }
 }
 
@@ -269,6 +309,7 @@ struct ProductArgs {
     float a, b, c;
     int sx, sa, sb;
     int parity;      // of the product step: which of the two buffers X is in
+    int keep_lo;     // the next step is not the last
     int step;        // a Muon step: its skip mark is looked at
     float lr, decay, lrwd;   // a step's last epilogue
 };
@@ -284,54 +325,117 @@ __device__ __forceinline__ void load_to_lds(const GLOBAL char* from, char* to)
     __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
+__device__ __forceinline__ f16x4 read_transposed(const char* p)
+{
+    return __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4*)const_cast<char*>(p)));
+}
+
+// A workgroup's waves take 2 x wx parts of its tile.  `stages` runs of kPad summed elements of both
+// factors are in LDS at once, all but one of them on their way.
 template <int KIND>
-struct TileShape;
-template <>
-struct TileShape<0> {
-    static constexpr int side = 256, wy = 2, wx = 4;
-};
-template <>
-struct TileShape<1> {
-    static constexpr int side = 128, wy = 2, wx = 2;
-};
-template <>
-struct TileShape<2> {
-    static constexpr int side = 64, wy = 2, wx = 2;
+struct TileShape {
+    static constexpr int rows = kTileRows[KIND], cols = kTileCols[KIND], lanes = kTileLanes[KIND], waves = lanes / 64;
+    static constexpr int wx = waves / 2, stages = KIND == 2 ? 4 : 2;
 };
 
-// Loads `side` rows of one summing step (kPad elements, 128 bytes a row) of a factor into
-// LDS without passing registers.  A wave's access fills 8 rows (1 KiB) in order; the 16-byte words of row r
-// are exchanged, word c in place c ^ (r & 7), by the addresses that the lanes read from,
-// so that the reads of a matrix instruction's operand, one word of 32 rows each, spread
-// over all banks.  Rows past the matrix read its last row again; what they give is not stored.
-template <int SIDE, int WAVES>
-struct Stage {
-    static constexpr int kLoads = SIDE / 8 / WAVES;
+// Loads of one summing step of a factor into LDS that do not pass registers.  A wave's access fills 1 KiB in order;
+// 16-byte words are exchanged by the addresses that the lanes read from.
+
+// ROWS rows of 128 bytes.  Word w of row r lies in place w ^ (r / 2 % 8): the operand of a matrix
+// instruction takes one word of 32 rows, 16 rows at a time ({0-3, 12-15, 20-23, 24-27} and the
+// others), which with this exchange lie in 16 different words of 256 bytes, all the banks
+// there are.  Rows past the factor read its last row again; what they give is not stored.
+template <int ROWS, int WAVES>
+struct RowStage {
+    static constexpr int kLoads = ROWS / 8 / WAVES;
     const GLOBAL char* src[kLoads];
-    uint32_t lds[kLoads];
 
-    __device__ __forceinline__ void init(const GLOBAL _Float16* p, uint32_t row0, uint32_t rows, uint32_t ld, uint32_t wave,
+    __device__ __forceinline__ void init(const GLOBAL _Float16* p, uint32_t row0, uint32_t rows, uint32_t pitch, uint32_t wave,
                                          uint32_t lane)
     {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t r = (wave * kLoads + (uint32_t)i) * 8 + lane / 8;
             const uint32_t row = row0 + r < rows ? row0 + r : rows - 1;
-            src[i] = reinterpret_cast<const GLOBAL char*>(p + (uint64_t)row * ld) + ((lane ^ (lane >> 3)) & 7u) * 16;
-            lds[i] = (wave * kLoads + (uint32_t)i) * 1024;
+            src[i] = reinterpret_cast<const GLOBAL char*>(p + (uint64_t)row * pitch) + ((lane ^ (r >> 1)) & 7u) * 16;
         }
     }
-    __device__ __forceinline__ void load(char* buf, uint32_t k)
+    __device__ __forceinline__ void load(char* buf, uint32_t k, uint32_t wave) const
     {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            load_to_lds(src[i] + (uint64_t)k * (kPad * 2), buf + lds[i]);
+            load_to_lds(src[i] + (uint64_t)k * (kPad * 2), buf + (wave * kLoads + (uint32_t)i) * 1024);
+    }
+    // word 2 kk + lane / 32 of row lane % 32 of the 32 rows from `row` on
+    static __device__ __forceinline__ f16x8 operand(const char* buf, uint32_t row, uint32_t kk, uint32_t lane)
+    {
+        const uint32_t r = row + (lane & 31u), w = (kk * 2 + (lane >> 5)) ^ ((r >> 1) & 7u);
+        return *reinterpret_cast<const f16x8*>(buf + r * (kPad * 2) + w * 16);
     }
 };
 
-__device__ __forceinline__ f16x8 operand(const char* buf, uint32_t row, uint32_t word)
+// 64 rows of COLS elements, whose columns are the operands.  A transposing read takes 4 rows by 32 columns
+// (64 bytes) for each half wave; 64 bytes number c of row r lie in place c ^ (r % 4) (two
+// rows to 256 bytes: c ^ (r / 2 % 2)), so that the four rows fall on all the banks.  Columns
+// past the factor read its last ones again.
+template <int COLS, int WAVES>
+struct ColumnStage {
+    static constexpr int kLoads = COLS / 8 / WAVES, kRowBytes = COLS * 2, kWords = COLS / 8;
+    const GLOBAL char* src[kLoads];
+    uint64_t step;
+
+    static __device__ __forceinline__ uint32_t exchange(uint32_t row)
+    {
+        return (COLS == 64 ? row >> 1 & 1u : row & 3u) * 4;
+    }
+    __device__ __forceinline__ void init(const GLOBAL _Float16* p, uint32_t col0, uint32_t cols, uint32_t pitch, uint32_t wave,
+                                         uint32_t lane)
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t w = (wave * kLoads + (uint32_t)i) * 64 + lane, r = w / kWords;
+            const uint32_t c = col0 + ((w % kWords) ^ exchange(r)) * 8;
+            src[i] = reinterpret_cast<const GLOBAL char*>(p + (uint64_t)r * pitch + (c < cols ? c : cols - 8));
+        }
+        step = (uint64_t)pitch * (kPad * 2);
+    }
+    __device__ __forceinline__ void load(char* buf, uint32_t k, uint32_t wave) const
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load_to_lds(src[i] + k * step, buf + (wave * kLoads + (uint32_t)i) * 1024);
+    }
+    // rows 16 kk + lane / 32 * 8 .. + 7 of column lane % 32 of the 32 from `col` on: two reads of 4 rows each, for
+    // which lane i of 16 gives the address of 4 columns of row i / 4 and gets column i
+    static __device__ __forceinline__ f16x8 operand(const char* buf, uint32_t col, uint32_t kk, uint32_t lane)
+    {
+        const uint32_t r = kk * 16 + (lane >> 5) * 8 + (lane >> 2 & 3u), c = col + (lane & 16u) + (lane & 3u) * 4;
+        const char* p = buf + r * kRowBytes + ((c / 8) ^ exchange(r)) * 16 + (c & 4u) * 2;
+        const f16x4 a = read_transposed(p), b = read_transposed(p + 4 * kRowBytes);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// Waits until at most N of the wave's loads are under way and its reads of LDS have arrived, then for the
+// other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_meet()
 {
-    return *reinterpret_cast<const f16x8*>(buf + row * 128 + ((word ^ (row & 7u)) << 4));
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// 8 neighbouring floats
+__device__ __forceinline__ void read8(const GLOBAL float* p, float (&x)[8])
+{
+    const GLOBAL f32x4* q = reinterpret_cast<const GLOBAL f32x4*>(p);
+    const f32x4 a = q[0], b = q[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[k] = a[k];
+        x[k + 4] = b[k];
+    }
 }
 
 __device__ __forceinline__ uint32_t join_master(uint32_t p16, uint32_t r16)
@@ -384,49 +488,90 @@ __device__ __forceinline__ void end_elem(const DevMatrix& mx, uint64_t i, float 
     }
 }
 
+// What the end reads of 8 neighbouring elements: master; param and remainder; param and compensation.
 template <int END>
-__device__ __forceinline__ void end_eight(const DevMatrix& mx, uint64_t i, const float (&o)[8], float stepf,
-                                          const ProductArgs& q)
+struct EndInput {
+    u32x4 p, aux0, aux1;
+};
+
+template <int END>
+__device__ __forceinline__ EndInput<END> end_input(const DevMatrix& mx, uint64_t i)
+{
+    constexpr bool kParam = END == kEndSplit || END == kEndPure || END == kEndKahan || END == kEndKahan32;
+    constexpr bool kAux32 = END == kEndMixedBf16 || END == kEndMixedF16 || END == kEndKahan32;
+    EndInput<END> in{};
+    if constexpr (kParam) in.p = *reinterpret_cast<const GLOBAL u32x4*>(gptr<const uint16_t>(mx.ptr[0], i));
+    if constexpr (kAux32) {
+        const GLOBAL u32x4* w = reinterpret_cast<const GLOBAL u32x4*>(gptr<const float>(mx.ptr[3], i));
+        in.aux0 = w[0];
+        in.aux1 = w[1];
+    } else if constexpr (END == kEndSplit || END == kEndKahan) {
+        in.aux0 = *reinterpret_cast<const GLOBAL u32x4*>(gptr<const uint16_t>(mx.ptr[3], i));
+    }
+    return in;
+}
+
+// 8 values of two words of four fp32, or of one of eight bf16
+__device__ __forceinline__ void as_floats(const u32x4& a, const u32x4& b, float (&x)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[e] = __uint_as_float(a[e]);
+        x[e + 4] = __uint_as_float(b[e]);
+    }
+}
+__device__ __forceinline__ void as_floats(const u32x4& a, float (&x)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const f32x2 v = widen2<false>(a[e]);
+        x[2 * e] = v.x;
+        x[2 * e + 1] = v.y;
+    }
+}
+
+template <int END>
+__device__ __forceinline__ void end_eight(const DevMatrix& mx, uint64_t i, const EndInput<END>& in, const float (&o)[8],
+                                          float stepf, const ProductArgs& q)
 {
     GLOBAL u32x4* p16 = reinterpret_cast<GLOBAL u32x4*>(gptr<uint16_t>(mx.ptr[0], i));
     float x[8];
     if constexpr (END == kEndOrtho) {
         *p16 = pack8<false>(o);
     } else if constexpr (END == kEndMixedBf16 || END == kEndMixedF16) {
-        load8<kInF32>(mx.ptr[3], i, x);
+        as_floats(in.aux0, in.aux1, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = x[e] * q.decay - stepf * o[e];
         store8_f32(gptr<float>(mx.ptr[3], i), x);
         *p16 = pack8<END == kEndMixedF16>(x);
     } else if constexpr (END == kEndSplit) {
-        GLOBAL u32x4* r16 = reinterpret_cast<GLOBAL u32x4*>(gptr<uint16_t>(mx.ptr[3], i));
-        const u32x4 pw = *p16, rw = *r16;
         u32x4 pn, rn;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             uint32_t r0, r1;
-            const float a = __uint_as_float(join_master(pw[e] & 0xffffu, rw[e] & 0xffffu)) * q.decay - stepf * o[2 * e];
-            const float b = __uint_as_float(join_master(pw[e] >> 16, rw[e] >> 16)) * q.decay - stepf * o[2 * e + 1];
+            const float a = __uint_as_float(join_master(in.p[e] & 0xffffu, in.aux0[e] & 0xffffu)) * q.decay - stepf * o[2 * e];
+            const float b = __uint_as_float(join_master(in.p[e] >> 16, in.aux0[e] >> 16)) * q.decay - stepf * o[2 * e + 1];
             const uint32_t h0 = split_master(__float_as_uint(a), r0), h1 = split_master(__float_as_uint(b), r1);
             pn[e] = h0 | h1 << 16;
             rn[e] = r0 | r1 << 16;
         }
         *p16 = pn;
-        *r16 = rn;
+        *reinterpret_cast<GLOBAL u32x4*>(gptr<uint16_t>(mx.ptr[3], i)) = rn;
     } else {
-        load8<kInBf16>((uint64_t)mx.ptr[0], i, x);
+        as_floats(in.p, x);
         if constexpr (END == kEndPure) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = x[e] * q.decay - stepf * o[e];
             *p16 = pack8<false>(x);
         } else {
-            float c[8], s[8];
-            load8<END == kEndKahan ? kInBf16 : kInF32>(mx.ptr[3], i, c);
+            float c[8], s[8], sum[8];
+            if constexpr (END == kEndKahan) as_floats(in.aux0, c);
+            else as_floats(in.aux0, in.aux1, c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = c[e] + (-(q.lrwd * x[e]) - stepf * o[e]);
-            float sum[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] = x[e] + s[e];
+            for (int e = 0; e < 8; ++e) {
+                s[e] = c[e] + (-(q.lrwd * x[e]) - stepf * o[e]);
+                sum[e] = x[e] + s[e];
+            }
             const u32x4 pn = pack8<false>(sum);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -450,50 +595,48 @@ __device__ __forceinline__ void store_diagonal(GLOBAL float* d, uint32_t r, uint
 }
 
 template <int KIND, int OP, int END>
-__global__ __launch_bounds__(TileShape<KIND>::wy * TileShape<KIND>::wx * 64) void ns_product_kernel(
-    const DevMatrix* __restrict__ mats, const DevTile* __restrict__ tiles, char* ws, ProductArgs q)
+__global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const DevMatrix* __restrict__ mats,
+                                                                        const DevTile* __restrict__ tiles, char* ws,
+                                                                        ProductArgs q)
 {
     using S = TileShape<KIND>;
-    constexpr int WAVES = S::wy * S::wx, WR = S::side / S::wy, WC = S::side / S::wx;   // a wave's part of the tile
+    constexpr bool kSquare = OP == kGram || OP == kPoly;
+    using StageP = RowStage<S::rows, S::waves>;
+    using StageQ = std::conditional_t<kSquare, RowStage<S::cols, S::waves>, ColumnStage<S::cols, S::waves>>;
+    constexpr int WR = S::rows / 2, WC = S::cols / S::wx;   // a wave's part of the tile
     constexpr int MI = WR / 32, NI = WC / 32;
-    constexpr int kStageBytes = S::side * kPad * 2;
+    constexpr int kBytesP = S::rows * kPad * 2, kStageBytes = kBytesP + S::cols * kPad * 2;
+    constexpr int kLoads = StageP::kLoads + StageQ::kLoads;   // of a wave, for one stage
     constexpr int kEpiLd = WC + 8;                      // floats: rows 4 apart fall on the other half of the banks
     constexpr int kEpiBytes = 32 * kEpiLd * 4;          // one wave's 32 rows on their way out
-    static_assert(WAVES * kEpiBytes <= 4 * kStageBytes, "the epilogue takes the place of the operands");
-    __shared__ alignas(16) char lds[4 * kStageBytes];
+    static_assert(S::waves * kEpiBytes <= S::stages * kStageBytes, "the epilogue takes the place of the operands");
+    __shared__ alignas(16) char lds[S::stages * kStageBytes];
     if (q.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
 
-    const DevTile t = tiles[blockIdx.x];
-    const DevMatrix& mx = mats[t.mat];
+    const DevTile tile = tiles[blockIdx.x];
+    const DevMatrix& mx = mats[tile.mat];
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t rp = (uint32_t)mx.rp, cp = (uint32_t)mx.cp, sp = (uint32_t)mx.sp;
-    const bool tall = mx.tall != 0;
-    // X in its own order and transposed: the one that apply reads changes its buffer with every step
-    const uint64_t hi_now = tall && q.parity ? mx.y : mx.hi, t_now = !tall && q.parity ? mx.y : mx.t;
-    const uint64_t hi_next = tall && !q.parity ? mx.y : mx.hi, t_next = !tall && !q.parity ? mx.y : mx.t;
+    const uint32_t sp = (uint32_t)mx.sp, lp = (uint32_t)mx.lp;
+    const uint32_t r0 = tile.row * S::rows, c0 = tile.col * S::cols;
+    const GLOBAL _Float16* x_now = at<const _Float16>(ws, mx.hi[q.parity]);
 
-    const GLOBAL _Float16 *P, *Q;
-    uint32_t rows_p, rows_q, ld;   // ld: elements summed
+    StageP stage_p;
+    StageQ stage_q;
     if constexpr (OP == kGram) {
-        P = Q = at<const _Float16>(ws, tall ? t_now : hi_now);
-        rows_p = rows_q = sp;
-        ld = tall ? rp : cp;
+        stage_p.init(x_now, r0, sp, lp, wave, lane);
+        stage_q.init(x_now, c0, sp, lp, wave, lane);
     } else if constexpr (OP == kPoly) {
-        P = Q = at<const _Float16>(ws, mx.a);
-        rows_p = rows_q = ld = sp;
+        stage_p.init(at<const _Float16>(ws, mx.a), r0, sp, sp, wave, lane);
+        stage_q.init(at<const _Float16>(ws, mx.a), c0, sp, sp, wave, lane);
     } else {
-        P = at<const _Float16>(ws, tall ? hi_now : mx.b);
-        Q = at<const _Float16>(ws, tall ? mx.b : t_now);
-        rows_p = rp;
-        rows_q = cp;
-        ld = sp;
+        stage_p.init(at<const _Float16>(ws, mx.b), r0, sp, sp, wave, lane);
+        stage_q.init(x_now, c0, lp, lp, wave, lane);
     }
-    const uint32_t r0 = t.row * S::side, c0 = t.col * S::side;
-
-    Stage<S::side, WAVES> sp_, sq_;
-    sp_.init(P, r0, rows_p, ld, wave, lane);
-    sq_.init(Q, c0, rows_q, ld, wave, lane);
+    const auto load = [&](uint32_t k, uint32_t buf) {
+        stage_p.load(lds + buf * kStageBytes, k, wave);
+        stage_q.load(lds + buf * kStageBytes + kBytesP, k, wave);
+    };
     const uint32_t wr = wave / S::wx * WR, wc = wave % S::wx * WC;   // the wave's place in the tile
 
     f32x16 acc[MI][NI];
@@ -504,55 +647,173 @@ __global__ __launch_bounds__(TileShape<KIND>::wy * TileShape<KIND>::wx * 64) voi
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const uint32_t nk = ld / kPad;
-    sp_.load(lds, 0);
-    sq_.load(lds + kStageBytes, 0);
-    for (uint32_t k = 0; k < nk; ++k) {
-        // the loads of this summing step have arrived, and every wave is past its reads of the last
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        const char* bp = lds + (k & 1u) * 2 * kStageBytes;
-        const char* bq = bp + kStageBytes;
-        if (k + 1 < nk) {
-            char* nb = lds + ((k + 1) & 1u) * 2 * kStageBytes;
-            sp_.load(nb, k + 1);
-            sq_.load(nb + kStageBytes, k + 1);
+    // Summing steps from the one whose rows of X are the tile's own on: apply meets there the elements that its
+    // linear term needs, in the registers that hold them as an operand.
+    const uint32_t nk = (OP == kGram ? lp : sp) / kPad, k0 = kSquare ? 0u : r0 / kPad;
+    const auto step_at = [&](uint32_t t) { return k0 + t < nk ? k0 + t : k0 + t - nk; };
+    struct Operands {
+        f16x8 a[MI], b[NI];
+    };
+    const auto read = [&](uint32_t buf, int kk, Operands& o) {
+        const char* bp = lds + buf * kStageBytes;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) o.a[i] = StageP::operand(bp, wr + i * 32, kk, lane);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) o.b[j] = StageQ::operand(bp + kBytesP, wc + j * 32, kk, lane);
+    };
+    // acc += (a + B_rr - fp16(B_rr)) X, for the 16 rows of X in `o` if they are the wave's; acc is under 2^(sb + sx)
+    const auto linear = [&](const Operands& o, uint32_t k, int kk) {
+        const uint32_t first = r0 + wr;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            if ((k * kPad + (uint32_t)kk * 16) / 32 != first / 32 + i) continue;
+            const uint32_t r = k * kPad + (uint32_t)kk * 16 + (lane >> 5) * 4;
+            const GLOBAL float* db = at<const float>(ws, mx.db) + r;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = db[e < 4 ? e : e + 4];
+                f[e] = q.a * pow2(q.sb) + (d - (float)(_Float16)d);
+            }
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                // a lane has 8 rows of its column; of 16 the results want rows 0-3 and 8-11 in the lower half wave, 4-7 and
+                // 12-15 in the upper
+                const u32x4 x = __builtin_bit_cast(u32x4, o.b[j]);
+                const auto s0 = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
+                const u32x4 y = {s0[0], s1[0], s0[1], s1[1]};
+                const f16x8 v = __builtin_bit_cast(f16x8, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = (kk & 1) * 8 + e;
+                    acc[i][j][c] = __builtin_fmaf(f[e], (float)v[e], acc[i][j][c]);
+                }
+            }
         }
+    };
+
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            f16x8 a[MI], b[NI];
-            const uint32_t word = (uint32_t)kk * 2 + (lane >> 5);
+    for (uint32_t t = 0; t + 1 < S::stages; ++t)
+        if (t < nk) load(step_at(t), t);
+    // stage 0 has arrived: all but the loads behind it
+    if (nk >= S::stages - 1) wait_and_meet<(S::stages - 2) * kLoads>();
+    else wait_and_meet<0>();
+    Operands o[2];
+    read(0, 0, o[0]);
+    uint32_t buf = 0, fill = S::stages - 1;
+    const auto summing_step = [&](uint32_t t, auto with_linear) {
+        if (t + S::stages - 1 < nk) load(step_at(t + S::stages - 1), fill);
 #pragma unroll
-            for (int i = 0; i < MI; ++i) a[i] = operand(bp, wr + i * 32 + (lane & 31u), word);
-#pragma unroll
-            for (int j = 0; j < NI; ++j) b[j] = operand(bq, wc + j * 32 + (lane & 31u), word);
+        for (int kk = 0; kk < kPad / 16; ++kk) {
+            if (kk + 1 < kPad / 16) {
+                read(buf, kk + 1, o[(kk + 1) & 1]);
+            } else if (t + 1 < nk) {
+                // The next stage has arrived, and every wave has its last operands of this one, whose room is
+                // loaded next; the matrix instructions below cover the reads.
+                if (t + S::stages - 1 < nk) wait_and_meet<(S::stages - 2) * kLoads>();
+                else wait_and_meet<0>();
+                fill = buf;
+                buf = buf + 1 == S::stages ? 0 : buf + 1;
+                read(buf, 0, o[0]);
+            }
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int j = 0; j < NI; ++j) acc[i][j] = mfma(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < NI; ++j) acc[i][j] = mfma(o[kk & 1].a[i], o[kk & 1].b[j], acc[i][j]);
+            if constexpr (decltype(with_linear)::value) linear(o[kk & 1], step_at(t), kk);
         }
-    }
-    __syncthreads();   // the operands' room is free
+    };
+    uint32_t t = 0;
+    if constexpr (!kSquare)
+        for (; t < S::rows / kPad && t < nk; ++t) summing_step(t, std::true_type{});
+    for (; t < nk; ++t) summing_step(t, std::false_type{});
+    wait_and_meet<0>();   // the operands' room is free
 
-    // Epilogue, 32 rows of the wave's part at a time through LDS of its own: 8 neighbours of a row
-    // to a lane, and for what is kept in both orders then 8 of a column.
+    // Epilogue, 32 rows of the wave's part at a time through LDS of its own: 8 neighbours of a row to a
+    // lane, and for what is needed by columns then 8 of a column.  What is read for it is read one round
+    // ahead, since a wait for a load waits for every store before it too; and inside the
+    // matrix wherever the lane lies, so that all reads are under way together.
     float* out = reinterpret_cast<float*>(lds + wave * kEpiBytes);
-    constexpr int kRowPacks = WC / 8;
+    constexpr int kRowPacks = WC / 8, kPacks = 32 * kRowPacks / 64;
+    const uint32_t lim_c = kSquare ? sp : lp;
     const float stepf = OP == kLast ? (float)((double)q.lr * mx.factor) : 0.0f;
+    const bool tall = OP == kLast && mx.tall != 0, row16 = OP == kLast && mx.row16 != 0;
+    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, col0 = c0 + wc;
+    struct Input {
+        f16x8 x[kPacks];    // A, or lo
+        float dr[kPacks];   // the diagonal of A or B at the rows
+    };
+    // ... and at the columns, the same in every round
+    float dc[8];
+    if constexpr (OP == kPoly) {
+        const uint32_t c = col0 + lane % kRowPacks * 8;
+        read8(at<const float>(ws, mx.da) + (c < sp ? c : sp - 8), dc);
+    }
+    const auto read_ahead = [&](int i, Input& in) {
+        if constexpr (OP == kPoly || OP == kApply) {
+#pragma unroll
+            for (int h = 0; h < kPacks; ++h) {
+                const uint32_t k = (uint32_t)h * 64 + lane;
+                uint32_t r = r0 + wr + (uint32_t)i * 32 + k / kRowPacks, c = col0 + k % kRowPacks * 8;
+                r = r < sp ? r : sp - 1;
+                c = c < lim_c ? c : lim_c - 8;
+                in.dr[h] = at<const float>(ws, OP == kPoly ? mx.da : mx.db)[r];
+                in.x[h] = *reinterpret_cast<const GLOBAL f16x8*>(at<const _Float16>(ws, OP == kPoly ? mx.a : mx.lo) +
+                                                                 (uint64_t)r * lim_c + c);
+            }
+        }
+    };
+    // The place in the matrix of pack k of round row0: of a tall one, 8 of a column of X.
+    const auto place = [&](uint32_t row0, uint32_t k, uint32_t& r, uint32_t& c) {
+        r = tall ? col0 + k / 4 : row0 + k / kRowPacks;
+        c = tall ? row0 + k % 4 * 8 : col0 + k % kRowPacks * 8;
+    };
+    const auto finish = [&](uint32_t r, uint32_t c, const EndInput<END>& in, const float(&v)[8]) {
+        if (r >= rows || c >= cols) return;
+        const uint64_t i = (uint64_t)r * cols + c;
+        if (row16) {
+            end_eight<END>(mx, i, in, v, stepf, q);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) end_elem<END>(mx, i + e, v[e], stepf, q);
+        }
+    };
+    Input in[2];
+    read_ahead(0, in[0]);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
+        const uint32_t row0 = r0 + wr + (uint32_t)i * 32;
+        const Input& now = in[i & 1];
+        if (i + 1 < MI) read_ahead(i + 1, in[(i + 1) & 1]);
+        EndInput<END> end[kPacks];
+        if constexpr (OP == kLast) {
+            if (row16) {
+#pragma unroll
+                for (int h = 0; h < kPacks; ++h) {
+                    // aligned rows are of a multiple of 8: the 8 elements lie inside
+                    uint32_t r, c;
+                    place(row0, (uint32_t)h * 64 + lane, r, c);
+                    r = r < rows ? r : rows - 1;
+                    c = c < cols ? c : cols - 8;
+                    end[h] = end_input<END>(mx, (uint64_t)r * cols + c);
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NI; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 out[((e & 3) + 8 * (e >> 2) + 4 * (lane >> 5)) * kEpiLd + j * 32 + (lane & 31u)] = acc[i][j][e];
         __builtin_amdgcn_wave_barrier();
-        const uint32_t row0 = r0 + wr + (uint32_t)i * 32, col0 = c0 + wc;
 #pragma unroll
-        for (int h = 0; h < 32 * kRowPacks / 64; ++h) {
+        for (int h = 0; h < kPacks; ++h) {
             const uint32_t k = (uint32_t)h * 64 + lane, lr = k / kRowPacks, lc = k % kRowPacks * 8;
             const uint32_t r = row0 + lr, c = col0 + lc;
             float* cell = out + lr * kEpiLd + lc;
+            const uint64_t at_rc = (uint64_t)r * lim_c + c;
+            const bool inside = r < sp && c < lim_c;
             float v[8];
             {
                 const f32x4 x = *reinterpret_cast<const f32x4*>(cell), y = *reinterpret_cast<const f32x4*>(cell + 4);
@@ -562,95 +823,79 @@ __global__ __launch_bounds__(TileShape<KIND>::wy * TileShape<KIND>::wx * 64) voi
                     v[e + 4] = y[e];
                 }
             }
-            const bool inside = OP == kGram || OP == kPoly ? r < sp && c < sp : r < rp && c < cp;
-            if (inside) {
-                if constexpr (OP == kGram || OP == kPoly) {
-                    if constexpr (OP == kGram) {
-                        const float f = pow2(q.sa - 2 * q.sx);
+            if constexpr (kSquare) {
+                if constexpr (OP == kGram) {
+                    const float f = pow2(q.sa - 2 * q.sx);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= f;
-                        store_diagonal(at<float>(ws, mx.da), r, c, v);
-                    } else {
-                        // b A + c A A, with A's diagonal in fp32: (A + E)(A + E) = A A + (e_r + e_c) A + E E
-                        const f16x8 ah = *reinterpret_cast<const GLOBAL f16x8*>(at<const _Float16>(ws, mx.a) +
-                                                                                (uint64_t)r * sp + c);
-                        const GLOBAL float* da = at<const float>(ws, mx.da);
-                        const float f = pow2(-q.sa);
-                        const float dr = da[r], er = (dr - (float)(_Float16)dr) * f;
+                    for (int e = 0; e < 8; ++e) v[e] *= f;
+                } else {
+                    // b A + c A A, with A's diagonal in fp32: (A + E)(A + E) = A A + (e_r + e_c) A + E E; all under 2^sb
+                    const float f = pow2(-q.sa), g = pow2(q.sb), er = (now.dr[h] - (float)(_Float16)now.dr[h]) * f;
+                    const float c2 = q.c * f * f * g, c1 = q.b * f * g, ce = q.c * f * g;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float dc = da[c + e], ec = (dc - (float)(_Float16)dc) * f;
-                            float x = (float)ah[e] * f, sq = v[e] * (f * f) + (er + ec) * x;
-                            if (r == c + e) {
-                                sq += er * er;
-                                x += er;
-                            }
-                            v[e] = (q.b * x + q.c * sq) * pow2(q.sb);
-                        }
-                        store_diagonal(at<float>(ws, mx.db), r, c, v);
+                    for (int e = 0; e < 8; ++e) {
+                        const float ec = (dc[e] - (float)(_Float16)dc[e]) * f;
+                        v[e] = __builtin_fmaf(c2, v[e], __builtin_fmaf(ce, er + ec, c1) * (float)now.x[h][e]);
+                        if (r == c + e) v[e] += (q.b * er + q.c * er * er) * g;
                     }
+                }
+                if (inside) {
+                    store_diagonal(at<float>(ws, OP == kGram ? mx.da : mx.db), r, c, v);
                     f16x8 w;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = (_Float16)v[e];
-                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? mx.a : mx.b) + (uint64_t)r * sp + c) = w;
-                } else {
-                    const uint64_t o = (uint64_t)r * cp + c;
-                    const f16x8 hi = *reinterpret_cast<const GLOBAL f16x8*>(at<const _Float16>(ws, hi_now) + o);
-                    const f16x8 lo = *reinterpret_cast<const GLOBAL f16x8*>(at<const _Float16>(ws, mx.lo) + o);
-                    const GLOBAL float* db = at<const float>(ws, mx.db);
-                    const float f = pow2(-q.sb);
-                    // X' * 2^sx
+                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? mx.a : mx.b) + at_rc) = w;
+                }
+            } else {
+                if constexpr (OP == kApply) {
+                    // X' * 2^sx; the last step reads no lo
+                    const float f = pow2(-q.sb), of_lo = __builtin_fmaf(now.dr[h], f, q.a) * (1.0f / kLoScale);
+                    f16x8 h8, l8;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float d = db[tall ? c + e : r], rest = (d - (float)(_Float16)d) * f;
-                        v[e] = (q.a + rest) * (float)hi[e] + v[e] * f + (q.a + d * f) * ((float)lo[e] * (1.0f / kLoScale));
+                        _Float16 x, y;
+                        split_pair(__builtin_fmaf(of_lo, (float)now.x[h][e], v[e] * f), x, y);
+                        h8[e] = x;
+                        l8[e] = y;
                     }
-                    if constexpr (OP == kApply) {
-                        f16x8 h8, l8;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            _Float16 x, y;
-                            split_pair(v[e], x, y);
-                            h8[e] = x;
-                            l8[e] = y;
-                        }
-                        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, hi_next) + o) = h8;
-                        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.lo) + o) = l8;
-                    } else if (r < (uint32_t)mx.rows && c < (uint32_t)mx.cols) {
-                        const float g = pow2(-q.sx);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= g;
-                        const uint64_t i0 = (uint64_t)r * (uint64_t)mx.cols + c;
-                        if (mx.row16) {
-                            end_eight<END>(mx, i0, v, stepf, q);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (c + e < (uint32_t)mx.cols) end_elem<END>(mx, i0 + e, v[e], stepf, q);
-                        }
+                    if (inside) {
+                        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.hi[q.parity ^ 1]) + at_rc) = h8;
+                        if (q.keep_lo) *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.lo) + at_rc) = l8;
                     }
+                } else {
+                    const float g = pow2(-q.sb - q.sx);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= g;
+                    if (!tall) finish(r, c, end[h], v);
                 }
-                if constexpr (OP != kLast) {
-                    *reinterpret_cast<f32x4*>(cell) = f32x4{v[0], v[1], v[2], v[3]};
-                    *reinterpret_cast<f32x4*>(cell + 4) = f32x4{v[4], v[5], v[6], v[7]};
-                }
+            }
+            if (OP == kGram || OP == kPoly || tall) {
+                *reinterpret_cast<f32x4*>(cell) = f32x4{v[0], v[1], v[2], v[3]};
+                *reinterpret_cast<f32x4*>(cell + 4) = f32x4{v[4], v[5], v[6], v[7]};
             }
         }
         __builtin_amdgcn_wave_barrier();
-        if constexpr (OP != kLast) {
+        if constexpr (kSquare || OP == kLast) {
             // by columns: 8 of a column to a lane, 4 lanes to a column of the 32 rows
-            const bool both = OP == kApply || t.row != t.col;   // a tile on the diagonal is its own mirror
-            GLOBAL _Float16* dst = at<_Float16>(ws, OP == kGram ? mx.a : OP == kPoly ? mx.b : t_next);
-            const uint32_t lim_r = OP == kApply ? rp : sp, lim_c = OP == kApply ? cp : sp;
+            const bool wanted = kSquare ? tile_mirrored(KIND, tile.row, tile.col) : tall;
+            if (wanted) {
 #pragma unroll
-            for (int h = 0; h < WC * 4 / 64; ++h) {
-                const uint32_t k = (uint32_t)h * 64 + lane, lc = k / 4, lr = k % 4 * 8;
-                const uint32_t r = row0 + lr, c = col0 + lc;
-                f16x8 w;
+                for (int h = 0; h < kPacks; ++h) {
+                    const uint32_t k = (uint32_t)h * 64 + lane, lc = k / 4, lr = k % 4 * 8;
+                    const uint32_t r = row0 + lr, c = col0 + lc;
+                    float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = (_Float16)out[(lr + e) * kEpiLd + lc];
-                if (both && r < lim_r && c < lim_c)
-                    *reinterpret_cast<GLOBAL f16x8*>(dst + (uint64_t)c * lim_r + r) = w;
+                    for (int e = 0; e < 8; ++e) v[e] = out[(lr + e) * kEpiLd + lc];
+                    if constexpr (kSquare) {
+                        f16x8 w;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = (_Float16)v[e];
+                        if (r < sp && c < sp)
+                            *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? mx.a : mx.b) + (uint64_t)c * sp + r) = w;
+                    } else {
+                        finish(c, r, end[h], v);
+                    }
+                }
             }
             __builtin_amdgcn_wave_barrier();
         }
@@ -675,7 +920,7 @@ namespace {
 template <int KIND, int OP, int END>
 hipError_t launch_product(const NsCall& call, const NsLaunch& l, const ProductArgs& q, hipStream_t stream)
 {
-    ns_product_kernel<KIND, OP, END><<<(uint32_t)l.count, TileShape<KIND>::wy * TileShape<KIND>::wx * 64, 0, stream>>>(
+    ns_product_kernel<KIND, OP, END><<<(uint32_t)l.count, kTileLanes[KIND], 0, stream>>>(
         call.mats, call.tiles + l.first, call.ws, q);
     return hipGetLastError();
 }
@@ -752,6 +997,7 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, hipStream_t
     if (e != hipSuccess) return e;
     for (int k = 0; k < call.ns.steps; ++k) {
         q.parity = k & 1;
+        q.keep_lo = k + 2 < call.ns.steps;
         if ((e = product<kGram>(call, batch.square, q, stream)) != hipSuccess) return e;
         if ((e = product<kPoly>(call, batch.square, q, stream)) != hipSuccess) return e;
         e = k + 1 < call.ns.steps ? product<kApply>(call, batch.apply, q, stream) : last_product(call, batch.apply, q, stream);

@@ -6,7 +6,7 @@
 // together.  One batch is a fixed sequence of launches, each over every matrix of it:
 //
 //   moments    sum of squares of each matrix; a step also advances m and writes u
-//   normalise  X = u / (|u| + eps) as fp16 pairs, in both orders
+//   normalise  X = u / (|u| + eps) as fp16 pairs
 //   per product step:  gram  A = X X^T (the shorter side),  poly  B = b A + c A A,
 //                      apply X = a X + B X, the last one with the result's own epilogue
 //
@@ -32,10 +32,21 @@ constexpr int64_t kNsBatchBytes = INT64_C(4) << 30;   // workspace of a batch of
 constexpr int64_t kMomentElems = 16384;   // elements of a workgroup of the moments kernel
 constexpr int kBlockMoments = 256;
 
-// Square tiles of the product kernels: side, and lanes of a workgroup.
+// Tiles of the product kernels: rows, columns, and lanes of a workgroup.
 constexpr int kTileKinds = 3;
-constexpr int kTileSide[kTileKinds] = {256, 128, 64};
+constexpr int kTileRows[kTileKinds] = {256, 128, 64};
+constexpr int kTileCols[kTileKinds] = {256, 128, 64};
 constexpr int kTileLanes[kTileKinds] = {512, 256, 256};
+// Of a symmetric product, the tiles that reach the diagonal or lie below it are computed;
+// those wholly below it are written to the mirrored place too.
+constexpr bool tile_needed(int kind, int64_t row, int64_t col)
+{
+    return col * kTileCols[kind] < (row + 1) * kTileRows[kind];
+}
+constexpr bool tile_mirrored(int kind, int64_t row, int64_t col)
+{
+    return (col + 1) * kTileCols[kind] <= row * kTileRows[kind];
+}
 
 // Tiles that a launch should have before it takes the larger kind: one for every CU.
 constexpr int64_t kTilesWanted = 256;
@@ -43,18 +54,18 @@ constexpr int64_t kMaxNsSide = INT64_C(1) << 30, kMaxNsShort = INT64_C(1) << 20;
 // A grid counts at most 2^32 - 1 lanes.
 constexpr int64_t kMaxNsTiles = (int64_t)UINT32_MAX / 512;
 
-// One matrix of a batch.  Parts of the workspace are byte offsets from its start.
-// hi, lo: X in its own order (rows x cp), the value is (hi + lo * 2^-11) * 2^-sx; t: hi's
-// transpose (cols x rp).  y: the other buffer of the one of hi and t that the product with
-// B reads (t of a wide matrix, hi of a tall one), since workgroups write the new
-// values while others read the old.  u (a step's fp32 matrix, not padded) lies where y, a and b
-// come to lie later.
+// One matrix of a batch.  X is held wide whatever the matrix is: s rows of l elements, s <= l, transposed for
+// a matrix that is taller than wide.  Parts of the workspace are byte offsets from its start.
+// hi, lo: X, sp rows of lp elements, of which l are used, the others zeros; the value is
+// (hi + lo * 2^-11) * 2^-sx; hi has two buffers, since workgroups of the product with B write
+// new values while others read the old.  a, b: the squares, sp x sp; da, db: their diagonals in
+// fp32.  u (a step's fp32 matrix as it lies in the caller's buffers) has the room of hi[1], a and b.
 struct alignas(16) DevMatrix {
     uint64_t ptr[4];          // element 0: result or param; u or grad; exp_avg; aux
-    uint64_t u, hi, lo, t, y, a, b, da, db, partials;
+    uint64_t u, hi[2], lo, a, b, da, db, partials;
     double factor;            // s of the step
-    int32_t rows, cols, rp, cp;
-    int32_t s, sp;            // the shorter side, padded
+    int32_t rows, cols;
+    int32_t s, l, sp, lp;   // lp, sp: padded
     int32_t tall;             // rows > cols
     uint32_t n_partials;
     uint32_t flat16;          // every stream's element 0 is 16-byte aligned

@@ -85,29 +85,28 @@ adamw_status shapes_of(const adamw_tensor_list* list, const int64_t* cols, std::
 }
 
 // Lays one matrix out from byte `at` of the workspace; returns the end.
-int64_t place(const Shape& sh, bool step, int64_t at, DevMatrix* m)
+int64_t place(const Shape& sh, int64_t at, DevMatrix* m)
 {
-    const int64_t rp = round_up(sh.rows, kPad), cp = round_up(sh.cols, kPad), s = std::min(sh.rows, sh.cols);
-    const int64_t sp = round_up(s, kPad), part = round_up(2 * rp * cp, kNsAlign), square = round_up(2 * sp * sp, kNsAlign);
-    const int64_t chunks = (sh.rows * sh.cols + kMomentElems - 1) / kMomentElems;
+    const int64_t s = std::min(sh.rows, sh.cols), l = std::max(sh.rows, sh.cols);
+    const int64_t sp = round_up(s, kPad), lp = round_up(l, kPad);
+    const int64_t part = round_up(2 * sp * lp, kNsAlign), square = round_up(2 * sp * sp, kNsAlign);
+    const int64_t chunks = (s * l + kMomentElems - 1) / kMomentElems;
     m->rows = (int32_t)sh.rows;
     m->cols = (int32_t)sh.cols;
-    m->rp = (int32_t)rp;
-    m->cp = (int32_t)cp;
     m->s = (int32_t)s;
+    m->l = (int32_t)l;
     m->sp = (int32_t)sp;
+    m->lp = (int32_t)lp;
     m->tall = sh.rows > sh.cols;
     m->n_partials = (uint32_t)chunks;
-    m->hi = (uint64_t)at;
-    m->lo = m->hi + (uint64_t)part;
-    m->t = m->lo + (uint64_t)part;
-    m->y = m->t + (uint64_t)part;
-    m->a = m->y + (uint64_t)part;
+    m->hi[0] = (uint64_t)at;
+    m->lo = m->hi[0] + (uint64_t)part;
+    m->hi[1] = m->lo + (uint64_t)part;
+    m->a = m->hi[1] + (uint64_t)part;
     m->b = m->a + (uint64_t)square;
-    m->u = m->y;
-    int64_t room = part + 2 * square;
-    if (step) room = std::max(room, round_up(4 * sh.rows * sh.cols, kNsAlign));
-    m->da = m->y + (uint64_t)room;
+    m->u = m->hi[1];
+    const int64_t room = std::max(part + 2 * square, round_up(4 * s * l, kNsAlign));
+    m->da = m->u + (uint64_t)room;
     m->db = m->da + (uint64_t)round_up(4 * sp, kNsAlign);
     m->partials = m->db + (uint64_t)round_up(4 * sp, kNsAlign);
     return (int64_t)m->partials + round_up(8 * chunks, kNsAlign);
@@ -117,7 +116,7 @@ int64_t place(const Shape& sh, bool step, int64_t at, DevMatrix* m)
 int64_t bytes_of(const Shape& s)
 {
     DevMatrix m;
-    return place(s, true, 0, &m);
+    return place(s, 0, &m);
 }
 
 // Workgroup order of a launch's tiles: those of the longest sums first, and runs of
@@ -138,10 +137,12 @@ void deal_tiles(const std::vector<DevTile>& in, std::vector<DevTile>* out)
 
 int64_t tiles_of(int64_t n, int side) { return (n + side - 1) / side; }
 
-int64_t square_tiles(int64_t s, int side)
+int64_t square_tiles(int64_t s, int kind)
 {
-    const int64_t t = tiles_of(s, side);
-    return t * (t + 1) / 2;
+    int64_t n = 0;
+    for (int64_t y = 0; y < tiles_of(s, kTileRows[kind]); ++y)
+        n += std::min(tiles_of(s, kTileCols[kind]), ((y + 1) * kTileRows[kind] - 1) / kTileCols[kind] + 1);
+    return n;
 }
 
 // The largest tile with which a launch has work for every CU.
@@ -149,7 +150,7 @@ template <typename Count>
 int pick_kind(const Count& count)
 {
     for (int k = 0; k < kTileKinds - 1; ++k)
-        if (count(kTileSide[k]) >= kTilesWanted) return k;
+        if (count(k) >= kTilesWanted) return k;
     return kTileKinds - 1;
 }
 
@@ -292,7 +293,7 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
     // that passes the limit is counted before its tiles are listed.
     for (const Shape& s : shapes)
         if (tiles_of(s.rows, kPad) * tiles_of(s.cols, kPad) > kMaxNsTiles) {
-            err = "a matrix needs more than 8,421,504 tiles in one launch";
+            err = "a matrix needs more than 8,388,607 tiles in one launch";
             return ADAMW_E_INVALID;
         }
     if (!out) return ADAMW_OK;
@@ -305,7 +306,7 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
         int64_t at = kNsHeadBytes, n_tiles = 0;
         for (; end < n; ++end) {
             DevMatrix m{};
-            const int64_t next = place(shapes[end], true, at, &m);
+            const int64_t next = place(shapes[end], at, &m);
             const int64_t t = tiles_of(shapes[end].rows, kPad) * tiles_of(shapes[end].cols, kPad);
             if (next > workspace_bytes || (end > i && n_tiles + t > kMaxNsTiles)) break;
             at = next;
@@ -325,7 +326,6 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
         // the longest sums first
         std::vector<size_t> order;
         for (size_t k = i; k < end; ++k) order.push_back(k);
-        const auto long_side = [&](size_t k) { return std::max(out->mats[k].rp, out->mats[k].cp); };
         NsBatch b;
         std::vector<DevTile> tiles;
         const auto take = [&](NsLaunch* l) {
@@ -338,35 +338,37 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
             for (uint32_t c = 0; c < out->mats[k].n_partials; ++c) tiles.push_back(DevTile{(uint32_t)k, c, 0, 0});
         take(&b.moments);
         for (size_t k : order)
-            for (int32_t y = 0; y < out->mats[k].rp / kPad; ++y)
-                for (int32_t x = 0; x < out->mats[k].cp / kPad; ++x)
+            for (int32_t y = 0; y < out->mats[k].sp / kPad; ++y)
+                for (int32_t x = 0; x < out->mats[k].lp / kPad; ++x)
                     tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
         take(&b.normalise);
-        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return long_side(x) > long_side(y); });
-        b.square.kind = pick_kind([&](int side) {
+        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].l > out->mats[y].l; });
+        b.square.kind = pick_kind([&](int kind) {
             int64_t t = 0;
-            for (size_t k : order) t += square_tiles(out->mats[k].s, side);
+            for (size_t k : order) t += square_tiles(out->mats[k].s, kind);
             return t;
         });
-        b.apply.kind = pick_kind([&](int side) {
+        b.apply.kind = pick_kind([&](int kind) {
             int64_t t = 0;
-            for (size_t k : order) t += tiles_of(out->mats[k].rows, side) * tiles_of(out->mats[k].cols, side);
+            for (size_t k : order)
+                t += tiles_of(out->mats[k].s, kTileRows[kind]) * tiles_of(out->mats[k].l, kTileCols[kind]);
             return t;
         });
         // bands of 4 tile rows, column by column
         constexpr int64_t kBand = 4;
         for (size_t k : order) {
-            const int64_t t = tiles_of(out->mats[k].s, kTileSide[b.square.kind]);
-            for (int64_t y0 = 0; y0 < t; y0 += kBand)
-                for (int64_t x = 0; x < std::min(t, y0 + kBand); ++x)
-                    for (int64_t y = std::max(y0, x); y < std::min(t, y0 + kBand); ++y)
-                        tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
+            const int kind = b.square.kind;
+            const int64_t ty = tiles_of(out->mats[k].s, kTileRows[kind]), tx = tiles_of(out->mats[k].s, kTileCols[kind]);
+            for (int64_t y0 = 0; y0 < ty; y0 += kBand)
+                for (int64_t x = 0; x < tx; ++x)
+                    for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
+                        if (tile_needed(kind, y, x)) tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
         }
         take(&b.square);
         std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].sp > out->mats[y].sp; });
         for (size_t k : order) {
-            const int64_t ty = tiles_of(out->mats[k].rows, kTileSide[b.apply.kind]);
-            const int64_t tx = tiles_of(out->mats[k].cols, kTileSide[b.apply.kind]);
+            const int64_t ty = tiles_of(out->mats[k].s, kTileRows[b.apply.kind]);
+            const int64_t tx = tiles_of(out->mats[k].l, kTileCols[b.apply.kind]);
             for (int64_t y0 = 0; y0 < ty; y0 += kBand)
                 for (int64_t x = 0; x < tx; ++x)
                     for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)

@@ -460,8 +460,9 @@ adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtyp
  *
  * Numerics.  |U| is summed in binary64.  X is held as a sum of two fp16 values (22 bits)
  * under a power of two, X X^T and the polynomial of it as fp16 with their diagonals in
- * fp32; products are of fp16 values with fp32 sums, and the linear term a X keeps all 22 bits, so
- * that small singular values, which a step multiplies by a, are not drowned in rounding.
+ * fp32; products are of fp16 values with fp32 sums, and the linear term a X keeps all 22 bits (in
+ * the last step 11), so that small singular values, which a step multiplies by a, are not drowned
+ * in rounding.
  * The result is within about 1e-3 (relative, in the Frobenius norm) of the definition's value;
  * the same call gives the same bits.  A matrix with an inf or NaN element has NaN in
  * every element of its result, a zero matrix zeros; no matrix changes another's.
@@ -479,7 +480,7 @@ typedef struct {
 
 /* Bytes of device workspace with which the two calls below work through `list` (its
  * numel, shard and ADAMW_FLAT_PAD8; pointers are not looked at) at full speed: room for
- * all its matrices, about 12 bytes an element, or of a longer list for 4 GiB of them at
+ * all its matrices, about 10 bytes an element, or of a longer list for 4 GiB of them at
  * a time.  With `least` != 0, the smallest workspace that they take: room for the
  * largest matrix.  -1 on an invalid argument.  No GPU work, no HIP call. */
 int64_t adamw_orthogonalize_workspace_bytes(const adamw_tensor_list* list, const int64_t* cols, int least);

@@ -24,16 +24,16 @@ def ns64(u, ns=NS):
 
 
 def ns_rounded(u, ns=NS):
-    """The same with the roundings that the header documents (X as fp16 pairs, products of fp16 values, diagonals
-    of the squares in full), every sum in 64 bits."""
+    """The same with the roundings that the header documents (X as fp16 pairs, in the last step as one fp16, products of
+    fp16 values, diagonals of the squares in full), every sum in 64 bits."""
     h = lambda x: x.to(torch.float16).double()  # noqa: E731
     x = u.double()
     x = x / (x.norm() + f32(ns.eps)) * 2.0 ** 14
     tall = x.shape[0] > x.shape[1]
     x = x.T if tall else x
-    for _ in range(ns.steps):
+    for k in range(ns.steps):
         hi = h(x)
-        lo = h((x - hi) * 2048.0) / 2048.0
+        lo = h((x - hi) * 2048.0) / 2048.0 if k + 1 < ns.steps else torch.zeros_like(hi)
         g = hi @ hi.T * 2.0 ** -14
         gh = h(g)
         e = (g - gh).diagonal()

@@ -83,30 +83,30 @@ void check_batch(const NsPlan& plan, const NsBatch& b, std::vector<int>& seen, i
         seen[kv.first] = 1;
         const DevMatrix& m = plan.mats[kv.first];
         for (int x : kv.second) CHECK(x);
-        const int64_t n = (int64_t)m.rows * m.cols, pad = (int64_t)m.rp * m.cp, sq = (int64_t)m.sp * m.sp;
+        const int64_t n = (int64_t)m.rows * m.cols, pad = (int64_t)m.sp * m.lp, sq = (int64_t)m.sp * m.sp;
         CHECK((int64_t)m.n_partials * kMomentElems >= n && ((int64_t)m.n_partials - 1) * kMomentElems < n);
-        CHECK(m.rp % kPad == 0 && m.rp >= m.rows && m.rp < m.rows + kPad && m.cp % kPad == 0 && m.cp >= m.cols &&
-              m.cp < m.cols + kPad);
-        CHECK(m.s == std::min(m.rows, m.cols) && m.sp == (m.tall ? m.cp : m.rp) && (m.tall != 0) == (m.rows > m.cols));
-        const Range r[8] = {{m.hi, m.hi + 2 * pad}, {m.lo, m.lo + 2 * pad}, {m.t, m.t + 2 * pad}, {m.y, m.y + 2 * pad},
-                            {m.a, m.a + 2 * sq}, {m.b, m.b + 2 * sq}, {m.da, m.da + 4 * m.sp}, {m.db, m.db + 4 * m.sp}};
+        CHECK(m.s == std::min(m.rows, m.cols) && m.l == std::max(m.rows, m.cols) && (m.tall != 0) == (m.rows > m.cols));
+        CHECK(m.sp % kPad == 0 && m.sp >= m.s && m.sp < m.s + kPad && m.lp % kPad == 0 && m.lp >= m.l && m.lp < m.l + kPad);
+        const Range r[8] = {{m.hi[0], m.hi[0] + 2 * pad}, {m.lo, m.lo + 2 * pad}, {m.hi[1], m.hi[1] + 2 * pad},
+                            {m.a, m.a + 2 * sq}, {m.b, m.b + 2 * sq}, {m.da, m.da + 4 * m.sp}, {m.db, m.db + 4 * m.sp},
+                            {m.partials, m.partials + 8 * (uint64_t)m.n_partials}};
         for (const Range& x : r) parts.push_back(x);
-        parts.push_back(Range{m.partials, m.partials + 8 * (uint64_t)m.n_partials});
-        if (step) {   // u's room: that of y, a and b, and nothing else's
+        if (step) {   // u's room: that of hi[1], a and b, and nothing else's
             const Range u{m.u, m.u + 4 * (uint64_t)n};
-            CHECK(u.hi <= (uint64_t)bytes && apart(u, r[0]) && apart(u, r[1]) && apart(u, r[2]) && apart(u, r[6]) &&
-                  apart(u, r[7]) && u.hi <= m.partials);
+            CHECK(u.hi <= (uint64_t)bytes);
+            for (int k : {0, 1, 5, 6, 7}) CHECK(apart(u, r[k]));
         }
-        for (int k : {0, 1, 2, 3, 4, 5, 6, 7}) CHECK(r[k].lo % kNsAlign == 0);
+        for (const Range& x : r) CHECK(x.lo % kNsAlign == 0);
         for (uint64_t x : {m.rows, m.cols, m.sp, m.tall}) mix(x);
-        mix(m.hi);
+        mix(m.hi[0]);
         mix(m.partials);
     }
     for (const Range& x : parts) CHECK(x.lo >= (uint64_t)kNsHeadBytes && x.hi <= (uint64_t)bytes);
     std::sort(parts.begin(), parts.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
     for (size_t i = 1; i < parts.size(); ++i) CHECK(apart(parts[i - 1], parts[i]));
 
-    const auto cover = [&](const NsLaunch& l, int side, bool square, bool padded) {
+    // 64 x 64 of the padded matrix each, the tiles of a kind of the matrix, or of its square
+    const auto cover = [&](const NsLaunch& l, int th, int tw, bool square) {
         std::map<uint32_t, std::map<std::pair<uint32_t, uint32_t>, int>> got;
         for (int64_t i = 0; i < l.count; ++i) {
             const DevTile& t = plan.tiles[(size_t)(l.first + i)];
@@ -116,19 +116,28 @@ void check_batch(const NsPlan& plan, const NsBatch& b, std::vector<int>& seen, i
         CHECK(got.size() == runs.size());
         for (auto& kv : got) {
             const DevMatrix& m = plan.mats[kv.first];
-            const int64_t h = square ? m.sp : padded ? m.rp : m.rows, w = square ? m.sp : padded ? m.cp : m.cols;
-            const int64_t ty = (h + side - 1) / side, tx = (w + side - 1) / side;
-            CHECK((int64_t)kv.second.size() == (square ? ty * (ty + 1) / 2 : ty * tx));
-            for (auto& t : kv.second) {
-                CHECK(t.first.first < ty && t.first.second < tx);
-                if (square) CHECK(t.first.second <= t.first.first);
+            const int64_t h = m.sp, w = square ? m.sp : m.lp;
+            for (auto& t : kv.second) CHECK(t.first.first * (int64_t)th < h && t.first.second * (int64_t)tw < w);
+            if (!square) {
+                CHECK((int64_t)kv.second.size() == (h + th - 1) / th * ((w + tw - 1) / tw));
+                continue;
             }
+            // every 64 x 64 block is written once: by its own tile, or as the mirror of a tile
+            const int64_t n = h / kPad;
+            std::vector<int> hit((size_t)(n * n));
+            for (auto& t : kv.second)
+                for (int64_t y = t.first.first * th / kPad; y < std::min(n, (int64_t)(t.first.first + 1) * th / kPad); ++y)
+                    for (int64_t x = t.first.second * tw / kPad; x < std::min(n, (int64_t)(t.first.second + 1) * tw / kPad); ++x) {
+                        ++hit[(size_t)(y * n + x)];
+                        if (tile_mirrored(l.kind, t.first.first, t.first.second)) ++hit[(size_t)(x * n + y)];
+                    }
+            for (int x : hit) CHECK(x == 1);
         }
         CHECK(l.count <= kMaxNsTiles);
     };
-    cover(b.normalise, kPad, false, true);
-    cover(b.square, kTileSide[b.square.kind], true, true);
-    cover(b.apply, kTileSide[b.apply.kind], false, true);
+    cover(b.normalise, kPad, kPad, false);
+    cover(b.square, kTileRows[b.square.kind], kTileCols[b.square.kind], true);
+    cover(b.apply, kTileRows[b.apply.kind], kTileCols[b.apply.kind], false);
 }
 
 void one_list(Rng& r)

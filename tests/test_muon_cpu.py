@@ -169,13 +169,13 @@ def test_matrix_list_checks_its_tensors():
 
 def test_workspace_bytes():
     one = A.adamw_orthogonalize_workspace_bytes(mats([(2048, 2048)]))
-    # four fp16 copies of the matrix, two squares, diagonals and partial sums
-    assert 12 * 2048 ** 2 <= one <= 12.1 * 2048 ** 2
+    # three fp16 copies of the matrix and two squares, diagonals and partial sums
+    assert 10 * 2048 ** 2 <= one <= 10.1 * 2048 ** 2
     many = A.adamw_orthogonalize_workspace_bytes(mats([(2048, 2048)] * 16))
     assert 15 * one < many <= 16 * one
     assert A.adamw_orthogonalize_workspace_bytes(mats([(2048, 2048)] * 16), least=True) == one
     assert A.adamw_orthogonalize_workspace_bytes(mats([(2048, 2048)] * 1000)) == (4 << 30) + 256
-    assert A.adamw_orthogonalize_workspace_bytes(mats([(65536, 65536)])) > 12 * 65536 ** 2
+    assert A.adamw_orthogonalize_workspace_bytes(mats([(65536, 65536)])) > 10 * 65536 ** 2
     assert A.adamw_orthogonalize_workspace_bytes(A.MatrixList([], [[]])) >= 256
     with pytest.raises(A.AdamWError):
         A.adamw_orthogonalize_workspace_bytes(cols_of(mats(SHAPES), 0, 3))
