@@ -515,7 +515,7 @@ void ns_key(const NsKind& kind, const adamw_tensor_list* list, const int64_t* co
 }
 
 // Validates a list of matrices (once per key), readies its plan on the stream's device and enqueues
-// the batches; for a step (d_step non-null) behind its prologue.
+// the batches (d_step non-null: of a step).
 adamw_status run_ns(const NsKind& kind, const NsScales& scales, const adamw_tensor_list* list, const int64_t* cols,
                     const adamw_muon_hparams& hp, const ClipRule& clip, int32_t* d_step, const int32_t* d_found_inf,
                     const adamw_loss_scale_state* d_amp, void* workspace, int64_t workspace_bytes, void* hip_stream)
@@ -555,13 +555,14 @@ adamw_status run_ns(const NsKind& kind, const NsScales& scales, const adamw_tens
     }
     hipError_t e;
     char* at = static_cast<char*>(workspace);
-    if (d_step) {
-        e = launch_ns_prologue(hp, clip, d_step, d_found_inf, d_amp, at, stream);
-        if (e != hipSuccess) return hip_fail("Muon prologue launch", e);
+    const NsCall call{kind, slot->matrices(), slot->tiles(), at, hp.ns, scales, hp, clip, d_step, d_found_inf, d_amp};
+    const auto& batches = slot->batches;
+    if (batches.empty() && d_step) {
+        e = launch_ns_count(call, stream);
+        if (e != hipSuccess) return hip_fail("Muon counter launch", e);
     }
-    const NsCall call{kind, slot->matrices(), slot->tiles(), at, hp.ns, scales, hp};
-    for (const NsBatch& b : slot->batches) {
-        e = launch_ns_batch(call, b, stream);
+    for (size_t i = 0; i < batches.size(); ++i) {
+        e = launch_ns_batch(call, batches[i], i + 1 == batches.size(), stream);
         if (e != hipSuccess) return hip_fail("Newton-Schulz launch", e);
     }
     return ADAMW_OK;

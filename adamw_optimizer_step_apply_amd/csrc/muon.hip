@@ -51,28 +51,36 @@ __device__ __forceinline__ GLOBAL T* at(char* ws, uint64_t off)
 }
 
 // ---------------------------------------------------------------------------
-// Prologue of a step: one lane.
+// Whether a step is taken, and its gradients' multiplier.
 // ---------------------------------------------------------------------------
 
-__global__ void ns_prologue_kernel(float inv_loss_scale, ClipRule clip, int32_t* __restrict__ step,
-                                   const int32_t* __restrict__ found_inf, const adamw_loss_scale_state* __restrict__ amp,
-                                   NsScalars* __restrict__ out)
+struct StepRule {
+    float inv_loss_scale;
+    ClipRule clip;
+    const int32_t* step;
+    const int32_t* found_inf;
+    const adamw_loss_scale_state* amp;
+};
+
+__device__ __forceinline__ bool begin_step(const StepRule& rule, float& mult)
 {
-    if (threadIdx.x != 0 || blockIdx.x != 0) return;
-    NsScalars s{1, 0.0f};
-    const int32_t step0 = *step;
-    bool take = step0 >= 0 && step0 != INT32_MAX && !(found_inf && *found_inf != 0);
-    float mult = amp ? (float)(1.0 / (double)amp->scale) : inv_loss_scale;
-    if (clip.sumsq) {
-        double factor = 1.0;
-        if (clip_factor(clip, *clip.sumsq, mult, factor)) mult = (float)((double)mult * factor);
-        else take = false;
+    const int32_t step = *rule.step, flag = rule.found_inf ? *rule.found_inf : 0;
+    const float scale = rule.amp ? rule.amp->scale : 1.0f;
+    const double sumsq = rule.clip.sumsq ? *rule.clip.sumsq : 0.0;
+    mult = rule.amp ? (float)(1.0 / (double)scale) : rule.inv_loss_scale;
+    if (step < 0 || step == INT32_MAX || flag != 0) return false;
+    if (rule.clip.sumsq) {
+        double factor;
+        if (!clip_factor(rule.clip, sumsq, mult, factor)) return false;
+        mult = (float)((double)mult * factor);
     }
-    if (take) {
-        s = NsScalars{0, mult};
-        *step = step0 + 1;
-    }
-    *out = s;
+    return true;
+}
+
+__global__ void ns_count_kernel(StepRule rule, int32_t* step)
+{
+    float mult;
+    if (threadIdx.x == 0 && begin_step(rule, mult)) *step += 1;
 }
 
 // ---------------------------------------------------------------------------
@@ -140,52 +148,70 @@ __device__ __forceinline__ float moment(float g, float mult, float& m, const Mom
 template <int IN, bool STEP, bool M16>
 __global__ __launch_bounds__(kBlockMoments) void ns_moments_kernel(const DevMatrix* __restrict__ mats,
                                                                     const DevTile* __restrict__ tiles, char* ws,
-                                                                    MomentCoef c)
+                                                                    MomentCoef c, StepRule rule)
 {
-    const NsScalars* sc = reinterpret_cast<const NsScalars*>(ws);
     float mult = 1.0f;
     if constexpr (STEP) {
-        if (sc->skip) return;
-        mult = sc->mult;
+        const bool take = begin_step(rule, mult);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<NsScalars*>(ws) = NsScalars{take ? 0 : 1};
+        if (!take) return;
     }
+    constexpr int IN_M = M16 ? kInBf16 : kInF32;
     const DevTile t = tiles[blockIdx.x];
     const DevMatrix& mx = mats[t.mat];
-    const uint64_t n = (uint64_t)mx.rows * (uint64_t)mx.cols, first = (uint64_t)t.row * kMomentElems;
-    const uint32_t count = (uint32_t)(n - first < (uint64_t)kMomentElems ? n - first : (uint64_t)kMomentElems);
+    const uint64_t n = (uint64_t)mx.rows * (uint64_t)mx.cols, first = (uint64_t)t.row * mx.chunk;
+    const uint32_t count = (uint32_t)(n - first < mx.chunk ? n - first : mx.chunk);
     const uint32_t packs = mx.flat16 ? count / 8 : 0, tid = threadIdx.x;
     const uint64_t in = mx.ptr[1];
-    GLOBAL float* u = at<float>(ws, mx.u) + first;
+    GLOBAL float* u = at<float>(ws, t.parts.u()) + first;
     double sum = 0.0;
-    for (uint32_t k = tid; k < packs; k += kBlockMoments) {
-        const uint64_t i = first + (uint64_t)k * 8;
-        float x[8];
-        load8<IN>(in, i, x);
-        if constexpr (STEP) {
-            float m[8], v[8];
-            load8<M16 ? kInBf16 : kInF32>(mx.ptr[2], i, m);
+    constexpr int U = 2;   // packs of a lane under way together
+    for (uint32_t k0 = tid; k0 < packs; k0 += kBlockMoments * U) {
+        float x[U][8], m[U][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = moment(x[e], mult, m[e], c);
-                x[e] = v[e];
+        for (int j = 0; j < U; ++j) {
+            // past the end the lane's first pack again, which is not used
+            const uint32_t k = k0 + j * kBlockMoments < packs ? k0 + j * kBlockMoments : k0;
+            load8<IN>(in, first + (uint64_t)k * 8, x[j]);
+            if constexpr (STEP) load8<IN_M>(mx.ptr[2], first + (uint64_t)k * 8, m[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t k = k0 + j * kBlockMoments;
+            if (k >= packs) break;
+            if constexpr (STEP) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[j][e] = moment(x[j][e], mult, m[j][e], c);
+                const uint64_t i = first + (uint64_t)k * 8;
+                if constexpr (M16) *reinterpret_cast<GLOBAL u32x4*>(gptr<uint16_t>(mx.ptr[2], i)) = pack8<false>(m[j]);
+                else store8_f32(gptr<float>(mx.ptr[2], i), m[j]);
+                store8_f32(u + (size_t)k * 8, x[j]);
             }
-            if constexpr (M16) *reinterpret_cast<GLOBAL u32x4*>(gptr<uint16_t>(mx.ptr[2], i)) = pack8<false>(m);
-            else store8_f32(gptr<float>(mx.ptr[2], i), m);
-            store8_f32(u + (size_t)k * 8, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += (double)x[j][e] * (double)x[j][e];
+        }
+    }
+    constexpr int V = 8;   // elements of a lane under way together
+    for (uint32_t k0 = packs * 8 + tid; k0 < count; k0 += kBlockMoments * V) {
+        float x[V], m[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint32_t k = k0 + j * kBlockMoments < count ? k0 + j * kBlockMoments : k0;
+            x[j] = load1<IN>(in, first + k);
+            if constexpr (STEP) m[j] = load1<IN_M>(mx.ptr[2], first + k);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += (double)x[e] * (double)x[e];
-    }
-    for (uint32_t k = packs * 8 + tid; k < count; k += kBlockMoments) {
-        const uint64_t i = first + k;
-        float x = load1<IN>(in, i);
-        if constexpr (STEP) {
-            float m = load1<M16 ? kInBf16 : kInF32>(mx.ptr[2], i);
-            x = moment(x, mult, m, c);
-            if constexpr (M16) *gptr<uint16_t>(mx.ptr[2], i) = narrow1<false>(m);
-            else *gptr<float>(mx.ptr[2], i) = m;
-            u[k] = x;
+        for (int j = 0; j < V; ++j) {
+            const uint32_t k = k0 + j * kBlockMoments;
+            if (k >= count) break;
+            if constexpr (STEP) {
+                x[j] = moment(x[j], mult, m[j], c);
+                if constexpr (M16) *gptr<uint16_t>(mx.ptr[2], first + k) = narrow1<false>(m[j]);
+                else *gptr<float>(mx.ptr[2], first + k) = m[j];
+                u[k] = x[j];
+            }
+            sum += (double)x[j] * (double)x[j];
         }
-        sum += (double)x * (double)x;
     }
     // in a fixed order: lanes of a wave by halves, then the waves
 #pragma unroll
@@ -247,7 +273,7 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
     const bool tall = mx.tall != 0;
     const uint32_t r0 = (tall ? t.col : t.row) * kPad, c0 = (tall ? t.row : t.col) * kPad;
     const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols;
-    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + mx.u : mx.ptr[1];
+    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
     const bool by4 = cols % 4 == 0 && (step || in % 16 == 0);
     f32x4 x[4];
 #pragma unroll
@@ -282,7 +308,7 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
     __syncthreads();
     for (uint32_t k = tid; k < kPad * 8; k += 256) {
         const uint32_t r = k / 8, c = k % 8 * 8;
-        const uint64_t o = (uint64_t)(t.row * kPad + r) * (uint64_t)mx.lp + t.col * kPad + c;
+        const uint64_t o = (uint64_t)(t.row * kPad + r) * (uint64_t)t.parts.lp + t.col * kPad + c;
         f16x8 h, l;
         if (tall) {
 #pragma unroll
@@ -294,8 +320,8 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
             h = *reinterpret_cast<const f16x8*>(hi + r * kLd + c);
             l = *reinterpret_cast<const f16x8*>(lo + r * kLd + c);
         }
-        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.hi[0]) + o) = h;
-        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.lo) + o) = l;
+        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, t.parts.hi(0)) + o) = h;
+        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, t.parts.lo()) + o) = l;
     }
 }
 
@@ -312,6 +338,7 @@ struct ProductArgs {
     int keep_lo;     // the next step is not the last
     int step;        // a Muon step: its skip mark is looked at
     float lr, decay, lrwd;   // a step's last epilogue
+    int32_t* count;          // the counter that the launch advances, or null
 };
 
 __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c)
@@ -452,32 +479,44 @@ __device__ __forceinline__ uint32_t split_master(uint32_t w, uint32_t& r16)
     return hi & 0xffffu;
 }
 
-// The end of the list's work: o = 8 neighbouring elements of the result, from element i.
-// V: 16-byte accesses; else the first n of the 8 one by one.
+// The end of the list's work for element i of a matrix: what it reads, and what it writes given the result o.
+struct EndScalar {
+    uint32_t p, aux;   // as stored
+};
+
 template <int END>
-__device__ __forceinline__ void end_elem(const DevMatrix& mx, uint64_t i, float o, float stepf, const ProductArgs& q)
+__device__ __forceinline__ EndScalar end_read(const DevMatrix& mx, uint64_t i)
 {
+    EndScalar in{};
+    if constexpr (END == kEndSplit || END == kEndPure || END == kEndKahan || END == kEndKahan32)
+        in.p = *gptr<const uint16_t>(mx.ptr[0], i);
+    if constexpr (END == kEndMixedBf16 || END == kEndMixedF16 || END == kEndKahan32) in.aux = *gptr<const uint32_t>(mx.ptr[3], i);
+    if constexpr (END == kEndSplit || END == kEndKahan) in.aux = *gptr<const uint16_t>(mx.ptr[3], i);
+    return in;
+}
+
+template <int END>
+__device__ __forceinline__ void end_write(const DevMatrix& mx, uint64_t i, const EndScalar& in, float o, float stepf,
+                                          const ProductArgs& q)
+{
+    GLOBAL uint16_t* p = gptr<uint16_t>(mx.ptr[0], i);
     if constexpr (END == kEndOrtho) {
-        *gptr<uint16_t>(mx.ptr[0], i) = narrow1<false>(o);
+        *p = narrow1<false>(o);
     } else if constexpr (END == kEndMixedBf16 || END == kEndMixedF16) {
-        GLOBAL float* w = gptr<float>(mx.ptr[3], i);
-        const float x = *w * q.decay - stepf * o;
-        *w = x;
-        *gptr<uint16_t>(mx.ptr[0], i) = narrow1<END == kEndMixedF16>(x);
+        const float x = __uint_as_float(in.aux) * q.decay - stepf * o;
+        *gptr<float>(mx.ptr[3], i) = x;
+        *p = narrow1<END == kEndMixedF16>(x);
     } else if constexpr (END == kEndSplit) {
-        GLOBAL uint16_t* p = gptr<uint16_t>(mx.ptr[0], i);
-        GLOBAL uint16_t* r = gptr<uint16_t>(mx.ptr[3], i);
-        const float x = __uint_as_float(join_master(*p, *r)) * q.decay - stepf * o;
+        const float x = __uint_as_float(join_master(in.p, in.aux)) * q.decay - stepf * o;
         uint32_t r16;
         *p = (uint16_t)split_master(__float_as_uint(x), r16);
-        *r = (uint16_t)r16;
+        *gptr<uint16_t>(mx.ptr[3], i) = (uint16_t)r16;
     } else {
-        GLOBAL uint16_t* p = gptr<uint16_t>(mx.ptr[0], i);
-        const float pf = widen1<false>(*p);
+        const float pf = widen1<false>((uint16_t)in.p);
         if constexpr (END == kEndPure) {
             *p = narrow1<false>(pf * q.decay - stepf * o);
         } else {
-            const float cf = END == kEndKahan ? widen1<false>(*gptr<uint16_t>(mx.ptr[3], i)) : *gptr<float>(mx.ptr[3], i);
+            const float cf = END == kEndKahan ? widen1<false>((uint16_t)in.aux) : __uint_as_float(in.aux);
             const float s = cf + (-(q.lrwd * pf) - stepf * o);
             const uint16_t pn = narrow1<false>(pf + s);
             const float rest = s - (widen1<false>(pn) - pf);
@@ -614,12 +653,12 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
     if (q.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
 
     const DevTile tile = tiles[blockIdx.x];
-    const DevMatrix& mx = mats[tile.mat];
+    const NsParts& parts = tile.parts;
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t sp = (uint32_t)mx.sp, lp = (uint32_t)mx.lp;
+    const uint32_t sp = parts.sp, lp = parts.lp;
     const uint32_t r0 = tile.row * S::rows, c0 = tile.col * S::cols;
-    const GLOBAL _Float16* x_now = at<const _Float16>(ws, mx.hi[q.parity]);
+    const GLOBAL _Float16* x_now = at<const _Float16>(ws, parts.hi(q.parity));
 
     StageP stage_p;
     StageQ stage_q;
@@ -627,10 +666,10 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         stage_p.init(x_now, r0, sp, lp, wave, lane);
         stage_q.init(x_now, c0, sp, lp, wave, lane);
     } else if constexpr (OP == kPoly) {
-        stage_p.init(at<const _Float16>(ws, mx.a), r0, sp, sp, wave, lane);
-        stage_q.init(at<const _Float16>(ws, mx.a), c0, sp, sp, wave, lane);
+        stage_p.init(at<const _Float16>(ws, parts.a()), r0, sp, sp, wave, lane);
+        stage_q.init(at<const _Float16>(ws, parts.a()), c0, sp, sp, wave, lane);
     } else {
-        stage_p.init(at<const _Float16>(ws, mx.b), r0, sp, sp, wave, lane);
+        stage_p.init(at<const _Float16>(ws, parts.b()), r0, sp, sp, wave, lane);
         stage_q.init(x_now, c0, lp, lp, wave, lane);
     }
     const auto load = [&](uint32_t k, uint32_t buf) {
@@ -638,6 +677,49 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         stage_q.load(lds + buf * kStageBytes + kBytesP, k, wave);
     };
     const uint32_t wr = wave / S::wx * WR, wc = wave % S::wx * WC;   // the wave's place in the tile
+
+    // What the epilogue reads.  A wait for a load waits for every store before it too, so each round's is asked for
+    // one round ahead, the first round's of the small tiles, which have registers to spare, before the
+    // summing; and inside the matrix wherever the lane lies, so that all are under way together.
+    constexpr int kRowPacks = WC / 8, kPacks = 32 * kRowPacks / 64;
+    const uint32_t lim_c = kSquare ? sp : lp, col0 = c0 + wc;
+    struct Input {
+        f16x8 x[kPacks];    // A, or lo
+        float dr[kPacks];   // the diagonal of A or B at the rows
+    };
+    const auto read_ahead = [&](int i, Input& in) {
+        if constexpr (OP == kPoly || OP == kApply) {
+#pragma unroll
+            for (int h = 0; h < kPacks; ++h) {
+                const uint32_t k = (uint32_t)h * 64 + lane;
+                uint32_t r = r0 + wr + (uint32_t)i * 32 + k / kRowPacks, c = col0 + k % kRowPacks * 8;
+                r = r < sp ? r : sp - 1;
+                c = c < lim_c ? c : lim_c - 8;
+                in.dr[h] = at<const float>(ws, OP == kPoly ? parts.da() : parts.db())[r];
+                in.x[h] = *reinterpret_cast<const GLOBAL f16x8*>(at<const _Float16>(ws, OP == kPoly ? parts.a() : parts.lo()) +
+                                                                 (uint64_t)r * lim_c + c);
+            }
+        }
+    };
+    float dc[8];   // the diagonal of A at the columns, the same in every round
+    if constexpr (OP == kPoly) {
+        const uint32_t c = col0 + lane % kRowPacks * 8;
+        read8(at<const float>(ws, parts.da()) + (c < sp ? c : sp - 8), dc);
+    }
+    Input in[2];
+    if constexpr (KIND != 0) read_ahead(0, in[0]);
+    // the matrix as the caller has it, for the last product
+    const DevMatrix& mx = mats[OP == kLast ? tile.mat : 0];
+    const bool tall = OP == kLast && mx.tall != 0, row16 = OP == kLast && mx.row16 != 0;
+    const uint32_t rows = OP == kLast ? (uint32_t)mx.rows : 0, cols = OP == kLast ? (uint32_t)mx.cols : 0;
+    const float stepf = OP == kLast ? (float)((double)q.lr * mx.factor) : 0.0f;
+    // The place in the matrix of pack k of round row0: of a tall one, 8 of a column of X.
+    const auto place = [&](uint32_t row0, uint32_t k, uint32_t& r, uint32_t& c) {
+        r = tall ? col0 + k / 4 : row0 + k / kRowPacks;
+        c = tall ? row0 + k % 4 * 8 : col0 + k % kRowPacks * 8;
+    };
+    if constexpr (OP == kLast)
+        if (q.count && blockIdx.x == 0 && tid == 0) *q.count += 1;   // the step is taken
 
     f32x16 acc[MI][NI];
 #pragma unroll
@@ -647,14 +729,11 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    // Summing steps from the one whose rows of X are the tile's own on: apply meets there the elements that its
-    // linear term needs, in the registers that hold them as an operand.
-    const uint32_t nk = (OP == kGram ? lp : sp) / kPad, k0 = kSquare ? 0u : r0 / kPad;
-    const auto step_at = [&](uint32_t t) { return k0 + t < nk ? k0 + t : k0 + t - nk; };
+    const uint32_t nk = (OP == kGram ? lp : sp) / kPad;
     struct Operands {
         f16x8 a[MI], b[NI];
     };
-    const auto read = [&](uint32_t buf, int kk, Operands& o) {
+    const auto read = [&](uint32_t buf, int kk, Operands& o) __attribute__((always_inline)) {
         const char* bp = lds + buf * kStageBytes;
 #pragma unroll
         for (int i = 0; i < MI; ++i) o.a[i] = StageP::operand(bp, wr + i * 32, kk, lane);
@@ -662,13 +741,13 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         for (int j = 0; j < NI; ++j) o.b[j] = StageQ::operand(bp + kBytesP, wc + j * 32, kk, lane);
     };
     // acc += (a + B_rr - fp16(B_rr)) X, for the 16 rows of X in `o` if they are the wave's; acc is under 2^(sb + sx)
-    const auto linear = [&](const Operands& o, uint32_t k, int kk) {
+    const auto linear = [&](const Operands& o, uint32_t k, int kk) __attribute__((always_inline)) {
         const uint32_t first = r0 + wr;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             if ((k * kPad + (uint32_t)kk * 16) / 32 != first / 32 + i) continue;
             const uint32_t r = k * kPad + (uint32_t)kk * 16 + (lane >> 5) * 4;
-            const GLOBAL float* db = at<const float>(ws, mx.db) + r;
+            const GLOBAL float* db = at<const float>(ws, parts.db()) + r;
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -695,98 +774,104 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 
 #pragma unroll
     for (uint32_t t = 0; t + 1 < S::stages; ++t)
-        if (t < nk) load(step_at(t), t);
+        if (t < nk) load(t, t);
     // stage 0 has arrived: all but the loads behind it
     if (nk >= S::stages - 1) wait_and_meet<(S::stages - 2) * kLoads>();
     else wait_and_meet<0>();
-    Operands o[2];
-    read(0, 0, o[0]);
     uint32_t buf = 0, fill = S::stages - 1;
-    const auto summing_step = [&](uint32_t t, auto with_linear) {
-        if (t + S::stages - 1 < nk) load(step_at(t + S::stages - 1), fill);
+    const auto multiply = [&](const Operands& o) __attribute__((always_inline)) {
 #pragma unroll
-        for (int kk = 0; kk < kPad / 16; ++kk) {
-            if (kk + 1 < kPad / 16) {
-                read(buf, kk + 1, o[(kk + 1) & 1]);
-            } else if (t + 1 < nk) {
-                // The next stage has arrived, and every wave has its last operands of this one, whose room is
-                // loaded next; the matrix instructions below cover the reads.
-                if (t + S::stages - 1 < nk) wait_and_meet<(S::stages - 2) * kLoads>();
-                else wait_and_meet<0>();
-                fill = buf;
-                buf = buf + 1 == S::stages ? 0 : buf + 1;
-                read(buf, 0, o[0]);
-            }
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < NI; ++j) acc[i][j] = mfma(o[kk & 1].a[i], o[kk & 1].b[j], acc[i][j]);
-            if constexpr (decltype(with_linear)::value) linear(o[kk & 1], step_at(t), kk);
-        }
+            for (int j = 0; j < NI; ++j) acc[i][j] = mfma(o.a[i], o.b[j], acc[i][j]);
     };
+    // Waits until the stage behind `buf` has arrived, and every wave has its last operands of this one, whose room is
+    // loaded next.
+    const auto next_stage = [&](uint32_t t) __attribute__((always_inline)) {
+        if (S::stages > 2 && t + S::stages - 1 < nk) wait_and_meet<(S::stages - 2) * kLoads>();
+        else wait_and_meet<0>();
+        fill = buf;
+        buf = buf + 1 == S::stages ? 0 : buf + 1;
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
     uint32_t t = 0;
-    if constexpr (!kSquare)
-        for (; t < S::rows / kPad && t < nk; ++t) summing_step(t, std::true_type{});
-    for (; t < nk; ++t) summing_step(t, std::false_type{});
+    if constexpr (KIND == 2) {
+        // One matrix instruction a wave for each 16 summed elements: the reads of a whole stage lie between its
+        // arrival and the instructions of the one before.
+        Operands o[2][kPad / 16];
+        const auto read_stage = [&](Operands(&to)[kPad / 16]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int kk = 0; kk < kPad / 16; ++kk) read(buf, kk, to[kk]);
+        };
+        const auto summing_step = [&](uint32_t t, auto odd, auto last) __attribute__((always_inline)) {
+            constexpr int now = decltype(odd)::value ? 1 : 0;
+            if (t + S::stages - 1 < nk) load(t + S::stages - 1, fill);
+            if constexpr (!decltype(last)::value) {
+                next_stage(t);
+                read_stage(o[now ^ 1]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int kk = 0; kk < kPad / 16; ++kk) {
+                multiply(o[now][kk]);
+                if constexpr (!kSquare) linear(o[now][kk], t, kk);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        read_stage(o[0]);
+        for (; t + 2 < nk; t += 2) {
+            summing_step(t, No{}, No{});
+            summing_step(t + 1, Yes{}, No{});
+        }
+        if (t + 1 < nk) {
+            summing_step(t, No{}, No{});
+            summing_step(t + 1, Yes{}, Yes{});
+        } else {
+            summing_step(t, No{}, Yes{});
+        }
+    } else {
+        Operands o[2];
+        read(0, 0, o[0]);
+        // One summing step.  The next operands are asked for before the matrix instructions of the present ones; left to
+        // itself the compiler moves the reads behind them and waits for each.
+        const auto summing_step = [&](uint32_t t, auto with_linear, auto last) __attribute__((always_inline)) {
+            if (S::stages == 2 ? !decltype(last)::value : t + S::stages - 1 < nk) load(t + S::stages - 1, fill);
+#pragma unroll
+            for (int kk = 0; kk < kPad / 16; ++kk) {
+                if (kk + 1 < kPad / 16) {
+                    read(buf, kk + 1, o[(kk + 1) & 1]);
+                } else if (!decltype(last)::value) {
+                    next_stage(t);
+                    read(buf, 0, o[0]);   // covered by the matrix instructions below
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(o[kk & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (decltype(with_linear)::value) linear(o[kk & 1], t, kk);
+            }
+        };
+        if constexpr (!kSquare) {
+            // the steps whose rows of X are the tile's own: apply meets there the elements that its linear term needs, in
+            // the registers that hold them as an operand
+            for (; t < r0 / kPad; ++t) summing_step(t, No{}, No{});
+            for (; t < (r0 + S::rows) / kPad && t + 1 < nk; ++t) summing_step(t, Yes{}, No{});
+        }
+        for (; t + 1 < nk; ++t) summing_step(t, No{}, No{});
+        summing_step(t, std::bool_constant<!kSquare>{}, Yes{});
+    }
     wait_and_meet<0>();   // the operands' room is free
 
     // Epilogue, 32 rows of the wave's part at a time through LDS of its own: 8 neighbours of a row to a
-    // lane, and for what is needed by columns then 8 of a column.  What is read for it is read one round
-    // ahead, since a wait for a load waits for every store before it too; and inside the
-    // matrix wherever the lane lies, so that all reads are under way together.
+    // lane, and for what is needed by columns then 8 of a column.
     float* out = reinterpret_cast<float*>(lds + wave * kEpiBytes);
-    constexpr int kRowPacks = WC / 8, kPacks = 32 * kRowPacks / 64;
-    const uint32_t lim_c = kSquare ? sp : lp;
-    const float stepf = OP == kLast ? (float)((double)q.lr * mx.factor) : 0.0f;
-    const bool tall = OP == kLast && mx.tall != 0, row16 = OP == kLast && mx.row16 != 0;
-    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, col0 = c0 + wc;
-    struct Input {
-        f16x8 x[kPacks];    // A, or lo
-        float dr[kPacks];   // the diagonal of A or B at the rows
-    };
-    // ... and at the columns, the same in every round
-    float dc[8];
-    if constexpr (OP == kPoly) {
-        const uint32_t c = col0 + lane % kRowPacks * 8;
-        read8(at<const float>(ws, mx.da) + (c < sp ? c : sp - 8), dc);
-    }
-    const auto read_ahead = [&](int i, Input& in) {
-        if constexpr (OP == kPoly || OP == kApply) {
-#pragma unroll
-            for (int h = 0; h < kPacks; ++h) {
-                const uint32_t k = (uint32_t)h * 64 + lane;
-                uint32_t r = r0 + wr + (uint32_t)i * 32 + k / kRowPacks, c = col0 + k % kRowPacks * 8;
-                r = r < sp ? r : sp - 1;
-                c = c < lim_c ? c : lim_c - 8;
-                in.dr[h] = at<const float>(ws, OP == kPoly ? mx.da : mx.db)[r];
-                in.x[h] = *reinterpret_cast<const GLOBAL f16x8*>(at<const _Float16>(ws, OP == kPoly ? mx.a : mx.lo) +
-                                                                 (uint64_t)r * lim_c + c);
-            }
-        }
-    };
-    // The place in the matrix of pack k of round row0: of a tall one, 8 of a column of X.
-    const auto place = [&](uint32_t row0, uint32_t k, uint32_t& r, uint32_t& c) {
-        r = tall ? col0 + k / 4 : row0 + k / kRowPacks;
-        c = tall ? row0 + k % 4 * 8 : col0 + k % kRowPacks * 8;
-    };
-    const auto finish = [&](uint32_t r, uint32_t c, const EndInput<END>& in, const float(&v)[8]) {
-        if (r >= rows || c >= cols) return;
-        const uint64_t i = (uint64_t)r * cols + c;
-        if (row16) {
-            end_eight<END>(mx, i, in, v, stepf, q);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < cols) end_elem<END>(mx, i + e, v[e], stepf, q);
-        }
-    };
-    Input in[2];
-    read_ahead(0, in[0]);
+    if constexpr (KIND == 0) read_ahead(0, in[0]);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const uint32_t row0 = r0 + wr + (uint32_t)i * 32;
         const Input& now = in[i & 1];
         if (i + 1 < MI) read_ahead(i + 1, in[(i + 1) & 1]);
+        const float scale = OP == kLast ? pow2(-q.sb - q.sx) : 1.0f;
         EndInput<END> end[kPacks];
         if constexpr (OP == kLast) {
             if (row16) {
@@ -805,8 +890,46 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         for (int j = 0; j < NI; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                out[((e & 3) + 8 * (e >> 2) + 4 * (lane >> 5)) * kEpiLd + j * 32 + (lane & 31u)] = acc[i][j][e];
+                out[((e & 3) + 8 * (e >> 2) + 4 * (lane >> 5)) * kEpiLd + j * 32 + (lane & 31u)] = acc[i][j][e] * scale;
         __builtin_amdgcn_wave_barrier();
+        if constexpr (OP == kLast) {
+            if (row16) {
+#pragma unroll
+                for (int h = 0; h < kPacks; ++h) {
+                    const uint32_t k = (uint32_t)h * 64 + lane;
+                    uint32_t r, c;
+                    place(row0, k, r, c);
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = tall ? out[(k % 4 * 8 + e) * kEpiLd + k / 4] : out[k / kRowPacks * kEpiLd + k % kRowPacks * 8 + e];
+                    if (r < rows && c < cols) end_eight<END>(mx, (uint64_t)r * cols + c, end[h], v, stepf, q);
+                }
+            } else {
+                // element by element along the matrix's rows, kSome of a lane under way together
+                constexpr uint32_t kSome = 8;
+                for (uint32_t k0 = lane; k0 < 32 * WC; k0 += 64 * kSome) {
+                    EndScalar some[kSome];
+                    float v[kSome];
+                    uint64_t at_rc[kSome];
+                    bool inside[kSome];
+#pragma unroll
+                    for (uint32_t h = 0; h < kSome; ++h) {
+                        const uint32_t k = k0 + h * 64, lr = tall ? k % 32 : k / WC, lc = tall ? k / 32 : k % WC;
+                        const uint32_t r = tall ? col0 + lc : row0 + lr, c = tall ? row0 + lr : col0 + lc;
+                        inside[h] = r < rows && c < cols;
+                        at_rc[h] = inside[h] ? (uint64_t)r * cols + c : 0;
+                        v[h] = out[lr * kEpiLd + lc];
+                        some[h] = end_read<END>(mx, at_rc[h]);
+                    }
+#pragma unroll
+                    for (uint32_t h = 0; h < kSome; ++h)
+                        if (inside[h]) end_write<END>(mx, at_rc[h], some[h], v[h], stepf, q);
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+            continue;
+        }
 #pragma unroll
         for (int h = 0; h < kPacks; ++h) {
             const uint32_t k = (uint32_t)h * 64 + lane, lr = k / kRowPacks, lc = k % kRowPacks * 8;
@@ -840,61 +963,44 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
                     }
                 }
                 if (inside) {
-                    store_diagonal(at<float>(ws, OP == kGram ? mx.da : mx.db), r, c, v);
+                    store_diagonal(at<float>(ws, OP == kGram ? parts.da() : parts.db()), r, c, v);
                     f16x8 w;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = (_Float16)v[e];
-                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? mx.a : mx.b) + at_rc) = w;
+                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? parts.a() : parts.b()) + at_rc) = w;
                 }
-            } else {
-                if constexpr (OP == kApply) {
-                    // X' * 2^sx; the last step reads no lo
-                    const float f = pow2(-q.sb), of_lo = __builtin_fmaf(now.dr[h], f, q.a) * (1.0f / kLoScale);
-                    f16x8 h8, l8;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        _Float16 x, y;
-                        split_pair(__builtin_fmaf(of_lo, (float)now.x[h][e], v[e] * f), x, y);
-                        h8[e] = x;
-                        l8[e] = y;
-                    }
-                    if (inside) {
-                        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.hi[q.parity ^ 1]) + at_rc) = h8;
-                        if (q.keep_lo) *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, mx.lo) + at_rc) = l8;
-                    }
-                } else {
-                    const float g = pow2(-q.sb - q.sx);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= g;
-                    if (!tall) finish(r, c, end[h], v);
-                }
-            }
-            if (OP == kGram || OP == kPoly || tall) {
                 *reinterpret_cast<f32x4*>(cell) = f32x4{v[0], v[1], v[2], v[3]};
                 *reinterpret_cast<f32x4*>(cell + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            } else {
+                // X' * 2^sx; the last step reads no lo
+                const float f = pow2(-q.sb), of_lo = __builtin_fmaf(now.dr[h], f, q.a) * (1.0f / kLoScale);
+                f16x8 h8, l8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    _Float16 x, y;
+                    split_pair(__builtin_fmaf(of_lo, (float)now.x[h][e], v[e] * f), x, y);
+                    h8[e] = x;
+                    l8[e] = y;
+                }
+                if (inside) {
+                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, parts.hi(q.parity ^ 1)) + at_rc) = h8;
+                    if (q.keep_lo) *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, parts.lo()) + at_rc) = l8;
+                }
             }
         }
         __builtin_amdgcn_wave_barrier();
-        if constexpr (kSquare || OP == kLast) {
-            // by columns: 8 of a column to a lane, 4 lanes to a column of the 32 rows
-            const bool wanted = kSquare ? tile_mirrored(KIND, tile.row, tile.col) : tall;
-            if (wanted) {
+        if constexpr (kSquare) {
+            if (tile_mirrored(KIND, tile.row, tile.col)) {
+                // by columns: 8 of a column to a lane, 4 lanes to a column of the 32 rows
 #pragma unroll
                 for (int h = 0; h < kPacks; ++h) {
                     const uint32_t k = (uint32_t)h * 64 + lane, lc = k / 4, lr = k % 4 * 8;
                     const uint32_t r = row0 + lr, c = col0 + lc;
-                    float v[8];
+                    f16x8 w;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = out[(lr + e) * kEpiLd + lc];
-                    if constexpr (kSquare) {
-                        f16x8 w;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = (_Float16)v[e];
-                        if (r < sp && c < sp)
-                            *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? mx.a : mx.b) + (uint64_t)c * sp + r) = w;
-                    } else {
-                        finish(c, r, end[h], v);
-                    }
+                    for (int e = 0; e < 8; ++e) w[e] = (_Float16)out[(lr + e) * kEpiLd + lc];
+                    if (r < sp && c < sp)
+                        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? parts.a() : parts.b()) + (uint64_t)c * sp + r) = w;
                 }
             }
             __builtin_amdgcn_wave_barrier();
@@ -905,15 +1011,6 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
-
-hipError_t launch_ns_prologue(const adamw_muon_hparams& hp, const ClipRule& clip, int32_t* d_step,
-                              const int32_t* d_found_inf, const adamw_loss_scale_state* d_amp, char* ws,
-                              hipStream_t stream)
-{
-    ns_prologue_kernel<<<1, 64, 0, stream>>>(hp.inv_loss_scale, clip, d_step, d_found_inf, d_amp,
-                                             reinterpret_cast<NsScalars*>(ws));
-    return hipGetLastError();
-}
 
 namespace {
 
@@ -947,13 +1044,14 @@ hipError_t last_product(const NsCall& call, const NsLaunch& l, const ProductArgs
 }
 
 template <int IN>
-hipError_t moments(const NsCall& call, const NsLaunch& l, bool step, const MomentCoef& c, hipStream_t stream)
+hipError_t moments(const NsCall& call, const NsLaunch& l, bool step, const MomentCoef& c, const StepRule& rule,
+                   hipStream_t stream)
 {
     const DevTile* tiles = call.tiles + l.first;
     const dim3 grid((uint32_t)l.count), block(kBlockMoments);
-    if (!step) ns_moments_kernel<IN, false, false><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, c);
-    else if (call.kind.m16) ns_moments_kernel<IN, true, true><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, c);
-    else ns_moments_kernel<IN, true, false><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, c);
+    if (!step) ns_moments_kernel<IN, false, false><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, c, rule);
+    else if (call.kind.m16) ns_moments_kernel<IN, true, true><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, c, rule);
+    else ns_moments_kernel<IN, true, false><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, c, rule);
     return hipGetLastError();
 }
 
@@ -965,9 +1063,20 @@ hipError_t normalise(const NsCall& call, const NsLaunch& l, bool step, hipStream
     return hipGetLastError();
 }
 
+StepRule step_rule(const NsCall& call)
+{
+    return StepRule{call.hp.inv_loss_scale, call.clip, call.step, call.found_inf, call.amp};
+}
+
 }  // namespace
 
-hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, hipStream_t stream)
+hipError_t launch_ns_count(const NsCall& call, hipStream_t stream)
+{
+    ns_count_kernel<<<1, 64, 0, stream>>>(step_rule(call), call.step);
+    return hipGetLastError();
+}
+
+hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, hipStream_t stream)
 {
     const bool step = call.kind.end != kEndOrtho;
     const int in = call.kind.in == ADAMW_F32 ? kInF32 : call.kind.in == ADAMW_BF16 ? kInBf16 : kInF16;
@@ -987,9 +1096,10 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, hipStream_t
         q.decay = (float)(1.0 - lr * wd);
         q.lrwd = (float)(lr * wd);
     }
-    hipError_t e = in == kInF32 ? moments<kInF32>(call, batch.moments, step, mc, stream)
-                 : in == kInBf16 ? moments<kInBf16>(call, batch.moments, step, mc, stream)
-                                 : moments<kInF16>(call, batch.moments, step, mc, stream);
+    const StepRule rule = step_rule(call);
+    hipError_t e = in == kInF32 ? moments<kInF32>(call, batch.moments, step, mc, rule, stream)
+                 : in == kInBf16 ? moments<kInBf16>(call, batch.moments, step, mc, rule, stream)
+                                 : moments<kInF16>(call, batch.moments, step, mc, rule, stream);
     if (e != hipSuccess) return e;
     e = step || in == kInF32 ? normalise<kInF32>(call, batch.normalise, step, stream)
       : in == kInBf16 ? normalise<kInBf16>(call, batch.normalise, step, stream)
@@ -1000,7 +1110,12 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, hipStream_t
         q.keep_lo = k + 2 < call.ns.steps;
         if ((e = product<kGram>(call, batch.square, q, stream)) != hipSuccess) return e;
         if ((e = product<kPoly>(call, batch.square, q, stream)) != hipSuccess) return e;
-        e = k + 1 < call.ns.steps ? product<kApply>(call, batch.apply, q, stream) : last_product(call, batch.apply, q, stream);
+        if (k + 1 < call.ns.steps) {
+            e = product<kApply>(call, batch.apply, q, stream);
+        } else {
+            q.count = last ? call.step : nullptr;
+            e = last_product(call, batch.apply, q, stream);
+        }
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -29,7 +29,9 @@ constexpr int kPad = 64;                  // padding of both sides, and elements
 constexpr int64_t kNsAlign = 256;         // of every part of the workspace
 constexpr int64_t kNsHeadBytes = 256;     // the step's scalars, at the workspace's start
 constexpr int64_t kNsBatchBytes = INT64_C(4) << 30;   // workspace of a batch of a long list
-constexpr int64_t kMomentElems = 16384;   // elements of a workgroup of the moments kernel
+// Elements of a workgroup of the moments kernel: a multiple of this, so that a matrix has at
+// most kMaxPartials partial sums, which every workgroup of the normalisation adds up.
+constexpr int64_t kMomentElems = 4096, kMaxPartials = 256;
 constexpr int kBlockMoments = 256;
 
 // Tiles of the product kernels: rows, columns, and lanes of a workgroup.
@@ -48,34 +50,52 @@ constexpr bool tile_mirrored(int kind, int64_t row, int64_t col)
     return (col + 1) * kTileCols[kind] <= row * kTileRows[kind];
 }
 
-// Tiles that a launch should have before it takes the larger kind: one for every CU.
-constexpr int64_t kTilesWanted = 256;
 constexpr int64_t kMaxNsSide = INT64_C(1) << 30, kMaxNsShort = INT64_C(1) << 20;
 // A grid counts at most 2^32 - 1 lanes.
 constexpr int64_t kMaxNsTiles = (int64_t)UINT32_MAX / 512;
 
-// One matrix of a batch.  X is held wide whatever the matrix is: s rows of l elements, s <= l, transposed for
-// a matrix that is taller than wide.  Parts of the workspace are byte offsets from its start.
-// hi, lo: X, sp rows of lp elements, of which l are used, the others zeros; the value is
-// (hi + lo * 2^-11) * 2^-sx; hi has two buffers, since workgroups of the product with B write
-// new values while others read the old.  a, b: the squares, sp x sp; da, db: their diagonals in
-// fp32.  u (a step's fp32 matrix as it lies in the caller's buffers) has the room of hi[1], a and b.
+// One matrix's parts of the workspace, one after another from byte `base` of it, where X is sp x lp: X is held
+// wide whatever the matrix is, s rows of l elements, s <= l, transposed for a matrix that is taller than wide, both
+// padded by zeros.
+// da, db: the diagonals of the squares A and B in fp32.  hi, lo: X is (hi + lo * 2^-11) * 2^-sx; hi has
+// two buffers, since workgroups of the product with B write new values while others read the
+// old.  a, b: the squares, sp x sp.  u, a step's fp32 matrix as it lies in the caller's
+// buffers, has the room of hi(1), a and b.
+struct NsParts {
+    uint64_t base;
+    uint32_t sp, lp;
+
+    constexpr uint64_t whole() const { return (uint64_t)sp * lp * 2; }
+    constexpr uint64_t square() const { return (uint64_t)sp * sp * 2; }
+    constexpr uint64_t da() const { return base; }
+    constexpr uint64_t db() const { return base + (uint64_t)sp * 4; }
+    constexpr uint64_t lo() const { return base + (uint64_t)sp * 8; }
+    constexpr uint64_t hi(int k) const { return lo() + whole() * (uint64_t)(1 + k); }
+    constexpr uint64_t u() const { return hi(1); }
+    constexpr uint64_t a() const { return hi(1) + whole(); }
+    constexpr uint64_t b() const { return a() + square(); }
+    constexpr uint64_t end() const { return b() + square(); }
+};
+
+// One matrix of a batch; its partial sums lie behind its parts.
 struct alignas(16) DevMatrix {
     uint64_t ptr[4];          // element 0: result or param; u or grad; exp_avg; aux
-    uint64_t u, hi[2], lo, a, b, da, db, partials;
+    NsParts parts;
+    uint64_t partials;        // offset in the workspace
     double factor;            // s of the step
     int32_t rows, cols;
-    int32_t s, l, sp, lp;   // lp, sp: padded
-    int32_t tall;             // rows > cols
-    uint32_t n_partials;
+    uint32_t tall;            // rows > cols
+    uint32_t chunk, n_partials;
     uint32_t flat16;          // every stream's element 0 is 16-byte aligned
     uint32_t row16;           // and so is every row of 8 elements' multiples
-    uint32_t pad[2];
+    uint32_t pad;
 };
 
 // One workgroup's part of a matrix: a tile of the products (row and column of the tile),
-// a 64 x 64 tile of the normalisation, or a run of elements (its number).
+// a 64 x 64 tile of the normalisation, or a run of elements (its number).  With the parts in
+// it a product's first loads hang on one load of its own.
 struct alignas(16) DevTile {
+    NsParts parts;
     uint32_t mat, row, col, pad;
 };
 
@@ -130,10 +150,9 @@ adamw_status ns_workspace_bytes(const adamw_tensor_list* list, const int64_t* co
 adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, const int64_t* cols, int scaling,
                            uint64_t workspace, int64_t workspace_bytes, NsPlan* out, std::string& err);
 
-// Scalars of one step, at the start of the workspace.
+// What the moments kernel leaves for the others at the start of the workspace.
 struct NsScalars {
     int32_t skip;
-    float mult;
 };
 
 }  // namespace adamw

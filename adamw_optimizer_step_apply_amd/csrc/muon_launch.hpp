@@ -15,11 +15,16 @@ struct NsCall {
     char* ws;
     adamw_newton_schulz ns;
     NsScales scales;
-    adamw_muon_hparams hp;   // a step's
+    // a step's
+    adamw_muon_hparams hp;
+    ClipRule clip;
+    int32_t* step;
+    const int32_t* found_inf;
+    const adamw_loss_scale_state* amp;
 };
-hipError_t launch_ns_prologue(const adamw_muon_hparams& hp, const ClipRule& clip, int32_t* d_step,
-                              const int32_t* d_found_inf, const adamw_loss_scale_state* d_amp, char* ws,
-                              hipStream_t stream);
-hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, hipStream_t stream);
+// `last`: the list's last batch, which advances a step's counter
+hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, hipStream_t stream);
+// A step over an empty list: the counter alone.
+hipError_t launch_ns_count(const NsCall& call, hipStream_t stream);
 
 }  // namespace adamw

@@ -70,10 +70,13 @@ adamw_status shapes_of(const adamw_tensor_list* list, const int64_t* cols, std::
                 return ADAMW_E_INVALID;
             }
             const Shape s{i, n / c, c};
-            // 32-bit row numbers, and byte counts that stay far from 2^63
-            if (s.rows > kMaxNsSide || s.cols > kMaxNsSide || std::min(s.rows, s.cols) > kMaxNsShort) {
-                snprintf(buf, sizeof buf, "matrix %lld of %lld x %lld is larger than 2^30 on a side or 2^20 on both",
-                         (long long)i, (long long)s.rows, (long long)s.cols);
+            // 32-bit row numbers, and byte counts that stay far from 2^63; the normalisation's launch has the most
+            // workgroups, one for 64 x 64 elements
+            if (s.rows > kMaxNsSide || s.cols > kMaxNsSide || std::min(s.rows, s.cols) > kMaxNsShort ||
+                round_up(s.rows, kPad) / kPad * (round_up(s.cols, kPad) / kPad) > kMaxNsTiles) {
+                snprintf(buf, sizeof buf,
+                         "matrix %lld of %lld x %lld is larger than 2^30 on a side, 2^20 on both or %lld tiles of 64 x 64",
+                         (long long)i, (long long)s.rows, (long long)s.cols, (long long)kMaxNsTiles);
                 err = buf;
                 return ADAMW_E_INVALID;
             }
@@ -87,29 +90,16 @@ adamw_status shapes_of(const adamw_tensor_list* list, const int64_t* cols, std::
 // Lays one matrix out from byte `at` of the workspace; returns the end.
 int64_t place(const Shape& sh, int64_t at, DevMatrix* m)
 {
-    const int64_t s = std::min(sh.rows, sh.cols), l = std::max(sh.rows, sh.cols);
-    const int64_t sp = round_up(s, kPad), lp = round_up(l, kPad);
-    const int64_t part = round_up(2 * sp * lp, kNsAlign), square = round_up(2 * sp * sp, kNsAlign);
-    const int64_t chunks = (s * l + kMomentElems - 1) / kMomentElems;
+    const int64_t n = sh.rows * sh.cols, s = std::min(sh.rows, sh.cols), l = std::max(sh.rows, sh.cols);
     m->rows = (int32_t)sh.rows;
     m->cols = (int32_t)sh.cols;
-    m->s = (int32_t)s;
-    m->l = (int32_t)l;
-    m->sp = (int32_t)sp;
-    m->lp = (int32_t)lp;
     m->tall = sh.rows > sh.cols;
-    m->n_partials = (uint32_t)chunks;
-    m->hi[0] = (uint64_t)at;
-    m->lo = m->hi[0] + (uint64_t)part;
-    m->hi[1] = m->lo + (uint64_t)part;
-    m->a = m->hi[1] + (uint64_t)part;
-    m->b = m->a + (uint64_t)square;
-    m->u = m->hi[1];
-    const int64_t room = std::max(part + 2 * square, round_up(4 * s * l, kNsAlign));
-    m->da = m->u + (uint64_t)room;
-    m->db = m->da + (uint64_t)round_up(4 * sp, kNsAlign);
-    m->partials = m->db + (uint64_t)round_up(4 * sp, kNsAlign);
-    return (int64_t)m->partials + round_up(8 * chunks, kNsAlign);
+    m->parts = NsParts{(uint64_t)at, (uint32_t)round_up(s, kPad), (uint32_t)round_up(l, kPad)};
+    m->chunk = (uint32_t)round_up((n + kMaxPartials - 1) / kMaxPartials, kMomentElems);
+    m->n_partials = (uint32_t)((n + m->chunk - 1) / m->chunk);
+    const int64_t end = std::max((int64_t)m->parts.end(), (int64_t)m->parts.u() + round_up(4 * n, kNsAlign));
+    m->partials = (uint64_t)end;
+    return end + round_up(8 * (int64_t)m->n_partials, kNsAlign);
 }
 
 // Bytes of a matrix's part of the workspace, the same for both calls.
@@ -145,13 +135,42 @@ int64_t square_tiles(int64_t s, int kind)
     return n;
 }
 
-// The largest tile with which a launch has work for every CU.
-template <typename Count>
-int pick_kind(const Count& count)
+// The tiles' costs in microseconds on one CU: cost + K * per_k for a tile of K summed elements, as fitted to single
+// launches on MI355X (K from 64 to 8192, 3 to 8192 tiles).  One launch takes about `start` and the larger of
+// its longest tile and its tiles' sum over 256 CUs; of the largest kind one workgroup fits on a CU, so its
+// tiles come in whole rounds.  Measured with kinds 0 / 1 / 2, in us: Gram products of 768 x 768 27.6 / 13.9 / 6.6, of
+// four of 768 x 2304 59.9 / 31.0 / 20.7, of four of 2048 x 8192 389 / 258 / 270; products with X of
+// four of 768 x 2304 36.1 / 25.8 / 40.6, of 64 of 512 x 1024 75 / 80 / 137, of four of 2048 x 2048 86 / 100 / 189.
+struct TileCost {
+    double start, square, apply, per_k;
+};
+constexpr TileCost kTileCost[kTileKinds] = {{2.0, 10.0, 22.0, 0.0285}, {3.0, 4.0, 4.0, 0.0115}, {2.5, 2.0, 2.0, 0.0032}};
+constexpr int64_t kCus = 256;
+
+// The kind of tile for a launch over matrices of (tiles of the kind, summed elements).
+template <typename Each>
+int pick_kind(bool square, const Each& each)
 {
-    for (int k = 0; k < kTileKinds - 1; ++k)
-        if (count(k) >= kTilesWanted) return k;
-    return kTileKinds - 1;
+    int best = 0;
+    double least = 0.0;
+    for (int kind = 0; kind < kTileKinds; ++kind) {
+        const TileCost& c = kTileCost[kind];
+        double sum = 0.0, longest = 0.0;
+        int64_t n = 0;
+        each(kind, [&](int64_t tiles, int64_t k) {
+            const double one = (square ? c.square : c.apply) + c.per_k * (double)k;
+            sum += one * (double)tiles;
+            longest = std::max(longest, one);
+            n += tiles;
+        });
+        const double rounds = kind == 0 ? (double)((n + kCus - 1) / kCus) * (double)kCus / (double)std::max<int64_t>(n, 1) : 1.0;
+        const double cost = c.start + std::max(longest, sum / (double)kCus * rounds);
+        if (kind == 0 || cost < least) {
+            best = kind;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -289,13 +308,6 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
         }
         (w ? end_w : end_r) = std::max(w ? end_w : end_r, r[i].hi);
     }
-    // The normalisation's launch has the most workgroups, one for 64 x 64 elements: a batch
-    // that passes the limit is counted before its tiles are listed.
-    for (const Shape& s : shapes)
-        if (tiles_of(s.rows, kPad) * tiles_of(s.cols, kPad) > kMaxNsTiles) {
-            err = "a matrix needs more than 8,388,607 tiles in one launch";
-            return ADAMW_E_INVALID;
-        }
     if (!out) return ADAMW_OK;
 
     *out = NsPlan();
@@ -328,6 +340,9 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
         for (size_t k = i; k < end; ++k) order.push_back(k);
         NsBatch b;
         std::vector<DevTile> tiles;
+        const auto tile = [&](size_t k, int64_t row, int64_t col) {
+            return DevTile{out->mats[k].parts, (uint32_t)k, (uint32_t)row, (uint32_t)col, 0};
+        };
         const auto take = [&](NsLaunch* l) {
             l->first = (int64_t)out->tiles.size();
             l->count = (int64_t)tiles.size();
@@ -335,44 +350,47 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
             tiles.clear();
         };
         for (size_t k : order)
-            for (uint32_t c = 0; c < out->mats[k].n_partials; ++c) tiles.push_back(DevTile{(uint32_t)k, c, 0, 0});
+            for (uint32_t c = 0; c < out->mats[k].n_partials; ++c) tiles.push_back(tile(k, c, 0));
         take(&b.moments);
         for (size_t k : order)
-            for (int32_t y = 0; y < out->mats[k].sp / kPad; ++y)
-                for (int32_t x = 0; x < out->mats[k].lp / kPad; ++x)
-                    tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
+            for (uint32_t y = 0; y < out->mats[k].parts.sp / kPad; ++y)
+                for (uint32_t x = 0; x < out->mats[k].parts.lp / kPad; ++x)
+                    tiles.push_back(tile(k, y, x));
         take(&b.normalise);
-        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].l > out->mats[y].l; });
-        b.square.kind = pick_kind([&](int kind) {
-            int64_t t = 0;
-            for (size_t k : order) t += square_tiles(out->mats[k].s, kind);
-            return t;
+        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.lp > out->mats[y].parts.lp; });
+        b.square.kind = pick_kind(true, [&](int kind, const auto& add) {
+            for (size_t k : order) {
+                const NsParts& p = out->mats[k].parts;
+                const int64_t n = square_tiles(p.sp, kind);
+                add(n, p.lp);
+                add(n, p.sp);
+            }
         });
-        b.apply.kind = pick_kind([&](int kind) {
-            int64_t t = 0;
-            for (size_t k : order)
-                t += tiles_of(out->mats[k].s, kTileRows[kind]) * tiles_of(out->mats[k].l, kTileCols[kind]);
-            return t;
+        b.apply.kind = pick_kind(false, [&](int kind, const auto& add) {
+            for (size_t k : order) {
+                const NsParts& p = out->mats[k].parts;
+                add(tiles_of(p.sp, kTileRows[kind]) * tiles_of(p.lp, kTileCols[kind]), p.sp);
+            }
         });
         // bands of 4 tile rows, column by column
         constexpr int64_t kBand = 4;
         for (size_t k : order) {
             const int kind = b.square.kind;
-            const int64_t ty = tiles_of(out->mats[k].s, kTileRows[kind]), tx = tiles_of(out->mats[k].s, kTileCols[kind]);
+            const int64_t ty = tiles_of(out->mats[k].parts.sp, kTileRows[kind]), tx = tiles_of(out->mats[k].parts.sp, kTileCols[kind]);
             for (int64_t y0 = 0; y0 < ty; y0 += kBand)
                 for (int64_t x = 0; x < tx; ++x)
                     for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
-                        if (tile_needed(kind, y, x)) tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
+                        if (tile_needed(kind, y, x)) tiles.push_back(tile(k, y, x));
         }
         take(&b.square);
-        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].sp > out->mats[y].sp; });
+        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.sp > out->mats[y].parts.sp; });
         for (size_t k : order) {
-            const int64_t ty = tiles_of(out->mats[k].s, kTileRows[b.apply.kind]);
-            const int64_t tx = tiles_of(out->mats[k].l, kTileCols[b.apply.kind]);
+            const int64_t ty = tiles_of(out->mats[k].parts.sp, kTileRows[b.apply.kind]);
+            const int64_t tx = tiles_of(out->mats[k].parts.lp, kTileCols[b.apply.kind]);
             for (int64_t y0 = 0; y0 < ty; y0 += kBand)
                 for (int64_t x = 0; x < tx; ++x)
                     for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
-                        tiles.push_back(DevTile{(uint32_t)k, (uint32_t)y, (uint32_t)x, 0});
+                        tiles.push_back(tile(k, y, x));
         }
         take(&b.apply);
         out->batches.push_back(b);

@@ -83,23 +83,23 @@ void check_batch(const NsPlan& plan, const NsBatch& b, std::vector<int>& seen, i
         seen[kv.first] = 1;
         const DevMatrix& m = plan.mats[kv.first];
         for (int x : kv.second) CHECK(x);
-        const int64_t n = (int64_t)m.rows * m.cols, pad = (int64_t)m.sp * m.lp, sq = (int64_t)m.sp * m.sp;
-        CHECK((int64_t)m.n_partials * kMomentElems >= n && ((int64_t)m.n_partials - 1) * kMomentElems < n);
-        CHECK(m.s == std::min(m.rows, m.cols) && m.l == std::max(m.rows, m.cols) && (m.tall != 0) == (m.rows > m.cols));
-        CHECK(m.sp % kPad == 0 && m.sp >= m.s && m.sp < m.s + kPad && m.lp % kPad == 0 && m.lp >= m.l && m.lp < m.l + kPad);
-        const Range r[8] = {{m.hi[0], m.hi[0] + 2 * pad}, {m.lo, m.lo + 2 * pad}, {m.hi[1], m.hi[1] + 2 * pad},
-                            {m.a, m.a + 2 * sq}, {m.b, m.b + 2 * sq}, {m.da, m.da + 4 * m.sp}, {m.db, m.db + 4 * m.sp},
-                            {m.partials, m.partials + 8 * (uint64_t)m.n_partials}};
+        const NsParts& p = m.parts;
+        const int64_t n = (int64_t)m.rows * m.cols, s = std::min(m.rows, m.cols), l = std::max(m.rows, m.cols);
+        CHECK((int64_t)m.n_partials * m.chunk >= n && ((int64_t)m.n_partials - 1) * m.chunk < n && m.chunk % kMomentElems == 0);
+        CHECK(m.n_partials <= kMaxPartials && (m.tall != 0) == (m.rows > m.cols));
+        CHECK(p.sp % kPad == 0 && p.sp >= s && p.sp < s + kPad && p.lp % kPad == 0 && p.lp >= l && p.lp < l + kPad);
+        const uint64_t whole = (uint64_t)2 * p.sp * p.lp, square = (uint64_t)2 * p.sp * p.sp;
+        const Range r[8] = {{p.hi(0), p.hi(0) + whole}, {p.lo(), p.lo() + whole}, {p.hi(1), p.hi(1) + whole},
+                            {p.a(), p.a() + square}, {p.b(), p.b() + square}, {p.da(), p.da() + 4 * p.sp},
+                            {p.db(), p.db() + 4 * p.sp}, {m.partials, m.partials + 8 * (uint64_t)m.n_partials}};
         for (const Range& x : r) parts.push_back(x);
-        if (step) {   // u's room: that of hi[1], a and b, and nothing else's
-            const Range u{m.u, m.u + 4 * (uint64_t)n};
+        if (step) {   // u's room: that of hi(1), a and b, and nothing else's
+            const Range u{p.u(), p.u() + 4 * (uint64_t)n};
             CHECK(u.hi <= (uint64_t)bytes);
             for (int k : {0, 1, 5, 6, 7}) CHECK(apart(u, r[k]));
         }
         for (const Range& x : r) CHECK(x.lo % kNsAlign == 0);
-        for (uint64_t x : {m.rows, m.cols, m.sp, m.tall}) mix(x);
-        mix(m.hi[0]);
-        mix(m.partials);
+        for (uint64_t x : {(uint64_t)m.rows, (uint64_t)m.cols, (uint64_t)p.sp, (uint64_t)m.tall, p.base, m.partials}) mix(x);
     }
     for (const Range& x : parts) CHECK(x.lo >= (uint64_t)kNsHeadBytes && x.hi <= (uint64_t)bytes);
     std::sort(parts.begin(), parts.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
@@ -111,12 +111,14 @@ void check_batch(const NsPlan& plan, const NsBatch& b, std::vector<int>& seen, i
         for (int64_t i = 0; i < l.count; ++i) {
             const DevTile& t = plan.tiles[(size_t)(l.first + i)];
             CHECK(runs.count(t.mat) && !got[t.mat][std::make_pair(t.row, t.col)]++);
+            const NsParts &x = t.parts, &y = plan.mats[t.mat].parts;
+            CHECK(x.base == y.base && x.sp == y.sp && x.lp == y.lp);
             mix(t.mat * 31 + t.row * 7 + t.col);
         }
         CHECK(got.size() == runs.size());
         for (auto& kv : got) {
             const DevMatrix& m = plan.mats[kv.first];
-            const int64_t h = m.sp, w = square ? m.sp : m.lp;
+            const int64_t h = m.parts.sp, w = square ? m.parts.sp : m.parts.lp;
             for (auto& t : kv.second) CHECK(t.first.first * (int64_t)th < h && t.first.second * (int64_t)tw < w);
             if (!square) {
                 CHECK((int64_t)kv.second.size() == (h + th - 1) / th * ((w + tw - 1) / tw));
