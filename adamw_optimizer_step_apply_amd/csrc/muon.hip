@@ -251,31 +251,29 @@ __device__ __forceinline__ f32x4 load4(uint64_t base, uint64_t i)
     }
 }
 
-template <int IN>
-__global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __restrict__ mats,
-                                                           const DevTile* __restrict__ tiles, char* ws, float eps,
-                                                           int sx, int step)
+// 2^sx / (|u| + eps) from the partial sums, by every workgroup alike; its barrier is the workgroup's.
+__device__ __forceinline__ double norm_scale(const DevMatrix& mx, const char* ws, float eps, int sx)
 {
-    if (step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
-    const DevTile t = tiles[blockIdx.x];
-    const DevMatrix& mx = mats[t.mat];
-    const uint32_t tid = threadIdx.x;
-    // the sum of the partial sums, by every workgroup alike
     __shared__ double part[4];
-    const GLOBAL double* partials = at<const double>(ws, mx.partials);
-    double sum = 0.0;
-    for (uint32_t k = tid; k < mx.n_partials; k += 256) sum += partials[k];
+    const uint32_t tid = threadIdx.x;
+    double sum = tid < mx.n_partials ? *at<const double>(const_cast<char*>(ws), mx.partials + (uint64_t)tid * 8) : 0.0;
 #pragma unroll
     for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
     if (tid % 64 == 0) part[tid / 64] = sum;
+    __syncthreads();
+    sum = ((part[0] + part[1]) + part[2]) + part[3];
+    const double len = __builtin_sqrt(sum) + (double)eps;
+    // a zero matrix without eps is zero
+    return len == 0.0 ? 0.0 : __builtin_ldexp(1.0, sx) / len;
+}
 
-    // the tile as it lies in the matrix: rows of `u`, by fours where every row starts at a multiple of 4 elements
-    const bool tall = mx.tall != 0;
-    const uint32_t r0 = (tall ? t.col : t.row) * kPad, c0 = (tall ? t.row : t.col) * kPad;
-    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols;
-    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
-    const bool by4 = cols % 4 == 0 && (step || in % 16 == 0);
-    f32x4 x[4];
+// A 64 x 64 tile of u as it lies in the matrix, from row r0 and column c0 on: 4 neighbours of row 16 k + tid / 16 in x[k]
+// of a lane, zeros outside.
+template <int IN>
+__device__ __forceinline__ void load_tile(uint64_t in, bool by4, uint32_t rows, uint32_t cols, uint32_t r0, uint32_t c0,
+                                          f32x4 (&x)[4])
+{
+    const uint32_t tid = threadIdx.x;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint32_t r = r0 + (uint32_t)k * 16 + tid / 16, c = c0 + tid % 16 * 4;
@@ -290,38 +288,50 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
                 if (c + e < cols) x[k][e] = load1<IN>(in, i + e);
         }
     }
-    __syncthreads();
-    sum = ((part[0] + part[1]) + part[2]) + part[3];
-    const double len = __builtin_sqrt(sum) + (double)eps;
-    // a zero matrix without eps is zero
-    const double scale = len == 0.0 ? 0.0 : __builtin_ldexp(1.0, sx) / len;
+}
 
-    constexpr int kLd = 72;   // 144-byte rows: 16-byte reads stay aligned
-    __shared__ alignas(16) _Float16 hi[kPad * kLd];
-    __shared__ alignas(16) _Float16 lo[kPad * kLd];
+// The tile's pairs to LDS, in rows of kTileLd elements (144 bytes: 16-byte reads stay aligned), or transposed.
+constexpr int kTileLd = 72;
+__device__ __forceinline__ void store_tile(const f32x4 (&x)[4], double scale, bool transposed, _Float16* hi, _Float16* lo)
+{
+    const uint32_t tid = threadIdx.x;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const uint32_t o = ((uint32_t)k * 16 + tid / 16) * kLd + tid % 16 * 4;
+        const uint32_t r = (uint32_t)k * 16 + tid / 16, c = tid % 16 * 4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_pair((float)((double)x[k][e] * scale), hi[o + e], lo[o + e]);
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t o = transposed ? (c + e) * kTileLd + r : r * kTileLd + c + e;
+            split_pair((float)((double)x[k][e] * scale), hi[o], lo[o]);
+        }
     }
+}
+
+// Rows start at a multiple of 4 elements
+__device__ __forceinline__ bool rows_by4(uint32_t cols, uint64_t in) { return cols % 4 == 0 && in % 16 == 0; }
+
+template <int IN>
+__global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __restrict__ mats,
+                                                           const DevTile* __restrict__ tiles, char* ws, float eps,
+                                                           int sx, int step)
+{
+    if (step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
+    const DevTile t = tiles[blockIdx.x];
+    const DevMatrix& mx = mats[t.mat];
+    const bool tall = mx.tall != 0;
+    const uint32_t cols = (uint32_t)mx.cols;
+    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
+    f32x4 x[4];
+    load_tile<IN>(in, rows_by4(cols, in), (uint32_t)mx.rows, cols, (tall ? t.col : t.row) * kPad, (tall ? t.row : t.col) * kPad, x);
+    const double scale = norm_scale(mx, ws, eps, sx);
+    __shared__ alignas(16) _Float16 hi[kPad * kTileLd];
+    __shared__ alignas(16) _Float16 lo[kPad * kTileLd];
+    store_tile(x, scale, tall, hi, lo);
     __syncthreads();
-    for (uint32_t k = tid; k < kPad * 8; k += 256) {
+    for (uint32_t k = threadIdx.x; k < kPad * 8; k += 256) {
         const uint32_t r = k / 8, c = k % 8 * 8;
         const uint64_t o = (uint64_t)(t.row * kPad + r) * (uint64_t)t.parts.lp + t.col * kPad + c;
-        f16x8 h, l;
-        if (tall) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[e] = hi[(c + e) * kLd + r];
-                l[e] = lo[(c + e) * kLd + r];
-            }
-        } else {
-            h = *reinterpret_cast<const f16x8*>(hi + r * kLd + c);
-            l = *reinterpret_cast<const f16x8*>(lo + r * kLd + c);
-        }
-        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, t.parts.hi(0)) + o) = h;
-        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, t.parts.lo()) + o) = l;
+        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, t.parts.hi(0)) + o) = *reinterpret_cast<const f16x8*>(hi + r * kTileLd + c);
+        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, t.parts.lo()) + o) = *reinterpret_cast<const f16x8*>(lo + r * kTileLd + c);
     }
 }
 
@@ -344,6 +354,11 @@ struct ProductArgs {
 __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c)
 {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
 // 16 bytes for every lane of the wave from its own address to LDS, lane after lane from `to` on
@@ -1009,6 +1024,260 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 }
 
 // ---------------------------------------------------------------------------
+// Matrices whose shorter side is at most 64: everything between the two passes over X in one workgroup.
+//
+// With A = X X^T and p(A) = a I + b A + c A A, a step is X <- p(A) X and A <- p(A) A p(A), all polynomials of the first
+// A, so Q = p_k(A_k) ... p_1(A_1) is found from 64 x 64 matrices alone and the result is Q X: 2 + 4 (steps - 1) products of
+// 64 x 64 that never leave LDS instead of three launches a step.  A loses what X has below the square root of its
+// precision, so it is held in 22 bits (products of pairs: hi hi + hi lo + lo hi): the result is within 1e-4 of the
+// definition (simulated in binary64 with these roundings, spectra as above: 3e-7 to 1e-4).  These
+// kernels are latencies: one 16 x 768 took 73 us in 17 launches on MI355X.
+// ---------------------------------------------------------------------------
+
+// A 64 x 64 matrix as fp16 pairs in LDS.
+struct alignas(16) PairTile {
+    _Float16 hi[kPad * kTileLd], lo[kPad * kTileLd];
+};
+
+// sum_k P[i][k] Q[j][k] over the 64 columns of two pair tiles, for the wave's 32 x 32 quarter (rows i from wr, j from
+// wc): hi hi to `main`, hi lo + lo hi, which are under 2^11 more, to `cross`.
+__device__ __forceinline__ void pair_product(const PairTile& p, const PairTile& q, uint32_t wr, uint32_t wc, uint32_t lane,
+                                             f32x16& main, f32x16& cross)
+{
+#pragma unroll
+    for (int kk = 0; kk < kPad / 16; ++kk) {
+        const uint32_t c = (uint32_t)kk * 16 + (lane >> 5) * 8, op = (wr + (lane & 31u)) * kTileLd + c, oq = (wc + (lane & 31u)) * kTileLd + c;
+        const f16x8 ph = *reinterpret_cast<const f16x8*>(p.hi + op), pl = *reinterpret_cast<const f16x8*>(p.lo + op);
+        const f16x8 qh = *reinterpret_cast<const f16x8*>(q.hi + oq), ql = *reinterpret_cast<const f16x8*>(q.lo + oq);
+        main = mfma(ph, qh, main);
+        cross = mfma(ph, ql, cross);
+        cross = mfma(pl, qh, cross);
+    }
+}
+
+__device__ __forceinline__ f32x16 zeros16()
+{
+    f32x16 z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+    return z;
+}
+
+// Row of result e of a wave's 32 x 32 quarter; the column is lane % 32.
+__device__ __forceinline__ uint32_t result_row(int e, uint32_t lane)
+{
+    return (uint32_t)((e & 3) + 8 * (e >> 2)) + 4 * (lane >> 5);
+}
+
+template <int IN>
+__global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __restrict__ mats,
+                                                            const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
+                                                            int step)
+{
+    if (step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
+    const DevTile t = tiles[blockIdx.x];
+    const DevMatrix& mx = mats[t.mat];
+    const bool tall = mx.tall != 0;
+    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols;
+    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
+    const bool by4 = rows_by4(cols, in);
+    const uint32_t run = (uint32_t)small_gram_cols(t.parts.lp), j0 = t.col * run, j1 = j0 + run < l ? j0 + run : l;
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, wr = wave / 2 * 32, wc = wave % 2 * 32;
+    __shared__ PairTile x;
+    f32x4 v[4];
+    load_tile<IN>(in, by4, rows, cols, tall ? j0 : 0, tall ? 0 : j0, v);
+    const double scale = norm_scale(mx, ws, eps, sx);
+    f32x16 main = zeros16(), cross = zeros16();
+    for (uint32_t j = j0; j < j1; j += kPad) {
+        store_tile(v, scale, tall, x.hi, x.lo);
+        __syncthreads();
+        if (j + kPad < j1) load_tile<IN>(in, by4, rows, cols, tall ? j + kPad : 0, tall ? 0 : j + kPad, v);
+        pair_product(x, x, wr, wc, lane, main, cross);
+        __syncthreads();
+    }
+    GLOBAL float* out = at<float>(ws, t.parts.lo()) + (uint64_t)t.col * (kPad * kPad);
+    const float f = pow2(-2 * sx);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        out[(wr + result_row(e, lane)) * kPad + wc + (lane & 31u)] = (main[e] + cross[e] * (1.0f / kLoScale)) * f;
+}
+
+struct ChainArgs {
+    float a, b, c;
+    int steps, sa, sp, sz, sq, step;
+};
+
+__device__ __forceinline__ u32x2* as_words(_Float16* p) { return reinterpret_cast<u32x2*>(p); }
+__device__ __forceinline__ GLOBAL u32x2* as_words(GLOBAL _Float16* p) { return reinterpret_cast<GLOBAL u32x2*>(p); }
+
+// Sixteen waves with a 16 x 16 part each: each product is one latency of reads, six matrix instructions and stores,
+// which four waves with 32 x 32 each took three times as long for (18.5 us a matrix on MI355X).
+constexpr int kBlockChain = 1024;
+
+__global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevTile* __restrict__ tiles, char* ws, ChainArgs g)
+{
+    if (g.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
+    const DevTile t = tiles[blockIdx.x];
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, wr = wave / 4 * 16, wc = wave % 4 * 16;
+    const uint32_t row = wr + (lane >> 4) * 4, col = wc + (lane & 15u);   // of the lane's first result; four rows
+    const uint32_t runs = (uint32_t)((t.parts.lp + small_gram_cols(t.parts.lp) - 1) / small_gram_cols(t.parts.lp));
+    __shared__ PairTile ta, tp, tq, tz;
+    // All that is held is symmetric, and has to stay so to the last bit: an antisymmetric part, which exact products of
+    // commuting matrices have not, grows by a^2 with every step (stored transposed, 1e-2 off the definition).  So the
+    // results on and below the diagonal count, and are stored twice.
+    const bool lower = wr > wc, diagonal = wr == wc;
+    using InTile = std::integral_constant<uint32_t, kTileLd>;
+    const GLOBAL f32x4* partial = reinterpret_cast<const GLOBAL f32x4*>(at<const float>(ws, t.parts.lo()) + col * kPad + row);
+    f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, p = a, q = a, z = a;
+    if (lower || diagonal) {
+#pragma unroll 8
+        for (uint32_t k = 0; k < runs; ++k) a += partial[(uint64_t)k * (kPad * kPad / 4)];
+    }
+    const float fa = pow2(g.sa), fp = pow2(g.sp), fz = pow2(g.sz), fq = pow2(g.sq);
+    const auto store = [&](const f32x4& v, float scale, auto hi, auto lo, auto pitch) __attribute__((always_inline)) {
+        constexpr uint32_t ld = decltype(pitch)::value;
+        if (!lower && !diagonal) return;
+        f16x4 h, l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = (_Float16)(v[e] * scale);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[e] = (_Float16)(__builtin_fmaf(v[e], scale, -(float)h[e]) * kLoScale);
+        const auto h0 = hi + row * ld + col, l0 = lo + row * ld + col, h1 = hi + col * ld + row, l1 = lo + col * ld + row;
+        if (lower) {
+            *as_words(h1) = __builtin_bit_cast(u32x2, h);
+            *as_words(l1) = __builtin_bit_cast(u32x2, l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h0[e * ld] = h[e];
+                l0[e * ld] = l[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (row + e >= col) {
+                    h0[e * ld] = h1[e] = h[e];
+                    l0[e * ld] = l1[e] = l[e];
+                }
+        }
+    };
+    const auto product = [&](const PairTile& x, const PairTile& y, float scale) __attribute__((always_inline)) {
+        f32x4 main = {0.0f, 0.0f, 0.0f, 0.0f}, hl = main, lh = main;
+        if (!lower && !diagonal) return main;
+#pragma unroll
+        for (int kk = 0; kk < kPad / 32; ++kk) {
+            const uint32_t c = (uint32_t)kk * 32 + (lane >> 4) * 8, ox = (wr + (lane & 15u)) * kTileLd + c, oy = (wc + (lane & 15u)) * kTileLd + c;
+            const f16x8 xh = *reinterpret_cast<const f16x8*>(x.hi + ox), xl = *reinterpret_cast<const f16x8*>(x.lo + ox);
+            const f16x8 yh = *reinterpret_cast<const f16x8*>(y.hi + oy), yl = *reinterpret_cast<const f16x8*>(y.lo + oy);
+            main = mfma16(xh, yh, main);
+            hl = mfma16(xh, yl, hl);
+            lh = mfma16(xl, yh, lh);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) main[e] = (main[e] + (hl[e] + lh[e]) * (1.0f / kLoScale)) * scale;
+        return main;
+    };
+    for (int k = 0;; ++k) {
+        store(a, fa, ta.hi, ta.lo, InTile{});
+        __syncthreads();
+        const f32x4 sq = product(ta, ta, pow2(-2 * g.sa));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[e] = __builtin_fmaf(g.c, sq[e], g.b * a[e]);
+            if (row + e == col) p[e] += g.a;
+        }
+        store(p, fp, tp.hi, tp.lo, InTile{});
+        __syncthreads();
+        q = k ? product(tp, tq, pow2(-g.sp - g.sq)) : p;
+        if (k + 1 == g.steps) break;
+        z = product(tp, ta, pow2(-g.sp - g.sa));
+        __syncthreads();   // every wave has read the old q
+        store(q, fq, tq.hi, tq.lo, InTile{});
+        store(z, fz, tz.hi, tz.lo, InTile{});
+        __syncthreads();
+        a = product(tz, tp, pow2(-g.sz - g.sp));
+    }
+    // over the partial sums, which every wave has read
+    GLOBAL _Float16* to = at<_Float16>(ws, t.parts.lo());
+    store(q, fq, to, to + kPad * kPad, std::integral_constant<uint32_t, kPad>{});
+}
+
+template <int IN, int END>
+__global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __restrict__ mats,
+                                                             const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
+                                                             int sq, ProductArgs g)
+{
+    if (g.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
+    const uint32_t tid = threadIdx.x;
+    if (g.count && blockIdx.x == 0 && tid == 0) *g.count += 1;   // the step is taken
+    const DevTile t = tiles[blockIdx.x];
+    const DevMatrix& mx = mats[t.mat];
+    const bool tall = mx.tall != 0, row16 = mx.row16 != 0;
+    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols;
+    const uint64_t in = g.step ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
+    const bool by4 = rows_by4(cols, in);
+    const uint32_t run = (uint32_t)small_apply_cols(t.parts.lp), j0 = t.col * run, j1 = j0 + run < l ? j0 + run : l;
+    const uint32_t lane = tid & 63u, wave = tid >> 6, wr = wave / 2 * 32, wc = wave % 2 * 32;
+    const float stepf = (float)((double)g.lr * mx.factor), f = pow2(-sq - sx);
+    __shared__ PairTile q, x;
+    constexpr int kOutLd = kPad + 4;
+    __shared__ alignas(16) float out[kPad * kOutLd];   // as the matrix lies: rows of the caller's
+    f32x4 v[4];
+    load_tile<IN>(in, by4, rows, cols, tall ? j0 : 0, tall ? 0 : j0, v);
+    for (uint32_t k = tid; k < kPad * 8; k += 256) {
+        const GLOBAL _Float16* from = at<const _Float16>(ws, t.parts.lo()) + k * 8;
+        const uint32_t o = k / 8 * kTileLd + k % 8 * 8;
+        *reinterpret_cast<f16x8*>(q.hi + o) = *reinterpret_cast<const GLOBAL f16x8*>(from);
+        *reinterpret_cast<f16x8*>(q.lo + o) = *reinterpret_cast<const GLOBAL f16x8*>(from + kPad * kPad);
+    }
+    const double scale = norm_scale(mx, ws, eps, sx);
+    for (uint32_t j = j0; j < j1; j += kPad) {
+        store_tile(v, scale, !tall, x.hi, x.lo);   // rows are columns of X
+        __syncthreads();
+        if (j + kPad < j1) load_tile<IN>(in, by4, rows, cols, tall ? j + kPad : 0, tall ? 0 : j + kPad, v);
+        f32x16 main = zeros16(), cross = zeros16();
+        pair_product(q, x, wr, wc, lane, main, cross);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t i = wr + result_row(e, lane), c = wc + (lane & 31u);
+            out[tall ? c * kOutLd + i : i * kOutLd + c] = (main[e] + cross[e] * (1.0f / kLoScale)) * f;
+        }
+        __syncthreads();
+        const uint32_t r0 = tall ? j : 0, c0 = tall ? 0 : j;
+        if (row16) {
+            EndInput<END> end[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t k = (uint32_t)h * 256 + tid, r = r0 + k / 8, c = c0 + k % 8 * 8;
+                if (r < rows && c < cols) end[h] = end_input<END>(mx, (uint64_t)r * cols + c);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t k = (uint32_t)h * 256 + tid, r = r0 + k / 8, c = c0 + k % 8 * 8;
+                const float* from = out + k / 8 * kOutLd + k % 8 * 8;
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = from[e];
+                if (r < rows && c < cols) end_eight<END>(mx, (uint64_t)r * cols + c, end[h], o, stepf, g);
+            }
+        } else {
+            EndScalar some[16];
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+                const uint32_t k = (uint32_t)h * 256 + tid, r = r0 + k / 64, c = c0 + k % 64;
+                if (r < rows && c < cols) some[h] = end_read<END>(mx, (uint64_t)r * cols + c);
+            }
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+                const uint32_t k = (uint32_t)h * 256 + tid, r = r0 + k / 64, c = c0 + k % 64;
+                if (r < rows && c < cols)
+                    end_write<END>(mx, (uint64_t)r * cols + c, some[h], out[k / 64 * kOutLd + k % 64], stepf, g);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 
@@ -1028,19 +1297,6 @@ hipError_t product(const NsCall& call, const NsLaunch& l, const ProductArgs& q, 
     return l.kind == 0 ? launch_product<0, OP, END>(call, l, q, stream)
          : l.kind == 1 ? launch_product<1, OP, END>(call, l, q, stream)
                        : launch_product<2, OP, END>(call, l, q, stream);
-}
-
-hipError_t last_product(const NsCall& call, const NsLaunch& l, const ProductArgs& q, hipStream_t stream)
-{
-    switch (call.kind.end) {
-    case kEndOrtho: return product<kLast, kEndOrtho>(call, l, q, stream);
-    case kEndMixedBf16: return product<kLast, kEndMixedBf16>(call, l, q, stream);
-    case kEndMixedF16: return product<kLast, kEndMixedF16>(call, l, q, stream);
-    case kEndSplit: return product<kLast, kEndSplit>(call, l, q, stream);
-    case kEndPure: return product<kLast, kEndPure>(call, l, q, stream);
-    case kEndKahan: return product<kLast, kEndKahan>(call, l, q, stream);
-    default: return product<kLast, kEndKahan32>(call, l, q, stream);
-    }
 }
 
 template <int IN>
@@ -1063,9 +1319,48 @@ hipError_t normalise(const NsCall& call, const NsLaunch& l, bool step, hipStream
     return hipGetLastError();
 }
 
+// Whatever depends on the end: the last product, or the small matrices' one.
+template <int END>
+hipError_t end_launch(const NsCall& call, const NsBatch& batch, int in, const ProductArgs& q, hipStream_t stream)
+{
+    if (!batch.small) return product<kLast, END>(call, batch.apply, q, stream);
+    const DevTile* tiles = call.tiles + batch.apply.first;
+    const dim3 grid((uint32_t)batch.apply.count), block(256);
+    const NsScales& s = call.scales;
+    if (in == kInF32)
+        ns_small_apply_kernel<kInF32, END><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, call.ns.eps, s.sx, s.sq, q);
+    else if (END == kEndOrtho && in == kInBf16)
+        ns_small_apply_kernel<kInBf16, kEndOrtho><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, call.ns.eps, s.sx, s.sq, q);
+    else
+        ns_small_apply_kernel<kInF16, kEndOrtho><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, call.ns.eps, s.sx, s.sq, q);
+    return hipGetLastError();
+}
+
+template <int IN>
+hipError_t small_gram(const NsCall& call, const NsLaunch& l, bool step, hipStream_t stream)
+{
+    ns_small_gram_kernel<IN><<<(uint32_t)l.count, 256, 0, stream>>>(call.mats, call.tiles + l.first, call.ws, call.ns.eps,
+                                                                    call.scales.sx, step);
+    return hipGetLastError();
+}
+
 StepRule step_rule(const NsCall& call)
 {
     return StepRule{call.hp.inv_loss_scale, call.clip, call.step, call.found_inf, call.amp};
+}
+
+// `in`: the type of u, which a step has in fp32
+hipError_t last_product(const NsCall& call, const NsBatch& batch, int in, const ProductArgs& q, hipStream_t stream)
+{
+    switch (call.kind.end) {
+    case kEndOrtho: return end_launch<kEndOrtho>(call, batch, in, q, stream);
+    case kEndMixedBf16: return end_launch<kEndMixedBf16>(call, batch, in, q, stream);
+    case kEndMixedF16: return end_launch<kEndMixedF16>(call, batch, in, q, stream);
+    case kEndSplit: return end_launch<kEndSplit>(call, batch, in, q, stream);
+    case kEndPure: return end_launch<kEndPure>(call, batch, in, q, stream);
+    case kEndKahan: return end_launch<kEndKahan>(call, batch, in, q, stream);
+    default: return end_launch<kEndKahan32>(call, batch, in, q, stream);
+    }
 }
 
 }  // namespace
@@ -1101,6 +1396,20 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
                  : in == kInBf16 ? moments<kInBf16>(call, batch.moments, step, mc, rule, stream)
                                  : moments<kInF16>(call, batch.moments, step, mc, rule, stream);
     if (e != hipSuccess) return e;
+    const int in_u = step ? kInF32 : in;
+    if (batch.small) {
+        e = in_u == kInF32 ? small_gram<kInF32>(call, batch.normalise, step, stream)
+          : in_u == kInBf16 ? small_gram<kInBf16>(call, batch.normalise, step, stream)
+                            : small_gram<kInF16>(call, batch.normalise, step, stream);
+        if (e != hipSuccess) return e;
+        const NsScales& s = call.scales;
+        ns_small_chain_kernel<<<(uint32_t)batch.square.count, kBlockChain, 0, stream>>>(
+            call.tiles + batch.square.first, call.ws,
+            ChainArgs{call.ns.a, call.ns.b, call.ns.c, call.ns.steps, s.sa, s.sp, s.sz, s.sq, step});
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        q.count = last ? call.step : nullptr;
+        return last_product(call, batch, in_u, q, stream);
+    }
     e = step || in == kInF32 ? normalise<kInF32>(call, batch.normalise, step, stream)
       : in == kInBf16 ? normalise<kInBf16>(call, batch.normalise, step, stream)
                       : normalise<kInF16>(call, batch.normalise, step, stream);
@@ -1114,7 +1423,7 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
             e = product<kApply>(call, batch.apply, q, stream);
         } else {
             q.count = last ? call.step : nullptr;
-            e = last_product(call, batch.apply, q, stream);
+            e = last_product(call, batch, in_u, q, stream);
         }
         if (e != hipSuccess) return e;
     }

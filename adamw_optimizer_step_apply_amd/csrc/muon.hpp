@@ -10,6 +10,14 @@
 //   per product step:  gram  A = X X^T (the shorter side),  poly  B = b A + c A A,
 //                      apply X = a X + B X, the last one with the result's own epilogue
 //
+// Where the shorter side of every matrix of a batch is at most kPad, all steps go on in one workgroup, on
+// polynomials of the first Gram matrix, and X is read twice instead:
+//
+//   moments      as above
+//   small gram   partial sums of A = X X^T for runs of columns
+//   small chain  Q, the product of every step's a I + b A + c A A
+//   small apply  Q X with the result's own epilogue
+//
 // The matrices of the products are held in the workspace with both sides padded to
 // kPad by zeros, so that the product kernels have no ragged edge in the summed dimension.
 #pragma once
@@ -33,6 +41,15 @@ constexpr int64_t kNsBatchBytes = INT64_C(4) << 30;   // workspace of a batch of
 // most kMaxPartials partial sums, which every workgroup of the normalisation adds up.
 constexpr int64_t kMomentElems = 4096, kMaxPartials = 256;
 constexpr int kBlockMoments = 256;
+// Columns of X of a workgroup of small gram: a multiple of kPad, so that a matrix has at most kMaxSmallRuns partial
+// Gram matrices (of kPad x kPad fp32, which lie where lo and hi(0) would); and of small apply.
+constexpr int64_t kMaxSmallRuns = 32;
+constexpr int64_t small_gram_cols(int64_t lp)
+{
+    const int64_t each = (lp + kMaxSmallRuns - 1) / kMaxSmallRuns;
+    return (each + kPad - 1) / kPad * kPad;
+}
+constexpr int64_t small_apply_cols(int64_t lp) { return lp <= 4096 ? kPad : 4 * kPad; }
 
 // Tiles of the product kernels: rows, columns, and lanes of a workgroup.
 constexpr int kTileKinds = 3;
@@ -105,7 +122,10 @@ struct NsLaunch {
 };
 
 struct NsBatch {
-    NsLaunch moments, normalise, square, apply;   // square: gram and poly
+    bool small = false;
+    // square: gram and poly.  Of a small batch, normalise: the runs of columns of small gram, square: the matrices
+    // (small chain), apply: the runs of small apply
+    NsLaunch moments, normalise, square, apply;
 };
 
 struct NsPlan {
@@ -132,9 +152,11 @@ struct NsKind {
     bool m16;              // exp_avg is bf16
 };
 
-// Powers of two under which X, A and B are held in fp16, and their limits.
+// Powers of two under which X, A and B are held in fp16; of a small batch, a I + b A + c A A, that
+// times A, and the product of those polynomials so far.
 struct NsScales {
     int sx, sa, sb;
+    int sp, sz, sq;
 };
 
 adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::string& err);

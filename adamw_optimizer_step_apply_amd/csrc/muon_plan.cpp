@@ -187,17 +187,44 @@ adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::stri
         err = "Newton-Schulz steps must lie in [1, ADAMW_NS_MAX_STEPS]";
         return ADAMW_E_INVALID;
     }
-    // The largest singular value on the way, from a grid on [0, top] with each step (the
-    // polynomial is smooth there: 4096 points miss less than the margin taken below).
-    double top = 1.0, most = 1.0, poly = 0.0;
+    // What the polynomials reach on the singular values of each step, [0, top]: at the ends or where a derivative is
+    // zero, in q = x^2.
+    const double a = ns->a, b = ns->b, c = ns->c;
+    double top = 1.0, most = 1.0, poly = 0.0, whole = 0.0, times_a = 0.0, product = 1.0;
     for (int k = 0; k < ns->steps; ++k) {
-        double next = 0.0;
-        for (int i = 0; i <= 4096; ++i) {
-            const double x = top * i / 4096.0, q = x * x, p = q * (ns->b + ns->c * q);
-            next = std::max(next, std::fabs(x * (ns->a + p)));
+        const double end = top * top;
+        double at[7] = {0.0, end}, next = 0.0, one = 0.0;
+        int n = 2;
+        const auto roots = [&](double r0, double r1, double r2) {   // of r0 + r1 q + r2 q^2 in (0, end)
+            double q[2];
+            int m = 0;
+            if (r2 != 0.0) {
+                const double d = r1 * r1 - 4.0 * r0 * r2;
+                if (d >= 0.0) {
+                    // without the difference of like numbers
+                    const double h = -0.5 * (r1 + (r1 < 0.0 ? -std::sqrt(d) : std::sqrt(d)));
+                    q[m++] = h / r2;
+                    if (h != 0.0) q[m++] = r0 / h;
+                }
+            } else if (r1 != 0.0) {
+                q[m++] = -r0 / r1;
+            }
+            for (int i = 0; i < m; ++i)
+                if (q[i] > 0.0 && q[i] < end) at[n++] = q[i];
+        };
+        roots(a, 3.0 * b, 5.0 * c);   // of x (a + b q + c q^2)
+        roots(b, 2.0 * c, 0.0);       // of b q + c q^2
+        roots(a, 2.0 * b, 3.0 * c);   // of q (a + b q + c q^2)
+        for (int i = 0; i < n; ++i) {
+            const double q = at[i], p = q * (b + c * q);
+            next = std::max(next, std::sqrt(q) * std::fabs(a + p));
             poly = std::max(poly, std::fabs(p));
+            one = std::max(one, std::fabs(a + p));
+            times_a = std::max(times_a, q * std::fabs(a + p));
         }
-        top = next * 1.01;   // rounding, and the grid
+        whole = std::max(whole, one * 1.02);
+        product *= one * 1.02;
+        top = next * 1.01;   // rounding
         most = std::max(most, top);
         if (!(most <= 64.0)) {
             err = "Newton-Schulz coefficients take singular values of [0, 1] past 64";
@@ -209,6 +236,10 @@ adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::stri
     scales->sx = under(most);
     scales->sa = under(most * most);
     scales->sb = under(poly * 1.02);
+    scales->sp = under(whole);
+    scales->sz = under(times_a * 1.02);
+    // a product of at most 16 of them; where it passes what fp16 can hold the small elements lose bits
+    scales->sq = std::max(under(product), -40);
     return ADAMW_OK;
 }
 
@@ -352,6 +383,24 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
         for (size_t k : order)
             for (uint32_t c = 0; c < out->mats[k].n_partials; ++c) tiles.push_back(tile(k, c, 0));
         take(&b.moments);
+        b.small = std::all_of(order.begin(), order.end(), [&](size_t k) { return out->mats[k].parts.sp == (uint32_t)kPad; });
+        if (b.small) {
+            const auto runs = [&](int64_t (*cols)(int64_t)) {
+                for (size_t k : order) {
+                    const int64_t lp = out->mats[k].parts.lp;
+                    for (int64_t x = 0; x < (lp + cols(lp) - 1) / cols(lp); ++x) tiles.push_back(tile(k, 0, x));
+                }
+            };
+            runs(small_gram_cols);
+            take(&b.normalise);
+            for (size_t k : order) tiles.push_back(tile(k, 0, 0));
+            take(&b.square);
+            runs(small_apply_cols);
+            take(&b.apply);
+            out->batches.push_back(b);
+            i = end;
+            continue;
+        }
         for (size_t k : order)
             for (uint32_t y = 0; y < out->mats[k].parts.sp / kPad; ++y)
                 for (uint32_t x = 0; x < out->mats[k].parts.lp / kPad; ++x)

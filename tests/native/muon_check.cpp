@@ -105,6 +105,30 @@ void check_batch(const NsPlan& plan, const NsBatch& b, std::vector<int>& seen, i
     std::sort(parts.begin(), parts.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
     for (size_t i = 1; i < parts.size(); ++i) CHECK(apart(parts[i - 1], parts[i]));
 
+    if (b.small) {
+        CHECK(b.square.count == (int64_t)runs.size());
+        std::map<uint32_t, int> once;
+        for (int64_t i = 0; i < b.square.count; ++i) CHECK(!once[plan.tiles[(size_t)(b.square.first + i)].mat]++);
+        for (const bool gram : {true, false}) {
+            const NsLaunch& l = gram ? b.normalise : b.apply;
+            std::map<uint32_t, std::vector<int>> got;
+            for (int64_t i = 0; i < l.count; ++i) {
+                const DevTile& t = plan.tiles[(size_t)(l.first + i)];
+                const NsParts& p = plan.mats[t.mat].parts;
+                const int64_t cols = gram ? small_gram_cols(p.lp) : small_apply_cols(p.lp), n = (p.lp + cols - 1) / cols;
+                CHECK(runs.count(t.mat) && p.sp == kPad && cols % kPad == 0 && t.parts.base == p.base && t.row == 0);
+                // the partial Gram matrices lie before u's room
+                if (gram) CHECK(n <= kMaxSmallRuns && p.lo() + (uint64_t)n * kPad * kPad * 4 <= p.u());
+                auto& v = got[t.mat];
+                v.resize((size_t)n);
+                CHECK((int64_t)t.col < n && !v[t.col]++);
+            }
+            CHECK(got.size() == runs.size());
+            for (auto& kv : got)
+                for (int x : kv.second) CHECK(x == 1);
+        }
+        return;
+    }
     // 64 x 64 of the padded matrix each, the tiles of a kind of the matrix, or of its square
     const auto cover = [&](const NsLaunch& l, int th, int tw, bool square) {
         std::map<uint32_t, std::map<std::pair<uint32_t, uint32_t>, int>> got;
