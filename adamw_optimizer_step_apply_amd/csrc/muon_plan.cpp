@@ -111,10 +111,11 @@ int64_t bytes_of(const Shape& s)
 
 // Workgroup order of a launch's tiles: those of the longest sums first, and runs of
 // neighbouring tiles (which read the same rows) to one XCD, whose L2 they then share.
-// Workgroup b runs on XCD b % 8.
+// Workgroup b runs on XCD b % 8.  Runs of n / 16 tiles against n / 64: Gram products of four of 768 x 2304
+// 20.7 -> 18.2 us, products with X of four of 1024 x 1024 27.0 -> 23.4 us (MI355X).
 void deal_tiles(const std::vector<DevTile>& in, std::vector<DevTile>* out)
 {
-    const size_t n = in.size(), run = std::min<size_t>(32, std::max<size_t>(1, n / 64));
+    const size_t n = in.size(), run = std::min<size_t>(32, (n + 15) / 16);
     std::vector<std::vector<DevTile>> of(kXcdParts);
     for (size_t i = 0; i < n; ++i) of[i / run % kXcdParts].push_back(in[i]);
     for (size_t q = 0, left = n; left; ++q)
@@ -135,16 +136,17 @@ int64_t square_tiles(int64_t s, int kind)
     return n;
 }
 
-// The tiles' costs in microseconds on one CU: cost + K * per_k for a tile of K summed elements, as fitted to single
-// launches on MI355X (K from 64 to 8192, 3 to 8192 tiles).  One launch takes about `start` and the larger of
-// its longest tile and its tiles' sum over 256 CUs; of the largest kind one workgroup fits on a CU, so its
-// tiles come in whole rounds.  Measured with kinds 0 / 1 / 2, in us: Gram products of 768 x 768 27.6 / 13.9 / 6.6, of
-// four of 768 x 2304 59.9 / 31.0 / 20.7, of four of 2048 x 8192 389 / 258 / 270; products with X of
-// four of 768 x 2304 36.1 / 25.8 / 40.6, of 64 of 512 x 1024 75 / 80 / 137, of four of 2048 x 2048 86 / 100 / 189.
+// The tiles' costs in microseconds: a tile of K summed elements alone on a CU takes cost + K * per_k, as fitted to
+// single launches on MI355X (K from 64 to 8192, 3 to 8192 tiles).  One launch takes about `start` and
+// the larger of its longest tile and its tiles in rounds: of the largest kind one workgroup fits on a CU, of the middle
+// one two, which take 1.8 times as long together, and the smallest one's overlap freely.  Measured with kinds 0 / 1 / 2,
+// in us: Gram products of 768 x 768 27.6 / 13.9 / 6.6, of four of 768 x 2304 59.9 / 31.0 / 20.7, of four of
+// 2048 x 8192 389 / 258 / 270; products with X of four of 768 x 2304 36.1 / 25.8 / 40.6, of 64 of 512 x 1024
+// 75 / 80 / 137, of four of 2048 x 2048 86 / 100 / 189.
 struct TileCost {
     double start, square, apply, per_k;
 };
-constexpr TileCost kTileCost[kTileKinds] = {{2.0, 10.0, 22.0, 0.0285}, {3.0, 4.0, 4.0, 0.0115}, {2.5, 2.0, 2.0, 0.0032}};
+constexpr TileCost kTileCost[kTileKinds] = {{2.0, 10.0, 22.0, 0.0285}, {3.0, 4.0, 4.6, 0.0115}, {2.5, 2.0, 2.0, 0.0032}};
 constexpr int64_t kCus = 256;
 
 // The kind of tile for a launch over matrices of (tiles of the kind, summed elements).
@@ -163,8 +165,14 @@ int pick_kind(bool square, const Each& each)
             longest = std::max(longest, one);
             n += tiles;
         });
-        const double rounds = kind == 0 ? (double)((n + kCus - 1) / kCus) * (double)kCus / (double)std::max<int64_t>(n, 1) : 1.0;
-        const double cost = c.start + std::max(longest, sum / (double)kCus * rounds);
+        double rounds = (double)n / (double)kCus;   // of one tile a CU
+        if (kind == 0) {
+            rounds = std::ceil(rounds);
+        } else if (kind == 1) {
+            const int64_t two = n / (2 * kCus), rest = n - two * 2 * kCus;
+            rounds = 1.8 * (double)two + (rest > kCus ? 1.8 : rest > 0 ? 1.0 : 0.0);
+        }
+        const double cost = c.start + std::max(longest, n ? sum / (double)n * rounds : 0.0);
         if (kind == 0 || cost < least) {
             best = kind;
             least = cost;

@@ -460,12 +460,14 @@ adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtyp
  *
  * Numerics.  |U| is summed in binary64.  X is held as a sum of two fp16 values (22 bits)
  * under a power of two, X X^T and the polynomial of it as fp16 with their diagonals in
- * fp32; products are of fp16 values with fp32 sums, and the linear term a X keeps all 22 bits (in
- * the last step 11), so that small singular values, which a step multiplies by a, are not drowned
- * in rounding.
- * The result is within about 1e-3 (relative, in the Frobenius norm) of the definition's value;
- * the same call gives the same bits.  A matrix with an inf or NaN element has NaN in
- * every element of its result, a zero matrix zeros; no matrix changes another's.
+ * fp32; products are of fp16 values with fp32 sums, and the linear term a X keeps all 22
+ * bits (in the last step 11), so that small singular values, which a step multiplies by
+ * a, are not drowned in rounding.  Matrices of at most 64 rows or columns, where a call
+ * (or the part of its list that the workspace takes at a time) has no others, are held
+ * in 22 bits throughout.  The result is within about 1e-3 (relative, in the Frobenius norm) of
+ * the definition's value, of such small matrices 1e-4; the same call gives the same bits.
+ * A matrix with an inf or NaN element has NaN in every element of its result, a zero matrix
+ * zeros; no matrix changes another's.
  *
  * Requirements: a, b, c finite, eps finite and >= 0, 1 <= steps <= ADAMW_NS_MAX_STEPS;
  * coefficients under which a singular value of [0, 1] passes 64 on the way are refused. */

@@ -24,6 +24,10 @@ SHAPES = {
     "wide": [(200, 1000)], "tall": [(1000, 200)], "long_sum": [(33, 20000)], "square_300": [(300, 300)],
     "edge_256": [(255, 257), (256, 256), (513, 256)], "mixed": [(64, 64), (1, 5), (700, 90), (90, 701), (320, 320)],
     "same": [(128, 256)] * 9, "large": [(1100, 1500)],
+    # shorter sides of 64 at most throughout: several runs of columns, long runs, both orders
+    "small_long": [(64, 2500), (3000, 50), (1, 5000), (7, 64)], "small_longer": [(9, 70001), (40000, 17)],
+    # lists that take the larger tiles
+    "many": [(768, 768)] * 24, "larger": [(2048, 4096), (4096, 2048)],
 }
 
 
@@ -52,6 +56,36 @@ def test_against_the_definition(name, dtype):
     outs, ins = run([gradient(r, c, gen) for r, c in SHAPES[name]], dtype)
     for o, u in zip(outs, ins):
         assert far(o, ns64(u)) <= TOL_NS + TOL_BF16, (tuple(u.shape), far(o, ns64(u)))
+
+
+@pytest.mark.parametrize("shape", [(64, 67_200_001), (66_200_003, 65)])
+def test_offsets_past_32_bits(shape):
+    """More than 2^32 elements, bf16 in place, against polynomials of the Gram matrix in 64 bits at both ends."""
+    r, c = shape
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    u = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    flat = u.view(-1)
+    piece = 1 << 28
+    for a in range(0, flat.numel(), piece):
+        b = min(flat.numel(), a + piece)
+        flat[a:b] = torch.randn(b - a, device="cuda", generator=gen)
+    long = u if r < c else u.T                   # the short side first
+    g = torch.zeros(min(shape), min(shape), dtype=torch.float64, device="cuda")
+    for a in range(0, max(shape), 1 << 20):
+        x = long[:, a:a + (1 << 20)].double().contiguous()
+        g += x @ x.T.contiguous()
+    norm = float(g.diagonal().sum().sqrt()) + 1e-7
+    a, q = g / norm ** 2, torch.eye(min(shape), dtype=torch.float64, device="cuda")
+    for _ in range(NS.steps):
+        p = 3.4445 * torch.eye(min(shape), dtype=torch.float64, device="cuda") - 4.7750 * a + 2.0315 * a @ a
+        q, a = p @ q, p @ a @ p
+    ends = [(0, 5000), (max(shape) // 2, max(shape) // 2 + 5000), (max(shape) - 5000, max(shape))]
+    want = [q @ long[:, b:e].double() / norm for b, e in ends]
+    mats = A.MatrixList([shape], [[u], [u]])
+    A.adamw_orthogonalize(A.BF16, mats, A.make_orthogonalize_workspace(mats))
+    torch.cuda.synchronize()
+    for (b, e), w in zip(ends, want):
+        assert far(long[:, b:e], w) <= TOL_NS + TOL_BF16
 
 
 @pytest.mark.parametrize("kind", ["normal", "decay", "momentum"])
