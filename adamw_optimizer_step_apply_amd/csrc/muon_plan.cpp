@@ -149,35 +149,35 @@ struct TileCost {
 constexpr TileCost kTileCost[kTileKinds] = {{2.0, 10.0, 22.0, 0.0285}, {3.0, 4.0, 4.6, 0.0115}, {2.5, 2.0, 2.0, 0.0032}};
 constexpr int64_t kCus = 256;
 
-// The kind of tile for a launch over matrices of (tiles of the kind, summed elements).
+// A launch's cost with one kind of tile: `each` calls back with every matrix's tiles and summed elements.
 template <typename Each>
-int pick_kind(bool square, const Each& each)
+double launch_cost(int kind, bool square, const Each& each)
+{
+    const TileCost& c = kTileCost[kind];
+    double sum = 0.0, longest = 0.0;
+    int64_t n = 0;
+    each([&](int64_t tiles, int64_t k) {
+        const double one = (square ? c.square : c.apply) + c.per_k * (double)k;
+        sum += one * (double)tiles;
+        longest = std::max(longest, one);
+        n += tiles;
+    });
+    double rounds = (double)n / (double)kCus;   // of one tile a CU
+    if (kind == 0) {
+        rounds = std::ceil(rounds);
+    } else if (kind == 1) {
+        const int64_t two = n / (2 * kCus), rest = n - two * 2 * kCus;
+        rounds = 1.8 * (double)two + (rest > kCus ? 1.8 : rest > 0 ? 1.0 : 0.0);
+    }
+    return c.start + std::max(longest, n ? sum / (double)n * rounds : 0.0);
+}
+
+template <typename Cost>
+int cheapest(const Cost& cost)
 {
     int best = 0;
-    double least = 0.0;
-    for (int kind = 0; kind < kTileKinds; ++kind) {
-        const TileCost& c = kTileCost[kind];
-        double sum = 0.0, longest = 0.0;
-        int64_t n = 0;
-        each(kind, [&](int64_t tiles, int64_t k) {
-            const double one = (square ? c.square : c.apply) + c.per_k * (double)k;
-            sum += one * (double)tiles;
-            longest = std::max(longest, one);
-            n += tiles;
-        });
-        double rounds = (double)n / (double)kCus;   // of one tile a CU
-        if (kind == 0) {
-            rounds = std::ceil(rounds);
-        } else if (kind == 1) {
-            const int64_t two = n / (2 * kCus), rest = n - two * 2 * kCus;
-            rounds = 1.8 * (double)two + (rest > kCus ? 1.8 : rest > 0 ? 1.0 : 0.0);
-        }
-        const double cost = c.start + std::max(longest, n ? sum / (double)n * rounds : 0.0);
-        if (kind == 0 || cost < least) {
-            best = kind;
-            least = cost;
-        }
-    }
+    for (int kind = 1; kind < kTileKinds; ++kind)
+        if (cost(kind) < cost(best)) best = kind;
     return best;
 }
 
@@ -415,19 +415,21 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
                     tiles.push_back(tile(k, y, x));
         take(&b.normalise);
         std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.lp > out->mats[y].parts.lp; });
-        b.square.kind = pick_kind(true, [&](int kind, const auto& add) {
-            for (size_t k : order) {
-                const NsParts& p = out->mats[k].parts;
-                const int64_t n = square_tiles(p.sp, kind);
-                add(n, p.lp);
-                add(n, p.sp);
-            }
+        const auto parts = [&](size_t k) -> const NsParts& { return out->mats[k].parts; };
+        b.square.kind = cheapest([&](int kind) {
+            const auto gram = [&](const auto& add) {
+                for (size_t k : order) add(square_tiles(parts(k).sp, kind), parts(k).lp);
+            };
+            const auto poly = [&](const auto& add) {
+                for (size_t k : order) add(square_tiles(parts(k).sp, kind), parts(k).sp);
+            };
+            return launch_cost(kind, true, gram) + launch_cost(kind, true, poly);
         });
-        b.apply.kind = pick_kind(false, [&](int kind, const auto& add) {
-            for (size_t k : order) {
-                const NsParts& p = out->mats[k].parts;
-                add(tiles_of(p.sp, kTileRows[kind]) * tiles_of(p.lp, kTileCols[kind]), p.sp);
-            }
+        b.apply.kind = cheapest([&](int kind) {
+            return launch_cost(kind, false, [&](const auto& add) {
+                for (size_t k : order)
+                    add(tiles_of(parts(k).sp, kTileRows[kind]) * tiles_of(parts(k).lp, kTileCols[kind]), parts(k).sp);
+            });
         });
         // bands of 4 tile rows, column by column
         constexpr int64_t kBand = 4;
