@@ -1072,21 +1072,21 @@ __device__ __forceinline__ uint32_t result_row(int e, uint32_t lane)
 template <int IN>
 __global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __restrict__ mats,
                                                             const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
-                                                            int step)
+                                                            int step, int again)
 {
     if (step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
     const DevTile t = tiles[blockIdx.x];
     const DevMatrix& mx = mats[t.mat];
     const bool tall = mx.tall != 0;
     const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols;
-    const uint64_t in = step ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
+    const uint64_t in = step || again ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
     const bool by4 = rows_by4(cols, in);
     const uint32_t run = (uint32_t)small_gram_cols(t.parts.lp), j0 = t.col * run, j1 = j0 + run < l ? j0 + run : l;
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, wr = wave / 2 * 32, wc = wave % 2 * 32;
     __shared__ PairTile x;
     f32x4 v[4];
     load_tile<IN>(in, by4, rows, cols, tall ? j0 : 0, tall ? 0 : j0, v);
-    const double scale = norm_scale(mx, ws, eps, sx);
+    const double scale = again ? pow2(sx) : norm_scale(mx, ws, eps, sx);
     f32x16 main = zeros16(), cross = zeros16();
     for (uint32_t j = j0; j < j1; j += kPad) {
         store_tile(v, scale, tall, x.hi, x.lo);
@@ -1201,10 +1201,13 @@ __global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevTi
     store(q, fq, to, to + kPad * kPad, std::integral_constant<uint32_t, kPad>{});
 }
 
+// The end of a run of steps that is not the last: X in fp32, as u lay.
+constexpr int kEndAgain = kNumEnds;
+
 template <int IN, int END>
 __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __restrict__ mats,
                                                              const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
-                                                             int sq, ProductArgs g)
+                                                             int sq, int again, ProductArgs g)
 {
     if (g.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
     const uint32_t tid = threadIdx.x;
@@ -1213,7 +1216,7 @@ __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __
     const DevMatrix& mx = mats[t.mat];
     const bool tall = mx.tall != 0, row16 = mx.row16 != 0;
     const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols;
-    const uint64_t in = g.step ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
+    const uint64_t in = g.step || again ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
     const bool by4 = rows_by4(cols, in);
     const uint32_t run = (uint32_t)small_apply_cols(t.parts.lp), j0 = t.col * run, j1 = j0 + run < l ? j0 + run : l;
     const uint32_t lane = tid & 63u, wave = tid >> 6, wr = wave / 2 * 32, wc = wave % 2 * 32;
@@ -1229,7 +1232,7 @@ __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __
         *reinterpret_cast<f16x8*>(q.hi + o) = *reinterpret_cast<const GLOBAL f16x8*>(from);
         *reinterpret_cast<f16x8*>(q.lo + o) = *reinterpret_cast<const GLOBAL f16x8*>(from + kPad * kPad);
     }
-    const double scale = norm_scale(mx, ws, eps, sx);
+    const double scale = again ? pow2(sx) : norm_scale(mx, ws, eps, sx);
     for (uint32_t j = j0; j < j1; j += kPad) {
         store_tile(v, scale, !tall, x.hi, x.lo);   // rows are columns of X
         __syncthreads();
@@ -1243,7 +1246,15 @@ __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __
         }
         __syncthreads();
         const uint32_t r0 = tall ? j : 0, c0 = tall ? 0 : j;
-        if (row16) {
+        if constexpr (END == kEndAgain) {
+            // in u's place, of which this workgroup has read the tile and no other one reads any of its run
+            GLOBAL float* to = at<float>(ws, t.parts.u());
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+                const uint32_t k = (uint32_t)h * 256 + tid, r = r0 + k / 64, c = c0 + k % 64;
+                if (r < rows && c < cols) to[(uint64_t)r * cols + c] = out[k / 64 * kOutLd + k % 64];
+            }
+        } else if (row16) {
             EndInput<END> end[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1319,28 +1330,38 @@ hipError_t normalise(const NsCall& call, const NsLaunch& l, bool step, hipStream
     return hipGetLastError();
 }
 
-// Whatever depends on the end: the last product, or the small matrices' one.
-template <int END>
-hipError_t end_launch(const NsCall& call, const NsBatch& batch, int in, const ProductArgs& q, hipStream_t stream)
+template <int IN, int END>
+hipError_t launch_small_apply(const NsCall& call, const NsBatch& batch, bool again, const ProductArgs& q, hipStream_t stream)
 {
-    if (!batch.small) return product<kLast, END>(call, batch.apply, q, stream);
-    const DevTile* tiles = call.tiles + batch.apply.first;
-    const dim3 grid((uint32_t)batch.apply.count), block(256);
-    const NsScales& s = call.scales;
-    if (in == kInF32)
-        ns_small_apply_kernel<kInF32, END><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, call.ns.eps, s.sx, s.sq, q);
-    else if (END == kEndOrtho && in == kInBf16)
-        ns_small_apply_kernel<kInBf16, kEndOrtho><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, call.ns.eps, s.sx, s.sq, q);
-    else
-        ns_small_apply_kernel<kInF16, kEndOrtho><<<grid, block, 0, stream>>>(call.mats, tiles, call.ws, call.ns.eps, s.sx, s.sq, q);
+    ns_small_apply_kernel<IN, END><<<(uint32_t)batch.apply.count, 256, 0, stream>>>(
+        call.mats, call.tiles + batch.apply.first, call.ws, call.ns.eps, call.scales.sx, call.scales.sq, again, q);
     return hipGetLastError();
 }
 
+// `in`: the type of what is read, which is fp32 of a step and of X between two runs
+template <int END>
+hipError_t small_apply(const NsCall& call, const NsBatch& batch, int in, bool again, const ProductArgs& q, hipStream_t stream)
+{
+    if constexpr (END == kEndOrtho || END == kEndAgain) {
+        if (in == kInBf16) return launch_small_apply<kInBf16, END>(call, batch, again, q, stream);
+        if (in == kInF16) return launch_small_apply<kInF16, END>(call, batch, again, q, stream);
+    }
+    return launch_small_apply<kInF32, END>(call, batch, again, q, stream);
+}
+
+// Whatever depends on the end: the last product, or the small matrices' one.
+template <int END>
+hipError_t end_launch(const NsCall& call, const NsBatch& batch, int in, bool again, const ProductArgs& q, hipStream_t stream)
+{
+    return batch.small ? small_apply<END>(call, batch, in, again, q, stream)
+                       : product<kLast, END>(call, batch.apply, q, stream);
+}
+
 template <int IN>
-hipError_t small_gram(const NsCall& call, const NsLaunch& l, bool step, hipStream_t stream)
+hipError_t small_gram(const NsCall& call, const NsLaunch& l, bool step, bool again, hipStream_t stream)
 {
     ns_small_gram_kernel<IN><<<(uint32_t)l.count, 256, 0, stream>>>(call.mats, call.tiles + l.first, call.ws, call.ns.eps,
-                                                                    call.scales.sx, step);
+                                                                    call.scales.sx, step, again);
     return hipGetLastError();
 }
 
@@ -1350,16 +1371,17 @@ StepRule step_rule(const NsCall& call)
 }
 
 // `in`: the type of u, which a step has in fp32
-hipError_t last_product(const NsCall& call, const NsBatch& batch, int in, const ProductArgs& q, hipStream_t stream)
+hipError_t last_product(const NsCall& call, const NsBatch& batch, int in, bool again, const ProductArgs& q,
+                        hipStream_t stream)
 {
     switch (call.kind.end) {
-    case kEndOrtho: return end_launch<kEndOrtho>(call, batch, in, q, stream);
-    case kEndMixedBf16: return end_launch<kEndMixedBf16>(call, batch, in, q, stream);
-    case kEndMixedF16: return end_launch<kEndMixedF16>(call, batch, in, q, stream);
-    case kEndSplit: return end_launch<kEndSplit>(call, batch, in, q, stream);
-    case kEndPure: return end_launch<kEndPure>(call, batch, in, q, stream);
-    case kEndKahan: return end_launch<kEndKahan>(call, batch, in, q, stream);
-    default: return end_launch<kEndKahan32>(call, batch, in, q, stream);
+    case kEndOrtho: return end_launch<kEndOrtho>(call, batch, in, again, q, stream);
+    case kEndMixedBf16: return end_launch<kEndMixedBf16>(call, batch, in, again, q, stream);
+    case kEndMixedF16: return end_launch<kEndMixedF16>(call, batch, in, again, q, stream);
+    case kEndSplit: return end_launch<kEndSplit>(call, batch, in, again, q, stream);
+    case kEndPure: return end_launch<kEndPure>(call, batch, in, again, q, stream);
+    case kEndKahan: return end_launch<kEndKahan>(call, batch, in, again, q, stream);
+    default: return end_launch<kEndKahan32>(call, batch, in, again, q, stream);
     }
 }
 
@@ -1398,17 +1420,26 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
     if (e != hipSuccess) return e;
     const int in_u = step ? kInF32 : in;
     if (batch.small) {
-        e = in_u == kInF32 ? small_gram<kInF32>(call, batch.normalise, step, stream)
-          : in_u == kInBf16 ? small_gram<kInBf16>(call, batch.normalise, step, stream)
-                            : small_gram<kInF16>(call, batch.normalise, step, stream);
-        if (e != hipSuccess) return e;
         const NsScales& s = call.scales;
-        ns_small_chain_kernel<<<(uint32_t)batch.square.count, kBlockChain, 0, stream>>>(
-            call.tiles + batch.square.first, call.ws,
-            ChainArgs{call.ns.a, call.ns.b, call.ns.c, call.ns.steps, s.sa, s.sp, s.sz, s.sq, step});
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        q.count = last ? call.step : nullptr;
-        return last_product(call, batch, in_u, q, stream);
+        for (int left = call.ns.steps, from = in_u;; from = kInF32) {
+            const bool again = left < call.ns.steps;
+            e = from == kInF32 ? small_gram<kInF32>(call, batch.normalise, step, again, stream)
+              : from == kInBf16 ? small_gram<kInBf16>(call, batch.normalise, step, again, stream)
+                                : small_gram<kInF16>(call, batch.normalise, step, again, stream);
+            if (e != hipSuccess) return e;
+            const int run = left < s.run ? left : s.run;
+            left -= run;
+            ns_small_chain_kernel<<<(uint32_t)batch.square.count, kBlockChain, 0, stream>>>(
+                call.tiles + batch.square.first, call.ws,
+                ChainArgs{call.ns.a, call.ns.b, call.ns.c, run, s.sa, s.sp, s.sz, s.sq, step});
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            if (left == 0) {
+                q.count = last ? call.step : nullptr;
+                return last_product(call, batch, from, again, q, stream);
+            }
+            e = small_apply<kEndAgain>(call, batch, from, again, q, stream);
+            if (e != hipSuccess) return e;
+        }
     }
     e = step || in == kInF32 ? normalise<kInF32>(call, batch.normalise, step, stream)
       : in == kInBf16 ? normalise<kInBf16>(call, batch.normalise, step, stream)
@@ -1423,7 +1454,7 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
             e = product<kApply>(call, batch.apply, q, stream);
         } else {
             q.count = last ? call.step : nullptr;
-            e = last_product(call, batch, in_u, q, stream);
+            e = last_product(call, batch, in_u, false, q, stream);
         }
         if (e != hipSuccess) return e;
     }

@@ -18,6 +18,8 @@
 //   small chain  Q, the product of every step's a I + b A + c A A
 //   small apply  Q X with the result's own epilogue
 //
+// (of more than NsScales::run steps, run by run, with X in fp32 between them).
+//
 // The matrices of the products are held in the workspace with both sides padded to
 // kPad by zeros, so that the product kernels have no ragged edge in the summed dimension.
 #pragma once
@@ -157,6 +159,11 @@ struct NsKind {
 struct NsScales {
     int sx, sa, sb;
     int sp, sz, sq;
+    // Steps that small chain takes of one Gram matrix.  A rounding of 2^-22 in it grows by a^2 with every step where X has
+    // no singular value, and nothing in the polynomials brings it back, as products with X do.  So the largest
+    // a + b q + c q^2 of all of them but the last may multiply to 2^11 (the usual coefficients: 7 steps; 9 took
+    // matrices of rank one to NaN); after them X is formed and its Gram matrix anew.
+    int run;
 };
 
 adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::string& err);

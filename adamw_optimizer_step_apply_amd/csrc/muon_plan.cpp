@@ -198,7 +198,7 @@ adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::stri
     // What the polynomials reach on the singular values of each step, [0, top]: at the ends or where a derivative is
     // zero, in q = x^2.
     const double a = ns->a, b = ns->b, c = ns->c;
-    double top = 1.0, most = 1.0, poly = 0.0, whole = 0.0, times_a = 0.0, product = 1.0;
+    double top = 1.0, most = 1.0, poly = 0.0, whole = 0.0, times_a = 0.0;
     for (int k = 0; k < ns->steps; ++k) {
         const double end = top * top;
         double at[7] = {0.0, end}, next = 0.0, one = 0.0;
@@ -231,7 +231,6 @@ adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::stri
             times_a = std::max(times_a, q * std::fabs(a + p));
         }
         whole = std::max(whole, one * 1.02);
-        product *= one * 1.02;
         top = next * 1.01;   // rounding
         most = std::max(most, top);
         if (!(most <= 64.0)) {
@@ -246,8 +245,12 @@ adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::stri
     scales->sb = under(poly * 1.02);
     scales->sp = under(whole);
     scales->sz = under(times_a * 1.02);
-    // a product of at most 16 of them; where it passes what fp16 can hold the small elements lose bits
-    scales->sq = std::max(under(product), -40);
+    // runs of equal length, of at most the steps whose polynomials stay under 2^11
+    const int most_run = whole > 1.0 ? 1 + (int)std::min(std::log(2048.0) / std::log(whole), (double)ADAMW_NS_MAX_STEPS)
+                                     : (int)ADAMW_NS_MAX_STEPS;
+    const int runs = (ns->steps + most_run - 1) / most_run;
+    scales->run = (ns->steps + runs - 1) / runs;
+    scales->sq = under(std::pow(std::max(whole, 1.0), scales->run));
     return ADAMW_OK;
 }
 
