@@ -86,6 +86,10 @@ __global__ void ns_count_kernel(StepRule rule, int32_t* step)
 // ---------------------------------------------------------------------------
 // Moments: the sum of squares of each matrix, as a partial sum for each run of elements; in a
 // step m = beta m + (1 - beta) g first, and u to the workspace.
+//
+// Bound by HBM: a step reads g and m and writes m and u, 14 bytes an element with fp32 m, at 4.7 TB/s (302 M elements
+// in 904 us on MI355X), the rate of a large copy.  Each workgroup sums one run of 4,096 elements or more into one
+// binary64 partial, so that no atomic orders the sum and the readers add at most 256 of them.
 // ---------------------------------------------------------------------------
 
 enum { kInF32 = 0, kInBf16 = 1, kInF16 = 2 };
@@ -229,6 +233,10 @@ __global__ __launch_bounds__(kBlockMoments) void ns_moments_kernel(const DevMatr
 
 // ---------------------------------------------------------------------------
 // Normalisation: X = u / (|u| + eps) into hi and lo, zeros in the padding.
+//
+// Bound by HBM: 8 bytes an element of an fp32 u, at 5.1 TB/s (302 M elements in 471 us on MI355X).  Tiles of 64 x 64 go
+// through LDS, since a tall matrix is transposed on the way and a wide one shares the path; every workgroup adds the
+// partial sums by itself, which costs one load a lane and saves a launch.
 // ---------------------------------------------------------------------------
 
 // x * 2^sx as hi + lo * 2^-11
@@ -336,7 +344,21 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
 }
 
 // ---------------------------------------------------------------------------
-// Products
+// Products: A = X X^T, B = b A + c A A and X' = a X + B X, tile by tile.
+//
+// A tile's two factors come in runs of 64 summed elements straight to LDS, in two stages (four of the small tiles) that
+// turn about: while the matrix instructions of one run go on, the next one is under way, and one wait and one
+// barrier stand between two runs.  Sums stay in registers; the epilogue takes them through LDS, 32 rows of a wave
+// at a time, so that global memory sees 16-byte words of rows (of columns where a square is mirrored).
+//
+// 256 x 256 tiles on 8 waves read 1 byte for 128 operations, 128 x 128 and 64 x 64 half and a quarter as many
+// operations, and are for launches that would leave CUs idle.  On MI355X, 24 matrices of 2048 x 2048 and 12 of
+// 2048 x 8192 (tiles of 256): gram 749 us (929 TFLOP/s over the tiles on and below the diagonal), poly 417 us (835),
+// apply 1,653 us (748), with a step's epilogue 1,911 us (647); a library product of 8192 x 8192 in fp16, which writes
+// little and sums long, reaches 1,402.  What bounds them: the matrix instructions, at the 2.0 to 2.2 GHz that the power
+// limit leaves, take 44, 39, 33 and 27 % of the cycles; the rest is each tile's epilogue, which no other workgroup of
+// the CU covers (one fits): of apply 2 bytes an element read and 4 written, of the squares 2 written, of a mixed step 4 read and 6 written.  Tiles
+// of 64 in launches of 78 to 144 (768 x 768) are latencies, 7 to 10 us each.
 // ---------------------------------------------------------------------------
 
 enum NsOp { kGram, kPoly, kApply, kLast };
@@ -1027,11 +1049,12 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 // Matrices whose shorter side is at most 64: everything between the two passes over X in one workgroup.
 //
 // With A = X X^T and p(A) = a I + b A + c A A, a step is X <- p(A) X and A <- p(A) A p(A), all polynomials of the first
-// A, so Q = p_k(A_k) ... p_1(A_1) is found from 64 x 64 matrices alone and the result is Q X: 2 + 4 (steps - 1) products of
+// A, so Q = p_k(A_k) ... p_1(A_1) is found from 64 x 64 matrices alone and the result is Q X: 4 steps - 3 products of
 // 64 x 64 that never leave LDS instead of three launches a step.  A loses what X has below the square root of its
 // precision, so it is held in 22 bits (products of pairs: hi hi + hi lo + lo hi): the result is within 1e-4 of the
 // definition (simulated in binary64 with these roundings, spectra as above: 3e-7 to 1e-4).  These
-// kernels are latencies: one 16 x 768 took 73 us in 17 launches on MI355X.
+// kernels are latencies.  One 16 x 768 on MI355X, in us: moments 2.5, small gram 5.1, small chain 18.6, small apply 5.7,
+// as passes follow each other 31; step by step in 17 launches it took 73.
 // ---------------------------------------------------------------------------
 
 // A 64 x 64 matrix as fp16 pairs in LDS.
@@ -1069,6 +1092,8 @@ __device__ __forceinline__ uint32_t result_row(int e, uint32_t lane)
     return (uint32_t)((e & 3) + 8 * (e >> 2)) + 4 * (lane >> 5);
 }
 
+// A run of columns' part of A, at most 32 runs a matrix, so that chain adds few and a long matrix still takes 32 CUs;
+// the next 64 columns are under way while the last ones are multiplied.
 template <int IN>
 __global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __restrict__ mats,
                                                             const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
@@ -1111,7 +1136,8 @@ __device__ __forceinline__ u32x2* as_words(_Float16* p) { return reinterpret_cas
 __device__ __forceinline__ GLOBAL u32x2* as_words(GLOBAL _Float16* p) { return reinterpret_cast<GLOBAL u32x2*>(p); }
 
 // Sixteen waves with a 16 x 16 part each: each product is one latency of reads, six matrix instructions and stores,
-// which four waves with 32 x 32 each took three times as long for (18.5 us a matrix on MI355X).
+// which four waves with 32 x 32 each took three times as long for.  18.6 us for five steps (17 products) on
+// MI355X; each matrix takes a CU of its own.
 constexpr int kBlockChain = 1024;
 
 __global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevTile* __restrict__ tiles, char* ws, ChainArgs g)
@@ -1204,6 +1230,8 @@ __global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevTi
 // The end of a run of steps that is not the last: X in fp32, as u lay.
 constexpr int kEndAgain = kNumEnds;
 
+// Q X, 64 columns at a time as small gram reads them; workgroups of 64 columns up to 4,096 and of 256 beyond, where
+// reading Q anew would cost as much as X.
 template <int IN, int END>
 __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __restrict__ mats,
                                                              const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
