@@ -463,6 +463,9 @@ class MatrixList(TensorList):
                     raise ValueError(f"stream {k}, tensor {i}: {x.numel()} elements are no matrix of {self.shapes[i]}")
         super().__init__(numels, streams, shard_begin, shard_end, flat_mask)
         self.cols = (ctypes.c_int64 * max(len(numels), 1))(*[max(c, 1) for _, c in self.shapes])
+        # of each stream's tensors, for _check_streams
+        self._kinds = [{(x.element_size(), x.is_cuda) for x in items or () if isinstance(x, torch.Tensor)}
+                       for items in streams]
 
 
 @dataclass
@@ -516,13 +519,28 @@ def make_orthogonalize_workspace(matrices: MatrixList, device=None) -> torch.Ten
 
 
 def _workspace(x):
-    """Address and bytes of a workspace: a contiguous tensor, or (address, bytes)."""
+    """Address and bytes of a workspace: a contiguous tensor on the GPU, or (address, bytes)."""
     if isinstance(x, torch.Tensor):
         if not x.is_contiguous():
             raise ValueError("workspace: a contiguous tensor is needed")
+        if not x.is_cuda:
+            raise ValueError(f"workspace: a tensor on the GPU is needed, got {x.device}")
         return x.data_ptr(), x.numel() * x.element_size()
     address, nbytes = x
     return int(address), int(nbytes)
+
+
+_ELEMENT_BYTES = {F32: 4, BF16: 2, F16: 2}
+
+
+def _check_streams(matrices: MatrixList, sizes) -> None:
+    """The tensors of a list of matrices are on the GPU and of the element sizes that a call reads and writes (0 or
+    None: not looked at)."""
+    for k, (kinds, size) in enumerate(zip(matrices._kinds, sizes)):
+        for got, on_gpu in kinds if size else ():
+            if not on_gpu or got != size:
+                raise ValueError(f"stream {k}: tensors of {size} bytes an element on the GPU are needed, got "
+                                 f"{got} bytes{'' if on_gpu else ' on the host'}")
 
 
 def adamw_orthogonalize(u_dtype: int, matrices: MatrixList, workspace, ns: NewtonSchulz = None, stream=None) -> None:
@@ -530,8 +548,10 @@ def adamw_orthogonalize(u_dtype: int, matrices: MatrixList, workspace, ns: Newto
     (``u_dtype``) into stream 0 (bf16), which may be the same bf16 tensors; ``workspace``
     from make_orthogonalize_workspace (C ABI adamw_orthogonalize)."""
     c = (ns or NewtonSchulz()).struct()
-    _check(_lib.adamw_orthogonalize(u_dtype, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(c),
-                                    *_workspace(workspace), _stream(stream)))
+    ws = _workspace(workspace)
+    _check_streams(matrices, (2, _ELEMENT_BYTES.get(u_dtype)))
+    _check(_lib.adamw_orthogonalize(u_dtype, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(c), *ws,
+                                    _stream(stream)))
 
 
 def adamw_muon_multi_tensor_step(mode: int, p_dtype: int, matrices: MatrixList, hp, d_step, workspace,
@@ -544,9 +564,16 @@ def adamw_muon_multi_tensor_step(mode: int, p_dtype: int, matrices: MatrixList, 
     h = (hp or MuonHParams()).c()
     pc = ctypes.byref(prec.c()) if prec is not None else None
     cc = ctypes.byref(clip.c()) if clip is not None else None
+    ws = _workspace(workspace)
+    if prec is not None:
+        sizes = (2, 2, _ELEMENT_BYTES.get(prec.exp_avg), None, {KAHAN_BF16: 2, KAHAN_F32: 4}.get(prec.kahan))
+    else:
+        sizes = {MIXED: (2, 2, 4, None, 4), MIXED_SPLIT: (2, 2, 4, None, 2), PURE_KAHAN: (2, 2, 2, None, 2)}.get(mode, ())
+    _check_streams(matrices, sizes)
     _check(_lib.adamw_muon_multi_tensor_step(mode, p_dtype, pc, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(h),
-                                             cc, _addr(d_step), _addr(d_found_inf), _addr(d_scale),
-                                             *_workspace(workspace), _stream(stream)))
+                                             cc, _result(d_step, torch.int32, 1, "d_step"),
+                                             _result(d_found_inf, torch.int32, 1, "d_found_inf"), _addr(d_scale),
+                                             *ws, _stream(stream)))
 
 
 def adamw_last_error() -> str:
