@@ -12,6 +12,7 @@
 #include <stdlib.h>
 
 #include <algorithm>
+#include <cmath>
 #include <map>
 #include <string>
 #include <utility>
@@ -268,10 +269,54 @@ void one_list(Rng& r)
 
 }  // namespace
 
+// Random coefficients: refused where a singular value passes 64 on a grid, and else the powers of two hold what a
+// grid of singular values reaches, and a run of steps multiplies a rounding by at most 2^11 before its last step.
+static void one_scale(Rng& r)
+{
+    const auto value = [&](double most) { return (float)((double)(r.below(2000001) - 1000000) * 1e-6 * most); };
+    const adamw_newton_schulz ns{value(8.0), value(16.0), value(8.0), 1e-7f, (int32_t)(1 + r.below(ADAMW_NS_MAX_STEPS))};
+    NsScales s{};
+    std::string err;
+    const bool taken = check_ns(&ns, &s, err) == ADAMW_OK;
+    double top = 1.0, most = 1.0, poly = 0.0, whole = 0.0, times_a = 0.0;
+    for (int k = 0; k < ns.steps && most <= 64.0; ++k) {
+        double next = 0.0;
+        for (int i = 0; i <= 400; ++i) {
+            const double x = top * i / 400, q = x * x, b = q * ((double)ns.b + (double)ns.c * q), p = (double)ns.a + b;
+            next = std::max(next, std::fabs(x * p));
+            poly = std::max(poly, std::fabs(b));
+            whole = std::max(whole, std::fabs(p));
+            times_a = std::max(times_a, std::fabs(q * p));
+        }
+        most = std::max(most, top = next);
+    }
+    if (!taken) return;
+    CHECK(most <= 64.0 && s.run >= 1 && s.run <= ns.steps);
+    CHECK(std::ldexp(most, s.sx) <= 61440.0 && std::ldexp(most * most, s.sa) <= 61440.0 && std::ldexp(poly, s.sb) <= 61440.0);
+    CHECK(std::ldexp(whole, s.sp) <= 61440.0 && std::ldexp(times_a, s.sz) <= 61440.0);
+    CHECK(std::ldexp(std::pow(whole, s.run), s.sq) <= 61440.0 && std::pow(whole, s.run - 1) <= 2048.0);
+    mix((uint64_t)s.run);
+    mix((uint64_t)(int64_t)s.sq);
+}
+
+// The usual coefficients' runs: 7 steps in one, more in runs of like length.
+static void usual_runs()
+{
+    const int want[ADAMW_NS_MAX_STEPS] = {1, 2, 3, 4, 5, 6, 7, 4, 5, 5, 6, 6, 7, 7, 5, 6};
+    for (int steps = 1; steps <= ADAMW_NS_MAX_STEPS; ++steps) {
+        const adamw_newton_schulz ns{3.4445f, -4.7750f, 2.0315f, 1e-7f, steps};
+        NsScales s{};
+        std::string err;
+        CHECK(check_ns(&ns, &s, err) == ADAMW_OK && s.run == want[steps - 1]);
+    }
+}
+
 int main()
 {
     Rng r{88172645463325252ull};
     for (int i = 0; i < 1500; ++i) one_list(r);
+    for (int i = 0; i < 20000; ++i) one_scale(r);
+    usual_runs();
     printf("muon_check ok %016llx\n", (unsigned long long)g_sum);
     return 0;
 }

@@ -122,3 +122,49 @@ def test_one_matrix_read_twice():
     A.adamw_orthogonalize(A.F32, mats, A.make_orthogonalize_workspace(mats))
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and far(outs[0], ns64(u)) <= TOL_NS + TOL_BF16
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("gap,phase", [(8, 0), (1, 3)])
+def test_runs_of_steps_of_long_and_unaligned_matrices(dtype, gap, phase):
+    """Nine steps go in two runs, with X in the workspace between them; workgroups of one and of several tiles."""
+    gen = torch.Generator().manual_seed(36)
+    ns = A.NewtonSchulz(steps=9)
+    outs, ins = run([gradient(r, c, gen) for r, c in [(9, 20001), (5000, 33), (64, 64), (1, 4097), (63, 130)]], dtype, ns, gap, phase)
+    for o, u in zip(outs, ins):
+        assert far(o, ns64(u, ns)) <= TOL_NS + TOL_BF16, (tuple(u.shape), far(o, ns64(u, ns)))
+
+
+def test_runs_of_steps_in_place_with_zeros_and_nan():
+    gen = torch.Generator().manual_seed(37)
+    ns = A.NewtonSchulz(steps=12)
+    us = [gradient(30, 500, gen), torch.zeros(40, 70, dtype=torch.float64), gradient(20, 20, gen), gradient(50, 90, gen)]
+    us[2][3, 4] = float("nan")
+    outs, ins = run(us, "bf16", ns, inplace=True)
+    assert far(outs[0], ns64(ins[0], ns)) <= TOL_NS + TOL_BF16 and far(outs[3], ns64(ins[3], ns)) <= TOL_NS + TOL_BF16
+    assert bool((outs[1] == 0).all()) and bool(torch.isnan(outs[2]).all())
+
+
+def test_runs_of_steps_captured_and_replayed():
+    gen = torch.Generator().manual_seed(38)
+    ns = A.NewtonSchulz(steps=16)
+    us = [gradient(r, c, gen) for r, c in SMALL]
+    a_in, a_out = Arena(us, torch.float16), Arena([0 * u for u in us], torch.bfloat16)
+    mats = A.MatrixList(SMALL, [a_out.views(), a_in.views()])
+    ws = A.make_orthogonalize_workspace(mats)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        A.adamw_orthogonalize(A.F16, mats, ws, ns)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            A.adamw_orthogonalize(A.F16, mats, ws, ns)
+    eager, _ = run(us, "f16", ns)
+    for k in range(3):
+        for v in a_out.views():
+            v.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(a_out.views(), eager)), k
