@@ -39,6 +39,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLoScale = 2048.0f;   // lo is held as lo * 2^11, of the size of hi
 
@@ -259,18 +260,25 @@ __device__ __forceinline__ f32x4 load4(uint64_t base, uint64_t i)
     }
 }
 
-// 2^sx / (|u| + eps) from the partial sums, by every workgroup alike; its barrier is the workgroup's.
-__device__ __forceinline__ double norm_scale(const DevMatrix& mx, const char* ws, float eps, int sx)
+// |u| + eps from the partial sums, by every workgroup alike; its barrier is the workgroup's.
+__device__ __forceinline__ double norm_of(const DevMatrix& mx, const char* ws, float eps)
 {
+    static_assert(kMaxPartials == 256, "four waves add the partial sums");
     __shared__ double part[4];
     const uint32_t tid = threadIdx.x;
     double sum = tid < mx.n_partials ? *at<const double>(const_cast<char*>(ws), mx.partials + (uint64_t)tid * 8) : 0.0;
 #pragma unroll
     for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-    if (tid % 64 == 0) part[tid / 64] = sum;
+    if (tid % 64 == 0 && tid < 256) part[tid / 64] = sum;
     __syncthreads();
     sum = ((part[0] + part[1]) + part[2]) + part[3];
-    const double len = __builtin_sqrt(sum) + (double)eps;
+    return __builtin_sqrt(sum) + (double)eps;
+}
+
+// 2^sx / (|u| + eps)
+__device__ __forceinline__ double norm_scale(const DevMatrix& mx, const char* ws, float eps, int sx)
+{
+    const double len = norm_of(mx, ws, eps);
     // a zero matrix without eps is zero
     return len == 0.0 ? 0.0 : __builtin_ldexp(1.0, sx) / len;
 }
@@ -1092,44 +1100,106 @@ __device__ __forceinline__ uint32_t result_row(int e, uint32_t lane)
     return (uint32_t)((e & 3) + 8 * (e >> 2)) + 4 * (lane >> 5);
 }
 
-// A run of columns' part of A, at most 32 runs a matrix, so that chain adds few and a long matrix still takes 32 CUs;
-// the next 64 columns are under way while the last ones are multiplied.
+// Place of element (i, j), j <= i, of a lower triangle.
+__device__ __forceinline__ uint32_t tri_at(uint32_t i, uint32_t j) { return i * (i + 1) / 2 + j; }
+
+__device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c)
+{
+    return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+// Row of result e of a 16 x 16 product in binary64; the column is lane % 16.
+__device__ __forceinline__ uint32_t result_row64(int e, uint32_t lane) { return (uint32_t)e * 4 + (lane >> 4); }
+
+// A tile of u to LDS as fp32, in rows of kXLd elements, or transposed.  17 words of 16 bytes a row: the operands of a
+// product in binary64, 4 neighbours of each of 16 rows, lie in all 64 banks.
+constexpr int kXLd = 68;
+__device__ __forceinline__ void store_tile_f32(const f32x4 (&x)[4], bool transposed, float* to)
+{
+    const uint32_t tid = threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t r = (uint32_t)k * 16 + tid / 16, c = tid % 16 * 4;
+        if (transposed) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[(c + e) * kXLd + r] = x[k][e];
+        } else {
+            *reinterpret_cast<f32x4*>(to + r * kXLd + c) = x[k];
+        }
+    }
+}
+
+// A run of columns' part of U U^T, in binary64: products of two fp32 are exact there, and the sum's rounding, 2^-53 of it
+// a term at most, is nothing beside what the inputs are known to however long the run is.  Sums in fp32 are not good
+// enough: like terms, as of a matrix of rank one with equal columns, are all rounded the same way (9e-5 of the sum of 4 M of
+// them), and the steps multiply what is wrong by a^2 each where X has no singular value.  Each wave takes 16 of
+// 64 columns and all 16 x 16 blocks on and below the diagonal that the matrix has rows for, so that a row block's operand is
+// read once; the next 64 columns are under way while the last ones are multiplied.
 template <int IN>
 __global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __restrict__ mats,
-                                                            const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
-                                                            int step, int again)
+                                                            const DevTile* __restrict__ tiles, char* ws, int step, int again)
 {
     if (step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
     const DevTile t = tiles[blockIdx.x];
     const DevMatrix& mx = mats[t.mat];
     const bool tall = mx.tall != 0;
-    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols;
+    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols, s = tall ? cols : rows;
     const uint64_t in = step || again ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
     const bool by4 = rows_by4(cols, in);
     const uint32_t run = (uint32_t)small_gram_cols(t.parts.lp), j0 = t.col * run, j1 = j0 + run < l ? j0 + run : l;
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, wr = wave / 2 * 32, wc = wave % 2 * 32;
-    __shared__ PairTile x;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, blocks = (s + 15) / 16;
+    constexpr int kBlocks = kPad / 16;
+    __shared__ alignas(16) float x[kPad * kXLd];
+    __shared__ double sum[kSmallTri];
     f32x4 v[4];
     load_tile<IN>(in, by4, rows, cols, tall ? j0 : 0, tall ? 0 : j0, v);
-    const double scale = again ? pow2(sx) : norm_scale(mx, ws, eps, sx);
-    f32x16 main = zeros16(), cross = zeros16();
+    f64x4 acc[kBlocks][kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) acc[i][j] = f64x4{0.0, 0.0, 0.0, 0.0};
     for (uint32_t j = j0; j < j1; j += kPad) {
-        store_tile(v, scale, tall, x.hi, x.lo);
+        store_tile_f32(v, tall, x);
         __syncthreads();
         if (j + kPad < j1) load_tile<IN>(in, by4, rows, cols, tall ? j + kPad : 0, tall ? 0 : j + kPad, v);
-        pair_product(x, x, wr, wc, lane, main, cross);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t c = wave * 16 + (uint32_t)kk * 4 + (lane >> 4);
+            double o[kBlocks];
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                if ((uint32_t)i >= blocks) break;
+                o[i] = (double)x[((uint32_t)i * 16 + (lane & 15u)) * kXLd + c];
+#pragma unroll
+                for (int k = 0; k <= i; ++k) acc[i][k] = mfma64(o[i], o[k], acc[i][k]);
+            }
+        }
         __syncthreads();
     }
-    GLOBAL float* out = at<float>(ws, t.parts.lo()) + (uint64_t)t.col * (kPad * kPad);
-    const float f = pow2(-2 * sx);
+    // the waves' parts, one after another
+    for (uint32_t w = 0; w < 4; ++w) {
+        if (wave == w) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        out[(wr + result_row(e, lane)) * kPad + wc + (lane & 31u)] = (main[e] + cross[e] * (1.0f / kLoScale)) * f;
+            for (int i = 0; i < kBlocks; ++i) {
+                if ((uint32_t)i >= blocks) break;
+#pragma unroll
+                for (int j = 0; j <= i; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t r = (uint32_t)i * 16 + result_row64(e, lane), c = (uint32_t)j * 16 + (lane & 15u);
+                        if (c <= r) sum[tri_at(r, c)] = (w ? sum[tri_at(r, c)] : 0.0) + acc[i][j][e];
+                    }
+            }
+        }
+        __syncthreads();
+    }
+    GLOBAL double* out = at<double>(ws, t.parts.base) + (uint64_t)t.col * kSmallTri;
+    const uint32_t n = tri_at(blocks * 16, 0);
+    for (uint32_t k = tid; k < n; k += 256) out[k] = sum[k];
 }
 
 struct ChainArgs {
-    float a, b, c;
-    int steps, sa, sp, sz, sq, step;
+    float a, b, c, eps;
+    int steps, sa, sp, sz, sq, step, again;
 };
 
 __device__ __forceinline__ u32x2* as_words(_Float16* p) { return reinterpret_cast<u32x2*>(p); }
@@ -1140,7 +1210,8 @@ __device__ __forceinline__ GLOBAL u32x2* as_words(GLOBAL _Float16* p) { return r
 // MI355X; each matrix takes a CU of its own.
 constexpr int kBlockChain = 1024;
 
-__global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevTile* __restrict__ tiles, char* ws, ChainArgs g)
+__global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevMatrix* __restrict__ mats,
+                                                                       const DevTile* __restrict__ tiles, char* ws, ChainArgs g)
 {
     if (g.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
     const DevTile t = tiles[blockIdx.x];
@@ -1153,11 +1224,20 @@ __global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevTi
     // results on and below the diagonal count, and are stored twice.
     const bool lower = wr > wc, diagonal = wr == wc;
     using InTile = std::integral_constant<uint32_t, kTileLd>;
-    const GLOBAL f32x4* partial = reinterpret_cast<const GLOBAL f32x4*>(at<const float>(ws, t.parts.lo()) + col * kPad + row);
+    const DevMatrix& mx = mats[t.mat];
+    const uint32_t held = ((uint32_t)(mx.tall ? mx.cols : mx.rows) + 15) / 16 * 16;   // rows that small gram has written
+    const double len = g.again ? 1.0 : norm_of(mx, ws, g.eps), inv = len == 0.0 ? 0.0 : 1.0 / len;
+    const GLOBAL double* partial = at<const double>(ws, t.parts.base);
     f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, p = a, q = a, z = a;
-    if (lower || diagonal) {
+    if ((lower || diagonal) && wr < held) {
+        double sum[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 8
-        for (uint32_t k = 0; k < runs; ++k) a += partial[(uint64_t)k * (kPad * kPad / 4)];
+        for (uint32_t k = 0; k < runs; ++k)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+                sum[e] += partial[(uint64_t)k * kSmallTri + (row + e >= col ? tri_at(row + e, col) : tri_at(col, row + e))];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = (float)(sum[e] * inv * inv);
     }
     const float fa = pow2(g.sa), fp = pow2(g.sp), fz = pow2(g.sz), fq = pow2(g.sq);
     const auto store = [&](const f32x4& v, float scale, auto hi, auto lo, auto pitch) __attribute__((always_inline)) {
@@ -1388,8 +1468,7 @@ hipError_t end_launch(const NsCall& call, const NsBatch& batch, int in, bool aga
 template <int IN>
 hipError_t small_gram(const NsCall& call, const NsLaunch& l, bool step, bool again, hipStream_t stream)
 {
-    ns_small_gram_kernel<IN><<<(uint32_t)l.count, 256, 0, stream>>>(call.mats, call.tiles + l.first, call.ws, call.ns.eps,
-                                                                    call.scales.sx, step, again);
+    ns_small_gram_kernel<IN><<<(uint32_t)l.count, 256, 0, stream>>>(call.mats, call.tiles + l.first, call.ws, step, again);
     return hipGetLastError();
 }
 
@@ -1458,8 +1537,8 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
             const int run = left < s.run ? left : s.run;
             left -= run;
             ns_small_chain_kernel<<<(uint32_t)batch.square.count, kBlockChain, 0, stream>>>(
-                call.tiles + batch.square.first, call.ws,
-                ChainArgs{call.ns.a, call.ns.b, call.ns.c, run, s.sa, s.sp, s.sz, s.sq, step});
+                call.mats, call.tiles + batch.square.first, call.ws,
+                ChainArgs{call.ns.a, call.ns.b, call.ns.c, call.ns.eps, run, s.sa, s.sp, s.sz, s.sq, step, again});
             if ((e = hipGetLastError()) != hipSuccess) return e;
             if (left == 0) {
                 q.count = last ? call.step : nullptr;

@@ -14,8 +14,8 @@
 // polynomials of the first Gram matrix, and X is read twice instead:
 //
 //   moments      as above
-//   small gram   partial sums of A = X X^T for runs of columns
-//   small chain  Q, the product of every step's a I + b A + c A A
+//   small gram   partial sums of U U^T for runs of columns, in binary64
+//   small chain  A = U U^T / (|U| + eps)^2, and Q, the product of every step's a I + b A + c A A
 //   small apply  Q X with the result's own epilogue
 //
 // (of more than NsScales::run steps, run by run, with X in fp32 between them).
@@ -43,12 +43,21 @@ constexpr int64_t kNsBatchBytes = INT64_C(4) << 30;   // workspace of a batch of
 // most kMaxPartials partial sums, which every workgroup of the normalisation adds up.
 constexpr int64_t kMomentElems = 4096, kMaxPartials = 256;
 constexpr int kBlockMoments = 256;
-// Columns of X of a workgroup of small gram: a multiple of kPad, so that a matrix has at most kMaxSmallRuns partial
-// Gram matrices (of kPad x kPad fp32, which lie where lo and hi(0) would); and of small apply.
-constexpr int64_t kMaxSmallRuns = 32;
+// Columns of X of a workgroup of small gram, a multiple of kPad, so that a matrix has at most kMaxSmallRuns partial Gram
+// matrices: 32 of them, which chain adds up quickly, until a run has 2,048 columns, and then more, since one
+// CU multiplies in binary64 no faster than 64 x 64 x 2,048 in 35 us. A partial Gram matrix is its lower triangle in
+// binary64, row after row (kSmallTri elements). They lie one after another from the matrix's base on, before u: runs of
+// 128 columns or more leave 32 KiB for each.
+constexpr int64_t kMaxSmallRuns = 256;
+constexpr int64_t kSmallTri = (int64_t)kPad * (kPad + 1) / 2;
 constexpr int64_t small_gram_cols(int64_t lp)
 {
-    const int64_t each = (lp + kMaxSmallRuns - 1) / kMaxSmallRuns;
+    int64_t each = (lp + 31) / 32;
+    if (each > 2048) {
+        each = (lp + kMaxSmallRuns - 1) / kMaxSmallRuns;
+        if (each < 2048) each = 2048;
+    }
+    if (each < 2 * kPad) each = 2 * kPad;
     return (each + kPad - 1) / kPad * kPad;
 }
 constexpr int64_t small_apply_cols(int64_t lp) { return lp <= 4096 ? kPad : 4 * kPad; }
