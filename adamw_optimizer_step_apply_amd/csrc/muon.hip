@@ -386,11 +386,6 @@ __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
 // 16 bytes for every lane of the wave from its own address to LDS, lane after lane from `to` on
 __device__ __forceinline__ void load_to_lds(const GLOBAL char* from, char* to)
 {
@@ -1054,51 +1049,18 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 }
 
 // ---------------------------------------------------------------------------
-// Matrices whose shorter side is at most 64: everything between the two passes over X in one workgroup.
+// Matrices whose shorter side is at most 64: everything between the two passes over u in one workgroup, in binary64.
 //
 // With A = X X^T and p(A) = a I + b A + c A A, a step is X <- p(A) X and A <- p(A) A p(A), all polynomials of the first
-// A, so Q = p_k(A_k) ... p_1(A_1) is found from 64 x 64 matrices alone and the result is Q X: 4 steps - 3 products of
-// 64 x 64 that never leave LDS instead of three launches a step.  A loses what X has below the square root of its
-// precision, so it is held in 22 bits (products of pairs: hi hi + hi lo + lo hi): the result is within 1e-4 of the
-// definition (simulated in binary64 with these roundings, spectra as above: 3e-7 to 1e-4).  These
-// kernels are latencies.  One 16 x 768 on MI355X, in us: moments 2.5, small gram 5.1, small chain 18.6, small apply 5.7,
-// as passes follow each other 31; step by step in 17 launches it took 73.
+// A, so Q = p_k(A_k) ... p_1(A_1) is found from 64 x 64 matrices alone and the result is Q X = (Q / (|u| + eps)) u:
+// 4 steps - 3 products of at most 64 x 64 that never leave LDS instead of three launches a step.
+//
+// Where X has no singular value nothing in those polynomials brings a rounding of A back, which step-by-step products with
+// X do: it grows by a^2 a step.  With A, Q and X as fp16 pairs (22 bits) a 64 x 2048 matrix of one direction and 0.3 % of noise
+// came out 5e-2 off after seven steps, where the definition in fp32 is 3e-5 off.  So all of it is binary64, on its
+// matrix instructions: the 2^-53 of a run of steps (NsScales::run) grows to 2^-31 at most, the result is rounded once, to
+// fp32, and X is fp32 between runs.
 // ---------------------------------------------------------------------------
-
-// A 64 x 64 matrix as fp16 pairs in LDS.
-struct alignas(16) PairTile {
-    _Float16 hi[kPad * kTileLd], lo[kPad * kTileLd];
-};
-
-// sum_k P[i][k] Q[j][k] over the 64 columns of two pair tiles, for the wave's 32 x 32 quarter (rows i from wr, j from
-// wc): hi hi to `main`, hi lo + lo hi, which are under 2^11 more, to `cross`.
-__device__ __forceinline__ void pair_product(const PairTile& p, const PairTile& q, uint32_t wr, uint32_t wc, uint32_t lane,
-                                             f32x16& main, f32x16& cross)
-{
-#pragma unroll
-    for (int kk = 0; kk < kPad / 16; ++kk) {
-        const uint32_t c = (uint32_t)kk * 16 + (lane >> 5) * 8, op = (wr + (lane & 31u)) * kTileLd + c, oq = (wc + (lane & 31u)) * kTileLd + c;
-        const f16x8 ph = *reinterpret_cast<const f16x8*>(p.hi + op), pl = *reinterpret_cast<const f16x8*>(p.lo + op);
-        const f16x8 qh = *reinterpret_cast<const f16x8*>(q.hi + oq), ql = *reinterpret_cast<const f16x8*>(q.lo + oq);
-        main = mfma(ph, qh, main);
-        cross = mfma(ph, ql, cross);
-        cross = mfma(pl, qh, cross);
-    }
-}
-
-__device__ __forceinline__ f32x16 zeros16()
-{
-    f32x16 z;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) z[e] = 0.0f;
-    return z;
-}
-
-// Row of result e of a wave's 32 x 32 quarter; the column is lane % 32.
-__device__ __forceinline__ uint32_t result_row(int e, uint32_t lane)
-{
-    return (uint32_t)((e & 3) + 8 * (e >> 2)) + 4 * (lane >> 5);
-}
 
 // Place of element (i, j), j <= i, of a lower triangle.
 __device__ __forceinline__ uint32_t tri_at(uint32_t i, uint32_t j) { return i * (i + 1) / 2 + j; }
@@ -1199,123 +1161,98 @@ __global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __r
 
 struct ChainArgs {
     float a, b, c, eps;
-    int steps, sa, sp, sz, sq, step, again;
+    int steps, step, again;
 };
 
-__device__ __forceinline__ u32x2* as_words(_Float16* p) { return reinterpret_cast<u32x2*>(p); }
-__device__ __forceinline__ GLOBAL u32x2* as_words(GLOBAL _Float16* p) { return reinterpret_cast<GLOBAL u32x2*>(p); }
-
-// Sixteen waves with a 16 x 16 part each: each product is one latency of reads, six matrix instructions and stores,
-// which four waves with 32 x 32 each took three times as long for.  18.6 us for five steps (17 products) on
-// MI355X; each matrix takes a CU of its own.
-constexpr int kBlockChain = 1024;
+// A wave has one of the ten 16 x 16 blocks on and below the diagonal, of which a matrix of s rows needs those of its
+// first ceil(s / 16) block rows.  All that is held is symmetric, and has to stay so to the last bit: an antisymmetric part,
+// which exact products of commuting matrices have not, grows by a^2 with every step.  So the results on and below the
+// diagonal count, and are stored twice.  Rows of 66 elements: the operands of a product, 4 neighbours of each of
+// 16 rows, lie in all 64 banks twice.
+constexpr int kBlockChain = 640;
+constexpr int kChainLd = kPad + 2;
 
 __global__ __launch_bounds__(kBlockChain) void ns_small_chain_kernel(const DevMatrix* __restrict__ mats,
                                                                        const DevTile* __restrict__ tiles, char* ws, ChainArgs g)
 {
     if (g.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
     const DevTile t = tiles[blockIdx.x];
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, wr = wave / 4 * 16, wc = wave % 4 * 16;
-    const uint32_t row = wr + (lane >> 4) * 4, col = wc + (lane & 15u);   // of the lane's first result; four rows
-    const uint32_t runs = (uint32_t)((t.parts.lp + small_gram_cols(t.parts.lp) - 1) / small_gram_cols(t.parts.lp));
-    __shared__ PairTile ta, tp, tq, tz;
-    // All that is held is symmetric, and has to stay so to the last bit: an antisymmetric part, which exact products of
-    // commuting matrices have not, grows by a^2 with every step (stored transposed, 1e-2 off the definition).  So the
-    // results on and below the diagonal count, and are stored twice.
-    const bool lower = wr > wc, diagonal = wr == wc;
-    using InTile = std::integral_constant<uint32_t, kTileLd>;
     const DevMatrix& mx = mats[t.mat];
-    const uint32_t held = ((uint32_t)(mx.tall ? mx.cols : mx.rows) + 15) / 16 * 16;   // rows that small gram has written
-    const double len = g.again ? 1.0 : norm_of(mx, ws, g.eps), inv = len == 0.0 ? 0.0 : 1.0 / len;
-    const GLOBAL double* partial = at<const double>(ws, t.parts.base);
-    f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, p = a, q = a, z = a;
-    if ((lower || diagonal) && wr < held) {
-        double sum[4] = {0.0, 0.0, 0.0, 0.0};
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t bi = wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3, bj = wave - bi * (bi + 1) / 2;
+    const uint32_t blocks = ((uint32_t)(mx.tall ? mx.cols : mx.rows) + 15) / 16;
+    const bool active = bi < blocks;
+    const uint32_t row = bi * 16 + result_row64(0, lane), col = bj * 16 + (lane & 15u);   // of result e: row + 4 e
+    const uint32_t runs = (uint32_t)((t.parts.lp + small_gram_cols(t.parts.lp) - 1) / small_gram_cols(t.parts.lp));
+    __shared__ double ta[kPad * kChainLd], tp[kPad * kChainLd], tq[kPad * kChainLd], tz[kPad * kChainLd];
+    // NaN for a norm that is inf or NaN, so that every element of the result is; a zero matrix without eps is zero
+    const double len = g.again ? 1.0 : norm_of(mx, ws, g.eps);
+    const double inv = !(len < __builtin_inf()) ? __builtin_nan("") : len == 0.0 ? 0.0 : 1.0 / len;
+    GLOBAL double* at_base = at<double>(ws, t.parts.base);
+    f64x4 a = {0.0, 0.0, 0.0, 0.0}, p = a, q = a;
+    if (active) {
 #pragma unroll 8
         for (uint32_t k = 0; k < runs; ++k)
 #pragma unroll
-            for (uint32_t e = 0; e < 4; ++e)
-                sum[e] += partial[(uint64_t)k * kSmallTri + (row + e >= col ? tri_at(row + e, col) : tri_at(col, row + e))];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = (float)(sum[e] * inv * inv);
-    }
-    const float fa = pow2(g.sa), fp = pow2(g.sp), fz = pow2(g.sz), fq = pow2(g.sq);
-    const auto store = [&](const f32x4& v, float scale, auto hi, auto lo, auto pitch) __attribute__((always_inline)) {
-        constexpr uint32_t ld = decltype(pitch)::value;
-        if (!lower && !diagonal) return;
-        f16x4 h, l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = (_Float16)(v[e] * scale);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) l[e] = (_Float16)(__builtin_fmaf(v[e], scale, -(float)h[e]) * kLoScale);
-        const auto h0 = hi + row * ld + col, l0 = lo + row * ld + col, h1 = hi + col * ld + row, l1 = lo + col * ld + row;
-        if (lower) {
-            *as_words(h1) = __builtin_bit_cast(u32x2, h);
-            *as_words(l1) = __builtin_bit_cast(u32x2, l);
-#pragma unroll
             for (int e = 0; e < 4; ++e) {
-                h0[e * ld] = h[e];
-                l0[e * ld] = l[e];
+                const uint32_t r = row + (uint32_t)e * 4;
+                a[e] += at_base[(uint64_t)k * kSmallTri + (r >= col ? tri_at(r, col) : tri_at(col, r))];
             }
-        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (row + e >= col) {
-                    h0[e * ld] = h1[e] = h[e];
-                    l0[e * ld] = l1[e] = l[e];
-                }
-        }
-    };
-    const auto product = [&](const PairTile& x, const PairTile& y, float scale) __attribute__((always_inline)) {
-        f32x4 main = {0.0f, 0.0f, 0.0f, 0.0f}, hl = main, lh = main;
-        if (!lower && !diagonal) return main;
-#pragma unroll
-        for (int kk = 0; kk < kPad / 32; ++kk) {
-            const uint32_t c = (uint32_t)kk * 32 + (lane >> 4) * 8, ox = (wr + (lane & 15u)) * kTileLd + c, oy = (wc + (lane & 15u)) * kTileLd + c;
-            const f16x8 xh = *reinterpret_cast<const f16x8*>(x.hi + ox), xl = *reinterpret_cast<const f16x8*>(x.lo + ox);
-            const f16x8 yh = *reinterpret_cast<const f16x8*>(y.hi + oy), yl = *reinterpret_cast<const f16x8*>(y.lo + oy);
-            main = mfma16(xh, yh, main);
-            hl = mfma16(xh, yl, hl);
-            lh = mfma16(xl, yh, lh);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) main[e] = (main[e] + (hl[e] + lh[e]) * (1.0f / kLoScale)) * scale;
-        return main;
-    };
-    for (int k = 0;; ++k) {
-        store(a, fa, ta.hi, ta.lo, InTile{});
-        __syncthreads();
-        const f32x4 sq = product(ta, ta, pow2(-2 * g.sa));
+        for (int e = 0; e < 4; ++e) a[e] = a[e] * inv * inv;
+    }
+    const auto store = [&](const f64x4& v, double* to) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            p[e] = __builtin_fmaf(g.c, sq[e], g.b * a[e]);
-            if (row + e == col) p[e] += g.a;
+            const uint32_t r = row + (uint32_t)e * 4;
+            if (active && r >= col) to[r * kChainLd + col] = to[col * kChainLd + r] = v[e];
         }
-        store(p, fp, tp.hi, tp.lo, InTile{});
+    };
+    const auto product = [&](const double* x, const double* y) __attribute__((always_inline)) {
+        f64x4 sum = {0.0, 0.0, 0.0, 0.0};
+        if (!active) return sum;
+        const double* px = x + (bi * 16 + (lane & 15u)) * kChainLd + (lane >> 4);
+        const double* py = y + (bj * 16 + (lane & 15u)) * kChainLd + (lane >> 4);
+        for (uint32_t k = 0; k < blocks * 16; k += 16)
+#pragma unroll
+            for (uint32_t kk = 0; kk < 16; kk += 4) sum = mfma64(px[k + kk], py[k + kk], sum);
+        return sum;
+    };
+    for (int k = 0;; ++k) {
+        store(a, ta);
+        if (k) store(q, tq);
         __syncthreads();
-        q = k ? product(tp, tq, pow2(-g.sp - g.sq)) : p;
+        const f64x4 sq = product(ta, ta);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[e] = (double)g.c * sq[e] + (double)g.b * a[e];
+            if (row + (uint32_t)e * 4 == col) p[e] += (double)g.a;
+        }
+        store(p, tp);
+        __syncthreads();
+        q = k ? product(tp, tq) : p;
         if (k + 1 == g.steps) break;
-        z = product(tp, ta, pow2(-g.sp - g.sa));
-        __syncthreads();   // every wave has read the old q
-        store(q, fq, tq.hi, tq.lo, InTile{});
-        store(z, fz, tz.hi, tz.lo, InTile{});
+        store(product(tp, ta), tz);
         __syncthreads();
-        a = product(tz, tp, pow2(-g.sz - g.sp));
+        a = product(tz, tp);
     }
-    // over the partial sums, which every wave has read
-    GLOBAL _Float16* to = at<_Float16>(ws, t.parts.lo());
-    store(q, fq, to, to + kPad * kPad, std::integral_constant<uint32_t, kPad>{});
+    // Q / (|u| + eps) over the partial sums, which every wave has read
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t r = row + (uint32_t)e * 4;
+        if (active && r >= col) at_base[tri_at(r, col)] = q[e] * inv;
+    }
 }
 
 // The end of a run of steps that is not the last: X in fp32, as u lay.
 constexpr int kEndAgain = kNumEnds;
 
-// Q X, 64 columns at a time as small gram reads them; workgroups of 64 columns up to 4,096 and of 256 beyond, where
-// reading Q anew would cost as much as X.
+// Q X, 64 columns at a time as small gram reads them, 16 to a wave; workgroups of 64 columns up to 4,096 and of 256
+// beyond, where reading Q anew would cost as much as X.
 template <int IN, int END>
 __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __restrict__ mats,
-                                                             const DevTile* __restrict__ tiles, char* ws, float eps, int sx,
-                                                             int sq, int again, ProductArgs g)
+                                                             const DevTile* __restrict__ tiles, char* ws, int again,
+                                                             ProductArgs g)
 {
     if (g.step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
     const uint32_t tid = threadIdx.x;
@@ -1323,34 +1260,49 @@ __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __
     const DevTile t = tiles[blockIdx.x];
     const DevMatrix& mx = mats[t.mat];
     const bool tall = mx.tall != 0, row16 = mx.row16 != 0;
-    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols;
+    const uint32_t rows = (uint32_t)mx.rows, cols = (uint32_t)mx.cols, l = tall ? rows : cols, s = tall ? cols : rows;
     const uint64_t in = g.step || again ? (uint64_t)(uintptr_t)ws + t.parts.u() : mx.ptr[1];
     const bool by4 = rows_by4(cols, in);
     const uint32_t run = (uint32_t)small_apply_cols(t.parts.lp), j0 = t.col * run, j1 = j0 + run < l ? j0 + run : l;
-    const uint32_t lane = tid & 63u, wave = tid >> 6, wr = wave / 2 * 32, wc = wave % 2 * 32;
-    const float stepf = (float)((double)g.lr * mx.factor), f = pow2(-sq - sx);
-    __shared__ PairTile q, x;
+    const uint32_t lane = tid & 63u, wave = tid >> 6, blocks = (s + 15) / 16;
+    const float stepf = (float)((double)g.lr * mx.factor);
+    constexpr uint32_t kBlocks = kPad / 16;
+    __shared__ double q[kPad * kChainLd];
+    __shared__ alignas(16) float x[kPad * kXLd];
     constexpr int kOutLd = kPad + 4;
     __shared__ alignas(16) float out[kPad * kOutLd];   // as the matrix lies: rows of the caller's
     f32x4 v[4];
     load_tile<IN>(in, by4, rows, cols, tall ? j0 : 0, tall ? 0 : j0, v);
-    for (uint32_t k = tid; k < kPad * 8; k += 256) {
-        const GLOBAL _Float16* from = at<const _Float16>(ws, t.parts.lo()) + k * 8;
-        const uint32_t o = k / 8 * kTileLd + k % 8 * 8;
-        *reinterpret_cast<f16x8*>(q.hi + o) = *reinterpret_cast<const GLOBAL f16x8*>(from);
-        *reinterpret_cast<f16x8*>(q.lo + o) = *reinterpret_cast<const GLOBAL f16x8*>(from + kPad * kPad);
+    const GLOBAL double* from_q = at<const double>(ws, t.parts.base);
+    for (uint32_t k = tid; k < blocks * 16 * kPad; k += 256) {
+        const uint32_t r = k / kPad, c = k % kPad;
+        if (c < blocks * 16) q[r * kChainLd + c] = from_q[r >= c ? tri_at(r, c) : tri_at(c, r)];
     }
-    const double scale = again ? pow2(sx) : norm_scale(mx, ws, eps, sx);
     for (uint32_t j = j0; j < j1; j += kPad) {
-        store_tile(v, scale, !tall, x.hi, x.lo);   // rows are columns of X
+        store_tile_f32(v, tall, x);
         __syncthreads();
         if (j + kPad < j1) load_tile<IN>(in, by4, rows, cols, tall ? j + kPad : 0, tall ? 0 : j + kPad, v);
-        f32x16 main = zeros16(), cross = zeros16();
-        pair_product(q, x, wr, wc, lane, main, cross);
+        f64x4 acc[kBlocks];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t i = wr + result_row(e, lane), c = wc + (lane & 31u);
-            out[tall ? c * kOutLd + i : i * kOutLd + c] = (main[e] + cross[e] * (1.0f / kLoScale)) * f;
+        for (uint32_t i = 0; i < kBlocks; ++i) acc[i] = f64x4{0.0, 0.0, 0.0, 0.0};
+        const uint32_t c = wave * 16 + (lane & 15u);
+        for (uint32_t k4 = 0; k4 < blocks * 16; k4 += 4) {
+            const uint32_t k = k4 + (lane >> 4);
+            const double o = (double)x[k * kXLd + c];
+#pragma unroll
+            for (uint32_t i = 0; i < kBlocks; ++i) {
+                if (i >= blocks) break;
+                acc[i] = mfma64(q[(i * 16 + (lane & 15u)) * kChainLd + k], o, acc[i]);
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kBlocks; ++i) {
+            if (i >= blocks) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t r = i * 16 + result_row64(e, lane);
+                out[tall ? c * kOutLd + r : r * kOutLd + c] = (float)acc[i][e];
+            }
         }
         __syncthreads();
         const uint32_t r0 = tall ? j : 0, c0 = tall ? 0 : j;
@@ -1442,7 +1394,7 @@ template <int IN, int END>
 hipError_t launch_small_apply(const NsCall& call, const NsBatch& batch, bool again, const ProductArgs& q, hipStream_t stream)
 {
     ns_small_apply_kernel<IN, END><<<(uint32_t)batch.apply.count, 256, 0, stream>>>(
-        call.mats, call.tiles + batch.apply.first, call.ws, call.ns.eps, call.scales.sx, call.scales.sq, again, q);
+        call.mats, call.tiles + batch.apply.first, call.ws, again, q);
     return hipGetLastError();
 }
 
@@ -1538,7 +1490,7 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
             left -= run;
             ns_small_chain_kernel<<<(uint32_t)batch.square.count, kBlockChain, 0, stream>>>(
                 call.mats, call.tiles + batch.square.first, call.ws,
-                ChainArgs{call.ns.a, call.ns.b, call.ns.c, call.ns.eps, run, s.sa, s.sp, s.sz, s.sq, step, again});
+                ChainArgs{call.ns.a, call.ns.b, call.ns.c, call.ns.eps, run, step, again});
             if ((e = hipGetLastError()) != hipSuccess) return e;
             if (left == 0) {
                 q.count = last ? call.step : nullptr;

@@ -163,15 +163,16 @@ struct NsKind {
     bool m16;              // exp_avg is bf16
 };
 
-// Powers of two under which X, A and B are held in fp16; of a small batch, a I + b A + c A A, that
-// times A, and the product of those polynomials so far.
+// Powers of two under which X, A and B are held in fp16 (sx, sa, sb).  What small chain holds, a I + b A + c A A, that times A,
+// and the product of a run's polynomials, would fit fp16 under sp, sz and sq; it is binary64 and needs no scale, but
+// these say how far its values can reach.
 struct NsScales {
     int sx, sa, sb;
     int sp, sz, sq;
-    // Steps that small chain takes of one Gram matrix.  A rounding of 2^-22 in it grows by a^2 with every step where X has
+    // Steps that small chain takes of one Gram matrix.  A rounding of 2^-53 in it grows by a^2 with every step where X has
     // no singular value, and nothing in the polynomials brings it back, as products with X do.  So the largest
-    // a + b q + c q^2 of all of them but the last may multiply to 2^11 (the usual coefficients: 7 steps; 9 took
-    // matrices of rank one to NaN); after them X is formed and its Gram matrix anew.
+    // a + b q + c q^2 of all of them but the last may multiply to 2^11, which takes it to 2^-31 (the usual coefficients:
+    // 7 steps); after them X is formed, in fp32, and its Gram matrix anew.
     int run;
 };
 

@@ -1,11 +1,18 @@
 """Matrices of at most 64 on the shorter side against their definition in 64 bits, through the update that a step makes of
 them: a mixed step from master weights of zero with lr 1 and no decay leaves w = -O, O as the step uses it, in fp32 and
-without a 16-bit rounding.  With no gradient and a momentum of 1/2, u is half of the momentum given, exactly."""
+without a 16-bit rounding.  With no gradient and a momentum of 1/2, u is half of the momentum given, exactly.
+
+Tolerances, relative in the Frobenius norm.  Everything but u and O is in 64 bits.  A run of at most 7 steps goes on
+polynomials of one Gram matrix: at most three symmetric products a step, each rounded by at most 2^-53 of its elements,
+so by 2^-53 sqrt(64) of their largest eigenvalue; and a step multiplies what is wrong in the Gram matrix by at most a^2:
+3 K 8 a^(2 K) 2^-53 after K steps.  Between two runs X is rounded to fp32, by 2^-24, and every step after that multiplies that by a
+at most; the result's norm is at least 0.68 that of X.  O's own rounding is 2^-24.
+"""
 import pytest
 import torch
 
 import adamw_optimizer_step_apply_amd as A
-from muon_util import f32
+from muon_util import f32, far, ns64
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +30,13 @@ def updates(us, ns, company=()):
     torch.cuda.synchronize()
     assert all(torch.equal(x, u) for x, u in zip(m, every))
     return [-x for x in w[:len(us)]]
+
+
+def tolerance(ns):
+    runs = -(-ns.steps // 7)
+    run = -(-ns.steps // runs)
+    held = 3 * run * 8 * ns.a ** (2 * run) * 2.0 ** -53
+    return 2.0 ** -24 + held + sum((held + 1.5 * 2.0 ** -24) * ns.a ** (ns.steps - k * run) for k in range(1, runs))
 
 
 def polynomial(x, ns):
@@ -59,3 +73,59 @@ def test_long_matrices_of_rank_one(rows, cols, steps, signs):
     o = updates([u], ns)[0]
     assert bool(torch.isfinite(o).all())
     assert far_from_rank_one(o if rows < cols else o.T, left, right, ns) <= 3 * steps * 8 * ns.a ** steps * 2.0 ** -23
+
+
+SHAPES = [(64, 64), (64, 2048), (16, 768), (768, 16), (17, 33), (48, 100), (33, 5000), (20001, 49), (4, 64), (1, 300),
+          (300, 1), (1, 1)]
+KINDS = {"full": None, "rank_one": 0.0, "noise_1e-1": 1e-1, "noise_1e-2": 1e-2, "noise_3e-3": 3e-3, "noise_1e-4": 1e-4}
+
+
+def matrices(kind, gen, shapes=SHAPES):
+    """Normal matrices, or one direction and so much noise."""
+    rand = lambda *s: torch.randn(s, device="cuda", generator=gen, dtype=torch.float64)  # noqa: E731
+    noise = KINDS[kind]
+    return [(rand(r, c) if noise is None else rand(r, 1) * rand(1, c) + noise * rand(r, c)).float() * 1e-3
+            for r, c in shapes]
+
+
+@pytest.mark.parametrize("steps", [1, 3, 5, 7, 8, 12, 16])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_update_of_spectra(kind, steps):
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    us, ns = matrices(kind, gen), A.NewtonSchulz(steps=steps)
+    for o, u in zip(updates(us, ns), us):
+        assert far(o, ns64(u, ns)) <= tolerance(ns), (tuple(u.shape), far(o, ns64(u, ns)), tolerance(ns))
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["full", "noise_1e-2"])
+def test_results_are_the_definition_s_rounded_once(name, kind):
+    """An element is off by half a step of bf16, 2^-8 of it, and the tolerance above."""
+    code, dtype = {"f32": (A.F32, torch.float32), "bf16": (A.BF16, torch.bfloat16), "f16": (A.F16, torch.float16)}[name]
+    gen = torch.Generator(device="cuda").manual_seed(62)
+    us = [u.to(dtype) for u in matrices(kind, gen)]
+    outs = [torch.zeros(u.shape, dtype=torch.bfloat16, device="cuda") for u in us]
+    ml = A.MatrixList(SHAPES, [outs, us])
+    A.adamw_orthogonalize(code, ml, A.make_orthogonalize_workspace(ml))
+    torch.cuda.synchronize()
+    for o, u in zip(outs, us):
+        want = ns64(u)
+        most = 2.0 ** -8 * want.abs() + tolerance(A.NewtonSchulz()) * want.norm()
+        assert bool(((o.double() - want).abs() <= most).all()), tuple(u.shape)
+
+
+@pytest.mark.parametrize("magnitude", [1e-35, 1e-12, 1e12, 1e35])
+def test_magnitudes(magnitude):
+    gen = torch.Generator(device="cuda").manual_seed(63)
+    ns = A.NewtonSchulz(eps=0.0)
+    us = [(u.double() * 1e3 * magnitude).float() for u in matrices("full", gen)]
+    for o, u in zip(updates(us, ns), us):
+        assert far(o, ns64(u.double() / magnitude, ns)) <= tolerance(ns), tuple(u.shape)
+
+
+def test_a_norm_far_below_eps():
+    """X is then as small as that, and what the steps make of it is a^5 X."""
+    gen = torch.Generator(device="cuda").manual_seed(64)
+    us = [u * 1e-20 for u in matrices("full", gen)]
+    for o, u in zip(updates(us, A.NewtonSchulz()), us):
+        assert far(o, ns64(u)) <= tolerance(A.NewtonSchulz()), tuple(u.shape)
