@@ -546,6 +546,7 @@ adamw_status run_ns(const NsKind& kind, const NsScales& scales, const adamw_tens
         st = build_ns_plan(kind, list, cols, hp.scaling, (uint64_t)(uintptr_t)workspace, workspace_bytes, &plan, err);
         if (st != ADAMW_OK) return fail(st, err);
         if (cap) return refuse_under_capture();
+        plan.flatten();
         std::vector<Table> tables;
         tables.emplace_back(plan.mats);
         tables.emplace_back(plan.tiles);

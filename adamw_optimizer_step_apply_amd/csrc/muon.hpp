@@ -10,7 +10,7 @@
 //   per product step:  gram  A = X X^T (the shorter side),  poly  B = b A + c A A,
 //                      apply X = a X + B X, the last one with the result's own epilogue
 //
-// Where the shorter side of every matrix of a batch is at most kPad, all steps go on in one workgroup, on
+// Matrices whose shorter side is at most kPad go in batches of their own: all steps go on in one workgroup, on
 // polynomials of the first Gram matrix, and X is read twice instead:
 //
 //   moments      as above
@@ -26,6 +26,7 @@
 
 #include <stdint.h>
 
+#include <memory>
 #include <string>
 #include <vector>
 
@@ -139,10 +140,16 @@ struct NsBatch {
     NsLaunch moments, normalise, square, apply;
 };
 
+// The batches of one sort of matrices, small ones (at most kPad on the shorter side) or others; where a list has both,
+// the small ones' are a plan beside the others'.  So a matrix's launches, and the bits of its result, depend on its shape
+// alone, not on what else is in the list or how the workspace cuts it into batches.
 struct NsPlan {
     std::vector<DevMatrix> mats;
     std::vector<DevTile> tiles;
     std::vector<NsBatch> batches;
+    std::unique_ptr<NsPlan> small;
+
+    void flatten();   // one plan of both, the small ones' batches last
 };
 
 // What the two entry points do at both ends of the products.

@@ -181,6 +181,123 @@ int cheapest(const Cost& cost)
     return best;
 }
 
+// Matrices of one sort: every batch by the launches for small ones, or by the others.
+struct PlacedShape {
+    Shape shape;
+    uint64_t ptr[4];
+};
+constexpr int kStreamOf[4] = {ADAMW_STREAM_PARAM, ADAMW_STREAM_GRAD, ADAMW_STREAM_EXP_AVG, ADAMW_STREAM_AUX};
+
+bool is_small(const Shape& s) { return std::min(s.rows, s.cols) <= kPad; }
+
+void lay_out(const std::vector<PlacedShape>& shapes, bool small, int scaling, int64_t workspace_bytes, NsPlan* out)
+{
+    const size_t n = shapes.size();
+    out->mats.resize(n);
+    for (size_t i = 0; i < n;) {
+        size_t end = i;
+        int64_t at = kNsHeadBytes, n_tiles = 0;
+        for (; end < n; ++end) {
+            DevMatrix m{};
+            const int64_t next = place(shapes[end].shape, at, &m);
+            const int64_t t = tiles_of(shapes[end].shape.rows, kPad) * tiles_of(shapes[end].shape.cols, kPad);
+            if (next > workspace_bytes || (end > i && n_tiles + t > kMaxNsTiles)) break;
+            at = next;
+            n_tiles += t;
+            m.flat16 = 1;
+            for (int s = 0; s < 4; ++s) {
+                m.ptr[s] = shapes[end].ptr[s];
+                if (m.ptr[s] % 16) m.flat16 = 0;
+            }
+            m.row16 = m.flat16 && m.cols % 8 == 0;
+            const double R = (double)m.rows, C = (double)m.cols;
+            m.factor = scaling == ADAMW_MUON_SCALE_SPECTRAL ? std::sqrt(std::max(1.0, R / C))
+                     : scaling == ADAMW_MUON_SCALE_RMS ? 0.2 * std::sqrt(std::max(R, C)) : 1.0;
+            out->mats[end] = m;
+        }
+        // the longest sums first
+        std::vector<size_t> order;
+        for (size_t k = i; k < end; ++k) order.push_back(k);
+        NsBatch b;
+        std::vector<DevTile> tiles;
+        const auto tile = [&](size_t k, int64_t row, int64_t col) {
+            return DevTile{out->mats[k].parts, (uint32_t)k, (uint32_t)row, (uint32_t)col, 0};
+        };
+        const auto take = [&](NsLaunch* l) {
+            l->first = (int64_t)out->tiles.size();
+            l->count = (int64_t)tiles.size();
+            deal_tiles(tiles, &out->tiles);
+            tiles.clear();
+        };
+        for (size_t k : order)
+            for (uint32_t c = 0; c < out->mats[k].n_partials; ++c) tiles.push_back(tile(k, c, 0));
+        take(&b.moments);
+        b.small = small;
+        if (small) {
+            const auto runs = [&](int64_t (*cols)(int64_t)) {
+                for (size_t k : order) {
+                    const int64_t lp = out->mats[k].parts.lp;
+                    for (int64_t x = 0; x < (lp + cols(lp) - 1) / cols(lp); ++x) tiles.push_back(tile(k, 0, x));
+                }
+            };
+            runs(small_gram_cols);
+            take(&b.normalise);
+            for (size_t k : order) tiles.push_back(tile(k, 0, 0));
+            take(&b.square);
+            runs(small_apply_cols);
+            take(&b.apply);
+            out->batches.push_back(b);
+            i = end;
+            continue;
+        }
+        for (size_t k : order)
+            for (uint32_t y = 0; y < out->mats[k].parts.sp / kPad; ++y)
+                for (uint32_t x = 0; x < out->mats[k].parts.lp / kPad; ++x)
+                    tiles.push_back(tile(k, y, x));
+        take(&b.normalise);
+        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.lp > out->mats[y].parts.lp; });
+        const auto parts = [&](size_t k) -> const NsParts& { return out->mats[k].parts; };
+        b.square.kind = cheapest([&](int kind) {
+            const auto gram = [&](const auto& add) {
+                for (size_t k : order) add(square_tiles(parts(k).sp, kind), parts(k).lp);
+            };
+            const auto poly = [&](const auto& add) {
+                for (size_t k : order) add(square_tiles(parts(k).sp, kind), parts(k).sp);
+            };
+            return launch_cost(kind, true, gram) + launch_cost(kind, true, poly);
+        });
+        b.apply.kind = cheapest([&](int kind) {
+            return launch_cost(kind, false, [&](const auto& add) {
+                for (size_t k : order)
+                    add(tiles_of(parts(k).sp, kTileRows[kind]) * tiles_of(parts(k).lp, kTileCols[kind]), parts(k).sp);
+            });
+        });
+        // bands of 4 tile rows, column by column
+        constexpr int64_t kBand = 4;
+        for (size_t k : order) {
+            const int kind = b.square.kind;
+            const int64_t ty = tiles_of(out->mats[k].parts.sp, kTileRows[kind]), tx = tiles_of(out->mats[k].parts.sp, kTileCols[kind]);
+            for (int64_t y0 = 0; y0 < ty; y0 += kBand)
+                for (int64_t x = 0; x < tx; ++x)
+                    for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
+                        if (tile_needed(kind, y, x)) tiles.push_back(tile(k, y, x));
+        }
+        take(&b.square);
+        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.sp > out->mats[y].parts.sp; });
+        for (size_t k : order) {
+            const int64_t ty = tiles_of(out->mats[k].parts.sp, kTileRows[b.apply.kind]);
+            const int64_t tx = tiles_of(out->mats[k].parts.lp, kTileCols[b.apply.kind]);
+            for (int64_t y0 = 0; y0 < ty; y0 += kBand)
+                for (int64_t x = 0; x < tx; ++x)
+                    for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
+                        tiles.push_back(tile(k, y, x));
+        }
+        take(&b.apply);
+        out->batches.push_back(b);
+        i = end;
+    }
+}
+
 }  // namespace
 
 adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::string& err)
@@ -352,113 +469,38 @@ adamw_status build_ns_plan(const NsKind& kind, const adamw_tensor_list* list, co
     }
     if (!out) return ADAMW_OK;
 
+    // the matrices in the workspace by themselves, each sort for its own launches
+    std::vector<PlacedShape> of[2];
+    for (size_t i = 0; i < shapes.size(); ++i) {
+        PlacedShape p{shapes[i], {}};
+        for (int s = 0; s < 4; ++s) p.ptr[s] = plan.segs[i].ptr[kStreamOf[s]];
+        of[is_small(shapes[i])].push_back(p);
+    }
     *out = NsPlan();
-    const size_t n = shapes.size();
-    out->mats.resize(n);
-    for (size_t i = 0; i < n;) {
-        size_t end = i;
-        int64_t at = kNsHeadBytes, n_tiles = 0;
-        for (; end < n; ++end) {
-            DevMatrix m{};
-            const int64_t next = place(shapes[end], at, &m);
-            const int64_t t = tiles_of(shapes[end].rows, kPad) * tiles_of(shapes[end].cols, kPad);
-            if (next > workspace_bytes || (end > i && n_tiles + t > kMaxNsTiles)) break;
-            at = next;
-            n_tiles += t;
-            static const int kOf[4] = {ADAMW_STREAM_PARAM, ADAMW_STREAM_GRAD, ADAMW_STREAM_EXP_AVG, ADAMW_STREAM_AUX};
-            m.flat16 = 1;
-            for (int s = 0; s < 4; ++s) {
-                m.ptr[s] = plan.segs[end].ptr[kOf[s]];
-                if (m.ptr[s] % 16) m.flat16 = 0;
-            }
-            m.row16 = m.flat16 && m.cols % 8 == 0;
-            const double R = (double)m.rows, C = (double)m.cols;
-            m.factor = scaling == ADAMW_MUON_SCALE_SPECTRAL ? std::sqrt(std::max(1.0, R / C))
-                     : scaling == ADAMW_MUON_SCALE_RMS ? 0.2 * std::sqrt(std::max(R, C)) : 1.0;
-            out->mats[end] = m;
-        }
-        // the longest sums first
-        std::vector<size_t> order;
-        for (size_t k = i; k < end; ++k) order.push_back(k);
-        NsBatch b;
-        std::vector<DevTile> tiles;
-        const auto tile = [&](size_t k, int64_t row, int64_t col) {
-            return DevTile{out->mats[k].parts, (uint32_t)k, (uint32_t)row, (uint32_t)col, 0};
-        };
-        const auto take = [&](NsLaunch* l) {
-            l->first = (int64_t)out->tiles.size();
-            l->count = (int64_t)tiles.size();
-            deal_tiles(tiles, &out->tiles);
-            tiles.clear();
-        };
-        for (size_t k : order)
-            for (uint32_t c = 0; c < out->mats[k].n_partials; ++c) tiles.push_back(tile(k, c, 0));
-        take(&b.moments);
-        b.small = std::all_of(order.begin(), order.end(), [&](size_t k) { return out->mats[k].parts.sp == (uint32_t)kPad; });
-        if (b.small) {
-            const auto runs = [&](int64_t (*cols)(int64_t)) {
-                for (size_t k : order) {
-                    const int64_t lp = out->mats[k].parts.lp;
-                    for (int64_t x = 0; x < (lp + cols(lp) - 1) / cols(lp); ++x) tiles.push_back(tile(k, 0, x));
-                }
-            };
-            runs(small_gram_cols);
-            take(&b.normalise);
-            for (size_t k : order) tiles.push_back(tile(k, 0, 0));
-            take(&b.square);
-            runs(small_apply_cols);
-            take(&b.apply);
-            out->batches.push_back(b);
-            i = end;
-            continue;
-        }
-        for (size_t k : order)
-            for (uint32_t y = 0; y < out->mats[k].parts.sp / kPad; ++y)
-                for (uint32_t x = 0; x < out->mats[k].parts.lp / kPad; ++x)
-                    tiles.push_back(tile(k, y, x));
-        take(&b.normalise);
-        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.lp > out->mats[y].parts.lp; });
-        const auto parts = [&](size_t k) -> const NsParts& { return out->mats[k].parts; };
-        b.square.kind = cheapest([&](int kind) {
-            const auto gram = [&](const auto& add) {
-                for (size_t k : order) add(square_tiles(parts(k).sp, kind), parts(k).lp);
-            };
-            const auto poly = [&](const auto& add) {
-                for (size_t k : order) add(square_tiles(parts(k).sp, kind), parts(k).sp);
-            };
-            return launch_cost(kind, true, gram) + launch_cost(kind, true, poly);
-        });
-        b.apply.kind = cheapest([&](int kind) {
-            return launch_cost(kind, false, [&](const auto& add) {
-                for (size_t k : order)
-                    add(tiles_of(parts(k).sp, kTileRows[kind]) * tiles_of(parts(k).lp, kTileCols[kind]), parts(k).sp);
-            });
-        });
-        // bands of 4 tile rows, column by column
-        constexpr int64_t kBand = 4;
-        for (size_t k : order) {
-            const int kind = b.square.kind;
-            const int64_t ty = tiles_of(out->mats[k].parts.sp, kTileRows[kind]), tx = tiles_of(out->mats[k].parts.sp, kTileCols[kind]);
-            for (int64_t y0 = 0; y0 < ty; y0 += kBand)
-                for (int64_t x = 0; x < tx; ++x)
-                    for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
-                        if (tile_needed(kind, y, x)) tiles.push_back(tile(k, y, x));
-        }
-        take(&b.square);
-        std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.sp > out->mats[y].parts.sp; });
-        for (size_t k : order) {
-            const int64_t ty = tiles_of(out->mats[k].parts.sp, kTileRows[b.apply.kind]);
-            const int64_t tx = tiles_of(out->mats[k].parts.lp, kTileCols[b.apply.kind]);
-            for (int64_t y0 = 0; y0 < ty; y0 += kBand)
-                for (int64_t x = 0; x < tx; ++x)
-                    for (int64_t y = y0; y < std::min(ty, y0 + kBand); ++y)
-                        tiles.push_back(tile(k, y, x));
-        }
-        take(&b.apply);
-        out->batches.push_back(b);
-        i = end;
+    const bool first = of[0].empty();
+    lay_out(of[first], first, scaling, workspace_bytes, out);
+    if (!first && !of[1].empty()) {
+        out->small.reset(new NsPlan());
+        lay_out(of[1], true, scaling, workspace_bytes, out->small.get());
     }
     return ADAMW_OK;
+}
+
+void NsPlan::flatten()
+{
+    if (!small) return;
+    const uint32_t n_mats = (uint32_t)mats.size();
+    const int64_t n_tiles = (int64_t)tiles.size();
+    mats.insert(mats.end(), small->mats.begin(), small->mats.end());
+    for (DevTile t : small->tiles) {
+        t.mat += n_mats;
+        tiles.push_back(t);
+    }
+    for (NsBatch b : small->batches) {
+        for (NsLaunch* l : {&b.moments, &b.normalise, &b.square, &b.apply}) l->first += n_tiles;
+        batches.push_back(b);
+    }
+    small.reset();
 }
 
 }  // namespace adamw

@@ -129,3 +129,46 @@ def test_a_norm_far_below_eps():
     us = [u * 1e-20 for u in matrices("full", gen)]
     for o, u in zip(updates(us, A.NewtonSchulz()), us):
         assert far(o, ns64(u)) <= tolerance(A.NewtonSchulz()), tuple(u.shape)
+
+
+COMPANY = [(16, 48), (300, 520), (64, 64), (65, 66), (700, 30), (1, 9), (520, 260), (33, 5000)]
+
+
+def results(us, least=False):
+    outs = [torch.zeros(u.shape, dtype=torch.bfloat16, device="cuda") for u in us]
+    ml = A.MatrixList([tuple(u.shape) for u in us], [outs, us])
+    n = A.adamw_orthogonalize_workspace_bytes(ml, least=least)
+    A.adamw_orthogonalize(A.F32, ml, torch.full((n,), 0x7e, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    return outs
+
+
+def test_a_matrix_has_the_same_bits_alone_in_company_and_batch_by_batch():
+    gen = torch.Generator(device="cuda").manual_seed(65)
+    us = matrices("noise_1e-2", gen, COMPANY)
+    alone = [results([u])[0] for u in us]
+    for got in (results(us), results(us, least=True), results(us + matrices("full", gen, [(768, 768)] * 24))):
+        assert all(torch.equal(x, y) for x, y in zip(alone, got))
+    ns, one = A.NewtonSchulz(), [updates([u], A.NewtonSchulz())[0] for u in us]
+    assert all(torch.equal(x, y) for x, y in zip(one, updates(us, ns)))
+    assert all(torch.equal(x, y) for x, y in zip(one, updates(us, ns, matrices("full", gen, [(768, 768)] * 24))))
+    for o, u in zip(one, us):
+        if min(u.shape) <= 64:
+            assert far(o, ns64(u)) <= tolerance(ns)
+
+
+@pytest.mark.parametrize("flag", [0, 1])
+def test_a_skipped_step_of_both_sorts(flag):
+    """The counter goes on once for all batches, small matrices' or others', and not at all under the flag."""
+    gen = torch.Generator(device="cuda").manual_seed(66)
+    ms = matrices("full", gen, COMPANY)
+    p, g = ([torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in COMPANY] for _ in range(2))
+    kept, w = [m.clone() for m in ms], [torch.zeros(s, device="cuda") for s in COMPANY]
+    ml = A.MatrixList(COMPANY, [p, g, ms, None, w])
+    ws = torch.empty(A.adamw_orthogonalize_workspace_bytes(ml, least=True), dtype=torch.uint8, device="cuda")
+    d_step, found = (torch.tensor([v], dtype=torch.int32, device="cuda") for v in (6, flag))
+    A.adamw_muon_multi_tensor_step(A.MIXED, A.BF16, ml, A.MuonHParams(), d_step, ws, d_found_inf=found)
+    torch.cuda.synchronize()
+    assert int(d_step) == 7 - flag
+    for m, k, x in zip(ms, kept, w):
+        assert torch.equal(m, k) == bool(flag) and bool((x == 0).all()) == bool(flag)
