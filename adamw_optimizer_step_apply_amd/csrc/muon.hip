@@ -1111,7 +1111,7 @@ __global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __r
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, blocks = (s + 15) / 16;
     constexpr int kBlocks = kPad / 16;
     __shared__ alignas(16) float x[kPad * kXLd];
-    __shared__ double sum[kSmallTri];
+    __shared__ double join[2][kBlocks * (kBlocks + 1) / 2 * 256];
     f32x4 v[4];
     load_tile<IN>(in, by4, rows, cols, tall ? j0 : 0, tall ? 0 : j0, v);
     f64x4 acc[kBlocks][kBlocks];
@@ -1137,26 +1137,36 @@ __global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __r
         }
         __syncthreads();
     }
-    // the waves' parts, one after another
-    for (uint32_t w = 0; w < 4; ++w) {
-        if (wave == w) {
+    // The waves' parts: the third and fourth's to the first and second, theirs to the first.
+    const auto each = [&](auto&& f) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                if ((uint32_t)i >= blocks) break;
+        for (int i = 0; i < kBlocks; ++i) {
+            if ((uint32_t)i >= blocks) break;
 #pragma unroll
-                for (int j = 0; j <= i; ++j)
+            for (int j = 0; j <= i; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t r = (uint32_t)i * 16 + result_row64(e, lane), c = (uint32_t)j * 16 + (lane & 15u);
-                        if (c <= r) sum[tri_at(r, c)] = (w ? sum[tri_at(r, c)] : 0.0) + acc[i][j][e];
-                    }
-            }
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = f((double)acc[i][j][e], (uint32_t)((i * (i + 1) / 2 + j) * 256 + e * 64) + lane);
         }
+    };
+    for (uint32_t half = 2; half; half /= 2) {
+        if (wave >= half && wave < 2 * half) each([&](double v, uint32_t k) { return join[wave - half][k] = v; });
+        __syncthreads();
+        if (wave < half) each([&](double v, uint32_t k) { return v + join[wave][k]; });
         __syncthreads();
     }
+    if (wave) return;
     GLOBAL double* out = at<double>(ws, t.parts.base) + (uint64_t)t.col * kSmallTri;
-    const uint32_t n = tri_at(blocks * 16, 0);
-    for (uint32_t k = tid; k < n; k += 256) out[k] = sum[k];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+        if ((uint32_t)i >= blocks) break;
+#pragma unroll
+        for (int j = 0; j <= i; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t r = (uint32_t)i * 16 + result_row64(e, lane), c = (uint32_t)j * 16 + (lane & 15u);
+                if (c <= r) out[tri_at(r, c)] = acc[i][j][e];
+            }
+    }
 }
 
 struct ChainArgs {
@@ -1273,10 +1283,18 @@ __global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __
     __shared__ alignas(16) float out[kPad * kOutLd];   // as the matrix lies: rows of the caller's
     f32x4 v[4];
     load_tile<IN>(in, by4, rows, cols, tall ? j0 : 0, tall ? 0 : j0, v);
-    const GLOBAL double* from_q = at<const double>(ws, t.parts.base);
-    for (uint32_t k = tid; k < blocks * 16 * kPad; k += 256) {
-        const uint32_t r = k / kPad, c = k % kPad;
-        if (c < blocks * 16) q[r * kChainLd + c] = from_q[r >= c ? tri_at(r, c) : tri_at(c, r)];
+    {
+        // Q, all of a lane's loads under way together
+        const GLOBAL double* from = at<const double>(ws, t.parts.base);
+        const uint32_t c = lane, n = blocks * 16;
+        double w[kPad / 4];
+#pragma unroll
+        for (uint32_t i = 0; i < kPad / 4; ++i) {
+            const uint32_t r = i * 4 + wave;
+            w[i] = r < n && c < n ? from[r >= c ? tri_at(r, c) : tri_at(c, r)] : 0.0;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kPad / 4; ++i) q[(i * 4 + wave) * kChainLd + c] = w[i];
     }
     for (uint32_t j = j0; j < j1; j += kPad) {
         store_tile_f32(v, tall, x);
