@@ -375,7 +375,6 @@ struct ProductArgs {
     float a, b, c;
     int sx, sa, sb;
     int parity;      // of the product step: which of the two buffers X is in
-    int keep_lo;     // the next step is not the last
     int step;        // a Muon step: its skip mark is looked at
     float lr, decay, lrwd;   // a step's last epilogue
     int32_t* count;          // the counter that the launch advances, or null
@@ -728,7 +727,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         float dr[kPacks];   // the diagonal of A or B at the rows
     };
     const auto read_ahead = [&](int i, Input& in) {
-        if constexpr (OP == kPoly || OP == kApply) {
+        if constexpr (OP == kPoly || !kSquare) {
 #pragma unroll
             for (int h = 0; h < kPacks; ++h) {
                 const uint32_t k = (uint32_t)h * 64 + lane;
@@ -747,7 +746,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         read8(at<const float>(ws, parts.da()) + (c < sp ? c : sp - 8), dc);
     }
     Input in[2];
-    if constexpr (KIND != 0) read_ahead(0, in[0]);
+    if constexpr (KIND != 0 && OP != kLast) read_ahead(0, in[0]);
     // the matrix as the caller has it, for the last product
     const DevMatrix& mx = mats[OP == kLast ? tile.mat : 0];
     const bool tall = OP == kLast && mx.tall != 0, row16 = OP == kLast && mx.row16 != 0;
@@ -905,12 +904,15 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
     // Epilogue, 32 rows of the wave's part at a time through LDS of its own: 8 neighbours of a row to a
     // lane, and for what is needed by columns then 8 of a column.
     float* out = reinterpret_cast<float*>(lds + wave * kEpiBytes);
-    if constexpr (KIND == 0) read_ahead(0, in[0]);
+    if constexpr (KIND == 0 && OP != kLast) read_ahead(0, in[0]);
+    const float diagonal = pow2(-q.sb);   // of lo in X', a + B_ii
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const uint32_t row0 = r0 + wr + (uint32_t)i * 32;
-        const Input& now = in[i & 1];
-        if (i + 1 < MI) read_ahead(i + 1, in[(i + 1) & 1]);
+        // the last product's epilogue has no registers for a round ahead
+        const Input& now = in[OP == kLast ? 0 : i & 1];
+        if constexpr (OP == kLast) read_ahead(i, in[0]);
+        else if (i + 1 < MI) read_ahead(i + 1, in[(i + 1) & 1]);
         const float scale = OP == kLast ? pow2(-q.sb - q.sx) : 1.0f;
         EndInput<END> end[kPacks];
         if constexpr (OP == kLast) {
@@ -933,6 +935,22 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
                 out[((e & 3) + 8 * (e >> 2) + 4 * (lane >> 5)) * kEpiLd + j * 32 + (lane & 31u)] = acc[i][j][e] * scale;
         __builtin_amdgcn_wave_barrier();
         if constexpr (OP == kLast) {
+            // lo's part, by rows of X as lo lies
+#pragma unroll
+            for (int h = 0; h < kPacks; ++h) {
+                const uint32_t k = (uint32_t)h * 64 + lane;
+                f32x4* cell = reinterpret_cast<f32x4*>(out + k / kRowPacks * kEpiLd + k % kRowPacks * 8);
+                const float of_lo = __builtin_fmaf(now.dr[h], diagonal, q.a) * (1.0f / kLoScale) * pow2(-q.sx);
+                f32x4 x = cell[0], y = cell[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = __builtin_fmaf(of_lo, (float)now.x[h][e], x[e]);
+                    y[e] = __builtin_fmaf(of_lo, (float)now.x[h][e + 4], y[e]);
+                }
+                cell[0] = x;
+                cell[1] = y;
+            }
+            __builtin_amdgcn_wave_barrier();
             if (row16) {
 #pragma unroll
                 for (int h = 0; h < kPacks; ++h) {
@@ -1012,8 +1030,8 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
                 *reinterpret_cast<f32x4*>(cell) = f32x4{v[0], v[1], v[2], v[3]};
                 *reinterpret_cast<f32x4*>(cell + 4) = f32x4{v[4], v[5], v[6], v[7]};
             } else {
-                // X' * 2^sx; the last step reads no lo
-                const float f = pow2(-q.sb), of_lo = __builtin_fmaf(now.dr[h], f, q.a) * (1.0f / kLoScale);
+                // X' * 2^sx
+                const float f = pow2(-q.sb), of_lo = __builtin_fmaf(now.dr[h], diagonal, q.a) * (1.0f / kLoScale);
                 f16x8 h8, l8;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -1024,7 +1042,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
                 }
                 if (inside) {
                     *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, parts.hi(q.parity ^ 1)) + at_rc) = h8;
-                    if (q.keep_lo) *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, parts.lo()) + at_rc) = l8;
+                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, parts.lo()) + at_rc) = l8;
                 }
             }
         }
@@ -1524,7 +1542,6 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
     if (e != hipSuccess) return e;
     for (int k = 0; k < call.ns.steps; ++k) {
         q.parity = k & 1;
-        q.keep_lo = k + 2 < call.ns.steps;
         if ((e = product<kGram>(call, batch.square, q, stream)) != hipSuccess) return e;
         if ((e = product<kPoly>(call, batch.square, q, stream)) != hipSuccess) return e;
         if (k + 1 < call.ns.steps) {

@@ -1,0 +1,79 @@
+"""Matrices of more than 64 rows and columns against their definition in 64 bits, through the update that a step makes of
+them (test_gpu_small_products.py), on spectra where single roundings count: low rank, one direction and weak noise, one
+step and many.
+
+The tolerance is the distance of the documented roundings, modelled in 64 bits, from the definition, and a quarter of it
+more: where an fp32 sum differs in its last bits an element of A, B or X may be rounded the other way, which moves it as
+much as rounding did, but the same number of elements is rounded by steps of the same size.  2^-13 is for models that
+hardly round at all, of one step, where the fp32 sums' own roundings show.  And where X has no singular value those
+roundings grow like any other: an element of the next X is a sum of s / 16 matrix instructions, the linear term and lo's
+part (s: the shorter side), rounded to fp32 after each, by 0.41 2^-24 of the partial sum in the root mean square, at
+random.  Partial sums are a X and a part of B X, or a part of B X before a X joins it, and B lies in [-2.75, 0]: at most
+a |X|.  So 0.41 a sqrt(s / 16 + 2) 2^-24 of |X| together, which every later step multiplies by a at most.
+"""
+import math
+
+import pytest
+import torch
+
+import adamw_optimizer_step_apply_amd as A
+from muon_util import f32, far, ns64
+from test_gpu_small_products import updates
+
+pytestmark = pytest.mark.gpu
+SHAPES = [(65, 65), (128, 512), (512, 100), (300, 300), (768, 768), (66, 4000)]
+KINDS = ["normal", "decay", "rank 1", "rank 8", "rank 60", "rank 1 + 1e-1", "rank 1 + 1e-2", "rank 1 + 1e-3", "rank 8 + 1e-3"]
+
+
+def documented(u, ns, diagonal_steps=16):
+    """The products with the roundings that the header documents, every sum in 64 bits."""
+    h = lambda x: x.to(torch.float16).double()  # noqa: E731
+    a, b, c = f32(ns.a), f32(ns.b), f32(ns.c)
+    x = u.double()
+    x = x / (x.norm() + f32(ns.eps)) * 2.0 ** 14
+    tall = x.shape[0] > x.shape[1]
+    x = x.T if tall else x
+    for k in range(ns.steps):
+        hi = h(x)
+        lo = h((x - hi) * 2048.0) / 2048.0
+        g = hi @ hi.T * 2.0 ** -14
+        gh = h(g)
+        e = (g - gh).diagonal()
+        p = (b * (gh + torch.diag(e)) + c * (gh @ gh + (e[:, None] + e[None, :]) * gh) * 2.0 ** -14) * 2.0 ** -2
+        ph = h(p)
+        rest = (p - ph).diagonal()[:, None] * 2.0 ** -12
+        of_lo = a + (p.diagonal()[:, None] * 2.0 ** -12 if k + diagonal_steps >= ns.steps else 0.0)
+        x = (a + rest) * hi + ph @ hi * 2.0 ** -12 + of_lo * lo
+    return (x.T if tall else x) * 2.0 ** -14
+
+
+def matrix(kind, shape, gen):
+    rand = lambda *s: torch.randn(s, device="cuda", generator=gen, dtype=torch.float64)  # noqa: E731
+    x = rand(*shape)
+    if kind == "decay":
+        u, _, v = torch.linalg.svd(x.cpu(), full_matrices=False)
+        x = (u * torch.arange(1, min(shape) + 1, dtype=torch.float64) ** -1.0 @ v).cuda()
+    elif kind != "normal":
+        rank, _, noise = kind[5:].partition(" + ")
+        k = int(rank)
+        x = rand(shape[0], k) @ rand(k, shape[1]) / math.sqrt(k) + (float(noise) if noise else 0.0) * x
+    return (x * 1e-3).float()
+
+
+def sums(shape, ns):
+    one = 0.41 * ns.a * math.sqrt(min(shape) / 16 + 2) * 2.0 ** -24
+    return one * sum(ns.a ** k for k in range(ns.steps))
+
+
+def check(us, ns, diagonal_steps=16):
+    for o, u in zip(updates(us, ns), us):
+        true = ns64(u, ns)
+        model = far(documented(u, ns, diagonal_steps), true)
+        assert far(o, true) <= 1.25 * model + 2.0 ** -13 + sums(u.shape, ns), (tuple(u.shape), far(o, true), model)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3])
+@pytest.mark.parametrize("kind", KINDS)
+def test_update_of_spectra(kind, steps):
+    gen = torch.Generator(device="cuda").manual_seed(70)
+    check([matrix(kind, s, gen) for s in SHAPES], A.NewtonSchulz(steps=steps))
