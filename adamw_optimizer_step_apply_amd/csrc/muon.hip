@@ -17,12 +17,14 @@
 // sx, the products take hi (11 bits), and the epilogue of apply forms
 //   X' = (a + B_ii - fp16(B_ii)) hi + sum_k fp16(B)_ik hi_k + (a + B_ii) lo :
 // the linear term, all there is of a small singular value, is exact to 22 bits; the diagonal of B, whose
-// rounding would be the same for a whole row, is fp32; and lo takes part with the
-// diagonal of B, nearly all of B once the singular values are near 1.  A's diagonal
-// is treated alike in poly.  On matrices with a decaying spectrum (500 to 1000 rows,
-// simulated in binary64 with these roundings) the result is 2.5e-4 from the exact one in
-// the Frobenius norm, on normal random ones 3.6e-4 to 1.1e-3; fp16 X alone 3.7e-3 and
-// bf16 throughout 3e-2.
+// rounding would be the same for a whole row, is fp32; and in the last steps lo takes part with the
+// diagonal of B, nearly all of B once the singular values are near 1.  In the steps before those its factor is a alone:
+// where X has no singular value lo has to go the way of a hi, whose rounding it undoes, and B_ii lo would be left over and be
+// multiplied by a in every step that follows (a 65 x 65 matrix of rank one after eight steps: 0.2 off with B_ii in all of
+// them, 1.2e-3 with it in three; normal random matrices of full rank the other way round, 1.4e-3 and 2e-3).  A's diagonal
+// is treated like B's in poly.  Simulated in binary64 with these roundings (65 to 768 rows), five steps: 3.5e-4 to 8e-4 from
+// the definition in the Frobenius norm on full rank, 2e-4 to 1.2e-3 on rank 1 to 60, with noise of 1e-3 and without;
+// fp16 X alone 3.7e-3 and bf16 throughout 3e-2 on full rank.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -375,6 +377,7 @@ struct ProductArgs {
     float a, b, c;
     int sx, sa, sb;
     int parity;      // of the product step: which of the two buffers X is in
+    int diagonal_lo; // B's diagonal takes part in the product with lo (NsScales::lo_steps)
     int step;        // a Muon step: its skip mark is looked at
     float lr, decay, lrwd;   // a step's last epilogue
     int32_t* count;          // the counter that the launch advances, or null
@@ -905,7 +908,8 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
     // lane, and for what is needed by columns then 8 of a column.
     float* out = reinterpret_cast<float*>(lds + wave * kEpiBytes);
     if constexpr (KIND == 0 && OP != kLast) read_ahead(0, in[0]);
-    const float diagonal = pow2(-q.sb);   // of lo in X', a + B_ii
+    // of lo in X': a, and where it takes part B's diagonal
+    const float diagonal = q.diagonal_lo ? pow2(-q.sb) : 0.0f;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const uint32_t row0 = r0 + wr + (uint32_t)i * 32;
@@ -1542,6 +1546,7 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
     if (e != hipSuccess) return e;
     for (int k = 0; k < call.ns.steps; ++k) {
         q.parity = k & 1;
+        q.diagonal_lo = k + call.scales.lo_steps >= call.ns.steps;
         if ((e = product<kGram>(call, batch.square, q, stream)) != hipSuccess) return e;
         if ((e = product<kPoly>(call, batch.square, q, stream)) != hipSuccess) return e;
         if (k + 1 < call.ns.steps) {

@@ -181,6 +181,9 @@ struct NsScales {
     // a + b q + c q^2 of all of them but the last may multiply to 2^11, which takes it to 2^-31 (the usual coefficients:
     // 7 steps); after them X is formed, in fp32, and its Gram matrix anew.
     int run;
+    // Last steps of the larger matrices in which B's diagonal takes part in the product with lo (muon.hip): as many as
+    // multiply what that leaves in absent directions by at most 16 after it (the usual coefficients: 3).
+    int lo_steps;
 };
 
 adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::string& err);

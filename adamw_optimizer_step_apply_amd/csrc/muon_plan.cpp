@@ -365,6 +365,8 @@ adamw_status check_ns(const adamw_newton_schulz* ns, NsScales* scales, std::stri
     // runs of equal length, of at most the steps whose polynomials stay under 2^11
     const int most_run = whole > 1.0 ? 1 + (int)std::min(std::log(2048.0) / std::log(whole), (double)ADAMW_NS_MAX_STEPS)
                                      : (int)ADAMW_NS_MAX_STEPS;
+    scales->lo_steps = whole > 1.0 ? 1 + (int)std::min(std::log(16.0) / std::log(whole), (double)ADAMW_NS_MAX_STEPS)
+                                   : (int)ADAMW_NS_MAX_STEPS;
     const int runs = (ns->steps + most_run - 1) / most_run;
     scales->run = (ns->steps + runs - 1) / runs;
     scales->sq = under(std::pow(std::max(whole, 1.0), scales->run));

@@ -458,19 +458,23 @@ adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtyp
  * five steps singular values above about a hundredth of |U| end between 0.68 and 1.14, as
  * the Muon optimizer uses them.
  *
- * Numerics.  |U| is summed in binary64.  X is held as a sum of two fp16 values (22 bits)
+ * Numerics.  |U| is summed in binary64.  The results are those of the definition within the distances below (relative, in
+ * the Frobenius norm), beside the rounding to bf16 where that is the result's type (1.7e-3); the same call gives
+ * the same bits.
+ * Matrices of more than 64 rows and columns: X is held as a sum of two fp16 values (22 bits)
  * under a power of two, X X^T and the polynomial of it as fp16 with their diagonals in
  * fp32; products are of fp16 values with fp32 sums, and the linear term a X keeps all 22
- * bits (in the last step 11), so that small singular values, which a step multiplies by
- * a, are not drowned in rounding.  Matrices of at most 64 rows or columns, where a call
- * (or the part of its list that the workspace takes at a time) has no others, are held
- * in 22 bits throughout.  The result is within about 1e-3 (relative, in the Frobenius norm) of
- * the definition's value, of such small matrices 1e-4, beside its rounding to bf16 (1.7e-3); the same call
- * gives the same bits.  Where a matrix has few singular values, or some far below the others, each step
- * multiplies by a what rounding put in the others' place: after five steps a matrix of rank one is within
- * 7e-3 (65 x 65) to 1.3e-3 (768 x 768), 3.4 times that with each step more, until from 9 steps on its result
- * holds directions that are rounding's; small matrices by themselves are as near as binary32, which comes there
- * with 12.
+ * bits, so that small singular values, which a step multiplies by a, are not drowned in rounding.  With the default
+ * coefficients 3e-4 to 1e-3 after up to five steps where the singular values are of one order, and at most, on any spectrum,
+ * 1e-3 after one or two steps, 1.5e-3 after three, 3.5e-3 after five, 5e-3 after seven and 8e-3 after eight (bounds from the
+ * roundings' model, held by tests on 65 to 768 rows).  Where singular values are missing, each step multiplies by a what
+ * rounding put in their place: 2.5e-2 after nine steps, 3.4 times that with each step more, until from 12 steps on the result
+ * holds directions that are rounding's (binary32 throughout comes there with 12 as well).  Elements of X below 2^-49, as
+ * of a matrix whose norm is far below eps, count as zero.
+ * Matrices of at most 64 rows or columns: everything between U and the result is binary64, and the result is rounded once
+ * to binary32: 7e-7 up to seven steps on any spectrum.  Of more steps X is rounded to binary32 once or twice on the way,
+ * which each step after that multiplies by a where singular values are missing: 1e-5 after eight steps, 2e-4 after
+ * twelve, 3e-2 after sixteen.
  * A matrix with an inf or NaN element has NaN in every element of its result, a zero matrix
  * zeros; no matrix changes another's.
  *
