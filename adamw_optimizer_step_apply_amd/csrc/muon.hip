@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
 // of 64 in launches of 78 to 144 (768 x 768) are latencies, 7 to 10 us each.
 // ---------------------------------------------------------------------------
 
-enum NsOp { kGram, kPoly, kApply, kLast };
+enum NsOp { kGram, kGramLong, kPoly, kApply, kLast };
 
 struct ProductArgs {
     float a, b, c;
@@ -681,7 +681,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
                                                                         ProductArgs q)
 {
     using S = TileShape<KIND>;
-    constexpr bool kSquare = OP == kGram || OP == kPoly;
+    constexpr bool kGramOp = OP == kGram || OP == kGramLong, kSquare = kGramOp || OP == kPoly;
     using StageP = RowStage<S::rows, S::waves>;
     using StageQ = std::conditional_t<kSquare, RowStage<S::cols, S::waves>, ColumnStage<S::cols, S::waves>>;
     constexpr int WR = S::rows / 2, WC = S::cols / S::wx;   // a wave's part of the tile
@@ -704,7 +704,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 
     StageP stage_p;
     StageQ stage_q;
-    if constexpr (OP == kGram) {
+    if constexpr (kGramOp) {
         stage_p.init(x_now, r0, sp, lp, wave, lane);
         stage_q.init(x_now, c0, sp, lp, wave, lane);
     } else if constexpr (OP == kPoly) {
@@ -771,7 +771,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const uint32_t nk = (OP == kGram ? lp : sp) / kPad;
+    const uint32_t nk = (kGramOp ? lp : sp) / kPad;
     struct Operands {
         f16x8 a[MI], b[NI];
     };
@@ -835,6 +835,30 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         fill = buf;
         buf = buf + 1 == S::stages ? 0 : buf + 1;
     };
+    // A long sum in two levels.  An fp32 sum of l / 16 like terms, as of equal columns, is off by l / 16 2^-25 of it at worst,
+    // each element by its own share: 65 x 4 M of rank one came out 6.4e-3 off after five steps, 1.9e-3 this way, as 65 x 64 K is.
+    f32x16 total[MI][NI];
+    const bool in_two = OP == kGramLong && lp > kLongSum;
+    if constexpr (OP == kGramLong) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) total[i][j] = acc[i][j];
+    }
+    const auto carry = [&](uint32_t done) __attribute__((always_inline)) {
+        if constexpr (OP == kGramLong) {
+            if (!in_two || done % kLongRun) return;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        total[i][j][e] += acc[i][j][e];
+                        acc[i][j][e] = 0.0f;
+                    }
+        }
+    };
     using Yes = std::true_type;
     using No = std::false_type;
     uint32_t t = 0;
@@ -865,6 +889,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
         for (; t + 2 < nk; t += 2) {
             summing_step(t, No{}, No{});
             summing_step(t + 1, Yes{}, No{});
+            carry(t + 2);
         }
         if (t + 1 < nk) {
             summing_step(t, No{}, No{});
@@ -899,8 +924,19 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
             for (; t < r0 / kPad; ++t) summing_step(t, No{}, No{});
             for (; t < (r0 + S::rows) / kPad && t + 1 < nk; ++t) summing_step(t, Yes{}, No{});
         }
-        for (; t + 1 < nk; ++t) summing_step(t, No{}, No{});
+        for (; t + 1 < nk; ++t) {
+            summing_step(t, No{}, No{});
+            carry(t + 1);
+        }
         summing_step(t, std::bool_constant<!kSquare>{}, Yes{});
+    }
+    if constexpr (OP == kGramLong) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] += total[i][j][e];
     }
     wait_and_meet<0>();   // the operands' room is free
 
@@ -1009,7 +1045,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
                 }
             }
             if constexpr (kSquare) {
-                if constexpr (OP == kGram) {
+                if constexpr (kGramOp) {
                     const float f = pow2(q.sa - 2 * q.sx);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= f;
@@ -1025,11 +1061,11 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
                     }
                 }
                 if (inside) {
-                    store_diagonal(at<float>(ws, OP == kGram ? parts.da() : parts.db()), r, c, v);
+                    store_diagonal(at<float>(ws, kGramOp ? parts.da() : parts.db()), r, c, v);
                     f16x8 w;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = (_Float16)v[e];
-                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? parts.a() : parts.b()) + at_rc) = w;
+                    *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, kGramOp ? parts.a() : parts.b()) + at_rc) = w;
                 }
                 *reinterpret_cast<f32x4*>(cell) = f32x4{v[0], v[1], v[2], v[3]};
                 *reinterpret_cast<f32x4*>(cell + 4) = f32x4{v[4], v[5], v[6], v[7]};
@@ -1062,7 +1098,7 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = (_Float16)out[(lr + e) * kEpiLd + lc];
                     if (r < sp && c < sp)
-                        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, OP == kGram ? parts.a() : parts.b()) + (uint64_t)c * sp + r) = w;
+                        *reinterpret_cast<GLOBAL f16x8*>(at<_Float16>(ws, kGramOp ? parts.a() : parts.b()) + (uint64_t)c * sp + r) = w;
                 }
             }
             __builtin_amdgcn_wave_barrier();
@@ -1410,6 +1446,14 @@ hipError_t product(const NsCall& call, const NsLaunch& l, const ProductArgs& q, 
                        : launch_product<2, OP, END>(call, l, q, stream);
 }
 
+// Tiles of 256 have no registers for a long sum's second level (planner).
+hipError_t gram(const NsCall& call, const NsBatch& batch, const ProductArgs& q, hipStream_t stream)
+{
+    if (!batch.long_sums) return product<kGram>(call, batch.square, q, stream);
+    return batch.square.kind == 1 ? launch_product<1, kGramLong, 0>(call, batch.square, q, stream)
+                                  : launch_product<2, kGramLong, 0>(call, batch.square, q, stream);
+}
+
 template <int IN>
 hipError_t moments(const NsCall& call, const NsLaunch& l, bool step, const MomentCoef& c, const StepRule& rule,
                    hipStream_t stream)
@@ -1547,7 +1591,7 @@ hipError_t launch_ns_batch(const NsCall& call, const NsBatch& batch, bool last, 
     for (int k = 0; k < call.ns.steps; ++k) {
         q.parity = k & 1;
         q.diagonal_lo = k + call.scales.lo_steps >= call.ns.steps;
-        if ((e = product<kGram>(call, batch.square, q, stream)) != hipSuccess) return e;
+        if ((e = gram(call, batch, q, stream)) != hipSuccess) return e;
         if ((e = product<kPoly>(call, batch.square, q, stream)) != hipSuccess) return e;
         if (k + 1 < call.ns.steps) {
             e = product<kApply>(call, batch.apply, q, stream);

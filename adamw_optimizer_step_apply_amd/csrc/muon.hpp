@@ -79,6 +79,11 @@ constexpr bool tile_mirrored(int kind, int64_t row, int64_t col)
     return (col + 1) * kTileCols[kind] <= row * kTileRows[kind];
 }
 
+// Gram matrices of more columns are summed in two levels, the first over kLongRun summing steps (an even number): of shorter
+// ones the fp32 sums are off by at most 2^-11, of these by 2^-14 and 2^-25 for each run.
+constexpr int64_t kLongSum = INT64_C(1) << 18;
+constexpr uint32_t kLongRun = 512;
+
 constexpr int64_t kMaxNsSide = INT64_C(1) << 30, kMaxNsShort = INT64_C(1) << 20;
 // A grid counts at most 2^32 - 1 lanes.
 constexpr int64_t kMaxNsTiles = (int64_t)UINT32_MAX / 512;
@@ -135,6 +140,7 @@ struct NsLaunch {
 
 struct NsBatch {
     bool small = false;
+    bool long_sums = false;   // a matrix has more than kLongSum columns, and the squares' tiles are of kind 1 or 2
     // square: gram and poly.  Of a small batch, normalise: the runs of columns of small gram, square: the matrices
     // (small chain), apply: the runs of small apply
     NsLaunch moments, normalise, square, apply;

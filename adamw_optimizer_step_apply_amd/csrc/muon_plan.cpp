@@ -173,10 +173,10 @@ double launch_cost(int kind, bool square, const Each& each)
 }
 
 template <typename Cost>
-int cheapest(const Cost& cost)
+int cheapest(int first, const Cost& cost)
 {
-    int best = 0;
-    for (int kind = 1; kind < kTileKinds; ++kind)
+    int best = first;
+    for (int kind = first + 1; kind < kTileKinds; ++kind)
         if (cost(kind) < cost(best)) best = kind;
     return best;
 }
@@ -257,7 +257,8 @@ void lay_out(const std::vector<PlacedShape>& shapes, bool small, int scaling, in
         take(&b.normalise);
         std::stable_sort(order.begin(), order.end(), [&](size_t x, size_t y) { return out->mats[x].parts.lp > out->mats[y].parts.lp; });
         const auto parts = [&](size_t k) -> const NsParts& { return out->mats[k].parts; };
-        b.square.kind = cheapest([&](int kind) {
+        b.long_sums = std::any_of(order.begin(), order.end(), [&](size_t k) { return parts(k).lp > kLongSum; });
+        b.square.kind = cheapest(b.long_sums ? 1 : 0, [&](int kind) {
             const auto gram = [&](const auto& add) {
                 for (size_t k : order) add(square_tiles(parts(k).sp, kind), parts(k).lp);
             };
@@ -266,7 +267,7 @@ void lay_out(const std::vector<PlacedShape>& shapes, bool small, int scaling, in
             };
             return launch_cost(kind, true, gram) + launch_cost(kind, true, poly);
         });
-        b.apply.kind = cheapest([&](int kind) {
+        b.apply.kind = cheapest(0, [&](int kind) {
             return launch_cost(kind, false, [&](const auto& add) {
                 for (size_t k : order)
                     add(tiles_of(parts(k).sp, kTileRows[kind]) * tiles_of(parts(k).lp, kTileCols[kind]), parts(k).sp);

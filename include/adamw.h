@@ -473,8 +473,8 @@ adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtyp
  * of a matrix whose norm is far below eps, count as zero.
  * Matrices of at most 64 rows or columns: everything between U and the result is binary64, and the result is rounded once
  * to binary32: 7e-7 up to seven steps on any spectrum.  Of more steps X is rounded to binary32 once or twice on the way,
- * which each step after that multiplies by a where singular values are missing: 1e-5 after eight steps, 2e-4 after
- * twelve, 3e-2 after sixteen.
+ * which each step after that multiplies by a where singular values are missing: 1.3e-5 after eight steps, 2.3e-4 after
+ * twelve, 3.3e-2 after sixteen.
  * A matrix with an inf or NaN element has NaN in every element of its result, a zero matrix
  * zeros; no matrix changes another's.
  *

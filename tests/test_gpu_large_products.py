@@ -18,7 +18,7 @@ import torch
 
 import adamw_optimizer_step_apply_amd as A
 from muon_util import f32, far, ns64
-from test_gpu_small_products import updates
+from test_gpu_small_products import far_from_rank_one, updates
 
 pytestmark = pytest.mark.gpu
 SHAPES = [(65, 65), (128, 512), (512, 100), (300, 300), (768, 768), (66, 4000)]
@@ -100,3 +100,34 @@ def test_other_coefficients(kind, coefficients, diagonal_steps):
     """Steps in which B's diagonal takes part with lo: those after which the others multiply by at most 16 together."""
     gen = torch.Generator(device="cuda").manual_seed(72)
     check([matrix(kind, s, gen) for s in SHAPES], A.NewtonSchulz(*coefficients, steps=8), diagonal_steps)
+
+
+# long matrices, whose sums go in two levels, and one whose sums do not
+LONG = [(65, 4194304), (8388609, 66), (130, 1048576), (300, 400000), (65, 262144)]
+
+
+@pytest.mark.parametrize("signs", [False, True])
+@pytest.mark.parametrize("shape", LONG)
+def test_long_matrices_of_rank_one(shape, signs):
+    """Equal columns (but for their sign) add up like terms, whose roundings in fp32 add up too.  The length is no reason
+    for more than the header's bound of five steps."""
+    gen = torch.Generator(device="cuda").manual_seed(73)
+    short, long = min(shape), max(shape)
+    left, right = torch.randn(short, device="cuda", generator=gen) * 1e-3, torch.ones(long, device="cuda")
+    if signs:
+        right = torch.where(torch.rand(long, device="cuda", generator=gen) < 0.5, -right, right)
+    wide = shape[0] < shape[1]
+    ns = A.NewtonSchulz()
+    o = updates([torch.outer(left, right) if wide else torch.outer(right, left)], ns)[0]
+    assert far_from_rank_one(o if wide else o.T, left, right, ns) <= 3.5e-3
+
+
+def test_a_long_matrix_changes_no_other_s_bits():
+    """Next to one, the others' squares go through the same launches, in one level as by themselves."""
+    gen = torch.Generator(device="cuda").manual_seed(74)
+    us = [matrix("normal", s, gen) for s in [(100, 200), (66, 200000), (768, 768), (66, 300001)]]
+    ns = A.NewtonSchulz()
+    alone = [updates([u], ns)[0] for u in us]
+    assert all(torch.equal(x, y) for x, y in zip(alone, updates(us, ns)))
+    for o, u in zip(alone, us):
+        assert far(o, ns64(u, ns)) <= 3.5e-3
