@@ -1123,6 +1123,8 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 // Place of element (i, j), j <= i, of a lower triangle.
 __device__ __forceinline__ uint32_t tri_at(uint32_t i, uint32_t j) { return i * (i + 1) / 2 + j; }
 
+// The kernels that use it are compiled for two waves a SIMD or more, so that sums lie in VGPRs: in AGPRs, which the compiler
+// takes where it may use 512 registers, a wave's instructions took 140 cycles each instead of 64 (MI355X).
 __device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c)
 {
     return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
@@ -1155,7 +1157,7 @@ __device__ __forceinline__ void store_tile_f32(const f32x4 (&x)[4], bool transpo
 // 64 columns and all 16 x 16 blocks on and below the diagonal that the matrix has rows for, so that a row block's operand is
 // read once; the next 64 columns are under way while the last ones are multiplied.
 template <int IN>
-__global__ __launch_bounds__(256) void ns_small_gram_kernel(const DevMatrix* __restrict__ mats,
+__global__ __launch_bounds__(256, 2) void ns_small_gram_kernel(const DevMatrix* __restrict__ mats,
                                                             const DevTile* __restrict__ tiles, char* ws, int step, int again)
 {
     if (step && reinterpret_cast<const NsScalars*>(ws)->skip) return;
@@ -1318,7 +1320,7 @@ constexpr int kEndAgain = kNumEnds;
 // Q X, 64 columns at a time as small gram reads them, 16 to a wave; workgroups of 64 columns up to 4,096 and of 256
 // beyond, where reading Q anew would cost as much as X.
 template <int IN, int END>
-__global__ __launch_bounds__(256) void ns_small_apply_kernel(const DevMatrix* __restrict__ mats,
+__global__ __launch_bounds__(256, 2) void ns_small_apply_kernel(const DevMatrix* __restrict__ mats,
                                                              const DevTile* __restrict__ tiles, char* ws, int again,
                                                              ProductArgs g)
 {
