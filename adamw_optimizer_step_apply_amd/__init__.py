@@ -264,7 +264,8 @@ class TensorList:
             if items is None:
                 s.ptr[k] = ctypes.POINTER(ctypes.c_void_p)()
                 continue
-            arr = (ctypes.c_void_p * max(len(items), 1))(*[_addr(x) for x in items])
+            # a stream with too few entries has null in the others' place, which a call that uses it refuses
+            arr = (ctypes.c_void_p * max(len(items), n, 1))(*[_addr(x) for x in items])
             self._arrays.append(arr)
             s.ptr[k] = ctypes.cast(arr, ctypes.POINTER(ctypes.c_void_p))
         s.shard_begin = int(shard_begin)

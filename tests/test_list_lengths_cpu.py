@@ -1,0 +1,62 @@
+"""Lists whose streams have too few entries, or too short a flat buffer, are refused before any HIP call: the library would
+read past the array of addresses, or a kernel past the buffer."""
+import pytest
+import torch
+
+import adamw_optimizer_step_apply_amd as A
+
+FAKE, WS = 0x7f0000000000, (0x600000000000, 1 << 34)     # never dereferenced
+COUNTER = FAKE - 4096
+
+
+def entries(streams, short, given):
+    """Three entries for each stream of `streams`, `given` for the stream `short`."""
+    at = lambda s, i: FAKE + ((s * 8 + i) << 20)  # noqa: E731
+    return [[at(s, i) for i in range(given if s == short else 3)] if s in streams else None for s in range(5)]
+
+
+@pytest.mark.parametrize("given", [0, 1, 2])
+@pytest.mark.parametrize("short", range(5))
+def test_steps(short, given):
+    tl = A.TensorList([64, 64, 64], entries(range(5), short, given))
+    with pytest.raises(A.AdamWError, match="null") as e:
+        A.adamw_multi_tensor_step(A.MIXED, A.BF16, tl, A.HParams(), COUNTER, stream=0)
+    assert e.value.status == A.E_INVALID
+
+
+@pytest.mark.parametrize("given", [0, 1, 2])
+@pytest.mark.parametrize("call", ["check", "norm", "clip"])
+def test_gradients(call, given):
+    tl = A.TensorList([64, 64, 64], entries([1], 1, given))
+    with pytest.raises(A.AdamWError, match="null") as e:
+        if call == "check":
+            A.adamw_check_finite(A.BF16, tl, COUNTER, stream=0)
+        elif call == "norm":
+            A.adamw_grad_norm(A.BF16, tl, COUNTER, stream=0)
+        else:
+            A.adamw_clip_grads(A.BF16, tl, A.GradClip(COUNTER), stream=0)
+    assert e.value.status == A.E_INVALID
+
+
+@pytest.mark.parametrize("given", [0, 1, 2])
+@pytest.mark.parametrize("short", [0, 1, 2, 4])
+def test_matrices(short, given):
+    shapes = [(4, 16)] * 3
+    with pytest.raises(A.AdamWError, match="null") as e:
+        A.adamw_muon_multi_tensor_step(A.MIXED, A.BF16, A.MatrixList(shapes, entries([0, 1, 2, 4], short, given)), None,
+                                       COUNTER, WS, stream=0)
+    assert e.value.status == A.E_INVALID
+    if short < 2:
+        with pytest.raises(A.AdamWError, match="null"):
+            A.adamw_orthogonalize(A.F32, A.MatrixList(shapes, entries([0, 1], short, given)), WS, stream=0)
+
+
+def test_one_entry_is_enough_for_a_flat_or_blocked_stream():
+    """Only the first HIP call fails, on a host without a GPU."""
+    if torch.cuda.is_available():
+        pytest.skip("would run on made-up addresses")
+    for streams, mask in ([[[FAKE + (s << 20)] for s in range(5)], 0x1f],
+                          [entries([0, 1], 9, 0)[:2] + [[FAKE], None, None], A.BLOCKED_STATE]):
+        with pytest.raises(A.AdamWError) as e:
+            A.adamw_multi_tensor_step(A.MIXED, A.BF16, A.TensorList([64, 64, 64], streams, flat_mask=mask), A.HParams(), COUNTER, stream=0)
+        assert e.value.status == A.E_HIP
