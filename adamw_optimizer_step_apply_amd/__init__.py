@@ -448,20 +448,26 @@ def adamw_multi_tensor_step_clipped(mode: int, p_dtype: int, tensors: TensorList
 class MatrixList(TensorList):
     """A list of row-major matrices: a TensorList with each tensor's (rows, columns).
     Tensors given have to be contiguous and of rows * columns elements (a flat
-    shard buffer: of the shard's), since only their addresses go to the library."""
+    shard buffer: of the shard's at least), since only their addresses go to the library."""
 
     def __init__(self, shapes: Sequence[Sequence[int]], streams, shard_begin: int = 0, shard_end: int = -1,
                  flat_mask: int = 0):
         self.shapes = [(int(r), int(c)) for r, c in shapes]
         numels = [r * c for r, c in self.shapes]
+        length = shard_end - shard_begin if shard_end >= 0 else sum(
+            -(-n // 8) * 8 if flat_mask & FLAT_PAD8 else n for n in numels) - shard_begin
         for k, items in enumerate(streams):
             for i, x in enumerate(items or ()):
                 if not isinstance(x, torch.Tensor):
                     continue
                 if not x.is_contiguous():
                     raise ValueError(f"stream {k}, tensor {i}: a contiguous tensor is needed, got strides {x.stride()}")
-                if not (flat_mask >> k) & 1 and x.numel() != numels[i]:
-                    raise ValueError(f"stream {k}, tensor {i}: {x.numel()} elements are no matrix of {self.shapes[i]}")
+                if (flat_mask >> k) & 1:
+                    if x.numel() < length:
+                        raise ValueError(f"stream {k}: a flat buffer of {x.numel()} elements for a shard of {length}")
+                elif i >= len(numels) or x.numel() != numels[i]:
+                    raise ValueError(f"stream {k}, tensor {i}: {x.numel()} elements are no matrix of "
+                                     f"{self.shapes[i] if i < len(numels) else 'the list'}")
         super().__init__(numels, streams, shard_begin, shard_end, flat_mask)
         self.cols = (ctypes.c_int64 * max(len(numels), 1))(*[max(c, 1) for _, c in self.shapes])
         # of each stream's tensors, for _check_streams

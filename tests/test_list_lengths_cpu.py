@@ -60,3 +60,21 @@ def test_one_entry_is_enough_for_a_flat_or_blocked_stream():
         with pytest.raises(A.AdamWError) as e:
             A.adamw_multi_tensor_step(A.MIXED, A.BF16, A.TensorList([64, 64, 64], streams, flat_mask=mask), A.HParams(), COUNTER, stream=0)
         assert e.value.status == A.E_HIP
+
+
+@pytest.mark.parametrize("mask,begin,end,length", [(0b10, 0, -1, 63 + 64 + 9), (0b10, 63, -1, 64 + 9), (0b10, 63, 127, 64),
+                                                   (0b10 | A.FLAT_PAD8, 0, -1, 64 + 64 + 16)])
+def test_a_flat_shard_buffer_of_matrices(mask, begin, end, length):
+    shapes = [(7, 9), (8, 8), (3, 3)]
+    for n, ok in ((length, True), (length + 5, True), (length - 1, False), (0, False)):
+        streams = [[FAKE, FAKE + 4096, FAKE + 8192], [torch.zeros(n, dtype=torch.bfloat16)]]
+        if ok:
+            A.MatrixList(shapes, streams, begin, end, mask)
+            continue
+        with pytest.raises(ValueError, match="flat buffer"):
+            A.MatrixList(shapes, streams, begin, end, mask)
+
+
+def test_a_tensor_too_many():
+    with pytest.raises(ValueError, match="no matrix"):
+        A.MatrixList([(2, 3)], [[torch.zeros(2, 3)] * 2])
