@@ -16,6 +16,14 @@ def entries(streams, short, given):
 
 
 @pytest.mark.parametrize("given", [0, 1, 2])
+def test_address_arrays_are_as_long_as_the_list(given):
+    """What lies behind a shorter one may be null too, so that the refusals below do not show it."""
+    tl = A.TensorList([64, 64, 64], entries(range(5), 3, given))
+    assert [len(a) for a in tl._arrays] == [3] * 5
+    assert list(tl._arrays[3])[given:] == [None] * (3 - given)
+
+
+@pytest.mark.parametrize("given", [0, 1, 2])
 @pytest.mark.parametrize("short", range(5))
 def test_steps(short, given):
     tl = A.TensorList([64, 64, 64], entries(range(5), short, given))
