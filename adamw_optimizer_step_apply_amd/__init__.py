@@ -214,6 +214,14 @@ def _result(x, dtype: torch.dtype, numel: int, name: str) -> int:
     return _addr(x)
 
 
+def _scale(x) -> int:
+    """The address of a device loss-scale state (8 bytes)."""
+    if isinstance(x, torch.Tensor) and not (x.is_cuda and x.numel() * x.element_size() >= 8 and x.is_contiguous()):
+        raise ValueError(f"d_scale: a contiguous tensor of 8 bytes on the GPU is needed (loss_scale_state), got "
+                         f"{tuple(x.shape)} {x.dtype} on {x.device}")
+    return _addr(x)
+
+
 # The current stream's address without a torch.cuda.Stream object around it, whose making takes
 # 2.7 us of host time per call (a small list's kernel takes 3.6); None on a torch without it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -327,7 +335,7 @@ def adamw_multi_tensor_step_amp(mode: int, p_dtype: int, tensors: TensorList, hp
     h = _hp(hp)
     sc = (scaler or LossScaler()).c()
     _check(_lib.adamw_multi_tensor_step_amp(mode, p_dtype, ctypes.byref(tensors.c), ctypes.byref(h), _addr(d_step),
-                                            _addr(d_found_inf), _addr(d_scale), ctypes.byref(sc),
+                                            _addr(d_found_inf), _scale(d_scale), ctypes.byref(sc),
                                             _stream(stream)))
 
 
@@ -426,7 +434,7 @@ def adamw_clip_grads(g_dtype: int, grads: TensorList, clip: GradClip, inv_loss_s
     norm is the unscaled gradients', by ``d_scale`` (a device loss-scale state) or
     ``inv_loss_scale`` (C ABI adamw_clip_grads)."""
     c = clip.c()
-    _check(_lib.adamw_clip_grads(g_dtype, ctypes.byref(grads.c), ctypes.byref(c), inv_loss_scale, _addr(d_scale),
+    _check(_lib.adamw_clip_grads(g_dtype, ctypes.byref(grads.c), ctypes.byref(c), inv_loss_scale, _scale(d_scale),
                                  _stream(stream)))
 
 
@@ -441,7 +449,7 @@ def adamw_multi_tensor_step_clipped(mode: int, p_dtype: int, tensors: TensorList
     h, c, sc = _hp(hp), clip.c(), (scaler or LossScaler()).c()
     pc = ctypes.byref(prec.c()) if prec is not None else None
     _check(_lib.adamw_multi_tensor_step_clipped(mode, p_dtype, pc, ctypes.byref(tensors.c), ctypes.byref(h),
-                                                ctypes.byref(c), _addr(d_step), _addr(d_found_inf), _addr(d_scale),
+                                                ctypes.byref(c), _addr(d_step), _addr(d_found_inf), _scale(d_scale),
                                                 ctypes.byref(sc) if advance_scale else None, _stream(stream)))
 
 
@@ -579,7 +587,7 @@ def adamw_muon_multi_tensor_step(mode: int, p_dtype: int, matrices: MatrixList, 
     _check_streams(matrices, sizes)
     _check(_lib.adamw_muon_multi_tensor_step(mode, p_dtype, pc, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(h),
                                              cc, _result(d_step, torch.int32, 1, "d_step"),
-                                             _result(d_found_inf, torch.int32, 1, "d_found_inf"), _addr(d_scale),
+                                             _result(d_found_inf, torch.int32, 1, "d_found_inf"), _scale(d_scale),
                                              *ws, _stream(stream)))
 
 
