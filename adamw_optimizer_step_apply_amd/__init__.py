@@ -478,7 +478,8 @@ class MatrixList(TensorList):
                                      f"{self.shapes[i] if i < len(numels) else 'the list'}")
         super().__init__(numels, streams, shard_begin, shard_end, flat_mask)
         self.cols = (ctypes.c_int64 * max(len(numels), 1))(*[max(c, 1) for _, c in self.shapes])
-        # of each stream's tensors, for _check_streams
+        # of each stream's tensors, for _check_streams and _check_types
+        self._types = [{x.dtype for x in items or () if isinstance(x, torch.Tensor)} for items in streams]
         self._kinds = [{(x.element_size(), x.is_cuda) for x in items or () if isinstance(x, torch.Tensor)}
                        for items in streams]
 
@@ -558,6 +559,18 @@ def _check_streams(matrices: MatrixList, sizes) -> None:
                                  f"{got} bytes{'' if on_gpu else ' on the host'}")
 
 
+_TYPES = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
+
+
+def _check_types(matrices: MatrixList, types) -> None:
+    """Floating-point tensors of a list of matrices are of the types that a call reads and writes (None: not looked at);
+    others, such as int16 words, stand for whatever the call takes them for."""
+    for k, (got, want) in enumerate(zip(matrices._types, types)):
+        for t in got if want else ():
+            if t.is_floating_point and t != want:
+                raise ValueError(f"stream {k}: {want} tensors are needed, got {t}")
+
+
 def adamw_orthogonalize(u_dtype: int, matrices: MatrixList, workspace, ns: NewtonSchulz = None, stream=None) -> None:
     """Orthogonalises every matrix of a list: the Newton-Schulz products of stream 1
     (``u_dtype``) into stream 0 (bf16), which may be the same bf16 tensors; ``workspace``
@@ -565,6 +578,7 @@ def adamw_orthogonalize(u_dtype: int, matrices: MatrixList, workspace, ns: Newto
     c = (ns or NewtonSchulz()).struct()
     ws = _workspace(workspace)
     _check_streams(matrices, (2, _ELEMENT_BYTES.get(u_dtype)))
+    _check_types(matrices, (torch.bfloat16, _TYPES.get(u_dtype)))
     _check(_lib.adamw_orthogonalize(u_dtype, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(c), *ws,
                                     _stream(stream)))
 
@@ -580,11 +594,16 @@ def adamw_muon_multi_tensor_step(mode: int, p_dtype: int, matrices: MatrixList, 
     pc = ctypes.byref(prec.c()) if prec is not None else None
     cc = ctypes.byref(clip.c()) if clip is not None else None
     ws = _workspace(workspace)
+    f32, bf16, p16 = torch.float32, torch.bfloat16, _TYPES.get(p_dtype)
     if prec is not None:
         sizes = (2, 2, _ELEMENT_BYTES.get(prec.exp_avg), None, {KAHAN_BF16: 2, KAHAN_F32: 4}.get(prec.kahan))
+        types = (bf16, bf16, _TYPES.get(prec.exp_avg), None, {KAHAN_BF16: bf16, KAHAN_F32: f32}.get(prec.kahan))
     else:
         sizes = {MIXED: (2, 2, 4, None, 4), MIXED_SPLIT: (2, 2, 4, None, 2), PURE_KAHAN: (2, 2, 2, None, 2)}.get(mode, ())
+        types = {MIXED: (p16, p16, f32, None, f32), MIXED_SPLIT: (bf16, bf16, f32, None, torch.int16),
+                 PURE_KAHAN: (bf16, bf16, bf16, None, bf16)}.get(mode, ())
     _check_streams(matrices, sizes)
+    _check_types(matrices, types)
     _check(_lib.adamw_muon_multi_tensor_step(mode, p_dtype, pc, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(h),
                                              cc, _result(d_step, torch.int32, 1, "d_step"),
                                              _result(d_found_inf, torch.int32, 1, "d_found_inf"), _scale(d_scale),
