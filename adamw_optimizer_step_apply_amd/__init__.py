@@ -480,6 +480,9 @@ class MatrixList(TensorList):
         self.cols = (ctypes.c_int64 * max(len(numels), 1))(*[max(c, 1) for _, c in self.shapes])
         # of each stream's tensors, for _check_streams and _check_types
         self._types = [{x.dtype for x in items or () if isinstance(x, torch.Tensor)} for items in streams]
+        # for _check_devices
+        self._devices = frozenset(x.device.index for items in streams for x in items or ()
+                                  if isinstance(x, torch.Tensor) and x.is_cuda)
         self._kinds = [{(x.element_size(), x.is_cuda) for x in items or () if isinstance(x, torch.Tensor)}
                        for items in streams]
 
@@ -571,6 +574,20 @@ def _check_types(matrices: MatrixList, types) -> None:
                 raise ValueError(f"stream {k}: {want} tensors are needed, got {t}")
 
 
+def _check_devices(matrices: MatrixList, workspace, stream) -> None:
+    """A list's tensors and the workspace are on the GPU that the call's stream is on."""
+    devices = matrices._devices
+    if isinstance(workspace, torch.Tensor):
+        devices = devices | {workspace.device.index}
+    if devices and stream is None:
+        devices = devices | {torch.cuda.current_device()}
+    elif isinstance(stream, torch.cuda.Stream):
+        devices = devices | {stream.device.index}
+    if len(devices) > 1:
+        raise ValueError(f"matrices, workspace and stream (the current device's by default) are on the GPUs {sorted(devices)}: "
+                         "one is needed")
+
+
 def adamw_orthogonalize(u_dtype: int, matrices: MatrixList, workspace, ns: NewtonSchulz = None, stream=None) -> None:
     """Orthogonalises every matrix of a list: the Newton-Schulz products of stream 1
     (``u_dtype``) into stream 0 (bf16), which may be the same bf16 tensors; ``workspace``
@@ -579,6 +596,7 @@ def adamw_orthogonalize(u_dtype: int, matrices: MatrixList, workspace, ns: Newto
     ws = _workspace(workspace)
     _check_streams(matrices, (2, _ELEMENT_BYTES.get(u_dtype)))
     _check_types(matrices, (torch.bfloat16, _TYPES.get(u_dtype)))
+    _check_devices(matrices, workspace, stream)
     _check(_lib.adamw_orthogonalize(u_dtype, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(c), *ws,
                                     _stream(stream)))
 
@@ -604,6 +622,7 @@ def adamw_muon_multi_tensor_step(mode: int, p_dtype: int, matrices: MatrixList, 
                  PURE_KAHAN: (bf16, bf16, bf16, None, bf16)}.get(mode, ())
     _check_streams(matrices, sizes)
     _check_types(matrices, types)
+    _check_devices(matrices, workspace, stream)
     _check(_lib.adamw_muon_multi_tensor_step(mode, p_dtype, pc, ctypes.byref(matrices.c), matrices.cols, ctypes.byref(h),
                                              cc, _result(d_step, torch.int32, 1, "d_step"),
                                              _result(d_found_inf, torch.int32, 1, "d_found_inf"), _scale(d_scale),
