@@ -491,9 +491,13 @@ typedef struct {
 
 /* Bytes of device workspace with which the two calls below work through `list` (its
  * numel, shard and ADAMW_FLAT_PAD8; pointers are not looked at) at full speed: room for
- * all its matrices, about 10 bytes an element, or of a longer list for 4 GiB of them at
- * a time.  With `least` != 0, the smallest workspace that they take: room for the
- * largest matrix.  -1 on an invalid argument.  No GPU work, no HIP call. */
+ * all its matrices, or of a longer list for 4 GiB of them at a time.  With `least` != 0, the smallest workspace that they
+ * take: room for the largest matrix.  -1 on an invalid argument.  No GPU work, no HIP call.
+ * A matrix of n elements with sides s <= l, both rounded up to multiples of 64, takes
+ *     8 s + 4 s l + max(2 s l + 4 s^2, 4 n)
+ * bytes, and 8 for every run of 4,096 elements or more (at most 256 runs), each part rounded up to 256 bytes.  That is 10
+ * bytes an element of a large square matrix and 6 of a long one, but far more of one whose shorter side is
+ * much less than 64, which counts as 64: 24.6 of 16 x 2048, 384 of a vector. */
 int64_t adamw_orthogonalize_workspace_bytes(const adamw_tensor_list* list, const int64_t* cols, int least);
 
 /* Orthogonalises every matrix of a list: stream 0 (bf16, written) = the result of the
