@@ -496,7 +496,7 @@ typedef struct {
  * A matrix of n elements with sides s <= l, both rounded up to multiples of 64, takes
  *     8 s + 4 s l + max(2 s l + 4 s^2, 4 n)
  * bytes, and 8 for every run of 4,096 elements or more (at most 256 runs), each part rounded up to 256 bytes.  That is 10
- * bytes an element of a large square matrix and 6 of a long one, but far more of one whose shorter side is
+ * bytes an element of a large square matrix and 8 of a long one, but far more of one whose shorter side is
  * much less than 64, which counts as 64: 24.6 of 16 x 2048, 384 of a vector. */
 int64_t adamw_orthogonalize_workspace_bytes(const adamw_tensor_list* list, const int64_t* cols, int least);
 
