@@ -363,12 +363,14 @@ __global__ __launch_bounds__(256) void ns_normalise_kernel(const DevMatrix* __re
 //
 // 256 x 256 tiles on 8 waves read 1 byte for 128 operations, 128 x 128 and 64 x 64 half and a quarter as many
 // operations, and are for launches that would leave CUs idle.  On MI355X, 24 matrices of 2048 x 2048 and 12 of
-// 2048 x 8192 (tiles of 256): gram 749 us (929 TFLOP/s over the tiles on and below the diagonal), poly 417 us (835),
-// apply 1,653 us (748), with a step's epilogue 1,911 us (647); a library product of 8192 x 8192 in fp16, which writes
-// little and sums long, reaches 1,402.  What bounds them: the matrix instructions, at the 2.0 to 2.2 GHz that the power
-// limit leaves, take 44, 39, 33 and 27 % of the cycles; the rest is each tile's epilogue, which no other workgroup of
-// the CU covers (one fits): of apply 2 bytes an element read and 4 written, of the squares 2 written, of a mixed step 4 read and 6 written.  Tiles
-// of 64 in launches of 78 to 144 (768 x 768) are latencies, 7 to 10 us each.
+// 2048 x 8192 (tiles of 256): gram 733 us (949 TFLOP/s over the tiles on and below the diagonal), poly 409 us (851),
+// apply 1,662 us (744), with a step's epilogue 2,028 us (610); a library product of 8192 x 8192 in fp16, which writes
+// little and sums long, reaches 1,402.  What bounds them: the matrix instructions, at 2.0 to 2.2 GHz, take 44, 39, 33 and
+// 26 % of the cycles; the largest part of the rest is each tile's epilogue, which no other workgroup of
+// the CU covers (one fits): of apply 2 bytes an element read and 4 written, of the squares 2 written, of a mixed step 6 read
+// and 6 written.  An earlier build without epilogues took 667 us for gram (of 735), 346 for poly (448), and 1,070 for
+// either apply (1,770 and 1,844): two fifths of apply are its epilogue.
+// Tiles of 64 in launches of 78 to 144 (768 x 768) are latencies, 7 to 11 us each.
 // ---------------------------------------------------------------------------
 
 enum NsOp { kGram, kGramLong, kPoly, kApply, kLast };
@@ -1118,6 +1120,12 @@ __global__ __launch_bounds__(kTileLanes[KIND], 2) void ns_product_kernel(const D
 // came out 5e-2 off after seven steps, where the definition in fp32 is 3e-5 off.  So all of it is binary64, on its
 // matrix instructions: the 2^-53 of a run of steps (NsScales::run) grows to 2^-31 at most, the result is rounded once, to
 // fp32, and X is fp32 between runs.
+//
+// On MI355X, five steps, in us: one 16 x 768 moments 2.5, small gram 4.8, small chain 10, small apply 4.5; one
+// 64 x 768 4.5, 8.4, 35 and 7.5; 64 x 1,048,576 67, 199, 125 and 245.  Short ones are latencies but for
+// chain, which the matrix instructions bound where s is over 32: a 16 x 16 x 4 product takes a SIMD 64 cycles, so the
+// 17 products of ten blocks take 18 us on one CU at least, and 22 with three blocks on two of its SIMDs.  As fp16 pairs chain took
+// 18.6 us whatever s was, and a pass of either matrix 31, which take 20 and 55 now.
 // ---------------------------------------------------------------------------
 
 // Place of element (i, j), j <= i, of a lower triangle.
