@@ -476,7 +476,7 @@ adamw_status adamw_multi_tensor_step_clipped(adamw_mode mode, adamw_dtype p_dtyp
  * which each step after that multiplies by a where singular values are missing: 1.3e-5 after eight steps, 2.3e-4 after
  * twelve, 3.3e-2 after sixteen.
  * A matrix with an inf or NaN element has NaN in every element of its result, a zero matrix
- * zeros; no matrix changes another's.
+ * zeros.  No matrix changes another's result: its bits are the same alone, in any list and with any workspace.
  *
  * Requirements: a, b, c finite, eps finite and >= 0, 1 <= steps <= ADAMW_NS_MAX_STEPS;
  * coefficients under which a singular value of [0, 1] passes 64 on the way are refused. */

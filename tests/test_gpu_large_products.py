@@ -17,8 +17,9 @@ import pytest
 import torch
 
 import adamw_optimizer_step_apply_amd as A
-from muon_util import f32, far, ns64
-from test_gpu_small_products import far_from_rank_one, updates
+from muon_util import f32, far, gradient, ns64
+import test_gpu_orthogonalize
+from test_gpu_small_products import far_from_rank_one, results, tolerance, updates
 
 pytestmark = pytest.mark.gpu
 SHAPES = [(65, 65), (128, 512), (512, 100), (300, 300), (768, 768), (66, 4000)]
@@ -131,3 +132,17 @@ def test_a_long_matrix_changes_no_other_s_bits():
     assert all(torch.equal(x, y) for x, y in zip(alone, updates(us, ns)))
     for o, u in zip(alone, us):
         assert far(o, ns64(u, ns)) <= 3.5e-3
+
+
+@pytest.mark.parametrize("name", list(test_gpu_orthogonalize.SHAPES))
+def test_lists(name):
+    """Every list that adamw_orthogonalize is tested on, at the tolerance of its sort; and what adamw_orthogonalize makes
+    of it is the step's O rounded to bf16, bit for bit."""
+    gen = torch.Generator().manual_seed(75)
+    us = [gradient(r, c, gen).float().cuda() for r, c in test_gpu_orthogonalize.SHAPES[name]]
+    ns = A.NewtonSchulz()
+    for o, u, rounded in zip(updates(us, ns), us, results(us)):
+        true = ns64(u, ns)
+        most = tolerance(ns) if min(u.shape) <= 64 else 1.25 * far(documented(u, ns), true) + 2.0 ** -13 + sums(u.shape, ns)
+        assert far(o, true) <= most, (tuple(u.shape), far(o, true), most)
+        assert torch.equal(o.bfloat16(), rounded), tuple(u.shape)
